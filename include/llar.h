@@ -212,6 +212,96 @@ int llar_reduce_scatter(llar_comm* h, const void* const* partials, void* const* 
 int llar_all_gather(llar_comm* h, const void* const* inputs, void* const* outs, int n_outs, size_t send_count,
                     llar_dtype dtype, llar_protocol protocol, void* stream);
 
+/* ---- the layer around the AllReduce: feed-forward operators ------------- *
+ * What one tensor-parallel rank computes before its partial output is summed
+ * (the agihunt.info summary's introduction: every layer reduces its shards'
+ * outputs; the yololab.net article's tensor-parallel paragraph): the gated
+ * feed-forward block's column-parallel products and the row-parallel product
+ * with its epilogue, and their backward passes.
+ *
+ * Arithmetic: products of the I/O type summed in binary32 by the matrix units
+ * (binary32 inputs: as three bfloat16 parts, which keeps 24 bits), the
+ * epilogue in binary32, each output rounded once.  The backward passes round
+ * the gradient that both of their products read (dz, or dg and du) to the I/O
+ * type once.  No atomics: the same inputs and shapes give the same bits.
+ *
+ * These calls need no communicator, allocate nothing and only enqueue kernels
+ * on `stream` (they may be captured into graphs).  All pointers are on the
+ * current device; buffers stay alive until the stream has passed the call.
+ * Outputs must not overlap an input or each other, except that `residual` may
+ * be `out` itself. */
+typedef enum {
+  LLAR_ACT_NONE = 0,
+  LLAR_ACT_RELU = 1,
+  LLAR_ACT_GELU = 2,      /* z Phi(z), Phi the normal distribution */
+  LLAR_ACT_GELU_TANH = 3, /* its tanh form: z s(2 sqrt(2/pi) (z + 0.044715 z^3)), s the logistic function */
+  LLAR_ACT_SILU = 4       /* z s(z) */
+} llar_act;
+
+typedef enum {
+  LLAR_OP_LINEAR = 0,
+  LLAR_OP_LINEAR_BACKWARD = 1,
+  LLAR_OP_GATED_FFN = 2,
+  LLAR_OP_GATED_FFN_BACKWARD = 3
+} llar_ffn_op;
+
+/* rows x cols elements, element (i, j) at data + i*row_stride + j*col_stride
+ * (strides in elements, not negative; 0 repeats a row or column of an input).
+ * An input needs a stride of 1 along one axis (any layout when that axis has
+ * one element); where stated, and for every output, col_stride must be 1.
+ * Output rows must not overlap.  Any alignment is accepted; products read
+ * 16-byte aligned operands whose contiguous axis is a multiple of 16 bytes
+ * fastest. */
+typedef struct {
+  void* data;
+  int64_t rows, cols, row_stride, col_stride;
+} llar_matrix;
+
+/* Bytes of workspace a call needs for m tokens, n outputs and k inputs (0 is
+ * possible; then NULL may be passed).  The workspace is 256-byte aligned
+ * device memory, free for other use once the stream has passed the call. */
+size_t llar_ffn_workspace(llar_ffn_op op, int64_t m, int64_t n, int64_t k, llar_dtype dtype);
+
+/* out = act(x w^T + bias) + residual:  x m x k, w n x k, out m x n.
+ * bias: n contiguous elements, or NULL.  residual: m x n with contiguous
+ * rows, or NULL.  pre: m x n output that receives x w^T + bias (what the
+ * backward pass needs), or NULL.  k == 0 sums nothing; m or n == 0: no-op.
+ *
+ * Errors of all four calls, with nothing enqueued: LLAR_ERR_ARG for a bad
+ * type, activation, shape or stride, a missing matrix, a misaligned or too
+ * small workspace; LLAR_ERR_UNSUPPORTED for a layout other than those above
+ * or a dimension above 2^30; LLAR_ERR_HIP if a launch failed. */
+int llar_linear(const llar_matrix* x, const llar_matrix* w, const void* bias, const llar_matrix* residual,
+                const llar_matrix* out, const llar_matrix* pre, llar_dtype dtype, llar_act act, void* workspace,
+                size_t workspace_bytes, void* stream);
+
+/* Backward pass of llar_linear:  dz = dy act'(pre);  dx = dz w,  dw = dz^T x,
+ * db = sum of dz over the rows (the residual's gradient is dy itself).
+ * dx (m x k), dw (n x k) and db (n contiguous elements) may each be NULL.
+ * pre (contiguous rows) is needed unless act is LLAR_ACT_NONE; dy then needs
+ * contiguous rows, and so it does when db is asked for. */
+int llar_linear_backward(const llar_matrix* dy, const llar_matrix* x, const llar_matrix* w, const llar_matrix* pre,
+                         const llar_matrix* dx, const llar_matrix* dw, void* db, llar_dtype dtype, llar_act act,
+                         void* workspace, size_t workspace_bytes, void* stream);
+
+/* out = act(x w_gate^T) * (x w_up^T), element by element:  x m x k, both
+ * weights n x k with the same strides, out m x n.  Both products, the
+ * activation and the product are one pass over x and the weights.  gate, up:
+ * m x n outputs (the same row stride) that receive both products for the
+ * backward pass, or both NULL. */
+int llar_gated_ffn(const llar_matrix* x, const llar_matrix* w_gate, const llar_matrix* w_up, const llar_matrix* out,
+                   const llar_matrix* gate, const llar_matrix* up, llar_dtype dtype, llar_act act, void* workspace,
+                   size_t workspace_bytes, void* stream);
+
+/* Backward pass of llar_gated_ffn:  dg = dh up act'(gate), du = dh act(gate);
+ * dx = dg w_gate + du w_up,  dw_gate = dg^T x,  dw_up = du^T x.  dx may be
+ * NULL, and so may dw_gate and dw_up together (they have the same strides).
+ * dh, gate and up have contiguous rows. */
+int llar_gated_ffn_backward(const llar_matrix* dh, const llar_matrix* x, const llar_matrix* w_gate,
+                            const llar_matrix* w_up, const llar_matrix* gate, const llar_matrix* up,
+                            const llar_matrix* dx, const llar_matrix* dw_gate, const llar_matrix* dw_up,
+                            llar_dtype dtype, llar_act act, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Free all resources (synchronises the device first).  NULL is a no-op. */
 int llar_destroy(llar_comm* h);
 

@@ -16,7 +16,8 @@ Python names mirror the C ABI::
     llar_all_gather(h, inputs, outs, n_outs, send_count, dtype, protocol, stream)
     llar_destroy(h)
 
-and ``Communicator`` wraps them for torch tensors.
+and ``Communicator`` wraps them for torch tensors.  ``linear``, ``gated_ffn`` and
+their backward passes (module ``ffn``) compute the partial outputs themselves.
 """
 from __future__ import annotations
 
@@ -30,6 +31,7 @@ __all__ = [
     "llar_select_protocol", "llar_debug_copy_staging", "llar_staging_bytes", "llar_get_epoch",
     "llar_get_timing", "llar_wallclock_hz", "llar_launch_geometry", "llar_floor_measure",
     "llar_status_string", "llar_last_error", "llar_get_trace", "llar_get_pipeline_trace", "Communicator", "EXPORTED_SYMBOLS",
+    "ACTIVATIONS", "linear", "linear_backward", "gated_ffn", "gated_ffn_backward",
 ]
 
 FP32, FP16, BF16 = 0, 1, 2
@@ -46,7 +48,8 @@ EXPORTED_SYMBOLS = (
     "llar_select_protocol", "llar_debug_copy_staging", "llar_staging_bytes", "llar_get_epoch",
     "llar_get_timing", "llar_wallclock_hz", "llar_launch_geometry", "llar_floor_measure",
     "llar_get_trace", "llar_get_pipeline_trace", "llar_send_recv", "llar_reduce_scatter", "llar_all_gather",
-    "llar_allreduce_noalloc",
+    "llar_allreduce_noalloc", "llar_ffn_workspace", "llar_linear", "llar_linear_backward", "llar_gated_ffn",
+    "llar_gated_ffn_backward",
 )
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -69,6 +72,7 @@ def lib() -> ctypes.CDLL:
         raise LlarError(-4, "libllar.so is not built (run __graft_entry__.build()) at %s" % library_path)
     L = ctypes.CDLL(library_path)
     vp, sz, i32, ll = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int, ctypes.c_longlong
+    i64 = ctypes.c_int64
     u32p, u64p = ctypes.POINTER(ctypes.c_uint32), ctypes.POINTER(ctypes.c_uint64)
     ip = ctypes.POINTER(ctypes.c_int)
     sig = {
@@ -95,6 +99,11 @@ def lib() -> ctypes.CDLL:
         "llar_floor_measure": (i32, [i32, i32, ctypes.POINTER(ctypes.c_double)]),
         "llar_get_trace": (i32, [vp, u64p, i32]),
         "llar_get_pipeline_trace": (i32, [vp, u64p, i32]),
+        "llar_ffn_workspace": (sz, [i32, i64, i64, i64, i32]),
+        "llar_linear": (i32, [vp] * 6 + [i32, i32, vp, sz, vp]),
+        "llar_linear_backward": (i32, [vp] * 7 + [i32, i32, vp, sz, vp]),
+        "llar_gated_ffn": (i32, [vp] * 6 + [i32, i32, vp, sz, vp]),
+        "llar_gated_ffn_backward": (i32, [vp] * 9 + [i32, i32, vp, sz, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)
@@ -419,3 +428,6 @@ class Communicator:
             self.close()
         except Exception:
             pass
+
+
+from .ffn import ACTIVATIONS, gated_ffn, gated_ffn_backward, linear, linear_backward  # noqa: E402

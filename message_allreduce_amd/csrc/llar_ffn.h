@@ -1,0 +1,84 @@
+// llar_ffn.h -- argument blocks and launchers shared by the host side of the
+// feed-forward operators (llar_ffn.hip) and their kernels (not public).
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace llar_ffn {
+
+enum Act : int { kActNone = 0, kActRelu = 1, kActGelu = 2, kActGeluTanh = 3, kActSilu = 4 };
+
+// One matrix product, or two that share their shape and strides:
+//
+//   out[b][i][j] = epilogue( sum over s, k of x[s or b][i][k] * w[s or b][j][k] )
+//
+// i < M, j < N, k < K.  `segs` = 2 adds the products of both pairs (x[0],
+// w[0]) and (x[1], w[1]); `batch` = 2 keeps them apart in out[0] and out[1].
+// A gated product takes w[0] and w[1] with the same x and combines both sums
+// of an element in its epilogue.
+// A matrix lies k-contiguous (rows `ld` elements apart) or row-contiguous
+// (consecutive k `ld` elements apart); out, resid and z rows are contiguous.
+struct GemmArgs {
+  const void* x[2];
+  const void* w[2];
+  void* out[2];
+  void* z[2];           // linear: z[0] keeps the value before the activation; gated: both projections
+  const void* bias;     // N elements or null
+  const void* resid;    // M x N or null
+  float* partial;       // split over k: [split][plane][M][npad] sums, else null
+  int64_t xld, wld, outld, zld, rld;
+  int M, N, K;
+  int segs, batch, splits;
+  int act;
+  int npad;             // row length of a partial plane
+  int vec_out;          // every output row piece of 8 elements may be accessed as one vector
+};
+
+// Tile shapes of the product kernel (rows of x by rows of w by workgroup);
+// see llar_gemm.h.
+enum Tile : int { kTile256 = 0, kTile128 = 1, kTile64 = 2, kTileCount = 3 };
+constexpr int kTileM[kTileCount] = {256, 128, 64};
+constexpr int kTileN[kTileCount] = {256, 128, 64};
+constexpr int kTileKBytes = 128;  // k extent of a tile in bytes of one row
+
+struct GemmPlan {
+  int kind;        // llar_dtype
+  int tile;
+  bool x_rows;     // x is row-contiguous
+  bool w_rows;
+  bool vec;        // 16-byte loads allowed for every chunk (see the host's rule)
+  bool gated;
+};
+
+hipError_t launch_gemm(const GemmPlan& p, const GemmArgs& a, hipStream_t s);
+
+// Sums the partial planes of a product split over k and applies its epilogue.
+hipError_t launch_join(int kind, bool gated, const GemmArgs& a, hipStream_t s);
+
+// dg = dh u act'(g), du = dh act(g), element by element (rows contiguous).
+struct GateGradArgs {
+  const void *dh, *g, *u;
+  void *dg, *du;
+  int64_t dhld, gld, uld, dld;
+  int M, N;
+  int act;
+  int vec;
+};
+hipError_t launch_gate_grad(int kind, const GateGradArgs& a, hipStream_t s);
+
+// dz = dy act'(z) (dz and z null: no activation) and the sum of dz over the
+// rows: part[c][j] = sum over row chunk c, then db[j] = sum over c in order.
+struct ActGradArgs {
+  const void *dy, *z;
+  void* dz;
+  void* db;
+  float* part;
+  int64_t dyld, zld, dzld;
+  int M, N;
+  int act;
+  int chunks;
+  int vec;
+};
+hipError_t launch_act_grad(int kind, const ActGradArgs& a, hipStream_t s);
+
+}  // namespace llar_ffn

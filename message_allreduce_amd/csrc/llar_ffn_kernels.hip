@@ -1,0 +1,168 @@
+// llar_ffn_kernels.hip -- the feed-forward operators' kernels beside the
+// product itself: joining a product split over k, the gated block's and the
+// activation's gradients, and the dispatch over instances.
+#include "llar_gemm.h"
+
+namespace llar_ffn {
+
+#define LLAR_DECL(E, x, w) hipError_t launch_gemm_##E##_##x##w(const GemmPlan&, const GemmArgs&, hipStream_t);
+LLAR_DECL(F32, 0, 0) LLAR_DECL(F32, 0, 1) LLAR_DECL(F32, 1, 0) LLAR_DECL(F32, 1, 1)
+LLAR_DECL(F16, 0, 0) LLAR_DECL(F16, 0, 1) LLAR_DECL(F16, 1, 0) LLAR_DECL(F16, 1, 1)
+LLAR_DECL(BF16, 0, 0) LLAR_DECL(BF16, 0, 1) LLAR_DECL(BF16, 1, 0) LLAR_DECL(BF16, 1, 1)
+
+hipError_t launch_gemm(const GemmPlan& p, const GemmArgs& a, hipStream_t s) {
+  typedef hipError_t (*Fn)(const GemmPlan&, const GemmArgs&, hipStream_t);
+  static const Fn table[3][2][2] = {
+      {{launch_gemm_F32_00, launch_gemm_F32_01}, {launch_gemm_F32_10, launch_gemm_F32_11}},
+      {{launch_gemm_F16_00, launch_gemm_F16_01}, {launch_gemm_F16_10, launch_gemm_F16_11}},
+      {{launch_gemm_BF16_00, launch_gemm_BF16_01}, {launch_gemm_BF16_10, launch_gemm_BF16_11}}};
+  return table[p.kind][p.x_rows][p.w_rows](p, a, s);
+}
+
+// ---- join: out = epilogue(sum over splits, in order) -------------------------------
+template <class E, bool kGated>
+__global__ __launch_bounds__(256) void k_join(GemmArgs a) {
+  const int groups = (a.N + 3) / 4;
+  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t row = id / groups;
+  const int col = (int)(id - row * groups) * 4;
+  const int b = (int)(row / a.M), m = (int)(row - (int64_t)b * a.M);
+  if (b >= a.batch) return;
+  const int planes = kGated ? 2 : a.batch;
+  float v[2][4] = {};
+#pragma unroll
+  for (int p = 0; p < (kGated ? 2 : 1); p++) {
+    const float* src = a.partial + ((int64_t)(kGated ? p : b) * a.M + m) * a.npad + col;
+    const int64_t step = (int64_t)planes * a.M * a.npad;
+    f32x4 s = {0.f, 0.f, 0.f, 0.f};
+    for (int i = 0; i < a.splits; i++) {
+      const f32x4 t = *(const f32x4*)(src + i * step);
+#pragma unroll
+      for (int e = 0; e < 4; e++) s[e] += t[e];
+    }
+#pragma unroll
+    for (int e = 0; e < 4; e++) v[p][e] = s[e];
+  }
+  finish<E, kGated, 4>(a, b, m, col, v[0], v[1]);
+}
+
+template <class E>
+hipError_t join(bool gated, const GemmArgs& a, hipStream_t s) {
+  const int64_t n = (int64_t)a.batch * a.M * ((a.N + 3) / 4);
+  if (n == 0) return hipSuccess;
+  const dim3 grid((uint32_t)((n + 255) / 256));
+  if (gated)
+    k_join<E, true><<<grid, dim3(256), 0, s>>>(a);
+  else
+    k_join<E, false><<<grid, dim3(256), 0, s>>>(a);
+  return hipGetLastError();
+}
+hipError_t launch_join(int kind, bool gated, const GemmArgs& a, hipStream_t s) {
+  return kind == 0 ? join<F32>(gated, a, s) : kind == 1 ? join<F16>(gated, a, s) : join<BF16>(gated, a, s);
+}
+
+// ---- the gated block's element-wise gradient: 3 reads, 2 writes --------------------
+template <class E>
+__global__ __launch_bounds__(256) void k_gate_grad(GateGradArgs a) {
+  typedef typename E::T T;
+  const int groups = (a.N + 7) / 8;
+  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t m = id / groups;
+  const int col = (int)(id - m * groups) * 8;
+  if (m >= a.M) return;
+  const int cnt = a.N - col;
+  const bool vec = a.vec != 0;
+  const Vals<E, 8> dh = load_vals<E, 8>((const T*)a.dh + m * a.dhld + col, cnt, vec);
+  const Vals<E, 8> g = load_vals<E, 8>((const T*)a.g + m * a.gld + col, cnt, vec);
+  const Vals<E, 8> u = load_vals<E, 8>((const T*)a.u + m * a.uld + col, cnt, vec);
+  float dg[8], du[8];
+#pragma unroll
+  for (int i = 0; i < 8; i++) {
+    float value, slope;
+    act_both(g.v[i], a.act, value, slope);
+    dg[i] = dh.v[i] * u.v[i] * slope;
+    du[i] = dh.v[i] * value;
+  }
+  store_vals<E, 8>((T*)a.dg + m * a.dld + col, dg, cnt, vec);
+  store_vals<E, 8>((T*)a.du + m * a.dld + col, du, cnt, vec);
+}
+
+hipError_t launch_gate_grad(int kind, const GateGradArgs& a, hipStream_t s) {
+  const int64_t n = (int64_t)a.M * ((a.N + 7) / 8);
+  if (n == 0) return hipSuccess;
+  const dim3 grid((uint32_t)((n + 255) / 256)), block(256);
+  if (kind == 0)
+    k_gate_grad<F32><<<grid, block, 0, s>>>(a);
+  else if (kind == 1)
+    k_gate_grad<F16><<<grid, block, 0, s>>>(a);
+  else
+    k_gate_grad<BF16><<<grid, block, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+// ---- dz = dy act'(z), and column sums of dz ----------------------------------------
+// A workgroup takes 256 columns of one row chunk: 32 lanes of 8 columns by 8
+// rows at a time; its sums go to part[chunk], and a second kernel adds the
+// chunks in order, so the bias gradient does not depend on timing.
+template <class E>
+__global__ __launch_bounds__(256) void k_act_grad(ActGradArgs a) {
+  typedef typename E::T T;
+  __shared__ float sums[8][256];
+  const int lane = threadIdx.x & 31, r = threadIdx.x >> 5;
+  const int col = (blockIdx.x * 32 + lane) * 8;
+  const int cnt = a.N - col;
+  const bool vec = a.vec != 0;
+  const int64_t m0 = (int64_t)a.M * blockIdx.y / a.chunks, m1 = (int64_t)a.M * (blockIdx.y + 1) / a.chunks;
+  float acc[8] = {};
+  if (cnt > 0) {
+    for (int64_t m = m0 + r; m < m1; m += 8) {
+      Vals<E, 8> d = load_vals<E, 8>((const T*)a.dy + m * a.dyld + col, cnt, vec);
+      if (a.z) {
+        const Vals<E, 8> z = load_vals<E, 8>((const T*)a.z + m * a.zld + col, cnt, vec);
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+          float value, slope;
+          act_both(z.v[i], a.act, value, slope);
+          d.v[i] *= slope;
+        }
+        store_vals<E, 8>((T*)a.dz + m * a.dzld + col, d.v, cnt, vec);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; i++) acc[i] += d.v[i];
+    }
+  }
+  if (!a.db) return;
+#pragma unroll
+  for (int i = 0; i < 8; i++) sums[r][lane * 8 + i] = acc[i];
+  __syncthreads();
+  const int c = blockIdx.x * 256 + threadIdx.x;
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; i++) s += sums[i][threadIdx.x];
+  if (c < a.N) a.part[(int64_t)blockIdx.y * a.N + c] = s;
+}
+
+template <class E>
+__global__ __launch_bounds__(256) void k_bias_grad(ActGradArgs a) {
+  const int c = blockIdx.x * 256 + threadIdx.x;
+  if (c >= a.N) return;
+  float s = 0.f;
+  for (int i = 0; i < a.chunks; i++) s += a.part[(int64_t)i * a.N + c];
+  ((typename E::T*)a.db)[c] = E::from(s);
+}
+
+template <class E>
+hipError_t act_grad(const ActGradArgs& a, hipStream_t s) {
+  if (a.N == 0) return hipSuccess;
+  const uint32_t cols = (uint32_t)((a.N + 255) / 256);
+  k_act_grad<E><<<dim3(cols, (uint32_t)a.chunks), dim3(256), 0, s>>>(a);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || !a.db) return e;
+  k_bias_grad<E><<<dim3(cols), dim3(256), 0, s>>>(a);
+  return hipGetLastError();
+}
+hipError_t launch_act_grad(int kind, const ActGradArgs& a, hipStream_t s) {
+  return kind == 0 ? act_grad<F32>(a, s) : kind == 1 ? act_grad<F16>(a, s) : act_grad<BF16>(a, s);
+}
+
+}  // namespace llar_ffn

@@ -1,0 +1,498 @@
+// llar_gemm.h -- the matrix product of the feed-forward operators on the
+// gfx950 matrix units.  See llar_ffn.h for what one launch computes.
+#pragma once
+#include "llar_ffn.h"
+#include "llar_ffn_math.h"
+
+namespace llar_ffn {
+
+#define LLAR_LDS __attribute__((address_space(3)))
+typedef LLAR_LDS char lds_char;
+
+constexpr uint32_t kNoLoad = 0x80000000u;  // beyond every descriptor: the load writes zeros
+
+template <int TM_, int TN_, int WM_, int WN_>
+struct TileShape {
+  static constexpr int TM = TM_, TN = TN_, WM = WM_, WN = WN_;
+  static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
+  static constexpr int FM = TM / WM / 16;  // 16-row fragments of a wave along m
+  static constexpr int FN = TN / WN / 16;  // and along n
+};
+typedef TileShape<256, 256, 2, 4> Shape256;
+typedef TileShape<128, 128, 2, 2> Shape128;
+typedef TileShape<64, 64, 2, 2> Shape64;
+
+// ---- fragments -------------------------------------------------------------------
+// A 16 x 32 operand fragment: lane l holds row l % 16, k = 8 (l / 16) .. + 7.
+template <class E>
+struct Frag {
+  s16x8 v;
+};
+// binary32 as three bfloat16 whose sum is the value: each part is what the
+// parts before it leave, rounded to bfloat16's 8 bits.  Every remainder is
+// exact, and 8 bits at most are left for the third part.
+template <>
+struct Frag<F32> {
+  s16x8 hi, mid, lo;
+};
+
+template <class E>
+__device__ __forceinline__ f32x4 mma(const Frag<E>& a, const Frag<E>& b, f32x4 c);
+template <>
+__device__ __forceinline__ f32x4 mma<BF16>(const Frag<BF16>& a, const Frag<BF16>& b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a.v), __builtin_bit_cast(bf16x8, b.v), c,
+                                                 0, 0, 0);
+}
+template <>
+__device__ __forceinline__ f32x4 mma<F16>(const Frag<F16>& a, const Frag<F16>& b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a.v), __builtin_bit_cast(f16x8, b.v), c, 0,
+                                                0, 0);
+}
+// Of the nine products of parts the six above 2^-23 of the whole, small ones
+// first: 6 bfloat16 products at 16 times the binary32 unit's rate.
+template <>
+__device__ __forceinline__ f32x4 mma<F32>(const Frag<F32>& a, const Frag<F32>& b, f32x4 c) {
+#define LLAR_MMA(p, q) \
+  c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, p), __builtin_bit_cast(bf16x8, q), c, 0, 0, 0)
+  LLAR_MMA(a.mid, b.mid);
+  LLAR_MMA(a.lo, b.hi);
+  LLAR_MMA(a.hi, b.lo);
+  LLAR_MMA(a.mid, b.hi);
+  LLAR_MMA(a.hi, b.mid);
+  LLAR_MMA(a.hi, b.hi);
+#undef LLAR_MMA
+  return c;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {  // both rounded to nearest even
+  typedef __bf16 pair __attribute__((ext_vector_type(2)));
+  const pair p = {(__bf16)a, (__bf16)b};
+  return __builtin_bit_cast(uint32_t, p);
+}
+__device__ __forceinline__ Frag<F32> split3(const float (&x)[8]) {
+  union {
+    s16x8 v;
+    uint32_t u[4];
+  } hi, mid, lo;
+#pragma unroll
+  for (int i = 0; i < 4; i++) {
+    const uint32_t h = pack_bf16(x[2 * i], x[2 * i + 1]);
+    const float r0 = x[2 * i] - __uint_as_float(h << 16), r1 = x[2 * i + 1] - __uint_as_float(h & 0xffff0000u);
+    const uint32_t m = pack_bf16(r0, r1);
+    const float q0 = r0 - __uint_as_float(m << 16), q1 = r1 - __uint_as_float(m & 0xffff0000u);
+    hi.u[i] = h;
+    mid.u[i] = m;
+    lo.u[i] = pack_bf16(q0, q1);
+  }
+  Frag<F32> f;
+  f.hi = hi.v;
+  f.mid = mid.v;
+  f.lo = lo.v;
+  return f;
+}
+
+// ---- one operand's tile in LDS --------------------------------------------------------
+// R rows by 128 bytes of k, in one of two orders.
+//
+// k-contiguous source: [row][8 chunks of 16 bytes], chunk c of a row stored at
+// position c ^ key(row), so that the 16 rows of a fragment read the same chunk
+// from different banks.
+// Row-contiguous source: [k][row], chunk c of a k line stored at c ^ key(k);
+// 16-bit fragments come out through the transposing LDS read, which gathers
+// four k of one row into a lane.
+//
+// perm: fragment j's 16 rows are spread over the wave's rows as
+// n = 4 F b + 4 j + i (b, i = 0..3, F fragments in a run), so that a lane's
+// results of the run are 4 F neighbours of one output row.  Only the
+// k-contiguous order is read that way; the other keeps n = 16 j + r.
+template <class E, bool kRows, int R, int NT, int F, bool kPerm>
+struct Operand {
+  static constexpr bool kByRows = kRows, kSpread = kPerm;
+  static constexpr int kRun = F;
+  typedef typename E::T T;
+  static constexpr int kThreads = NT;
+  static constexpr int ES = sizeof(T);
+  static constexpr int CE = 16 / ES;          // elements of a chunk
+  static constexpr int BK = 128 / ES;         // k of a tile
+  static constexpr int kBytes = R * 128;
+  static constexpr int kLoads = R * 8 / NT;   // chunks a thread loads
+  static_assert(R * 8 % NT == 0, "whole chunks per thread");
+  static constexpr int kLine = R / CE;        // chunks of a k line (row-contiguous order)
+
+  static __device__ __forceinline__ int key_row(int row) {
+    return kPerm ? (row & 3) | (((row / (4 * F)) & 1) << 2) : row & 7;
+  }
+  static __device__ __forceinline__ int key_k(int k) {
+    if constexpr (ES == 2) {
+      return 2 * (((k & 3) | (((k >> 3) & 1) << 2)) & (kLine / 2 - 1));
+    } else {
+      return (4 * ((k >> 3) & 3)) & (kLine - 1);
+    }
+  }
+
+  // chunk number of load i of this thread, in LDS order
+  static __device__ __forceinline__ int slot(int i) { return i * NT + (int)threadIdx.x; }
+  // its row (or first row) and its k (or first k) within the tile
+  static __device__ __forceinline__ void where(int i, int& row, int& k) {
+    const int s = slot(i);
+    if constexpr (kRows) {
+      k = s / kLine;
+      row = ((s % kLine) ^ key_k(k)) * CE;
+    } else {
+      row = s / 8;
+      k = ((s % 8) ^ key_row(row)) * CE;
+    }
+  }
+};
+
+// This thread's byte offsets from the tile's first element, kNoLoad where the
+// row does not exist.
+template <class Op>
+__device__ __forceinline__ void direct_offsets(uint32_t (&voff)[Op::kLoads], int rows_left, int64_t ld) {
+#pragma unroll
+  for (int i = 0; i < Op::kLoads; i++) {
+    int row, k;
+    Op::where(i, row, k);
+    const int64_t at = Op::kByRows ? k * ld + row : row * ld + k;
+    voff[i] = row < rows_left ? (uint32_t)(at * Op::ES) : kNoLoad;
+  }
+}
+
+// Loads straight into LDS, 16 bytes a lane; the wave's 64 chunks land back to
+// back.  krem: how many k of the tile exist.
+template <class Op>
+__device__ __forceinline__ void load_direct(lds_char* lds, const char* base, const uint32_t (&voff)[Op::kLoads],
+                                            int krem) {
+  __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void*)base, (short)0, 0x7fffffff, 0x00020000);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+#pragma unroll
+  for (int i = 0; i < Op::kLoads; i++) {
+    int row, k;
+    Op::where(i, row, k);
+    const uint32_t off = k < krem ? voff[i] : kNoLoad;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (LLAR_LDS void*)(lds + (i * Op::kThreads + wave * 64) * 16), 16,
+                                             (int)off, 0, 0, 0);
+  }
+}
+
+// The same tile through registers, for operands whose chunks are not all whole
+// and 16-byte aligned: a chunk inside the matrix is one load at its element's
+// alignment, one at the border is put together from its elements.
+template <class Op>
+__device__ __forceinline__ void load_regs(u32x4 (&v)[Op::kLoads], const char* base, int64_t ld, int rows_left,
+                                          int krem) {
+  typedef typename Op::T T;
+  typedef u32x4 __attribute__((aligned(2))) loose;
+#pragma unroll
+  for (int i = 0; i < Op::kLoads; i++) {
+    int row, k;
+    Op::where(i, row, k);
+    const T* p = (const T*)base + (Op::kByRows ? k * ld + row : row * ld + k);
+    int cnt = Op::kByRows ? (k < krem ? rows_left - row : 0) : (row < rows_left ? krem - k : 0);
+    if (cnt >= Op::CE) {
+      v[i] = *(const loose*)p;
+    } else {
+      union {
+        T t[Op::CE];
+        u32x4 q;
+      } u;
+      u.q = u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+      for (int e = 0; e < Op::CE; e++)
+        if (e < cnt) u.t[e] = p[e];
+      v[i] = u.q;
+    }
+  }
+}
+template <class Op>
+__device__ __forceinline__ void store_regs(lds_char* lds, const u32x4 (&v)[Op::kLoads]) {
+#pragma unroll
+  for (int i = 0; i < Op::kLoads; i++) *(LLAR_LDS u32x4*)(lds + Op::slot(i) * 16) = v[i];
+}
+
+// The lane's address of fragment 0 (first tile row `row0`), k step 0.
+template <class Op>
+__device__ __forceinline__ uint32_t frag_base(int row0) {
+  const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+  if constexpr (Op::kByRows) {
+    if constexpr (Op::ES == 2) {
+      const int k = q * 8 + (r >> 2), col = row0 + (r & 3) * 4;
+      return (k * Op::kLine + ((col / 8) ^ Op::key_k(k))) * 16 + (col % 8) * 2;
+    } else {
+      const int k = q * 8, col = row0 + r;
+      return (k * Op::kLine + ((col / 4) ^ Op::key_k(k))) * 16 + (col % 4) * 4;
+    }
+  } else {
+    const int row = row0 + (Op::kSpread ? (r >> 2) * 4 * Op::kRun + (r & 3) : r);
+    return row * 128 + ((Op::ES == 2 ? q : 2 * q) ^ Op::key_row(row)) * 16;
+  }
+}
+
+// Fragment f (a constant after unrolling) of k step kk.
+template <class Op, class E>
+__device__ __forceinline__ Frag<E> read_frag(lds_char* lds, uint32_t base, int f, int kk) {
+  Frag<E> out;
+  if constexpr (Op::kByRows) {
+    if constexpr (Op::ES == 2) {
+      // lane i of 16 hands in row i / 4 of a 4 x 16 block and takes column i
+      const uint32_t at = (base ^ (f * 32)) + kk * 32 * Op::kLine * 16;
+      const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LLAR_LDS s16x4*)(lds + at));
+      const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LLAR_LDS s16x4*)(lds + at + 4 * Op::kLine * 16));
+      out.v = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+    } else {
+      float x[8];
+      const uint32_t at = base ^ (f * 64);
+#pragma unroll
+      for (int t = 0; t < 8; t++) x[t] = *(LLAR_LDS float*)(lds + at + t * Op::kLine * 16);
+      out = split3(x);
+    }
+  } else {
+    const uint32_t step = Op::kSpread ? 4 * 128 : 16 * 128;
+    if constexpr (Op::ES == 2) {
+      out.v = *(LLAR_LDS s16x8*)(lds + ((base ^ (kk * 64)) + f * step));
+    } else {
+      const f32x4 a = *(LLAR_LDS f32x4*)(lds + (base + f * step));
+      const f32x4 b = *(LLAR_LDS f32x4*)(lds + ((base ^ 16) + f * step));
+      const float x[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+      out = split3(x);
+    }
+  }
+  return out;
+}
+
+// Applies the epilogue to n neighbours of one output row and stores them.
+// acc0: the sums (gated: of the first projection), acc1: of the second.
+template <class E, bool kGated, int n>
+__device__ __forceinline__ void finish(const GemmArgs& a, int b, int m, int col, const float* acc0,
+                                       const float* acc1) {
+  typedef typename E::T T;
+  const int cnt = a.N - col;
+  const bool vec = a.vec_out != 0;
+  float y[n];
+  if constexpr (kGated) {
+    if (a.z[0]) {
+      store_vals<E, n>((T*)a.z[0] + m * a.zld + col, acc0, cnt, vec);
+      store_vals<E, n>((T*)a.z[1] + m * a.zld + col, acc1, cnt, vec);
+    }
+#pragma unroll
+    for (int i = 0; i < n; i++) y[i] = act_value(acc0[i], a.act) * acc1[i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < n; i++) y[i] = acc0[i];
+    if (a.bias) {
+      const Vals<E, n> v = load_vals<E, n>((const T*)a.bias + col, cnt, vec);
+#pragma unroll
+      for (int i = 0; i < n; i++) y[i] += v.v[i];
+    }
+    if (a.z[0]) store_vals<E, n>((T*)a.z[0] + m * a.zld + col, y, cnt, vec);
+    if (a.act != kActNone) {
+#pragma unroll
+      for (int i = 0; i < n; i++) y[i] = act_value(y[i], a.act);
+    }
+    if (a.resid) {
+      const Vals<E, n> v = load_vals<E, n>((const T*)a.resid + m * a.rld + col, cnt, vec);
+#pragma unroll
+      for (int i = 0; i < n; i++) y[i] += v.v[i];
+    }
+  }
+  store_vals<E, n>((T*)a.out[b] + m * a.outld + col, y, cnt, vec);
+}
+
+// The product of parts turns an infinity into a NaN (infinity times a zero
+// part, or infinity less infinity in a remainder; a value that rounds to
+// bfloat16's infinity does the same), so a NaN sum of binary32 inputs is taken
+// again from the inputs, in k order, up to the first true NaN.
+template <bool kXRows, bool kWRows>
+__device__ float sum_again(const GemmArgs& a, int b, int p, int m, int col, int64_t k0, int64_t k1) {
+  float s = 0.f;
+  for (int64_t k = k0; k < k1 && s == s; k++) {
+    const int seg = a.segs == 2 ? (int)(k / a.K) : b;
+    const int64_t kk = a.segs == 2 ? k % a.K : k;
+    const float* x = (const float*)a.x[seg];
+    const float* w = (const float*)a.w[a.segs == 2 || a.batch == 2 ? seg : p];
+    s = fmaf(x[kXRows ? kk * a.xld + m : m * a.xld + kk], w[kWRows ? kk * a.wld + col : col * a.wld + kk], s);
+  }
+  return s;
+}
+
+// One workgroup computes a TM x TN tile of the output (gated: TM x TN/2 of both
+// projections) over its share of the k tiles.  Two LDS buffers: while one is
+// multiplied, the other one's loads are in flight.
+template <class E, bool kXRows, bool kWRows, class Shape, bool kVec, bool kGated>
+__global__ __launch_bounds__(Shape::kThreads) void k_gemm(GemmArgs a) {
+  constexpr int TM = Shape::TM, NT = Shape::kThreads;
+  constexpr int P = kGated ? 2 : 1;              // projections
+  constexpr int TN = Shape::TN / P;              // output columns of the tile
+  constexpr int FM = Shape::FM, F = Shape::FN / P;
+  constexpr bool kSpread = !kWRows;
+  typedef Operand<E, kXRows, TM, NT, FM, false> X;
+  typedef Operand<E, kWRows, TN, NT, F, kSpread> W;
+  constexpr int BK = X::BK, ES = X::ES;
+  constexpr int kBuf = X::kBytes + P * W::kBytes;
+  __shared__ __attribute__((aligned(1024))) char smem[2 * kBuf];
+  lds_char* lds = (lds_char*)smem;
+
+  // ---- which tile: workgroup b runs on XCD b % 8; each XCD takes a run of
+  // neighbouring tiles, in groups of 8 along m, so that its L2 holds what they share
+  const int tm = (a.M + TM - 1) / TM, tn = (a.N + TN - 1) / TN;
+  const int total = gridDim.x;
+  int id;
+  {
+    const int b = blockIdx.x, xcd = b & 7, q = total >> 3, r = total & 7;
+    id = xcd * q + (xcd < r ? xcd : r) + (b >> 3);
+  }
+  const int tiles = tm * tn;
+  const int plane = id / tiles;
+  id -= plane * tiles;
+  const int b = plane % a.batch, split = plane / a.batch;
+  int m0, n0;
+  {
+    const int group = id / (8 * tn), in = id - group * 8 * tn;
+    const int gm = min(tm - group * 8, 8);
+    m0 = (group * 8 + in % gm) * TM;
+    n0 = in / gm * TN;
+  }
+  const int ktiles = (a.K + BK - 1) / BK;
+  const int all = ktiles * a.segs;
+  const int t0 = (int)((int64_t)all * split / a.splits), t1 = (int)((int64_t)all * (split + 1) / a.splits);
+
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave / Shape::WN, wn = wave % Shape::WN;
+
+  f32x4 acc[P][FM][F];
+#pragma unroll
+  for (int p = 0; p < P; p++)
+#pragma unroll
+    for (int f = 0; f < FM; f++)
+#pragma unroll
+      for (int j = 0; j < F; j++) acc[p][f][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  const int xleft = a.M - m0, wleft = a.N - n0;
+  uint32_t xoff[X::kLoads], woff[W::kLoads];
+  u32x4 xreg[X::kLoads], wreg[P][W::kLoads];
+  if constexpr (kVec) {
+    direct_offsets<X>(xoff, xleft, a.xld);
+    direct_offsets<W>(woff, wleft, a.wld);
+  }
+  auto fetch = [&](int t, int buf) {
+    const int seg = t / ktiles, kt = t - seg * ktiles;
+    const int from = a.segs == 2 ? seg : b;
+    const int64_t k = (int64_t)kt * BK;
+    const char* xb = (const char*)a.x[from] + (kXRows ? m0 + k * a.xld : m0 * a.xld + k) * ES;
+    const int krem = a.K - (int)k;
+    lds_char* at = lds + buf * kBuf;
+    if constexpr (kVec) {
+      load_direct<X>(at, xb, xoff, krem);
+    } else {
+      load_regs<X>(xreg, xb, a.xld, xleft, krem);
+    }
+#pragma unroll
+    for (int p = 0; p < P; p++) {
+      const char* wb = (const char*)a.w[kGated ? p : from] + (kWRows ? n0 + k * a.wld : n0 * a.wld + k) * ES;
+      if constexpr (kVec) {
+        load_direct<W>(at + X::kBytes + p * W::kBytes, wb, woff, krem);
+      } else {
+        load_regs<W>(wreg[p], wb, a.wld, wleft, krem);
+      }
+    }
+  };
+  auto settle = [&](int buf) {
+    if constexpr (!kVec) {
+      lds_char* at = lds + buf * kBuf;
+      store_regs<X>(at, xreg);
+#pragma unroll
+      for (int p = 0; p < P; p++) store_regs<W>(at + X::kBytes + p * W::kBytes, wreg[p]);
+    }
+  };
+
+  const uint32_t xbase = frag_base<X>(wm * 16 * FM), wbase = frag_base<W>(wn * 16 * F);
+  if (t0 < t1) {
+    fetch(t0, 0);
+    settle(0);
+  }
+  for (int t = t0; t < t1; t++) {
+    const int buf = (t - t0) & 1;
+    __syncthreads();  // this buffer has arrived; everyone is done with the other
+    if (t + 1 < t1) fetch(t + 1, buf ^ 1);
+    lds_char* at = lds + buf * kBuf;
+#pragma unroll
+    for (int kk = 0; kk < BK / 32; kk++) {
+      Frag<E> wf[P][F];
+#pragma unroll
+      for (int p = 0; p < P; p++)
+#pragma unroll
+        for (int j = 0; j < F; j++) wf[p][j] = read_frag<W, E>(at + X::kBytes + p * W::kBytes, wbase, j, kk);
+#pragma unroll
+      for (int f = 0; f < FM; f++) {
+        const Frag<E> xf = read_frag<X, E>(at, xbase, f, kk);
+#pragma unroll
+        for (int p = 0; p < P; p++)
+#pragma unroll
+          for (int j = 0; j < F; j++) acc[p][f][j] = mma<E>(wf[p][j], xf, acc[p][f][j]);
+      }
+    }
+    if (t + 1 < t1) settle(buf ^ 1);
+  }
+
+  // ---- results: lane l holds row m0 + .. + l % 16, and of fragment j the 4
+  // columns that follow 4 (l / 16) in it
+  const int lane = threadIdx.x & 63, q = lane >> 4;
+  auto k_of = [&](int t) { return (int64_t)(t / ktiles) * a.K + min((t % ktiles) * BK, a.K); };
+  constexpr int kRunLen = kSpread ? (4 * F < 8 ? 4 * F : 8) : 4;
+#pragma unroll
+  for (int f = 0; f < FM; f++) {
+    const int m = m0 + (wm * FM + f) * 16 + (lane & 15);
+#pragma unroll
+    for (int j = 0; j < F; j += kRunLen / 4) {
+      const int col = n0 + wn * 16 * F + (kSpread ? q * 4 * F + 4 * j : 16 * j + 4 * q);
+      if (m < a.M && col < a.N) {
+        float v[P][kRunLen];
+#pragma unroll
+        for (int p = 0; p < P; p++)
+#pragma unroll
+          for (int i = 0; i < kRunLen; i++) {
+            v[p][i] = acc[p][f][j + i / 4][i % 4];
+            if constexpr (E::kind == 0) {
+              if (v[p][i] != v[p][i] && col + i < a.N)
+                v[p][i] = sum_again<kXRows, kWRows>(a, b, p, m, col + i, k_of(t0), k_of(t1));
+            }
+          }
+        if (a.splits > 1) {
+#pragma unroll
+          for (int p = 0; p < P; p++) {
+            float* d = a.partial + (((int64_t)split * (kGated ? 2 : a.batch) + (kGated ? p : b)) * a.M + m) * a.npad + col;
+#pragma unroll
+            for (int i = 0; i < kRunLen; i += 4)
+              if (col + i < a.npad) *(f32x4*)(d + i) = f32x4{v[p][i], v[p][i + 1], v[p][i + 2], v[p][i + 3]};
+          }
+        } else {
+          finish<E, kGated, kRunLen>(a, b, m, col, v[0], v[P - 1]);
+        }
+      }
+    }
+  }
+}
+
+template <class E, bool kXRows, bool kWRows, class Shape, bool kVec, bool kGated>
+hipError_t launch_one(const GemmArgs& a, hipStream_t s) {
+  const int tn_cols = Shape::TN / (kGated ? 2 : 1);
+  const int64_t tiles = ((int64_t)a.M + Shape::TM - 1) / Shape::TM * (((int64_t)a.N + tn_cols - 1) / tn_cols);
+  const int64_t grid = tiles * a.batch * a.splits;
+  if (grid <= 0) return hipSuccess;
+  if (grid > 0x7fffffff) return hipErrorInvalidValue;
+  k_gemm<E, kXRows, kWRows, Shape, kVec, kGated><<<dim3((uint32_t)grid), dim3(Shape::kThreads), 0, s>>>(a);
+  return hipGetLastError();
+}
+
+template <class E, bool kXRows, bool kWRows, bool kGated>
+hipError_t launch_shape(const GemmPlan& p, const GemmArgs& a, hipStream_t s) {
+  if (p.vec) {
+    if (p.tile == kTile256) return launch_one<E, kXRows, kWRows, Shape256, true, kGated>(a, s);
+    if (p.tile == kTile128) return launch_one<E, kXRows, kWRows, Shape128, true, kGated>(a, s);
+    return launch_one<E, kXRows, kWRows, Shape64, true, kGated>(a, s);
+  }
+  if (p.tile == kTile64) return launch_one<E, kXRows, kWRows, Shape64, false, kGated>(a, s);
+  return launch_one<E, kXRows, kWRows, Shape128, false, kGated>(a, s);
+}
+
+}  // namespace llar_ffn

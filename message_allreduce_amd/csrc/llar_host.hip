@@ -24,11 +24,6 @@ namespace {
 
 thread_local int g_last_error = LLAR_OK;
 
-int fail(int status) {
-  g_last_error = status;
-  return status;
-}
-
 // Per-protocol size caps (bytes per rank) of the single-round protocols; the
 // pipelined protocols have no cap (their staging is chunk-sized).
 constexpr size_t kCapLL = 8ull << 20;
@@ -60,6 +55,11 @@ struct Region {
 };
 
 }  // namespace
+
+int llar::fail(int status) {
+  g_last_error = status;
+  return status;
+}
 
 struct llar_comm {
   int device = 0;

@@ -8,6 +8,9 @@ namespace llar {
 
 struct Ctrl;
 
+// records `status` for llar_last_error on this thread and returns it
+int fail(int status);
+
 // element kinds (same numbering as llar_dtype)
 constexpr int kKindF32 = 0;
 constexpr int kKindF16 = 1;

@@ -211,3 +211,41 @@ def test_null_handle_options_are_the_process_defaults(L):
     assert L.llar_set_option(None, b"auto_threshold_pipelined", 2 << 20) == 0
     assert L.llar_get_option(None, b"auto_threshold_pipelined", ctypes.byref(v)) == 0 and v.value == 2 << 20
     assert L.llar_set_option(None, b"auto_threshold_pipelined", 3 << 19) == 0  # the default again
+
+
+def test_feed_forward_calls_check_their_arguments_without_a_gpu(L):
+    import message_allreduce_amd as m
+
+    def mat(rows, cols, rs=None, cs=1, data=4096):
+        return (ctypes.c_int64 * 5)(data, rows, cols, cols if rs is None else rs, cs)
+
+    def linear(x, w, out, dtype=2, act=0, ws=None, n=0, residual=None, pre=None):
+        return L.llar_linear(x, w, None, residual, out, pre, dtype, act, ws, n, None)
+
+    ok = (mat(4, 64), mat(32, 64), mat(4, 32))
+    assert linear(None, *ok[1:]) == -1 and L.llar_last_error() == -1
+    assert linear(*ok, dtype=7) == -1 and linear(*ok, act=9) == -1 and linear(*ok, act=-1) == -1
+    assert linear(mat(4, 63), *ok[1:]) == -1                      # k differs
+    assert linear(*ok[:2], mat(4, 31)) == -1
+    assert linear(mat(4, 64, data=0), *ok[1:]) == -1
+    assert linear(mat(4, 64, -64), *ok[1:]) == -1                 # negative stride
+    assert linear(mat(4, 64, 128, 2), *ok[1:]) == -2              # no axis of stride 1
+    assert linear(*ok[:2], mat(4, 32, 1, 4)) == -2                # output columns not contiguous
+    assert linear(*ok[:2], mat(4, 32, 16)) == -1                  # output rows overlap
+    assert linear(mat(4, (1 << 30) + 8), mat(32, (1 << 30) + 8), ok[2]) == -2
+    assert linear(mat(-1, 64), *ok[1:]) == -1
+    assert linear(*ok, residual=mat(4, 32, 1, 4)) == -2 and linear(*ok, pre=mat(3, 32)) == -1
+    assert linear(*ok, ws=4096 + 8, n=1 << 20) == -1              # misaligned workspace
+    assert linear(mat(0, 64), mat(32, 64), mat(0, 32)) == 0       # nothing to do
+    need = L.llar_ffn_workspace(1, 4, 32, 64, 2)
+    assert need > 0 and L.llar_ffn_workspace(1, 4, 32, 64, 9) == 0 and L.llar_ffn_workspace(9, 4, 32, 64, 2) == 0
+    back = (mat(4, 32), mat(4, 64), mat(32, 64))
+    assert L.llar_linear_backward(*back, None, mat(4, 64), mat(32, 64), None, 2, 0, None, 0, None) == -1
+    assert L.llar_linear_backward(*back, None, mat(4, 64), mat(32, 64), None, 2, 4, 4096, need, None) == -1  # no pre
+    gated = (mat(4, 64), mat(32, 64), mat(32, 64), mat(4, 32))
+    assert L.llar_gated_ffn(*gated, mat(4, 32), None, 2, 4, None, 0, None) == -1   # gate without up
+    assert L.llar_gated_ffn(gated[0], gated[1], mat(32, 64, 72), gated[3], None, None, 2, 4, None, 0, None) == -2
+    h = mat(4, 32)
+    assert L.llar_gated_ffn_backward(h, *gated[:3], h, mat(4, 31), None, None, None, 2, 4, None, 0, None) == -1
+    assert L.llar_gated_ffn_backward(h, *gated[:3], h, h, mat(4, 64), mat(32, 64), None, 2, 4, None, 0, None) == -1
+    assert sorted(m.ACTIVATIONS.values()) == [0, 1, 2, 3, 4]
