@@ -249,18 +249,22 @@ typedef enum {
  * (strides in elements, not negative; 0 repeats a row or column of an input).
  * An input needs a stride of 1 along one axis (any layout when that axis has
  * one element); where stated, and for every output, col_stride must be 1.
- * Output rows must not overlap.  Any alignment is accepted; products read
- * 16-byte aligned operands whose contiguous axis is a multiple of 16 bytes
- * fastest. */
+ * Output rows must not overlap.  Any alignment is accepted; above 16
+ * tokens, operands that are not aligned as llar_ffn_workspace describes are
+ * copied into the workspace first. */
 typedef struct {
   void* data;
   int64_t rows, cols, row_stride, col_stride;
 } llar_matrix;
 
 /* Bytes of workspace a call needs for m tokens, n outputs and k inputs (0 is
- * possible; then NULL may be passed).  The workspace is 256-byte aligned
- * device memory, free for other use once the stream has passed the call. */
-size_t llar_ffn_workspace(llar_ffn_op op, int64_t m, int64_t n, int64_t k, llar_dtype dtype);
+ * possible; then NULL may be passed).  aligned: 1 if every input matrix (of
+ * linear_backward and gated_ffn_backward too) has 16-byte aligned data and,
+ * in bytes, a multiple of 16 as the length and the distance of its contiguous
+ * lines, which are less than 8 MiB apart; 0 otherwise, which adds room for copies that do.  The workspace is
+ * 256-byte aligned device memory, free for other use once the stream has
+ * passed the call. */
+size_t llar_ffn_workspace(llar_ffn_op op, int64_t m, int64_t n, int64_t k, llar_dtype dtype, int aligned);
 
 /* out = act(x w^T + bias) + residual:  x m x k, w n x k, out m x n.
  * bias: n contiguous elements, or NULL.  residual: m x n with contiguous
@@ -270,7 +274,8 @@ size_t llar_ffn_workspace(llar_ffn_op op, int64_t m, int64_t n, int64_t k, llar_
  * Errors of all four calls, with nothing enqueued: LLAR_ERR_ARG for a bad
  * type, activation, shape or stride, a missing matrix, a misaligned or too
  * small workspace; LLAR_ERR_UNSUPPORTED for a layout other than those above
- * or a dimension above 2^30; LLAR_ERR_HIP if a launch failed. */
+ * or a dimension above 2^30, or above 2^21 - 8 along an input's contiguous
+ * axis; LLAR_ERR_HIP if a launch failed. */
 int llar_linear(const llar_matrix* x, const llar_matrix* w, const void* bias, const llar_matrix* residual,
                 const llar_matrix* out, const llar_matrix* pre, llar_dtype dtype, llar_act act, void* workspace,
                 size_t workspace_bytes, void* stream);

@@ -99,7 +99,7 @@ def lib() -> ctypes.CDLL:
         "llar_floor_measure": (i32, [i32, i32, ctypes.POINTER(ctypes.c_double)]),
         "llar_get_trace": (i32, [vp, u64p, i32]),
         "llar_get_pipeline_trace": (i32, [vp, u64p, i32]),
-        "llar_ffn_workspace": (sz, [i32, i64, i64, i64, i32]),
+        "llar_ffn_workspace": (sz, [i32, i64, i64, i64, i32, i32]),
         "llar_linear": (i32, [vp] * 6 + [i32, i32, vp, sz, vp]),
         "llar_linear_backward": (i32, [vp] * 7 + [i32, i32, vp, sz, vp]),
         "llar_gated_ffn": (i32, [vp] * 6 + [i32, i32, vp, sz, vp]),

@@ -18,6 +18,8 @@ enum Act : int { kActNone = 0, kActRelu = 1, kActGelu = 2, kActGeluTanh = 3, kAc
 // of an element in its epilogue.
 // A matrix lies k-contiguous (rows `ld` elements apart) or row-contiguous
 // (consecutive k `ld` elements apart); out, resid and z rows are contiguous.
+// The tiled kernel reads both operands in whole, 16-byte aligned chunks: lines
+// whose length is no multiple of one are followed by zeros up to it.
 struct GemmArgs {
   const void* x[2];
   const void* w[2];
@@ -46,16 +48,32 @@ struct GemmPlan {
   int tile;
   bool x_rows;     // x is row-contiguous
   bool w_rows;
-  bool vec;        // 16-byte loads allowed for every chunk (see the host's rule)
   bool gated;
 };
 
 hipError_t launch_gemm(const GemmPlan& p, const GemmArgs& a, hipStream_t s);
 
+// A product with M <= kFewRows rows of k-contiguous x, any alignment; a.batch is 1.
+constexpr int kFewRows = 16;
+hipError_t launch_few(int kind, bool w_rows, bool gated, const GemmArgs& a, hipStream_t s);
+
+// Copies of matrices in whole chunks: lines of `width` elements, `ld` apart,
+// written `dld` apart (a multiple of 8) with zeros behind them.
+constexpr int kRepackMax = 4;
+struct RepackArgs {
+  const void* src[kRepackMax];
+  void* dst[kRepackMax];
+  int64_t ld[kRepackMax], dld[kRepackMax], lines[kRepackMax], width[kRepackMax];
+  int64_t first[kRepackMax + 1];  // workgroup that starts each
+  int count;
+};
+hipError_t launch_repack(int kind, const RepackArgs& a, hipStream_t s);
+
 // Sums the partial planes of a product split over k and applies its epilogue.
 hipError_t launch_join(int kind, bool gated, const GemmArgs& a, hipStream_t s);
 
-// dg = dh u act'(g), du = dh act(g), element by element (rows contiguous).
+// dg = dh u act'(g), du = dh act(g), element by element (rows contiguous; those
+// of dg and du `dld` apart, a multiple of 8, with zeros behind column N).
 struct GateGradArgs {
   const void *dh, *g, *u;
   void *dg, *du;
@@ -68,6 +86,7 @@ hipError_t launch_gate_grad(int kind, const GateGradArgs& a, hipStream_t s);
 
 // dz = dy act'(z) (dz and z null: no activation) and the sum of dz over the
 // rows: part[c][j] = sum over row chunk c, then db[j] = sum over c in order.
+// dz rows as for the gated block.
 struct ActGradArgs {
   const void *dy, *z;
   void* dz;

@@ -4,6 +4,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <initializer_list>
 
 #include "llar.h"
 #include "llar_ffn.h"
@@ -14,6 +15,8 @@ using namespace llar_ffn;
 namespace {
 
 constexpr int64_t kMaxDim = 1 << 30;
+// a tile's 256 lines are addressed with 31 bits: lines of less than 8 MiB
+constexpr int64_t kMaxLine = (1 << 21) - 8;
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 size_t align256(size_t v) { return (v + 255) / 256 * 256; }
@@ -24,6 +27,7 @@ struct Operand {
   const void* p = nullptr;
   int64_t rows = 0, k = 0, ld = 0;
   bool by_rows = false;
+  bool padded = false;  // zeros follow every line up to a whole chunk
   Operand t() const {  // the transposed matrix
     Operand o = *this;
     o.rows = k;
@@ -32,6 +36,8 @@ struct Operand {
     return o;
   }
 };
+
+bool row_major(const llar_matrix* m) { return m->cols <= 1 || m->col_stride == 1; }
 
 int check(const llar_matrix* m, bool output = false) {
   if (!m) return LLAR_ERR_ARG;
@@ -45,9 +51,9 @@ int check(const llar_matrix* m, bool output = false) {
   } else if (m->cols > 1 && m->col_stride != 1 && m->rows > 1 && m->row_stride != 1) {
     return LLAR_ERR_UNSUPPORTED;
   }
+  if (!output && (row_major(m) ? m->cols : m->rows) > kMaxLine) return LLAR_ERR_UNSUPPORTED;
   return LLAR_OK;
 }
-bool row_major(const llar_matrix* m) { return m->cols <= 1 || m->col_stride == 1; }
 
 // Row distance of a row-contiguous matrix; one row has none, so it takes one
 // that keeps wide accesses possible.
@@ -64,26 +70,38 @@ Operand operand(const llar_matrix* m) {
 }
 bool same_shape(const llar_matrix* a, const llar_matrix* b) { return a->rows == b->rows && a->cols == b->cols; }
 
-// Whether every 16-byte chunk of the operand's tiles is whole and aligned, and
+// Whether every 16-byte chunk of the operand's lines is whole and aligned, and
 // a tile's offsets fit the buffer loads' 31 bits.
 bool chunks_whole(const Operand& o, int es) {
   const int ce = 16 / es;
   if (((uintptr_t)o.p & 15) || o.ld % ce) return false;
-  if ((o.by_rows ? o.rows : o.k) % ce) return false;
+  if (!o.padded && (o.by_rows ? o.rows : o.k) % ce) return false;
   return o.ld * es < (1ll << 31) / 256;
 }
 bool vec8(const void* p, int64_t ld, int es) { return !p || (((uintptr_t)p & 15) == 0 && ld * es % 16 == 0); }
 
+// How a product runs: the kernel for few rows, or tiles; and its split over k.
 struct Shape {
+  bool few;
   int tile, splits;
 };
 
-// Tile and split over k of a product with `outs` output planes of M x N and
-// `kt` k tiles in all.
-Shape choose(int64_t M, int64_t N, int64_t kt, int outs, bool gated, bool vec) {
-  Shape s{kTile64, 1};
+// `kt`: k tiles of a plane in all, `segs` products added; `outs`: output planes;
+// `few`: x is k-contiguous, so that few rows of it may go the direct way.
+Shape choose(int64_t M, int64_t N, int64_t K, int segs, int outs, bool gated, int es, bool few, bool w_rows) {
+  Shape s{false, kTile64, 1};
+  if (M == 0 || N == 0) return s;  // nothing to launch
+  if (few && M <= kFewRows && outs == 1) {
+    s.few = true;
+    if (w_rows) {
+      const int64_t groups = cdiv(N, 64), steps = cdiv(K, 32) * segs / ((gated ? 8 : 16) * 4);
+      if (groups < 128) s.splits = (int)std::max<int64_t>(1, std::min<int64_t>({cdiv(256, groups), steps, 16}));
+    }
+    return s;
+  }
+  const int64_t kt = cdiv(K * es, kTileKBytes) * segs;
   auto tiles = [&](int t) { return cdiv(M, kTileM[t]) * cdiv(N, kTileN[t] / (gated ? 2 : 1)) * outs; };
-  if (vec && tiles(kTile256) >= 192)
+  if (tiles(kTile256) >= 192)
     s.tile = kTile256;
   else if (tiles(kTile128) >= 256)
     s.tile = kTile128;
@@ -94,85 +112,15 @@ Shape choose(int64_t M, int64_t N, int64_t kt, int outs, bool gated, bool vec) {
 size_t partial_bytes(const Shape& s, int64_t M, int64_t N, int planes) {
   return s.splits <= 1 ? 0 : align256((size_t)s.splits * planes * M * (size_t)(cdiv(N, 8) * 8) * 4);
 }
-int64_t k_tiles(int64_t K, int es) { return cdiv(K * es, kTileKBytes); }
 
-// The workspace of a product of this shape, whatever its operands' alignment.
+// The space for partial sums of a product of this shape, whatever its operands' order.
 size_t product_space(int64_t M, int64_t N, int64_t K, int segs, int outs, bool gated, int es) {
   size_t need = 0;
-  for (int vec = 0; vec < 2; vec++) {
-    const Shape s = choose(M, N, k_tiles(K, es) * segs, outs, gated, vec);
+  for (int way = 0; way < 3; way++) {
+    const Shape s = choose(M, N, K, segs, outs, gated, es, way > 0, way > 1);
     need = std::max(need, partial_bytes(s, M, N, gated ? 2 : outs));
   }
   return need;
-}
-
-struct Product {
-  Operand x[2], w[2];
-  int n_x = 1, n_w = 1;  // pairs given
-  int segs = 1, batch = 1;
-  bool gated = false;
-  void* out[2] = {nullptr, nullptr};
-  int64_t outld = 0;
-  void* z[2] = {nullptr, nullptr};
-  int64_t zld = 0;
-  const void* bias = nullptr;
-  const void* resid = nullptr;
-  int64_t rld = 0;
-  int act = kActNone;
-};
-
-int run_product(const Product& p, int dtype, void* space, size_t space_bytes, hipStream_t s) {
-  const int es = elem_size(dtype);
-  GemmArgs a = {};
-  a.M = (int)p.x[0].rows;
-  a.N = (int)p.w[0].rows;
-  a.K = (int)p.x[0].k;
-  if (a.M == 0 || a.N == 0) return LLAR_OK;
-  bool vec = true, vec_out = true;
-  for (int i = 0; i < 2; i++) {
-    a.x[i] = p.x[std::min(i, p.n_x - 1)].p;
-    a.w[i] = p.w[std::min(i, p.n_w - 1)].p;
-    a.out[i] = p.out[i];
-    a.z[i] = p.z[i];
-    vec = vec && (i >= p.n_x || chunks_whole(p.x[i], es)) && (i >= p.n_w || chunks_whole(p.w[i], es));
-    vec_out = vec_out && vec8(p.out[i], p.outld, es) && vec8(p.z[i], p.zld, es);
-  }
-  a.bias = p.bias;
-  a.resid = p.resid;
-  a.vec_out = vec_out && vec8(p.resid, p.rld, es) && vec8(p.bias, 0, es);
-  a.xld = p.x[0].ld;
-  a.wld = p.w[0].ld;
-  a.outld = p.outld;
-  a.zld = p.zld;
-  a.rld = p.rld;
-  a.segs = p.segs;
-  a.batch = p.batch;
-  a.act = p.act;
-  a.npad = (int)(cdiv(a.N, 8) * 8);
-  const Shape sh = choose(a.M, a.N, k_tiles(a.K, es) * p.segs, p.batch, p.gated, vec);
-  a.splits = sh.splits;
-  if (sh.splits > 1) {
-    if (partial_bytes(sh, a.M, a.N, p.gated ? 2 : p.batch) > space_bytes) return LLAR_ERR_ARG;
-    a.partial = (float*)space;
-  }
-  GemmPlan plan;
-  plan.kind = dtype;
-  plan.tile = sh.tile;
-  plan.x_rows = p.x[0].by_rows;
-  plan.w_rows = p.w[0].by_rows;
-  plan.vec = vec;
-  plan.gated = p.gated;
-  if (launch_gemm(plan, a, s) != hipSuccess) return LLAR_ERR_HIP;
-  if (sh.splits > 1 && launch_join(dtype, p.gated, a, s) != hipSuccess) return LLAR_ERR_HIP;
-  return LLAR_OK;
-}
-
-bool dtype_ok(int t) { return t == LLAR_FP32 || t == LLAR_FP16 || t == LLAR_BF16; }
-bool act_ok(int a) { return a >= LLAR_ACT_NONE && a <= LLAR_ACT_SILU; }
-int row_chunks(int64_t M, int64_t N) {
-  // about 1024 workgroups of 256 columns, at least 32 rows each
-  const int64_t cols = std::max<int64_t>(cdiv(N, 256), 1);
-  return (int)std::max<int64_t>(1, std::min(cdiv(1024, cols), M / 32));
 }
 
 struct Carve {
@@ -191,7 +139,147 @@ struct Carve {
     return r;
   }
 };
+
+// An upper bound of the room a copy of rows x k elements in whole chunks takes.
+size_t copy_bytes(int64_t rows, int64_t k, int es) {
+  return align256((size_t)(std::max(rows * (cdiv(k, 8) * 8), k * (cdiv(rows, 8) * 8))) * es);
+}
+
+// Collects operands that the tiled kernel cannot read as they are, and copies
+// them in one launch.
+struct Packer {
+  RepackArgs a = {};
+  int es;
+  Carve* c;
+  Packer(int es_, Carve* c_) : es(es_), c(c_) {}
+  // a copy that another product of the call has made already is taken again
+  void add(Operand& o, bool force = false) {
+    if (!force && chunks_whole(o, es)) return;
+    const int i = a.count++;
+    const int64_t lines = o.by_rows ? o.k : o.rows, width = o.by_rows ? o.rows : o.k;
+    a.src[i] = o.p;
+    a.ld[i] = o.ld;
+    a.lines[i] = lines;
+    a.width[i] = width;
+    a.dld[i] = cdiv(width, 8) * 8;
+    a.dst[i] = c->take((size_t)lines * a.dld[i] * es);
+    a.first[i + 1] = a.first[i] + cdiv(lines * (a.dld[i] / 8), 256);
+    o.p = a.dst[i];
+    o.ld = a.dld[i];
+    o.padded = true;
+  }
+  int run(int dtype, hipStream_t s) {
+    if (a.count == 0) return LLAR_OK;
+    if (!c->ok) return LLAR_ERR_ARG;
+    return launch_repack(dtype, a, s) == hipSuccess ? LLAR_OK : LLAR_ERR_HIP;
+  }
+};
+
+struct Product {
+  Operand x[2], w[2];
+  int n_x = 1, n_w = 1;  // operands given
+  int segs = 1, batch = 1;
+  bool gated = false;
+  void* out[2] = {nullptr, nullptr};
+  int64_t outld = 0;
+  void* z[2] = {nullptr, nullptr};
+  int64_t zld = 0;
+  const void* bias = nullptr;
+  const void* resid = nullptr;
+  int64_t rld = 0;
+  int act = kActNone;
+  int64_t M() const { return x[0].rows; }
+  int64_t N() const { return w[0].rows; }
+  Shape shape(int es) const {
+    return choose(M(), N(), x[0].k, segs, batch, gated, es, !x[0].by_rows, w[0].by_rows);
+  }
+};
+
+// Operands that the product's kernel cannot read as they are go to the packer.
+void pack(Product& p, int es, Packer& k) {
+  if (p.M() == 0 || p.N() == 0 || p.x[0].k == 0 || p.shape(es).few) return;
+  // both of a pair change, or neither: they share their strides
+  bool x = false, w = false;
+  for (int i = 0; i < p.n_x; i++) x = x || !chunks_whole(p.x[i], es);
+  for (int i = 0; i < p.n_w; i++) w = w || !chunks_whole(p.w[i], es);
+  for (int i = 0; x && i < p.n_x; i++) k.add(p.x[i], true);
+  for (int i = 0; w && i < p.n_w; i++) k.add(p.w[i], true);
+}
+
+int run_product(const Product& p, int dtype, const Carve& space, hipStream_t s) {
+  const int es = elem_size(dtype);
+  GemmArgs a = {};
+  a.M = (int)p.M();
+  a.N = (int)p.N();
+  a.K = (int)p.x[0].k;
+  if (a.M == 0 || a.N == 0) return LLAR_OK;
+  bool vec_out = true;
+  for (int i = 0; i < 2; i++) {
+    a.x[i] = p.x[std::min(i, p.n_x - 1)].p;
+    a.w[i] = p.w[std::min(i, p.n_w - 1)].p;
+    a.out[i] = p.out[i];
+    a.z[i] = p.z[i];
+    vec_out = vec_out && vec8(p.out[i], p.outld, es) && vec8(p.z[i], p.zld, es);
+  }
+  a.bias = p.bias;
+  a.resid = p.resid;
+  a.vec_out = vec_out && vec8(p.resid, p.rld, es) && vec8(p.bias, 0, es);
+  a.xld = p.x[0].ld;
+  a.wld = p.w[0].ld;
+  a.outld = p.outld;
+  a.zld = p.zld;
+  a.rld = p.rld;
+  a.segs = p.segs;
+  a.batch = p.batch;
+  a.act = p.act;
+  a.npad = (int)(cdiv(a.N, 8) * 8);
+  const Shape sh = p.shape(es);
+  a.splits = sh.splits;
+  if (sh.splits > 1) {
+    if (partial_bytes(sh, a.M, a.N, p.gated ? 2 : p.batch) > space.left) return LLAR_ERR_ARG;
+    a.partial = (float*)space.p;
+  }
+  if (sh.few) {
+    if (launch_few(dtype, p.w[0].by_rows, p.gated, a, s) != hipSuccess) return LLAR_ERR_HIP;
+  } else {
+    GemmPlan plan;
+    plan.kind = dtype;
+    plan.tile = sh.tile;
+    plan.x_rows = p.x[0].by_rows;
+    plan.w_rows = p.w[0].by_rows;
+    plan.gated = p.gated;
+    if (launch_gemm(plan, a, s) != hipSuccess) return LLAR_ERR_HIP;
+  }
+  if (sh.splits > 1 && launch_join(dtype, p.gated, a, s) != hipSuccess) return LLAR_ERR_HIP;
+  return LLAR_OK;
+}
+
+// A product with the whole workspace to itself.
+int pack_and_run(Product& p, int dtype, void* space, size_t bytes, hipStream_t s) {
+  Carve c{(uint8_t*)space, bytes};
+  Packer k(elem_size(dtype), &c);
+  pack(p, elem_size(dtype), k);
+  const int st = k.run(dtype, s);
+  return st != LLAR_OK ? st : run_product(p, dtype, c, s);
+}
+
+bool dtype_ok(int t) { return t == LLAR_FP32 || t == LLAR_FP16 || t == LLAR_BF16; }
+bool act_ok(int a) { return a >= LLAR_ACT_NONE && a <= LLAR_ACT_SILU; }
+int row_chunks(int64_t M, int64_t N) {
+  // about 1024 workgroups of 256 columns, at least 32 rows each
+  const int64_t cols = std::max<int64_t>(cdiv(N, 256), 1);
+  return (int)std::max<int64_t>(1, std::min(cdiv(1024, cols), M / 32));
+}
+
 bool space_ok(void* w, size_t n) { return n == 0 || (w && ((uintptr_t)w & 255) == 0); }
+
+// Whether the workspace holds what a call on these inputs needs.
+bool enough(size_t bytes, llar_ffn_op op, const llar_matrix* x, const llar_matrix* w, llar_dtype dtype,
+            std::initializer_list<const llar_matrix*> inputs) {
+  bool aligned = true;
+  for (const llar_matrix* m : inputs) aligned = aligned && (!m || chunks_whole(operand(m), elem_size(dtype)));
+  return bytes >= llar_ffn_workspace(op, x->rows, w->rows, x->cols, dtype, aligned);
+}
 
 }  // namespace
 
@@ -203,17 +291,19 @@ bool space_ok(void* w, size_t n) { return n == 0 || (w && ((uintptr_t)w & 255) =
 
 extern "C" {
 
-size_t llar_ffn_workspace(llar_ffn_op op, int64_t m, int64_t n, int64_t k, llar_dtype dtype) {
+size_t llar_ffn_workspace(llar_ffn_op op, int64_t m, int64_t n, int64_t k, llar_dtype dtype, int aligned) {
   if (!dtype_ok(dtype) || m < 0 || n < 0 || k < 0 || m > kMaxDim || n > kMaxDim || k > kMaxDim) return 0;
   const int es = elem_size(dtype);
+  const size_t x = aligned ? 0 : copy_bytes(m, k, es), w = aligned ? 0 : copy_bytes(n, k, es);
+  const size_t dz = align256((size_t)m * (cdiv(n, 8) * 8) * es);
   switch (op) {
-    case LLAR_OP_LINEAR: return product_space(m, n, k, 1, 1, false, es);
-    case LLAR_OP_GATED_FFN: return product_space(m, n, k, 1, 1, true, es);
+    case LLAR_OP_LINEAR: return x + w + product_space(m, n, k, 1, 1, false, es);
+    case LLAR_OP_GATED_FFN: return x + 2 * w + product_space(m, n, k, 1, 1, true, es);
     case LLAR_OP_LINEAR_BACKWARD:
-      return align256((size_t)m * (cdiv(n, 8) * 8) * es) + align256((size_t)row_chunks(m, n) * n * 4) +
+      return x + w + (aligned ? dz : copy_bytes(m, n, es)) + align256((size_t)row_chunks(m, n) * n * 4) +
              std::max(product_space(m, k, n, 1, 1, false, es), product_space(n, k, m, 1, 1, false, es));
     case LLAR_OP_GATED_FFN_BACKWARD:
-      return 2 * align256((size_t)m * (cdiv(n, 8) * 8) * es) +
+      return x + 2 * w + 2 * dz +
              std::max(product_space(m, k, n, 2, 1, false, es), product_space(n, k, m, 1, 2, false, es));
   }
   return 0;
@@ -236,6 +326,7 @@ int llar_linear(const llar_matrix* x, const llar_matrix* w, const void* bias, co
     LLAR_TRY(check(pre, true));
     if (!same_shape(pre, out)) return llar::fail(LLAR_ERR_ARG);
   }
+  if (!enough(workspace_bytes, LLAR_OP_LINEAR, x, w, dtype, {x, w})) return llar::fail(LLAR_ERR_ARG);
   Product p;
   p.x[0] = operand(x);
   p.w[0] = operand(w);
@@ -251,7 +342,7 @@ int llar_linear(const llar_matrix* x, const llar_matrix* w, const void* bias, co
     p.zld = row_ld(pre);
   }
   p.act = act;
-  LLAR_TRY(run_product(p, dtype, workspace, workspace_bytes, (hipStream_t)stream));
+  LLAR_TRY(pack_and_run(p, dtype, workspace, workspace_bytes, (hipStream_t)stream));
   return LLAR_OK;
 }
 
@@ -278,8 +369,7 @@ int llar_linear_backward(const llar_matrix* dy, const llar_matrix* x, const llar
     LLAR_TRY(check(dw, true));
     if (!same_shape(dw, w)) return llar::fail(LLAR_ERR_ARG);
   }
-  if (workspace_bytes < llar_ffn_workspace(LLAR_OP_LINEAR_BACKWARD, x->rows, w->rows, x->cols, dtype))
-    return llar::fail(LLAR_ERR_ARG);
+  if (!enough(workspace_bytes, LLAR_OP_LINEAR_BACKWARD, x, w, dtype, {dy, x, w})) return llar::fail(LLAR_ERR_ARG);
   const int64_t M = dy->rows, N = dy->cols;
   const int es = elem_size(dtype);
   Carve c{(uint8_t*)workspace, workspace_bytes};
@@ -301,6 +391,7 @@ int llar_linear_backward(const llar_matrix* dy, const llar_matrix* x, const llar
       vec = vec && vec8(a.z, a.zld, es);
       dz.p = a.dz;
       dz.ld = a.dzld;
+      dz.padded = true;
     }
     if (db) {
       a.db = db;
@@ -310,21 +401,27 @@ int llar_linear_backward(const llar_matrix* dy, const llar_matrix* x, const llar
     if (!c.ok) return llar::fail(LLAR_ERR_ARG);
     if (launch_act_grad(dtype, a, (hipStream_t)stream) != hipSuccess) return llar::fail(LLAR_ERR_HIP);
   }
+  Product px, pw;
+  px.x[0] = dz;
+  px.w[0] = operand(w).t();
+  pw.x[0] = dz.t();
+  pw.w[0] = operand(x).t();
+  Packer k(es, &c);
+  if (dx) pack(px, es, k);
+  if (dw) {
+    if (px.x[0].p != dz.p) pw.x[0] = px.x[0].t();
+    pack(pw, es, k);
+  }
+  LLAR_TRY(k.run(dtype, (hipStream_t)stream));
   if (dx) {
-    Product p;
-    p.x[0] = dz;
-    p.w[0] = operand(w).t();
-    p.out[0] = dx->data;
-    p.outld = row_ld(dx);
-    LLAR_TRY(run_product(p, dtype, c.p, c.left, (hipStream_t)stream));
+    px.out[0] = dx->data;
+    px.outld = row_ld(dx);
+    LLAR_TRY(run_product(px, dtype, c, (hipStream_t)stream));
   }
   if (dw) {
-    Product p;
-    p.x[0] = dz.t();
-    p.w[0] = operand(x).t();
-    p.out[0] = dw->data;
-    p.outld = row_ld(dw);
-    LLAR_TRY(run_product(p, dtype, c.p, c.left, (hipStream_t)stream));
+    pw.out[0] = dw->data;
+    pw.outld = row_ld(dw);
+    LLAR_TRY(run_product(pw, dtype, c, (hipStream_t)stream));
   }
   return LLAR_OK;
 }
@@ -352,6 +449,8 @@ int llar_gated_ffn(const llar_matrix* x, const llar_matrix* w_gate, const llar_m
   p.w[1] = operand(w_up);
   p.n_w = 2;
   if (p.w[0].by_rows != p.w[1].by_rows || p.w[0].ld != p.w[1].ld) return llar::fail(LLAR_ERR_UNSUPPORTED);
+  if (!enough(workspace_bytes, LLAR_OP_GATED_FFN, x, w_gate, dtype, {x, w_gate, w_up}))
+    return llar::fail(LLAR_ERR_ARG);
   p.gated = true;
   p.out[0] = out->data;
   p.outld = row_ld(out);
@@ -361,7 +460,7 @@ int llar_gated_ffn(const llar_matrix* x, const llar_matrix* w_gate, const llar_m
     p.zld = row_ld(gate);
   }
   p.act = act;
-  LLAR_TRY(run_product(p, dtype, workspace, workspace_bytes, (hipStream_t)stream));
+  LLAR_TRY(pack_and_run(p, dtype, workspace, workspace_bytes, (hipStream_t)stream));
   return LLAR_OK;
 }
 
@@ -393,7 +492,7 @@ int llar_gated_ffn_backward(const llar_matrix* dh, const llar_matrix* x, const l
   }
   const Operand wg = operand(w_gate), wu = operand(w_up);
   if (wg.by_rows != wu.by_rows || wg.ld != wu.ld) return llar::fail(LLAR_ERR_UNSUPPORTED);
-  if (workspace_bytes < llar_ffn_workspace(LLAR_OP_GATED_FFN_BACKWARD, x->rows, w_gate->rows, x->cols, dtype))
+  if (!enough(workspace_bytes, LLAR_OP_GATED_FFN_BACKWARD, x, w_gate, dtype, {x, w_gate, w_up}))
     return llar::fail(LLAR_ERR_ARG);
   const int es = elem_size(dtype);
   const int64_t M = dh->rows, N = dh->cols;
@@ -419,31 +518,33 @@ int llar_gated_ffn_backward(const llar_matrix* dh, const llar_matrix* x, const l
   dg.rows = M;
   dg.k = N;
   dg.ld = a.dld;
+  dg.padded = true;
   du = dg;
   du.p = a.du;
+  Product px, pw;
+  px.x[0] = dg;
+  px.x[1] = du;
+  px.w[0] = wg.t();
+  px.w[1] = wu.t();
+  px.n_x = px.n_w = px.segs = 2;
+  pw.x[0] = dg.t();
+  pw.x[1] = du.t();
+  pw.w[0] = operand(x).t();
+  pw.n_x = pw.batch = 2;
+  Packer k(es, &c);
+  if (dx) pack(px, es, k);
+  if (dw_gate) pack(pw, es, k);
+  LLAR_TRY(k.run(dtype, (hipStream_t)stream));
   if (dx) {
-    Product p;
-    p.x[0] = dg;
-    p.x[1] = du;
-    p.w[0] = wg.t();
-    p.w[1] = wu.t();
-    p.n_x = p.n_w = 2;
-    p.segs = 2;
-    p.out[0] = dx->data;
-    p.outld = row_ld(dx);
-    LLAR_TRY(run_product(p, dtype, c.p, c.left, (hipStream_t)stream));
+    px.out[0] = dx->data;
+    px.outld = row_ld(dx);
+    LLAR_TRY(run_product(px, dtype, c, (hipStream_t)stream));
   }
   if (dw_gate) {
-    Product p;
-    p.x[0] = dg.t();
-    p.x[1] = du.t();
-    p.w[0] = operand(x).t();
-    p.n_x = 2;
-    p.batch = 2;
-    p.out[0] = dw_gate->data;
-    p.out[1] = dw_up->data;
-    p.outld = row_ld(dw_gate);
-    LLAR_TRY(run_product(p, dtype, c.p, c.left, (hipStream_t)stream));
+    pw.out[0] = dw_gate->data;
+    pw.out[1] = dw_up->data;
+    pw.outld = row_ld(dw_gate);
+    LLAR_TRY(run_product(pw, dtype, c, (hipStream_t)stream));
   }
   return LLAR_OK;
 }

@@ -1,7 +1,7 @@
 // llar_ffn_kernels.hip -- the feed-forward operators' kernels beside the
 // product itself: joining a product split over k, the gated block's and the
 // activation's gradients, and the dispatch over instances.
-#include "llar_gemm.h"
+#include "llar_few.h"
 
 namespace llar_ffn {
 
@@ -17,6 +17,60 @@ hipError_t launch_gemm(const GemmPlan& p, const GemmArgs& a, hipStream_t s) {
       {{launch_gemm_F16_00, launch_gemm_F16_01}, {launch_gemm_F16_10, launch_gemm_F16_11}},
       {{launch_gemm_BF16_00, launch_gemm_BF16_01}, {launch_gemm_BF16_10, launch_gemm_BF16_11}}};
   return table[p.kind][p.x_rows][p.w_rows](p, a, s);
+}
+
+// ---- few rows ------------------------------------------------------------------------
+template <class E, bool kGated>
+hipError_t few(bool w_rows, const GemmArgs& a, hipStream_t s) {
+  if (w_rows) {
+    constexpr int kC = 4, kWaves = kGated ? 8 : 16;
+    const int64_t grid = ((int64_t)a.N + 16 * kC - 1) / (16 * kC) * a.splits;
+    k_few_n<E, kGated, kC, kWaves><<<dim3((uint32_t)grid), dim3(kWaves * 64), 0, s>>>(a);
+  } else {
+    constexpr int kN = kGated ? 8 : 16, kWaves = 8;
+    k_few_k<E, kGated, kWaves><<<dim3((uint32_t)((a.N + kN - 1) / kN)), dim3(kWaves * 64), 0, s>>>(a);
+  }
+  return hipGetLastError();
+}
+hipError_t launch_few(int kind, bool w_rows, bool gated, const GemmArgs& a, hipStream_t s) {
+  if (kind == 0) return gated ? few<F32, true>(w_rows, a, s) : few<F32, false>(w_rows, a, s);
+  if (kind == 1) return gated ? few<F16, true>(w_rows, a, s) : few<F16, false>(w_rows, a, s);
+  return gated ? few<BF16, true>(w_rows, a, s) : few<BF16, false>(w_rows, a, s);
+}
+
+// ---- aligned copies ------------------------------------------------------------------
+template <class E>
+__global__ __launch_bounds__(256) void k_repack(RepackArgs a) {
+  typedef typename E::T T;
+  typedef T vec __attribute__((ext_vector_type(8)));
+  typedef vec loose __attribute__((aligned(2)));
+  int i = 0;
+  while (i + 1 < a.count && blockIdx.x >= a.first[i + 1]) i++;
+  const int64_t groups = a.dld[i] / 8;
+  const int64_t id = (blockIdx.x - a.first[i]) * 256 + threadIdx.x;
+  const int64_t line = id / groups;
+  const int64_t at = (id - line * groups) * 8;
+  if (line >= a.lines[i]) return;
+  const T* src = (const T*)a.src[i] + line * a.ld[i] + at;
+  vec v;
+  if (at + 8 <= a.width[i]) {
+    v = *(const loose*)src;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; e++) v[e] = at + e < a.width[i] ? src[e] : (T)0.f;
+  }
+  *(vec*)((T*)a.dst[i] + line * a.dld[i] + at) = v;
+}
+hipError_t launch_repack(int kind, const RepackArgs& a, hipStream_t s) {
+  const dim3 grid((uint32_t)a.first[a.count]), block(256);
+  if (a.first[a.count] == 0) return hipSuccess;
+  if (kind == 0)
+    k_repack<F32><<<grid, block, 0, s>>>(a);
+  else if (kind == 1)
+    k_repack<F16><<<grid, block, 0, s>>>(a);
+  else
+    k_repack<BF16><<<grid, block, 0, s>>>(a);
+  return hipGetLastError();
 }
 
 // ---- join: out = epilogue(sum over splits, in order) -------------------------------
@@ -83,8 +137,9 @@ __global__ __launch_bounds__(256) void k_gate_grad(GateGradArgs a) {
     dg[i] = dh.v[i] * u.v[i] * slope;
     du[i] = dh.v[i] * value;
   }
-  store_vals<E, 8>((T*)a.dg + m * a.dld + col, dg, cnt, vec);
-  store_vals<E, 8>((T*)a.du + m * a.dld + col, du, cnt, vec);
+  // what is loaded beyond column N is 0, and so is its gradient
+  store_vals<E, 8>((T*)a.dg + m * a.dld + col, dg, 8, true);
+  store_vals<E, 8>((T*)a.du + m * a.dld + col, du, 8, true);
 }
 
 hipError_t launch_gate_grad(int kind, const GateGradArgs& a, hipStream_t s) {
@@ -125,7 +180,7 @@ __global__ __launch_bounds__(256) void k_act_grad(ActGradArgs a) {
           act_both(z.v[i], a.act, value, slope);
           d.v[i] *= slope;
         }
-        store_vals<E, 8>((T*)a.dz + m * a.dzld + col, d.v, cnt, vec);
+        store_vals<E, 8>((T*)a.dz + m * a.dzld + col, d.v, 8, true);  // zeros beyond column N
       }
 #pragma unroll
       for (int i = 0; i < 8; i++) acc[i] += d.v[i];

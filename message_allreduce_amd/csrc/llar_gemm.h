@@ -175,41 +175,6 @@ __device__ __forceinline__ void load_direct(lds_char* lds, const char* base, con
   }
 }
 
-// The same tile through registers, for operands whose chunks are not all whole
-// and 16-byte aligned: a chunk inside the matrix is one load at its element's
-// alignment, one at the border is put together from its elements.
-template <class Op>
-__device__ __forceinline__ void load_regs(u32x4 (&v)[Op::kLoads], const char* base, int64_t ld, int rows_left,
-                                          int krem) {
-  typedef typename Op::T T;
-  typedef u32x4 __attribute__((aligned(2))) loose;
-#pragma unroll
-  for (int i = 0; i < Op::kLoads; i++) {
-    int row, k;
-    Op::where(i, row, k);
-    const T* p = (const T*)base + (Op::kByRows ? k * ld + row : row * ld + k);
-    int cnt = Op::kByRows ? (k < krem ? rows_left - row : 0) : (row < rows_left ? krem - k : 0);
-    if (cnt >= Op::CE) {
-      v[i] = *(const loose*)p;
-    } else {
-      union {
-        T t[Op::CE];
-        u32x4 q;
-      } u;
-      u.q = u32x4{0u, 0u, 0u, 0u};
-#pragma unroll
-      for (int e = 0; e < Op::CE; e++)
-        if (e < cnt) u.t[e] = p[e];
-      v[i] = u.q;
-    }
-  }
-}
-template <class Op>
-__device__ __forceinline__ void store_regs(lds_char* lds, const u32x4 (&v)[Op::kLoads]) {
-#pragma unroll
-  for (int i = 0; i < Op::kLoads; i++) *(LLAR_LDS u32x4*)(lds + Op::slot(i) * 16) = v[i];
-}
-
 // The lane's address of fragment 0 (first tile row `row0`), k step 0.
 template <class Op>
 __device__ __forceinline__ uint32_t frag_base(int row0) {
@@ -318,7 +283,7 @@ __device__ float sum_again(const GemmArgs& a, int b, int p, int m, int col, int6
 // One workgroup computes a TM x TN tile of the output (gated: TM x TN/2 of both
 // projections) over its share of the k tiles.  Two LDS buffers: while one is
 // multiplied, the other one's loads are in flight.
-template <class E, bool kXRows, bool kWRows, class Shape, bool kVec, bool kGated>
+template <class E, bool kXRows, bool kWRows, class Shape, bool kGated>
 __global__ __launch_bounds__(Shape::kThreads) void k_gemm(GemmArgs a) {
   constexpr int TM = Shape::TM, NT = Shape::kThreads;
   constexpr int P = kGated ? 2 : 1;              // projections
@@ -369,11 +334,8 @@ __global__ __launch_bounds__(Shape::kThreads) void k_gemm(GemmArgs a) {
 
   const int xleft = a.M - m0, wleft = a.N - n0;
   uint32_t xoff[X::kLoads], woff[W::kLoads];
-  u32x4 xreg[X::kLoads], wreg[P][W::kLoads];
-  if constexpr (kVec) {
-    direct_offsets<X>(xoff, xleft, a.xld);
-    direct_offsets<W>(woff, wleft, a.wld);
-  }
+  direct_offsets<X>(xoff, xleft, a.xld);
+  direct_offsets<W>(woff, wleft, a.wld);
   auto fetch = [&](int t, int buf) {
     const int seg = t / ktiles, kt = t - seg * ktiles;
     const int from = a.segs == 2 ? seg : b;
@@ -381,35 +343,15 @@ __global__ __launch_bounds__(Shape::kThreads) void k_gemm(GemmArgs a) {
     const char* xb = (const char*)a.x[from] + (kXRows ? m0 + k * a.xld : m0 * a.xld + k) * ES;
     const int krem = a.K - (int)k;
     lds_char* at = lds + buf * kBuf;
-    if constexpr (kVec) {
-      load_direct<X>(at, xb, xoff, krem);
-    } else {
-      load_regs<X>(xreg, xb, a.xld, xleft, krem);
-    }
+    load_direct<X>(at, xb, xoff, krem);
 #pragma unroll
     for (int p = 0; p < P; p++) {
       const char* wb = (const char*)a.w[kGated ? p : from] + (kWRows ? n0 + k * a.wld : n0 * a.wld + k) * ES;
-      if constexpr (kVec) {
-        load_direct<W>(at + X::kBytes + p * W::kBytes, wb, woff, krem);
-      } else {
-        load_regs<W>(wreg[p], wb, a.wld, wleft, krem);
-      }
+      load_direct<W>(at + X::kBytes + p * W::kBytes, wb, woff, krem);
     }
   };
-  auto settle = [&](int buf) {
-    if constexpr (!kVec) {
-      lds_char* at = lds + buf * kBuf;
-      store_regs<X>(at, xreg);
-#pragma unroll
-      for (int p = 0; p < P; p++) store_regs<W>(at + X::kBytes + p * W::kBytes, wreg[p]);
-    }
-  };
-
   const uint32_t xbase = frag_base<X>(wm * 16 * FM), wbase = frag_base<W>(wn * 16 * F);
-  if (t0 < t1) {
-    fetch(t0, 0);
-    settle(0);
-  }
+  if (t0 < t1) fetch(t0, 0);
   for (int t = t0; t < t1; t++) {
     const int buf = (t - t0) & 1;
     __syncthreads();  // this buffer has arrived; everyone is done with the other
@@ -431,7 +373,6 @@ __global__ __launch_bounds__(Shape::kThreads) void k_gemm(GemmArgs a) {
           for (int j = 0; j < F; j++) acc[p][f][j] = mma<E>(wf[p][j], xf, acc[p][f][j]);
       }
     }
-    if (t + 1 < t1) settle(buf ^ 1);
   }
 
   // ---- results: lane l holds row m0 + .. + l % 16, and of fragment j the 4
@@ -473,26 +414,22 @@ __global__ __launch_bounds__(Shape::kThreads) void k_gemm(GemmArgs a) {
   }
 }
 
-template <class E, bool kXRows, bool kWRows, class Shape, bool kVec, bool kGated>
+template <class E, bool kXRows, bool kWRows, class Shape, bool kGated>
 hipError_t launch_one(const GemmArgs& a, hipStream_t s) {
   const int tn_cols = Shape::TN / (kGated ? 2 : 1);
   const int64_t tiles = ((int64_t)a.M + Shape::TM - 1) / Shape::TM * (((int64_t)a.N + tn_cols - 1) / tn_cols);
   const int64_t grid = tiles * a.batch * a.splits;
   if (grid <= 0) return hipSuccess;
   if (grid > 0x7fffffff) return hipErrorInvalidValue;
-  k_gemm<E, kXRows, kWRows, Shape, kVec, kGated><<<dim3((uint32_t)grid), dim3(Shape::kThreads), 0, s>>>(a);
+  k_gemm<E, kXRows, kWRows, Shape, kGated><<<dim3((uint32_t)grid), dim3(Shape::kThreads), 0, s>>>(a);
   return hipGetLastError();
 }
 
 template <class E, bool kXRows, bool kWRows, bool kGated>
 hipError_t launch_shape(const GemmPlan& p, const GemmArgs& a, hipStream_t s) {
-  if (p.vec) {
-    if (p.tile == kTile256) return launch_one<E, kXRows, kWRows, Shape256, true, kGated>(a, s);
-    if (p.tile == kTile128) return launch_one<E, kXRows, kWRows, Shape128, true, kGated>(a, s);
-    return launch_one<E, kXRows, kWRows, Shape64, true, kGated>(a, s);
-  }
-  if (p.tile == kTile64) return launch_one<E, kXRows, kWRows, Shape64, false, kGated>(a, s);
-  return launch_one<E, kXRows, kWRows, Shape128, false, kGated>(a, s);
+  if (p.tile == kTile256) return launch_one<E, kXRows, kWRows, Shape256, kGated>(a, s);
+  if (p.tile == kTile128) return launch_one<E, kXRows, kWRows, Shape128, kGated>(a, s);
+  return launch_one<E, kXRows, kWRows, Shape64, kGated>(a, s);
 }
 
 }  // namespace llar_ffn

@@ -80,48 +80,67 @@ def _output(t, x, shape, what):
     return t
 
 
-def _call(fn, op, dims, dt, act, x, stream, mats, tail=()):
-    """mats: tensors of two dimensions, None, or ("ptr", tensor) for a plain
-    vector, in the C call's order."""
+def _raw_stream(device_index):
+    """The current stream's handle, without building a torch stream object where torch offers that."""
+    global _raw_stream
     import torch
-    words = []
-    for t in mats:
-        if t is not None and type(t) is not tuple:
-            r, c = t.stride()
-            words += (t.data_ptr(), t.shape[0], t.shape[1], r, c)
-    arr = (ctypes.c_int64 * len(words))(*words)
-    at = ctypes.addressof(arr)
-    args = []
-    for t in mats:
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    _raw_stream = raw or (lambda index: torch.cuda.current_stream(index).cuda_stream)
+    return _raw_stream(device_index)
+
+
+def _call(fn, op, dims, dt, act, x, stream, inputs, outputs):
+    """inputs, outputs: matrices (tensors of two dimensions), plain vectors (one dimension) or None, in the C
+    call's order.  stream: a handle."""
+    import torch
+    words, args, unaligned = [], [], 0  # a matrix's place among the words goes into args as a negative number
+    es = 4 if dt == 0 else 2
+    for t in inputs:
         if t is None:
             args.append(None)
-        elif type(t) is tuple:
-            args.append(t[1].data_ptr())
+        elif t.dim() == 1:
+            args.append(t.data_ptr())
         else:
-            args.append(at)
-            at += _MATRIX_BYTES
-    key = (op, dt) + dims
+            args.append(~(len(words) * 8))
+            p, (rows, cols), (r, c) = t.data_ptr(), t.shape, t.stride()
+            words += (p, rows, cols, r, c)
+            width, line = (cols, r if rows > 1 else 0) if cols <= 1 or c == 1 else (rows, c)
+            unaligned |= (p | (width | line) * es) & 15 | (line * es >= 1 << 23)
+    for t in outputs:
+        if t is None:
+            args.append(None)
+        elif t.dim() == 1:
+            args.append(t.data_ptr())
+        else:
+            args.append(~(len(words) * 8))
+            words += (t.data_ptr(), *t.shape, *t.stride())
+    arr = (ctypes.c_int64 * len(words))(*words)
+    at = ctypes.addressof(arr)
+    args = [a if a is None or a >= 0 else at + ~a for a in args]
+    key = (op, dt, unaligned) + dims
     need = _space.get(key)
+    L = lib()
     if need is None:
         if len(_space) > 4096:
             _space.clear()
-        need = _space[key] = lib().llar_ffn_workspace(op, dims[0], dims[1], dims[2], dt)
+        need = _space[key] = L.llar_ffn_workspace(op, dims[0], dims[1], dims[2], dt, not unaligned)
     ws = torch.empty(need, dtype=torch.uint8, device=x.device) if need else None
-    return getattr(lib(), fn)(*args, dt, act, ws.data_ptr() if need else None, need, stream.cuda_stream)
+    return getattr(L, fn)(*args, dt, act, ws.data_ptr() if need else None, need, stream)
 
 
 def _on(x, stream, body):
-    """Run body(stream) with x's device current and torch's allocations on the stream."""
+    """Run body(stream handle) with x's device current and torch's allocations on the stream."""
     import torch
     if stream is None:
-        if x.device.index == torch.cuda.current_device():
-            return body(torch.cuda.current_stream())
-        with torch.cuda.device(x.device):
-            return body(torch.cuda.current_stream())
+        at = x.get_device()
+        if at == torch.cuda.current_device():
+            return body(_raw_stream(at))
+        with torch.cuda.device(at):
+            return body(_raw_stream(at))
     if stream.device != x.device:
         raise ValueError("stream is on %s, x on %s" % (stream.device, x.device))
     with torch.cuda.stream(stream):
-        return body(stream)
+        return body(stream.cuda_stream)
 
 
 def linear(x, weight, bias=None, residual=None, activation="none", save=False, out=None, stream=None):
@@ -147,9 +166,8 @@ def linear(x, weight, bias=None, residual=None, activation="none", save=False, o
         y = _output(out, x, shape, "out")
         z = _output(None, x, shape, "pre") if save else None
         st = _call("llar_linear", _LINEAR, (x2.shape[0], n, x2.shape[1]), dt, act, x, s,
-                   (x2, weight, None if bias is None else ("ptr", bias),
-                    None if residual is None else _flat(residual, "residual"), _flat(y, "out"),
-                    _flat(z, "pre") if save else None))
+                   (x2, weight, bias, None if residual is None else _flat(residual, "residual")),
+                   (_flat(y, "out"), _flat(z, "pre") if save else None))
         _check(st, "llar_linear")
         return (y, z) if save else y
 
@@ -178,8 +196,8 @@ def linear_backward(dy, x, weight, pre=None, activation="none", input_grad=True,
         dw = torch.empty(weight.shape, dtype=x.dtype, device=x.device) if weight_grad else None
         db = torch.empty(n, dtype=x.dtype, device=x.device) if bias_grad else None
         st = _call("llar_linear_backward", _LINEAR_BACKWARD, (x2.shape[0], n, x2.shape[1]), dt, act, x, s,
-                   (dy2, x2, weight, _flat(pre, "pre") if act else None, _flat(dx, "dx") if input_grad else None, dw,
-                    ("ptr", db) if bias_grad else None))
+                   (dy2, x2, weight, _flat(pre, "pre") if act else None),
+                   (_flat(dx, "dx") if input_grad else None, dw, db))
         _check(st, "llar_linear_backward")
         return dx, dw, db
 
@@ -207,8 +225,8 @@ def gated_ffn(x, w_gate, w_up, activation="silu", save=False, out=None, stream=N
         g = _output(None, x, shape, "gate") if save else None
         u = _output(None, x, shape, "up") if save else None
         st = _call("llar_gated_ffn", _GATED, (x2.shape[0], n, x2.shape[1]), dt, act, x, s,
-                   (x2, w_gate, w_up, _flat(h, "out"), _flat(g, "gate") if save else None,
-                    _flat(u, "up") if save else None))
+                   (x2, w_gate, w_up),
+                   (_flat(h, "out"), _flat(g, "gate") if save else None, _flat(u, "up") if save else None))
         _check(st, "llar_gated_ffn")
         return (h, g, u) if save else h
 
@@ -232,8 +250,8 @@ def gated_ffn_backward(dh, x, w_gate, w_up, gate, up, activation="silu", input_g
         dwg = torch.empty(w_gate.shape, dtype=x.dtype, device=x.device) if weight_grad else None
         dwu = torch.empty(w_gate.shape, dtype=x.dtype, device=x.device) if weight_grad else None
         st = _call("llar_gated_ffn_backward", _GATED_BACKWARD, (x2.shape[0], n, x2.shape[1]), dt, act, x, s,
-                   (_flat(dh, "dh"), x2, w_gate, w_up, _flat(gate, "gate"), _flat(up, "up"),
-                    _flat(dx, "dx") if input_grad else None, dwg, dwu))
+                   (_flat(dh, "dh"), x2, w_gate, w_up, _flat(gate, "gate"), _flat(up, "up")),
+                   (_flat(dx, "dx") if input_grad else None, dwg, dwu))
         _check(st, "llar_gated_ffn_backward")
         return dx, dwg, dwu
 
