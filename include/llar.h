@@ -250,21 +250,27 @@ typedef enum {
  * An input needs a stride of 1 along one axis (any layout when that axis has
  * one element); where stated, and for every output, col_stride must be 1.
  * Output rows must not overlap.  Any alignment is accepted; above 16
- * tokens, operands that are not aligned as llar_ffn_workspace describes are
- * copied into the workspace first. */
+ * tokens, LLAR_LAYOUT_UNALIGNED operands are copied into
+ * the workspace first. */
 typedef struct {
   void* data;
   int64_t rows, cols, row_stride, col_stride;
 } llar_matrix;
 
+/* What llar_ffn_workspace has to know of a call's layout, added up. */
+enum {
+  LLAR_LAYOUT_UNALIGNED = 1,   /* an input matrix (x, a weight, linear_backward's dy) lacks 16-byte aligned data, or
+                                  its contiguous lines are, in bytes, not a multiple of 16 long or apart, or 8 MiB or
+                                  more apart: adds room for copies */
+  LLAR_LAYOUT_X_COLUMNS = 2,   /* x's columns are contiguous, not its rows (a transposed view) */
+  LLAR_LAYOUT_W_COLUMNS = 4,   /* so are the weights' */
+  LLAR_LAYOUT_DY_COLUMNS = 8   /* so are linear_backward's dy's */
+};
+
 /* Bytes of workspace a call needs for m tokens, n outputs and k inputs (0 is
- * possible; then NULL may be passed).  aligned: 1 if every input matrix (of
- * linear_backward and gated_ffn_backward too) has 16-byte aligned data and,
- * in bytes, a multiple of 16 as the length and the distance of its contiguous
- * lines, which are less than 8 MiB apart; 0 otherwise, which adds room for copies that do.  The workspace is
- * 256-byte aligned device memory, free for other use once the stream has
- * passed the call. */
-size_t llar_ffn_workspace(llar_ffn_op op, int64_t m, int64_t n, int64_t k, llar_dtype dtype, int aligned);
+ * possible; then NULL may be passed).  The workspace is 256-byte aligned
+ * device memory, free for other use once the stream has passed the call. */
+size_t llar_ffn_workspace(llar_ffn_op op, int64_t m, int64_t n, int64_t k, llar_dtype dtype, int layout);
 
 /* out = act(x w^T + bias) + residual:  x m x k, w n x k, out m x n.
  * bias: n contiguous elements, or NULL.  residual: m x n with contiguous

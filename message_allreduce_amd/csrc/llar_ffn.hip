@@ -113,14 +113,9 @@ size_t partial_bytes(const Shape& s, int64_t M, int64_t N, int planes) {
   return s.splits <= 1 ? 0 : align256((size_t)s.splits * planes * M * (size_t)(cdiv(N, 8) * 8) * 4);
 }
 
-// The space for partial sums of a product of this shape, whatever its operands' order.
-size_t product_space(int64_t M, int64_t N, int64_t K, int segs, int outs, bool gated, int es) {
-  size_t need = 0;
-  for (int way = 0; way < 3; way++) {
-    const Shape s = choose(M, N, K, segs, outs, gated, es, way > 0, way > 1);
-    need = std::max(need, partial_bytes(s, M, N, gated ? 2 : outs));
-  }
-  return need;
+size_t product_space(int64_t M, int64_t N, int64_t K, int segs, int outs, bool gated, int es, bool x_rows,
+                     bool w_rows) {
+  return partial_bytes(choose(M, N, K, segs, outs, gated, es, !x_rows, w_rows), M, N, gated ? 2 : outs);
 }
 
 struct Carve {
@@ -274,11 +269,16 @@ int row_chunks(int64_t M, int64_t N) {
 bool space_ok(void* w, size_t n) { return n == 0 || (w && ((uintptr_t)w & 255) == 0); }
 
 // Whether the workspace holds what a call on these inputs needs.
-bool enough(size_t bytes, llar_ffn_op op, const llar_matrix* x, const llar_matrix* w, llar_dtype dtype,
-            std::initializer_list<const llar_matrix*> inputs) {
-  bool aligned = true;
-  for (const llar_matrix* m : inputs) aligned = aligned && (!m || chunks_whole(operand(m), elem_size(dtype)));
-  return bytes >= llar_ffn_workspace(op, x->rows, w->rows, x->cols, dtype, aligned);
+bool enough(size_t bytes, llar_ffn_op op, const llar_matrix* x, const llar_matrix* w, const llar_matrix* w2,
+            const llar_matrix* dy, llar_dtype dtype) {
+  const int es = elem_size(dtype);
+  int layout = 0;
+  for (const llar_matrix* m : {x, w, w2, dy})
+    if (m && !chunks_whole(operand(m), es)) layout = LLAR_LAYOUT_UNALIGNED;
+  if (!row_major(x)) layout |= LLAR_LAYOUT_X_COLUMNS;
+  if (!row_major(w)) layout |= LLAR_LAYOUT_W_COLUMNS;
+  if (dy && !row_major(dy)) layout |= LLAR_LAYOUT_DY_COLUMNS;
+  return bytes >= llar_ffn_workspace(op, x->rows, w->rows, x->cols, dtype, layout);
 }
 
 }  // namespace
@@ -291,20 +291,24 @@ bool enough(size_t bytes, llar_ffn_op op, const llar_matrix* x, const llar_matri
 
 extern "C" {
 
-size_t llar_ffn_workspace(llar_ffn_op op, int64_t m, int64_t n, int64_t k, llar_dtype dtype, int aligned) {
+size_t llar_ffn_workspace(llar_ffn_op op, int64_t m, int64_t n, int64_t k, llar_dtype dtype, int layout) {
   if (!dtype_ok(dtype) || m < 0 || n < 0 || k < 0 || m > kMaxDim || n > kMaxDim || k > kMaxDim) return 0;
   const int es = elem_size(dtype);
-  const size_t x = aligned ? 0 : copy_bytes(m, k, es), w = aligned ? 0 : copy_bytes(n, k, es);
+  const bool copies = layout & LLAR_LAYOUT_UNALIGNED, xr = layout & LLAR_LAYOUT_X_COLUMNS,
+             wr = layout & LLAR_LAYOUT_W_COLUMNS, yr = layout & LLAR_LAYOUT_DY_COLUMNS;
+  const size_t x = copies ? copy_bytes(m, k, es) : 0, w = copies ? copy_bytes(n, k, es) : 0;
   const size_t dz = align256((size_t)m * (cdiv(n, 8) * 8) * es);
   switch (op) {
-    case LLAR_OP_LINEAR: return x + w + product_space(m, n, k, 1, 1, false, es);
-    case LLAR_OP_GATED_FFN: return x + 2 * w + product_space(m, n, k, 1, 1, true, es);
+    case LLAR_OP_LINEAR: return x + w + product_space(m, n, k, 1, 1, false, es, xr, wr);
+    case LLAR_OP_GATED_FFN: return x + 2 * w + product_space(m, n, k, 1, 1, true, es, xr, wr);
     case LLAR_OP_LINEAR_BACKWARD:
-      return x + w + (aligned ? dz : copy_bytes(m, n, es)) + align256((size_t)row_chunks(m, n) * n * 4) +
-             std::max(product_space(m, k, n, 1, 1, false, es), product_space(n, k, m, 1, 1, false, es));
+      return x + w + (copies ? copy_bytes(m, n, es) : dz) + align256((size_t)row_chunks(m, n) * n * 4) +
+             std::max(product_space(m, k, n, 1, 1, false, es, yr, !wr),
+                      product_space(n, k, m, 1, 1, false, es, !yr, !xr));
     case LLAR_OP_GATED_FFN_BACKWARD:
       return x + 2 * w + 2 * dz +
-             std::max(product_space(m, k, n, 2, 1, false, es), product_space(n, k, m, 1, 2, false, es));
+             std::max(product_space(m, k, n, 2, 1, false, es, false, !wr),
+                      product_space(n, k, m, 1, 2, false, es, true, !xr));
   }
   return 0;
 }
@@ -326,7 +330,7 @@ int llar_linear(const llar_matrix* x, const llar_matrix* w, const void* bias, co
     LLAR_TRY(check(pre, true));
     if (!same_shape(pre, out)) return llar::fail(LLAR_ERR_ARG);
   }
-  if (!enough(workspace_bytes, LLAR_OP_LINEAR, x, w, dtype, {x, w})) return llar::fail(LLAR_ERR_ARG);
+  if (!enough(workspace_bytes, LLAR_OP_LINEAR, x, w, nullptr, nullptr, dtype)) return llar::fail(LLAR_ERR_ARG);
   Product p;
   p.x[0] = operand(x);
   p.w[0] = operand(w);
@@ -369,7 +373,7 @@ int llar_linear_backward(const llar_matrix* dy, const llar_matrix* x, const llar
     LLAR_TRY(check(dw, true));
     if (!same_shape(dw, w)) return llar::fail(LLAR_ERR_ARG);
   }
-  if (!enough(workspace_bytes, LLAR_OP_LINEAR_BACKWARD, x, w, dtype, {dy, x, w})) return llar::fail(LLAR_ERR_ARG);
+  if (!enough(workspace_bytes, LLAR_OP_LINEAR_BACKWARD, x, w, nullptr, dy, dtype)) return llar::fail(LLAR_ERR_ARG);
   const int64_t M = dy->rows, N = dy->cols;
   const int es = elem_size(dtype);
   Carve c{(uint8_t*)workspace, workspace_bytes};
@@ -449,7 +453,7 @@ int llar_gated_ffn(const llar_matrix* x, const llar_matrix* w_gate, const llar_m
   p.w[1] = operand(w_up);
   p.n_w = 2;
   if (p.w[0].by_rows != p.w[1].by_rows || p.w[0].ld != p.w[1].ld) return llar::fail(LLAR_ERR_UNSUPPORTED);
-  if (!enough(workspace_bytes, LLAR_OP_GATED_FFN, x, w_gate, dtype, {x, w_gate, w_up}))
+  if (!enough(workspace_bytes, LLAR_OP_GATED_FFN, x, w_gate, w_up, nullptr, dtype))
     return llar::fail(LLAR_ERR_ARG);
   p.gated = true;
   p.out[0] = out->data;
@@ -492,7 +496,7 @@ int llar_gated_ffn_backward(const llar_matrix* dh, const llar_matrix* x, const l
   }
   const Operand wg = operand(w_gate), wu = operand(w_up);
   if (wg.by_rows != wu.by_rows || wg.ld != wu.ld) return llar::fail(LLAR_ERR_UNSUPPORTED);
-  if (!enough(workspace_bytes, LLAR_OP_GATED_FFN_BACKWARD, x, w_gate, dtype, {x, w_gate, w_up}))
+  if (!enough(workspace_bytes, LLAR_OP_GATED_FFN_BACKWARD, x, w_gate, w_up, nullptr, dtype))
     return llar::fail(LLAR_ERR_ARG);
   const int es = elem_size(dtype);
   const int64_t M = dh->rows, N = dh->cols;

@@ -237,12 +237,12 @@ def test_feed_forward_calls_check_their_arguments_without_a_gpu(L):
     assert linear(*ok, residual=mat(4, 32, 1, 4)) == -2 and linear(*ok, pre=mat(3, 32)) == -1
     assert linear(*ok, ws=4096 + 8, n=1 << 20) == -1              # misaligned workspace
     assert linear(mat(0, 64), mat(32, 64), mat(0, 32)) == 0       # nothing to do
-    need = L.llar_ffn_workspace(1, 4, 32, 64, 2, 1)
+    need = L.llar_ffn_workspace(1, 4, 32, 64, 2, 0)
     assert need > 0 and L.llar_ffn_workspace(1, 4, 32, 64, 9, 1) == 0 and L.llar_ffn_workspace(9, 4, 32, 64, 2, 1) == 0
     for op in range(4):                                           # empty products have a size too
         for dims in ((0, 8, 8), (3, 0, 8), (3, 8, 0), (0, 0, 0)):
-            for aligned in (0, 1):
-                assert L.llar_ffn_workspace(op, *dims, 2, aligned) < 4096
+            for layout in range(16):
+                assert L.llar_ffn_workspace(op, *dims, 2, layout) < 4096
     back = (mat(4, 32), mat(4, 64), mat(32, 64))
     assert L.llar_linear_backward(*back, None, mat(4, 64), mat(32, 64), None, 2, 0, None, 0, None) == -1
     assert L.llar_linear_backward(*back, None, mat(4, 64), mat(32, 64), None, 2, 4, 4096, need, None) == -1  # no pre
