@@ -101,7 +101,7 @@ Shape choose(int64_t M, int64_t N, int64_t K, int segs, int outs, bool gated, in
   }
   const int64_t kt = cdiv(K * es, kTileKBytes) * segs;
   auto tiles = [&](int t) { return cdiv(M, kTileM[t]) * cdiv(N, kTileN[t] / (gated ? 2 : 1)) * outs; };
-  if (tiles(kTile256) >= 192)
+  if (es == 2 && tiles(kTile256) >= 192)
     s.tile = kTile256;
   else if (tiles(kTile128) >= 256)
     s.tile = kTile128;

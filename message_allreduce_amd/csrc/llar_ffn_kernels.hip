@@ -130,13 +130,15 @@ __global__ __launch_bounds__(256) void k_gate_grad(GateGradArgs a) {
   const Vals<E, 8> g = load_vals<E, 8>((const T*)a.g + m * a.gld + col, cnt, vec);
   const Vals<E, 8> u = load_vals<E, 8>((const T*)a.u + m * a.uld + col, cnt, vec);
   float dg[8], du[8];
+  with_act(a.act, [&](auto c) {
 #pragma unroll
-  for (int i = 0; i < 8; i++) {
-    float value, slope;
-    act_both(g.v[i], a.act, value, slope);
-    dg[i] = dh.v[i] * u.v[i] * slope;
-    du[i] = dh.v[i] * value;
-  }
+    for (int i = 0; i < 8; i++) {
+      float value, slope;
+      act_two<decltype(c)::value>(g.v[i], value, slope);
+      dg[i] = dh.v[i] * u.v[i] * slope;
+      du[i] = dh.v[i] * value;
+    }
+  });
   // what is loaded beyond column N is 0, and so is its gradient
   store_vals<E, 8>((T*)a.dg + m * a.dld + col, dg, 8, true);
   store_vals<E, 8>((T*)a.du + m * a.dld + col, du, 8, true);
@@ -174,12 +176,14 @@ __global__ __launch_bounds__(256) void k_act_grad(ActGradArgs a) {
       Vals<E, 8> d = load_vals<E, 8>((const T*)a.dy + m * a.dyld + col, cnt, vec);
       if (a.z) {
         const Vals<E, 8> z = load_vals<E, 8>((const T*)a.z + m * a.zld + col, cnt, vec);
+        with_act(a.act, [&](auto c) {
 #pragma unroll
-        for (int i = 0; i < 8; i++) {
-          float value, slope;
-          act_both(z.v[i], a.act, value, slope);
-          d.v[i] *= slope;
-        }
+          for (int i = 0; i < 8; i++) {
+            float value, slope;
+            act_two<decltype(c)::value>(z.v[i], value, slope);
+            d.v[i] *= slope;
+          }
+        });
         store_vals<E, 8>((T*)a.dz + m * a.dzld + col, d.v, 8, true);  // zeros beyond column N
       }
 #pragma unroll

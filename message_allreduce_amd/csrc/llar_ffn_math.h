@@ -4,6 +4,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "llar_ffn.h"
 
 namespace llar_ffn {
@@ -88,47 +90,57 @@ constexpr float kInvSqrt2Pi = 0.3989422804014327f;
 // there is 0, where the plain product would be a NaN.
 __device__ __forceinline__ float fading(float z, float s) { return s == 0.f ? 0.f : z * s; }
 
-__device__ __forceinline__ float act_value(float z, int act) {
-  switch (act) {
-    case kActRelu: return z < 0.f ? 0.f : z;  // keeps a NaN
-    case kActGelu: return fading(z, 0.5f * erfcf(-z * kSqrtHalf));
-    case kActGeluTanh: return fading(z, sigmoid(2.f * kSqrt2OverPi * (z + kGeluCubic * z * z * z)));
-    case kActSilu: return fading(z, sigmoid(z));
-    default: return z;
-  }
+template <int act>
+__device__ __forceinline__ float act_one(float z) {
+  if constexpr (act == kActRelu) return z < 0.f ? 0.f : z;  // keeps a NaN
+  if constexpr (act == kActGelu) return fading(z, 0.5f * erfcf(-z * kSqrtHalf));
+  if constexpr (act == kActGeluTanh) return fading(z, sigmoid(2.f * kSqrt2OverPi * (z + kGeluCubic * z * z * z)));
+  if constexpr (act == kActSilu) return fading(z, sigmoid(z));
+  return z;
 }
 
 // The value and the derivative together: they share the exponential.
-__device__ __forceinline__ void act_both(float z, int act, float& value, float& slope) {
-  switch (act) {
-    case kActRelu:
-      value = z < 0.f ? 0.f : z;
-      slope = z > 0.f ? 1.f : (z <= 0.f ? 0.f : z);
-      break;
-    case kActGelu: {
-      const float p = 0.5f * erfcf(-z * kSqrtHalf);
-      value = fading(z, p);
-      slope = p + fading(z, kInvSqrt2Pi * expf(-0.5f * z * z));
-      break;
-    }
-    case kActGeluTanh: {
-      const float s = sigmoid(2.f * kSqrt2OverPi * (z + kGeluCubic * z * z * z));
-      value = fading(z, s);
-      // s (1 - s) is 0 long before the square would overflow
-      const float d = s * (1.f - s);
-      slope = d == 0.f ? s : s + z * d * 2.f * kSqrt2OverPi * (1.f + 3.f * kGeluCubic * z * z);
-      break;
-    }
-    case kActSilu: {
-      const float s = sigmoid(z);
-      value = fading(z, s);
-      slope = s + fading(z, s * (1.f - s));
-      break;
-    }
-    default:
-      value = z;
-      slope = 1.f;
+template <int act>
+__device__ __forceinline__ void act_two(float z, float& value, float& slope) {
+  value = z;
+  slope = 1.f;
+  if constexpr (act == kActRelu) {
+    value = z < 0.f ? 0.f : z;
+    slope = z > 0.f ? 1.f : (z <= 0.f ? 0.f : z);
+  } else if constexpr (act == kActGelu) {
+    const float p = 0.5f * erfcf(-z * kSqrtHalf);
+    value = fading(z, p);
+    slope = p + fading(z, kInvSqrt2Pi * expf(-0.5f * z * z));
+  } else if constexpr (act == kActGeluTanh) {
+    const float s = sigmoid(2.f * kSqrt2OverPi * (z + kGeluCubic * z * z * z));
+    value = fading(z, s);
+    // s (1 - s) is 0 long before the square would overflow
+    const float d = s * (1.f - s);
+    slope = d == 0.f ? s : s + z * d * 2.f * kSqrt2OverPi * (1.f + 3.f * kGeluCubic * z * z);
+  } else if constexpr (act == kActSilu) {
+    const float s = sigmoid(z);
+    value = fading(z, s);
+    slope = s + fading(z, s * (1.f - s));
   }
+}
+
+// Calls f with the activation as a constant.
+template <class F>
+__device__ __forceinline__ void with_act(int act, F f) {
+  switch (act) {
+    case kActRelu: return f(std::integral_constant<int, kActRelu>());
+    case kActGelu: return f(std::integral_constant<int, kActGelu>());
+    case kActGeluTanh: return f(std::integral_constant<int, kActGeluTanh>());
+    case kActSilu: return f(std::integral_constant<int, kActSilu>());
+    default: return f(std::integral_constant<int, kActNone>());
+  }
+}
+template <int n>
+__device__ __forceinline__ void act_values(float (&y)[n], int act) {
+  with_act(act, [&](auto c) {
+#pragma unroll
+    for (int i = 0; i < n; i++) y[i] = act_one<decltype(c)::value>(y[i]);
+  });
 }
 
 }  // namespace llar_ffn

@@ -17,6 +17,7 @@ struct TileShape {
   static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
   static constexpr int FM = TM / WM / 16;  // 16-row fragments of a wave along m
   static constexpr int FN = TN / WN / 16;  // and along n
+  static constexpr bool kPaired = WM == 2 && WN == 4;
 };
 typedef TileShape<256, 256, 2, 4> Shape256;
 typedef TileShape<128, 128, 2, 2> Shape128;
@@ -158,15 +159,15 @@ __device__ __forceinline__ void direct_offsets(uint32_t (&voff)[Op::kLoads], int
   }
 }
 
-// Loads straight into LDS, 16 bytes a lane; the wave's 64 chunks land back to
-// back.  krem: how many k of the tile exist.
-template <class Op>
+// Loads i0 .. i1 - 1 straight into LDS, 16 bytes a lane; the wave's 64 chunks
+// land back to back.  krem: how many k of the tile exist.
+template <class Op, int i0, int i1>
 __device__ __forceinline__ void load_direct(lds_char* lds, const char* base, const uint32_t (&voff)[Op::kLoads],
                                             int krem) {
   __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void*)base, (short)0, 0x7fffffff, 0x00020000);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 #pragma unroll
-  for (int i = 0; i < Op::kLoads; i++) {
+  for (int i = i0; i < i1; i++) {
     int row, k;
     Op::where(i, row, k);
     const uint32_t off = k < krem ? voff[i] : kNoLoad;
@@ -240,7 +241,10 @@ __device__ __forceinline__ void finish(const GemmArgs& a, int b, int m, int col,
       store_vals<E, n>((T*)a.z[1] + m * a.zld + col, acc1, cnt, vec);
     }
 #pragma unroll
-    for (int i = 0; i < n; i++) y[i] = act_value(acc0[i], a.act) * acc1[i];
+    for (int i = 0; i < n; i++) y[i] = acc0[i];
+    act_values<n>(y, a.act);
+#pragma unroll
+    for (int i = 0; i < n; i++) y[i] *= acc1[i];
   } else {
 #pragma unroll
     for (int i = 0; i < n; i++) y[i] = acc0[i];
@@ -250,10 +254,7 @@ __device__ __forceinline__ void finish(const GemmArgs& a, int b, int m, int col,
       for (int i = 0; i < n; i++) y[i] += v.v[i];
     }
     if (a.z[0]) store_vals<E, n>((T*)a.z[0] + m * a.zld + col, y, cnt, vec);
-    if (a.act != kActNone) {
-#pragma unroll
-      for (int i = 0; i < n; i++) y[i] = act_value(y[i], a.act);
-    }
+    act_values<n>(y, a.act);
     if (a.resid) {
       const Vals<E, n> v = load_vals<E, n>((const T*)a.resid + m * a.rld + col, cnt, vec);
 #pragma unroll
@@ -268,7 +269,7 @@ __device__ __forceinline__ void finish(const GemmArgs& a, int b, int m, int col,
 // bfloat16's infinity does the same), so a NaN sum of binary32 inputs is taken
 // again from the inputs, in k order, up to the first true NaN.
 template <bool kXRows, bool kWRows>
-__device__ float sum_again(const GemmArgs& a, int b, int p, int m, int col, int64_t k0, int64_t k1) {
+__device__ __forceinline__ float sum_again(const GemmArgs& a, int b, int p, int m, int col, int64_t k0, int64_t k1) {
   float s = 0.f;
   for (int64_t k = k0; k < k1 && s == s; k++) {
     const int seg = a.segs == 2 ? (int)(k / a.K) : b;
@@ -292,6 +293,7 @@ __global__ __launch_bounds__(Shape::kThreads) void k_gemm(GemmArgs a) {
   constexpr bool kSpread = !kWRows;
   typedef Operand<E, kXRows, TM, NT, FM, false> X;
   typedef Operand<E, kWRows, TN, NT, F, kSpread> W;
+  typedef typename E::T T;
   constexpr int BK = X::BK, ES = X::ES;
   constexpr int kBuf = X::kBytes + P * W::kBytes;
   __shared__ __attribute__((aligned(1024))) char smem[2 * kBuf];
@@ -336,81 +338,247 @@ __global__ __launch_bounds__(Shape::kThreads) void k_gemm(GemmArgs a) {
   uint32_t xoff[X::kLoads], woff[W::kLoads];
   direct_offsets<X>(xoff, xleft, a.xld);
   direct_offsets<W>(woff, wleft, a.wld);
-  auto fetch = [&](int t, int buf) {
-    const int seg = t / ktiles, kt = t - seg * ktiles;
-    const int from = a.segs == 2 ? seg : b;
-    const int64_t k = (int64_t)kt * BK;
-    const char* xb = (const char*)a.x[from] + (kXRows ? m0 + k * a.xld : m0 * a.xld + k) * ES;
-    const int krem = a.K - (int)k;
-    lds_char* at = lds + buf * kBuf;
-    load_direct<X>(at, xb, xoff, krem);
-#pragma unroll
-    for (int p = 0; p < P; p++) {
-      const char* wb = (const char*)a.w[kGated ? p : from] + (kWRows ? n0 + k * a.wld : n0 * a.wld + k) * ES;
-      load_direct<W>(at + X::kBytes + p * W::kBytes, wb, woff, krem);
-    }
+  // k tile t of both operands: first the tile's place, then parts of its loads
+  const int64_t x1 = (int64_t)a.x[1], w1 = (int64_t)a.w[1];
+  const int64_t x0 = b ? x1 : (int64_t)a.x[0], w0 = b ? w1 : (int64_t)a.w[0];
+  const int64_t xfirst = kXRows ? m0 : m0 * a.xld, xstep = kXRows ? BK * a.xld : BK;
+  const int64_t wfirst = kWRows ? n0 : n0 * a.wld, wstep = kWRows ? BK * a.wld : BK;
+  const char *xb, *wb[2];
+  int krem;
+  auto aim = [&](int t) {
+    const bool second = a.segs == 2 && t >= ktiles;
+    const int kt = second ? t - ktiles : t;
+    xb = (const char*)((second ? x1 : x0) + (xfirst + kt * xstep) * ES);
+    wb[0] = (const char*)((second ? w1 : w0) + (wfirst + kt * wstep) * ES);
+    if constexpr (kGated) wb[1] = (const char*)(w1 + (wfirst + kt * wstep) * ES);
+    krem = a.K - kt * BK;
   };
+  auto fetch_x = [&](int buf) { load_direct<X, 0, X::kLoads>(lds + buf * kBuf, xb, xoff, krem); };
+  auto fetch_w = [&](int buf) {
+#pragma unroll
+    for (int p = 0; p < P; p++)
+      load_direct<W, 0, W::kLoads>(lds + buf * kBuf + X::kBytes + p * W::kBytes, wb[p], woff, krem);
+  };
+
   const uint32_t xbase = frag_base<X>(wm * 16 * FM), wbase = frag_base<W>(wn * 16 * F);
-  if (t0 < t1) fetch(t0, 0);
-  for (int t = t0; t < t1; t++) {
-    const int buf = (t - t0) & 1;
-    __syncthreads();  // this buffer has arrived; everyone is done with the other
-    if (t + 1 < t1) fetch(t + 1, buf ^ 1);
-    lds_char* at = lds + buf * kBuf;
+  if constexpr (Shape::kPaired) {
+    // Two groups of four waves (one a SIMD) take turns: while one multiplies a
+    // quarter of its wave tiles (16 products of fragments), the other reads its
+    // next fragments and issues loads.  A barrier ends every half turn; the
+    // second group runs half a turn behind.
+    constexpr int KK = BK / 32, HM = FM / 2, HN = (P * F) / 2;
+    static_assert(FM % 2 == 0 && (P * F) % 2 == 0, "quarters");
+    Frag<E> xf[HM][KK], wf[2][HN][KK];
+    auto read_x = [&](lds_char* at, int h) {
 #pragma unroll
-    for (int kk = 0; kk < BK / 32; kk++) {
-      Frag<E> wf[P][F];
+      for (int kk = 0; kk < KK; kk++)
 #pragma unroll
-      for (int p = 0; p < P; p++)
+        for (int f = 0; f < HM; f++) xf[f][kk] = read_frag<X, E>(at, xbase, h * HM + f, kk);
+    };
+    auto read_w = [&](lds_char* at, int h) {
 #pragma unroll
-        for (int j = 0; j < F; j++) wf[p][j] = read_frag<W, E>(at + X::kBytes + p * W::kBytes, wbase, j, kk);
+      for (int kk = 0; kk < KK; kk++)
 #pragma unroll
-      for (int f = 0; f < FM; f++) {
-        const Frag<E> xf = read_frag<X, E>(at, xbase, f, kk);
+        for (int j = 0; j < HN; j++)
+          wf[h][j][kk] = read_frag<W, E>(at + X::kBytes + (h * HN + j) / F * W::kBytes, wbase, (h * HN + j) % F, kk);
+    };
+    auto multiply = [&](int hm, int hn) {
+      __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+      for (int kk = 0; kk < KK; kk++)
+#pragma unroll
+        for (int f = 0; f < HM; f++)
+#pragma unroll
+          for (int j = 0; j < HN; j++) {
+            f32x4& c = acc[(hn * HN + j) / F][hm * HM + f][(hn * HN + j) % F];
+            c = mma<E>(wf[hn][j][kk], xf[f][kk], c);
+          }
+      __builtin_amdgcn_s_setprio(0);
+    };
+    auto turn = [] {
+      __builtin_amdgcn_sched_barrier(0);
+      asm volatile("s_barrier" ::: "memory");
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    auto arrived = [] { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); };
+    if (t0 < t1) {
+      aim(t0);
+      fetch_x(0);
+      fetch_w(0);
+    }
+    arrived();
+    turn();
+    if (wm == 1) turn();
+    for (int t = t0; t < t1; t++) {
+      const int buf = (t - t0) & 1;
+      lds_char* at = lds + buf * kBuf;
+      const bool more = t + 1 < t1;
+      read_w(at, 0);
+      read_x(at, 0);
+      if (more) {
+        aim(t + 1);
+        fetch_x(buf ^ 1);
+      }
+      turn();
+      multiply(0, 0);
+      turn();
+      read_w(at, 1);
+      if (more) fetch_w(buf ^ 1);
+      turn();
+      multiply(0, 1);
+      turn();
+      read_x(at, 1);
+      turn();
+      multiply(1, 1);
+      turn();
+      arrived();
+      turn();
+      multiply(1, 0);
+      turn();
+    }
+    if (wm == 0) turn();
+  } else {
+    if (t0 < t1) {
+      aim(t0);
+      fetch_x(0);
+      fetch_w(0);
+    }
+    for (int t = t0; t < t1; t++) {
+      const int buf = (t - t0) & 1;
+      __syncthreads();  // this buffer has arrived; everyone is done with the other
+      if (t + 1 < t1) {
+        aim(t + 1);
+        fetch_x(buf ^ 1);
+        fetch_w(buf ^ 1);
+      }
+      lds_char* at = lds + buf * kBuf;
+#pragma unroll
+      for (int kk = 0; kk < BK / 32; kk++) {
+        Frag<E> wf[P][F];
 #pragma unroll
         for (int p = 0; p < P; p++)
 #pragma unroll
-          for (int j = 0; j < F; j++) acc[p][f][j] = mma<E>(wf[p][j], xf, acc[p][f][j]);
+          for (int j = 0; j < F; j++) wf[p][j] = read_frag<W, E>(at + X::kBytes + p * W::kBytes, wbase, j, kk);
+#pragma unroll
+        for (int f = 0; f < FM; f++) {
+          const Frag<E> xf = read_frag<X, E>(at, xbase, f, kk);
+#pragma unroll
+          for (int p = 0; p < P; p++)
+#pragma unroll
+            for (int j = 0; j < F; j++) acc[p][f][j] = mma<E>(wf[p][j], xf, acc[p][f][j]);
+        }
       }
     }
   }
 
-  // ---- results: lane l holds row m0 + .. + l % 16, and of fragment j the 4
-  // columns that follow 4 (l / 16) in it
+  // ---- results: of fragment (f, j) lane l holds row l % 16 and 4 neighbouring
+  // columns.  Bare sums (a gradient, a partial plane, a product without
+  // epilogue) are stored from there; everything else goes through LDS, where a
+  // lane takes 8 columns of one row, so that the epilogue is one piece of code
+  // and its accesses are whole lines.
   const int lane = threadIdx.x & 63, q = lane >> 4;
-  auto k_of = [&](int t) { return (int64_t)(t / ktiles) * a.K + min((t % ktiles) * BK, a.K); };
-  constexpr int kRunLen = kSpread ? (4 * F < 8 ? 4 * F : 8) : 4;
+  bool bare = !kGated && (a.splits > 1 || (a.vec_out && !a.bias && !a.resid && !a.z[0] && a.act == kActNone));
+  bool nan = false;
+  if constexpr (E::kind == 0) {
 #pragma unroll
-  for (int f = 0; f < FM; f++) {
-    const int m = m0 + (wm * FM + f) * 16 + (lane & 15);
+    for (int p = 0; p < P; p++)
 #pragma unroll
-    for (int j = 0; j < F; j += kRunLen / 4) {
-      const int col = n0 + wn * 16 * F + (kSpread ? q * 4 * F + 4 * j : 16 * j + 4 * q);
-      if (m < a.M && col < a.N) {
-        float v[P][kRunLen];
+      for (int f = 0; f < FM; f++)
 #pragma unroll
-        for (int p = 0; p < P; p++)
+        for (int j = 0; j < F; j++) {
+          const f32x4 c = acc[p][f][j];
+          const float s = (c[0] + c[1]) + (c[2] + c[3]);
+          nan = nan || s != s;
+        }
+    nan = __any(nan);
+    bare = bare && !nan;
+  }
+  if (bare) {
+    constexpr int kRunLen = kSpread ? (4 * F < 8 ? 4 * F : 8) : 4;
 #pragma unroll
-          for (int i = 0; i < kRunLen; i++) {
-            v[p][i] = acc[p][f][j + i / 4][i % 4];
-            if constexpr (E::kind == 0) {
-              if (v[p][i] != v[p][i] && col + i < a.N)
-                v[p][i] = sum_again<kXRows, kWRows>(a, b, p, m, col + i, k_of(t0), k_of(t1));
-            }
+    for (int f = 0; f < FM; f++) {
+      const int m = m0 + (wm * FM + f) * 16 + (lane & 15);
+#pragma unroll
+      for (int j = 0; j < F; j += kRunLen / 4) {
+        const int col = n0 + wn * 16 * F + (kSpread ? q * 4 * F + 4 * j : 16 * j + 4 * q);
+        if (m < a.M && col < a.N) {
+          if (a.splits > 1) {
+            float* d = a.partial + (((int64_t)split * a.batch + b) * a.M + m) * a.npad + col;
+#pragma unroll
+            for (int i = 0; i < kRunLen / 4; i++)
+              if (col + 4 * i < a.npad) *(f32x4*)(d + 4 * i) = acc[0][f][j + i];
+          } else {
+            float v[kRunLen];
+#pragma unroll
+            for (int i = 0; i < kRunLen; i++) v[i] = acc[0][f][j + i / 4][i % 4];
+            store_vals<E, kRunLen>((T*)a.out[b] + m * a.outld + col, v, a.N - col, true);
           }
-        if (a.splits > 1) {
-#pragma unroll
-          for (int p = 0; p < P; p++) {
-            float* d = a.partial + (((int64_t)split * (kGated ? 2 : a.batch) + (kGated ? p : b)) * a.M + m) * a.npad + col;
-#pragma unroll
-            for (int i = 0; i < kRunLen; i += 4)
-              if (col + i < a.npad) *(f32x4*)(d + i) = f32x4{v[p][i], v[p][i + 1], v[p][i + 2], v[p][i + 3]};
-          }
-        } else {
-          finish<E, kGated, kRunLen>(a, b, m, col, v[0], v[P - 1]);
         }
       }
     }
+    return;
+  }
+  // half of the wave's rows at a time; 16-byte chunk c of a row lies at c ^ row % 16
+  constexpr int kCols = 16 * F * P, kRows = FM * 16 / 2;
+  static_assert(Shape::kWaves * kRows * kCols * 4 <= 2 * kBuf, "the waves' sums fit the tile buffers");
+  lds_char* mine = lds + wave * (kRows * kCols * 4);
+  auto chunk = [&](int row, int c) { return (LLAR_LDS f32x4*)(mine + (row * (kCols / 4) + (c ^ (row % 16 % (kCols / 4)))) * 16); };
+  auto k_of = [&](int t) { return (int64_t)(t / ktiles) * a.K + min((t % ktiles) * BK, a.K); };
+  __syncthreads();  // everyone is done with the tiles
+#pragma unroll
+  for (int h = 0; h < 2; h++) {
+#pragma unroll
+    for (int f = 0; f < FM / 2; f++)
+#pragma unroll
+      for (int p = 0; p < P; p++)
+#pragma unroll
+        for (int j = 0; j < F; j++)
+          *chunk(f * 16 + (lane & 15), p * 4 * F + (kSpread ? q * F + j : 4 * j + q)) = acc[p][h * (FM / 2) + f][j];
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    if constexpr (E::kind == 0) {
+      // most calls have no NaN: the wave looks before it goes through them
+      if (nan) {
+#pragma clang loop unroll(disable)
+        for (int i = lane; i < kRows * kCols; i += 64) {
+          const int row = i / kCols, c = i % kCols, p = c / (16 * F);
+          const int m = m0 + (wm * FM + h * (FM / 2)) * 16 + row, col = n0 + wn * 16 * F + c % (16 * F);
+          LLAR_LDS float* v = (LLAR_LDS float*)chunk(row, c / 4) + c % 4;
+          if (*v != *v && m < a.M && col < a.N) *v = sum_again<kXRows, kWRows>(a, b, p, m, col, k_of(t0), k_of(t1));
+        }
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+      }
+    }
+    constexpr int kRuns = 2 * F;  // pieces of 8 columns of one projection
+#pragma clang loop unroll(disable)
+    for (int i = lane; i < kRows * kRuns; i += 64) {
+      const int row = i / kRuns, c = i % kRuns;
+      const int m = m0 + (wm * FM + h * (FM / 2)) * 16 + row, col = n0 + wn * 16 * F + 8 * c;
+      if (m >= a.M || col >= a.N) continue;
+      float v[P][8];
+#pragma unroll
+      for (int p = 0; p < P; p++) {
+        const f32x4 lo = *chunk(row, p * 4 * F + 2 * c), hi = *chunk(row, p * 4 * F + 2 * c + 1);
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+          v[p][e] = lo[e];
+          v[p][4 + e] = hi[e];
+        }
+      }
+      if (a.splits > 1) {
+#pragma unroll
+        for (int p = 0; p < P; p++) {
+          float* d = a.partial + (((int64_t)split * (kGated ? 2 : a.batch) + (kGated ? p : b)) * a.M + m) * a.npad + col;
+          *(f32x4*)d = f32x4{v[p][0], v[p][1], v[p][2], v[p][3]};
+          *(f32x4*)(d + 4) = f32x4{v[p][4], v[p][5], v[p][6], v[p][7]};
+        }
+      } else {
+        finish<E, kGated, 8>(a, b, m, col, v[0], v[P - 1]);
+      }
+    }
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
   }
 }
 
@@ -427,7 +595,8 @@ hipError_t launch_one(const GemmArgs& a, hipStream_t s) {
 
 template <class E, bool kXRows, bool kWRows, bool kGated>
 hipError_t launch_shape(const GemmPlan& p, const GemmArgs& a, hipStream_t s) {
-  if (p.tile == kTile256) return launch_one<E, kXRows, kWRows, Shape256, kGated>(a, s);
+  if constexpr (E::kind != 0)
+    if (p.tile == kTile256) return launch_one<E, kXRows, kWRows, Shape256, kGated>(a, s);
   if (p.tile == kTile128) return launch_one<E, kXRows, kWRows, Shape128, kGated>(a, s);
   return launch_one<E, kXRows, kWRows, Shape64, kGated>(a, s);
 }
