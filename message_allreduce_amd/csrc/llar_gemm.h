@@ -18,6 +18,7 @@ struct TileShape {
   static constexpr int FM = TM / WM / 16;  // 16-row fragments of a wave along m
   static constexpr int FN = TN / WN / 16;  // and along n
   static constexpr bool kPaired = WM == 2 && WN == 4;
+  static constexpr int kStages = kPaired || TM > 64 ? 2 : 4;  // tile buffers
 };
 typedef TileShape<256, 256, 2, 4> Shape256;
 typedef TileShape<128, 128, 2, 2> Shape128;
@@ -146,6 +147,12 @@ struct Operand {
   }
 };
 
+// Waits until at most n of this wave's loads are on their way; they arrive in order.
+template <int n>
+__device__ __forceinline__ void wait_loads() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(n) : "memory");
+}
+
 // This thread's byte offsets from the tile's first element, kNoLoad where the
 // row does not exist.
 template <class Op>
@@ -159,20 +166,29 @@ __device__ __forceinline__ void direct_offsets(uint32_t (&voff)[Op::kLoads], int
   }
 }
 
-// Loads i0 .. i1 - 1 straight into LDS, 16 bytes a lane; the wave's 64 chunks
-// land back to back.  krem: how many k of the tile exist.
-template <class Op, int i0, int i1>
-__device__ __forceinline__ void load_direct(lds_char* lds, const char* base, const uint32_t (&voff)[Op::kLoads],
+// Loads a tile straight into LDS, 16 bytes a lane; the wave's 64 chunks land
+// back to back.  krem: how many k of the tile exist.  The compiler would count
+// these loads against every later LDS read and wait for all of them; written
+// as assembly they are this code's own to wait for (wait_loads).  They have no
+// result registers.
+template <class Op>
+__device__ __forceinline__ void load_direct(lds_char* lds, int64_t base, const uint32_t (&voff)[Op::kLoads],
                                             int krem) {
-  __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void*)base, (short)0, 0x7fffffff, 0x00020000);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const u32x4 desc = {(uint32_t)__builtin_amdgcn_readfirstlane((int)base),
+                      (uint32_t)__builtin_amdgcn_readfirstlane((int)(base >> 32)) & 0xffffu, 0x7fffffffu, 0x00020000u};
+  const uint32_t at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)lds + wave * 1024);
 #pragma unroll
-  for (int i = i0; i < i1; i++) {
+  for (int i = 0; i < Op::kLoads; i++) {
     int row, k;
     Op::where(i, row, k);
     const uint32_t off = k < krem ? voff[i] : kNoLoad;
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (LLAR_LDS void*)(lds + (i * Op::kThreads + wave * 64) * 16), 16,
-                                             (int)off, 0, 0, 0);
+    asm volatile(
+        "s_mov_b32 m0, %0\n\t"
+        "s_nop 0\n\t"
+        "buffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(at + i * (Op::kThreads * 16)),
+        "v"(off), "s"(desc)
+        : "memory");
   }
 }
 
@@ -282,8 +298,8 @@ __device__ __forceinline__ float sum_again(const GemmArgs& a, int b, int p, int 
 }
 
 // One workgroup computes a TM x TN tile of the output (gated: TM x TN/2 of both
-// projections) over its share of the k tiles.  Two LDS buffers: while one is
-// multiplied, the other one's loads are in flight.
+// projections) over its share of the k tiles.  While a tile is multiplied the
+// next ones' loads are on their way to the other LDS buffers.
 template <class E, bool kXRows, bool kWRows, class Shape, bool kGated>
 __global__ __launch_bounds__(Shape::kThreads) void k_gemm(GemmArgs a) {
   constexpr int TM = Shape::TM, NT = Shape::kThreads;
@@ -296,7 +312,7 @@ __global__ __launch_bounds__(Shape::kThreads) void k_gemm(GemmArgs a) {
   typedef typename E::T T;
   constexpr int BK = X::BK, ES = X::ES;
   constexpr int kBuf = X::kBytes + P * W::kBytes;
-  __shared__ __attribute__((aligned(1024))) char smem[2 * kBuf];
+  __shared__ __attribute__((aligned(1024))) char smem[Shape::kStages * kBuf];
   lds_char* lds = (lds_char*)smem;
 
   // ---- which tile: workgroup b runs on XCD b % 8; each XCD takes a run of
@@ -341,31 +357,32 @@ __global__ __launch_bounds__(Shape::kThreads) void k_gemm(GemmArgs a) {
   // k tile t of both operands: first the tile's place, then parts of its loads
   const int64_t x1 = (int64_t)a.x[1], w1 = (int64_t)a.w[1];
   const int64_t x0 = b ? x1 : (int64_t)a.x[0], w0 = b ? w1 : (int64_t)a.w[0];
+  const int64_t xnext = x1 - x0, wnext = w1 - w0;  // to the second pair's
   const int64_t xfirst = kXRows ? m0 : m0 * a.xld, xstep = kXRows ? BK * a.xld : BK;
   const int64_t wfirst = kWRows ? n0 : n0 * a.wld, wstep = kWRows ? BK * a.wld : BK;
-  const char *xb, *wb[2];
-  int krem;
-  auto aim = [&](int t) {
+  auto load = [&](int t, int slot) {
     const bool second = a.segs == 2 && t >= ktiles;
     const int kt = second ? t - ktiles : t;
-    xb = (const char*)((second ? x1 : x0) + (xfirst + kt * xstep) * ES);
-    wb[0] = (const char*)((second ? w1 : w0) + (wfirst + kt * wstep) * ES);
-    if constexpr (kGated) wb[1] = (const char*)(w1 + (wfirst + kt * wstep) * ES);
-    krem = a.K - kt * BK;
-  };
-  auto fetch_x = [&](int buf) { load_direct<X, 0, X::kLoads>(lds + buf * kBuf, xb, xoff, krem); };
-  auto fetch_w = [&](int buf) {
-#pragma unroll
-    for (int p = 0; p < P; p++)
-      load_direct<W, 0, W::kLoads>(lds + buf * kBuf + X::kBytes + p * W::kBytes, wb[p], woff, krem);
+    const int krem = a.K - kt * BK;
+    const int64_t woffset = (wfirst + kt * wstep) * ES;
+    lds_char* at = lds + slot * kBuf;
+    load_direct<W>(at + X::kBytes, w0 + (second ? wnext : 0) + woffset, woff, krem);
+    if constexpr (kGated) load_direct<W>(at + X::kBytes + W::kBytes, w1 + woffset, woff, krem);
+    load_direct<X>(at, x0 + (second ? xnext : 0) + (xfirst + kt * xstep) * ES, xoff, krem);
   };
 
   const uint32_t xbase = frag_base<X>(wm * 16 * FM), wbase = frag_base<W>(wn * 16 * F);
   if constexpr (Shape::kPaired) {
     // Two groups of four waves (one a SIMD) take turns: while one multiplies a
-    // quarter of its wave tiles (16 products of fragments), the other reads its
-    // next fragments and issues loads.  A barrier ends every half turn; the
-    // second group runs half a turn behind.
+    // quarter of its wave tiles (half of its rows by half of its columns), the
+    // other reads its next fragments and issues loads.  A barrier ends every
+    // half turn; the second group runs half a turn behind.  The quarters go
+    // round so that each turn needs one new half of one operand, and start
+    // with the half of w that the tile before ended its reads with:
+    //   turn 0: x0 wa   turn 1: x0 wb   turn 2: x1 wb   turn 3: x1 wa
+    // with wa of the next tile (in wb's registers) read in turn 3.  Nobody
+    // reads the buffer after turn 2, so the tile after the next is loaded into
+    // it in turn 3 and has four turns to arrive.
     constexpr int KK = BK / 32, HM = FM / 2, HN = (P * F) / 2;
     static_assert(FM % 2 == 0 && (P * F) % 2 == 0, "quarters");
     Frag<E> xf[HM][KK], wf[2][HN][KK];
@@ -400,57 +417,71 @@ __global__ __launch_bounds__(Shape::kThreads) void k_gemm(GemmArgs a) {
       asm volatile("s_barrier" ::: "memory");
       __builtin_amdgcn_sched_barrier(0);
     };
-    auto arrived = [] { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); };
+    auto read_done = [] { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); };
+    constexpr int kXLoads = X::kLoads, kWLoads = P * W::kLoads;
     if (t0 < t1) {
-      aim(t0);
-      fetch_x(0);
-      fetch_w(0);
+      load(t0, 0);
+      if (t0 + 1 < t1) {
+        load(t0 + 1, 1);
+        wait_loads<kXLoads + kWLoads>();
+      } else {
+        wait_loads<0>();
+      }
     }
-    arrived();
     turn();
     if (wm == 1) turn();
-    for (int t = t0; t < t1; t++) {
-      const int buf = (t - t0) & 1;
-      lds_char* at = lds + buf * kBuf;
-      const bool more = t + 1 < t1;
-      read_w(at, 0);
-      read_x(at, 0);
-      if (more) {
-        aim(t + 1);
-        fetch_x(buf ^ 1);
+    if (t0 < t1) {
+      read_w(lds, 0);
+      auto tile = [&](int t, auto first) {
+        constexpr int wa = decltype(first)::value, wb = 1 - wa;
+        lds_char* at = lds + ((t - t0) & 1) * kBuf;
+        read_x(at, 0);
+        read_done();
+        turn();
+        multiply(0, wa);
+        turn();
+        read_w(at, wb);
+        read_done();
+        turn();
+        multiply(0, wb);
+        turn();
+        read_x(at, 1);
+        wait_loads<kXLoads>();  // w of the next tile
+        read_done();
+        turn();
+        multiply(1, wb);
+        turn();
+        if (t + 1 < t1) read_w(lds + ((t + 1 - t0) & 1) * kBuf, wb);
+        wait_loads<0>();  // and its x
+        if (t + 2 < t1) load(t + 2, (t - t0) & 1);
+        read_done();
+        turn();
+        multiply(1, wa);
+        turn();
+      };
+      int t = t0;
+      for (; t + 1 < t1; t += 2) {
+        tile(t, std::integral_constant<int, 0>());
+        tile(t + 1, std::integral_constant<int, 1>());
       }
-      turn();
-      multiply(0, 0);
-      turn();
-      read_w(at, 1);
-      if (more) fetch_w(buf ^ 1);
-      turn();
-      multiply(0, 1);
-      turn();
-      read_x(at, 1);
-      turn();
-      multiply(1, 1);
-      turn();
-      arrived();
-      turn();
-      multiply(1, 0);
-      turn();
+      if (t < t1) tile(t, std::integral_constant<int, 0>());
     }
     if (wm == 0) turn();
   } else {
-    if (t0 < t1) {
-      aim(t0);
-      fetch_x(0);
-      fetch_w(0);
-    }
+    // a ring of S buffers: S - 1 tiles are on their way while one is multiplied
+    constexpr int S = Shape::kStages, kLoads = X::kLoads + P * W::kLoads;
+    for (int i = 0; i < S - 1; i++)
+      if (t0 + i < t1) load(t0 + i, i);
+    int slot = 0;
     for (int t = t0; t < t1; t++) {
-      const int buf = (t - t0) & 1;
-      __syncthreads();  // this buffer has arrived; everyone is done with the other
-      if (t + 1 < t1) {
-        aim(t + 1);
-        fetch_x(buf ^ 1);
-        fetch_w(buf ^ 1);
-      }
+      if (t + S - 2 < t1)
+        wait_loads<(S - 2) * kLoads>();
+      else
+        wait_loads<0>();
+      __syncthreads();  // this tile has arrived; everyone is done with the one before
+      if (t + S - 1 < t1) load(t + S - 1, slot == 0 ? S - 1 : slot - 1);
+      const int buf = slot;
+      slot = slot == S - 1 ? 0 : slot + 1;
       lds_char* at = lds + buf * kBuf;
 #pragma unroll
       for (int kk = 0; kk < BK / 32; kk++) {
@@ -520,7 +551,7 @@ __global__ __launch_bounds__(Shape::kThreads) void k_gemm(GemmArgs a) {
   }
   // half of the wave's rows at a time; 16-byte chunk c of a row lies at c ^ row % 16
   constexpr int kCols = 16 * F * P, kRows = FM * 16 / 2;
-  static_assert(Shape::kWaves * kRows * kCols * 4 <= 2 * kBuf, "the waves' sums fit the tile buffers");
+  static_assert(Shape::kWaves * kRows * kCols * 4 <= Shape::kStages * kBuf, "the waves' sums fit the tile buffers");
   lds_char* mine = lds + wave * (kRows * kCols * 4);
   auto chunk = [&](int row, int c) { return (LLAR_LDS f32x4*)(mine + (row * (kCols / 4) + (c ^ (row % 16 % (kCols / 4)))) * 16); };
   auto k_of = [&](int t) { return (int64_t)(t / ktiles) * a.K + min((t % ktiles) * BK, a.K); };
