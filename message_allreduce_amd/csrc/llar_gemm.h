@@ -300,19 +300,28 @@ __device__ __forceinline__ float sum_again(const GemmArgs& a, int b, int p, int 
 // One workgroup computes a TM x TN tile of the output (gated: TM x TN/2 of both
 // projections) over its share of the k tiles.  While a tile is multiplied the
 // next ones' loads are on their way to the other LDS buffers.
+//
+// The tile's rows of w lie in LDS as kWParts operands (gated: one for each
+// projection), those of x as kXParts; a wave owns FX fragments of every part
+// of x and FW of every part of w.
 template <class E, bool kXRows, bool kWRows, class Shape, bool kGated>
 __global__ __launch_bounds__(Shape::kThreads) void k_gemm(GemmArgs a) {
+  typedef typename E::T T;
+  constexpr bool kPaired = Shape::kPaired;
   constexpr int TM = Shape::TM, NT = Shape::kThreads;
   constexpr int P = kGated ? 2 : 1;              // projections
   constexpr int TN = Shape::TN / P;              // output columns of the tile
-  constexpr int FM = Shape::FM, F = Shape::FN / P;
+  constexpr int kXParts = kPaired ? 2 : 1, kWParts = kPaired ? 2 : P;
+  constexpr int FX = Shape::FM / kXParts, FW = Shape::FN / kWParts;
+  constexpr int kXRowsPart = TM / kXParts, kWRowsPart = Shape::TN / kWParts;
+  constexpr int kWStep = kGated ? 0 : kWRowsPart;  // columns from one part of w to the next
   constexpr bool kSpread = !kWRows;
-  typedef Operand<E, kXRows, TM, NT, FM, false> X;
-  typedef Operand<E, kWRows, TN, NT, F, kSpread> W;
-  typedef typename E::T T;
+  typedef Operand<E, kXRows, kXRowsPart, NT, FX, false> X;
+  typedef Operand<E, kWRows, kWRowsPart, NT, FW, kSpread> W;
   constexpr int BK = X::BK, ES = X::ES;
-  constexpr int kBuf = X::kBytes + P * W::kBytes;
-  __shared__ __attribute__((aligned(1024))) char smem[Shape::kStages * kBuf];
+  constexpr int kBuf = kXParts * X::kBytes + kWParts * W::kBytes;
+  constexpr int kStages = Shape::kStages;
+  __shared__ __attribute__((aligned(1024))) char smem[kStages * kBuf];
   lds_char* lds = (lds_char*)smem;
 
   // ---- which tile: workgroup b runs on XCD b % 8; each XCD takes a run of
@@ -342,74 +351,81 @@ __global__ __launch_bounds__(Shape::kThreads) void k_gemm(GemmArgs a) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / Shape::WN, wn = wave % Shape::WN;
 
-  f32x4 acc[P][FM][F];
+  f32x4 acc[kXParts][kWParts][FX][FW];
 #pragma unroll
-  for (int p = 0; p < P; p++)
+  for (int h = 0; h < kXParts; h++)
 #pragma unroll
-    for (int f = 0; f < FM; f++)
+    for (int p = 0; p < kWParts; p++)
 #pragma unroll
-      for (int j = 0; j < F; j++) acc[p][f][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int f = 0; f < FX; f++)
+#pragma unroll
+        for (int j = 0; j < FW; j++) acc[h][p][f][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  const int xleft = a.M - m0, wleft = a.N - n0;
-  uint32_t xoff[X::kLoads], woff[W::kLoads];
-  direct_offsets<X>(xoff, xleft, a.xld);
-  direct_offsets<W>(woff, wleft, a.wld);
-  // k tile t of both operands: first the tile's place, then parts of its loads
+  uint32_t xoff[kXParts][X::kLoads], woff[kWParts][W::kLoads];
+#pragma unroll
+  for (int h = 0; h < kXParts; h++) direct_offsets<X>(xoff[h], a.M - m0 - h * kXRowsPart, a.xld);
+#pragma unroll
+  for (int p = 0; p < kWParts; p++) direct_offsets<W>(woff[p], a.N - n0 - p * kWStep, a.wld);
   const int64_t x1 = (int64_t)a.x[1], w1 = (int64_t)a.w[1];
   const int64_t x0 = b ? x1 : (int64_t)a.x[0], w0 = b ? w1 : (int64_t)a.w[0];
   const int64_t xnext = x1 - x0, wnext = w1 - w0;  // to the second pair's
+  const int64_t xpart = (kXRows ? kXRowsPart : kXRowsPart * a.xld) * ES;
+  const int64_t wpart = kGated ? wnext : (kWRows ? kWStep : kWStep * a.wld) * ES;
   const int64_t xfirst = kXRows ? m0 : m0 * a.xld, xstep = kXRows ? BK * a.xld : BK;
   const int64_t wfirst = kWRows ? n0 : n0 * a.wld, wstep = kWRows ? BK * a.wld : BK;
-  auto load = [&](int t, int slot) {
+  // k tile t's first elements and how many of its k exist (none beyond the last tile)
+  int64_t xat, wat;
+  int krem;
+  auto aim = [&](int t) {
     const bool second = a.segs == 2 && t >= ktiles;
     const int kt = second ? t - ktiles : t;
-    const int krem = a.K - kt * BK;
-    const int64_t woffset = (wfirst + kt * wstep) * ES;
-    lds_char* at = lds + slot * kBuf;
-    load_direct<W>(at + X::kBytes, w0 + (second ? wnext : 0) + woffset, woff, krem);
-    if constexpr (kGated) load_direct<W>(at + X::kBytes + W::kBytes, w1 + woffset, woff, krem);
-    load_direct<X>(at, x0 + (second ? xnext : 0) + (xfirst + kt * xstep) * ES, xoff, krem);
+    krem = t < t1 ? a.K - kt * BK : 0;
+    xat = x0 + (second ? xnext : 0) + (xfirst + kt * xstep) * ES;
+    wat = w0 + (second ? wnext : 0) + (wfirst + kt * wstep) * ES;
+  };
+  auto load_x = [&](int slot, int h) {
+    load_direct<X>(lds + slot * kBuf + h * X::kBytes, xat + h * xpart, xoff[h], krem);
+  };
+  auto load_w = [&](int slot, int p) {
+    load_direct<W>(lds + slot * kBuf + kXParts * X::kBytes + p * W::kBytes, wat + p * wpart, woff[p], krem);
   };
 
-  const uint32_t xbase = frag_base<X>(wm * 16 * FM), wbase = frag_base<W>(wn * 16 * F);
-  if constexpr (Shape::kPaired) {
+  const uint32_t xbase = frag_base<X>(wm * 16 * FX), wbase = frag_base<W>(wn * 16 * FW);
+  constexpr int KK = BK / 32;
+  if constexpr (kPaired) {
     // Two groups of four waves (one a SIMD) take turns: while one multiplies a
-    // quarter of its wave tiles (half of its rows by half of its columns), the
-    // other reads its next fragments and issues loads.  A barrier ends every
-    // half turn; the second group runs half a turn behind.  The quarters go
-    // round so that each turn needs one new half of one operand, and start
-    // with the half of w that the tile before ended its reads with:
+    // quarter of its wave tiles (one part of x by one of w), the other reads its
+    // next fragments and issues loads.  A barrier ends every half turn; the
+    // second group runs half a turn behind.  The quarters go round so that each
+    // turn reads one part of one operand, and a tile starts with the part of w
+    // that the tile before ended with:
     //   turn 0: x0 wa   turn 1: x0 wb   turn 2: x1 wb   turn 3: x1 wa
-    // with wa of the next tile (in wb's registers) read in turn 3.  Nobody
-    // reads the buffer after turn 2, so the tile after the next is loaded into
-    // it in turn 3 and has four turns to arrive.
-    constexpr int KK = BK / 32, HM = FM / 2, HN = (P * F) / 2;
-    static_assert(FM % 2 == 0 && (P * F) % 2 == 0, "quarters");
-    Frag<E> xf[HM][KK], wf[2][HN][KK];
-    auto read_x = [&](lds_char* at, int h) {
+    // where turn 0 reads x0, turn 1 wb, turn 2 x1 and turn 3 the next tile's
+    // first part of w (wb's registers).  Each turn loads, into the part that
+    // the turn before read for the last time, what lies two tiles on, and so
+    // has seven turns to arrive.
+    Frag<E> xf[FX][KK], wf[2][FW][KK];
+    auto read_x = [&](int slot, int h) {
 #pragma unroll
       for (int kk = 0; kk < KK; kk++)
 #pragma unroll
-        for (int f = 0; f < HM; f++) xf[f][kk] = read_frag<X, E>(at, xbase, h * HM + f, kk);
+        for (int f = 0; f < FX; f++) xf[f][kk] = read_frag<X, E>(lds + slot * kBuf + h * X::kBytes, xbase, f, kk);
     };
-    auto read_w = [&](lds_char* at, int h) {
+    auto read_w = [&](int slot, int p) {
 #pragma unroll
       for (int kk = 0; kk < KK; kk++)
 #pragma unroll
-        for (int j = 0; j < HN; j++)
-          wf[h][j][kk] = read_frag<W, E>(at + X::kBytes + (h * HN + j) / F * W::kBytes, wbase, (h * HN + j) % F, kk);
+        for (int j = 0; j < FW; j++)
+          wf[p][j][kk] = read_frag<W, E>(lds + slot * kBuf + kXParts * X::kBytes + p * W::kBytes, wbase, j, kk);
     };
-    auto multiply = [&](int hm, int hn) {
+    auto multiply = [&](int h, int p) {
       __builtin_amdgcn_s_setprio(1);
 #pragma unroll
       for (int kk = 0; kk < KK; kk++)
 #pragma unroll
-        for (int f = 0; f < HM; f++)
+        for (int f = 0; f < FX; f++)
 #pragma unroll
-          for (int j = 0; j < HN; j++) {
-            f32x4& c = acc[(hn * HN + j) / F][hm * HM + f][(hn * HN + j) % F];
-            c = mma<E>(wf[hn][j][kk], xf[f][kk], c);
-          }
+          for (int j = 0; j < FW; j++) acc[h][p][f][j] = mma<E>(wf[p][j][kk], xf[f][kk], acc[h][p][f][j]);
       __builtin_amdgcn_s_setprio(0);
     };
     auto turn = [] {
@@ -418,44 +434,49 @@ __global__ __launch_bounds__(Shape::kThreads) void k_gemm(GemmArgs a) {
       __builtin_amdgcn_sched_barrier(0);
     };
     auto read_done = [] { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); };
-    constexpr int kXLoads = X::kLoads, kWLoads = P * W::kLoads;
+    static_assert(X::kLoads == W::kLoads, "a turn's loads");
+    constexpr int kAhead = 6 * X::kLoads;  // loads of the six turns that may still be on their way
     if (t0 < t1) {
-      load(t0, 0);
-      if (t0 + 1 < t1) {
-        load(t0 + 1, 1);
-        wait_loads<kXLoads + kWLoads>();
-      } else {
-        wait_loads<0>();
+#pragma unroll
+      for (int i = 0; i < 2; i++) {
+        aim(t0 + i);
+        load_w(i, i);  // in the order of their use: tile t0 starts with part 0 of w, the next with part 1
+        load_x(i, 0);
+        load_w(i, 1 - i);
+        load_x(i, 1);
       }
-    }
-    turn();
-    if (wm == 1) turn();
-    if (t0 < t1) {
-      read_w(lds, 0);
+      wait_loads<kAhead>();
+      turn();
+      read_w(0, 0);
+      read_done();
+      turn();
+      if (wm == 1) turn();
       auto tile = [&](int t, auto first) {
-        constexpr int wa = decltype(first)::value, wb = 1 - wa;
-        lds_char* at = lds + ((t - t0) & 1) * kBuf;
-        read_x(at, 0);
-        read_done();
-        turn();
+        constexpr int wa = decltype(first)::value, wb = 1 - wa, slot = wa;
+        auto ready = [&] {
+          wait_loads<kAhead>();
+          read_done();
+          turn();
+        };
+        aim(t + 2);
+        read_x(slot, 0);
+        load_w(slot, wa);
+        ready();
         multiply(0, wa);
         turn();
-        read_w(at, wb);
-        read_done();
-        turn();
+        read_w(slot, wb);
+        load_x(slot, 0);
+        ready();
         multiply(0, wb);
         turn();
-        read_x(at, 1);
-        wait_loads<kXLoads>();  // w of the next tile
-        read_done();
-        turn();
+        read_x(slot, 1);
+        load_w(slot, wb);
+        ready();
         multiply(1, wb);
         turn();
-        if (t + 1 < t1) read_w(lds + ((t + 1 - t0) & 1) * kBuf, wb);
-        wait_loads<0>();  // and its x
-        if (t + 2 < t1) load(t + 2, (t - t0) & 1);
-        read_done();
-        turn();
+        read_w(1 - slot, wb);  // beyond the last tile: zeros, and not used
+        load_x(slot, 1);
+        ready();
         multiply(1, wa);
         turn();
       };
@@ -465,11 +486,19 @@ __global__ __launch_bounds__(Shape::kThreads) void k_gemm(GemmArgs a) {
         tile(t + 1, std::integral_constant<int, 1>());
       }
       if (t < t1) tile(t, std::integral_constant<int, 0>());
+      if (wm == 0) turn();
+      wait_loads<0>();
     }
-    if (wm == 0) turn();
   } else {
-    // a ring of S buffers: S - 1 tiles are on their way while one is multiplied
-    constexpr int S = Shape::kStages, kLoads = X::kLoads + P * W::kLoads;
+    // a ring of buffers: all but one are on their way while one is multiplied
+    constexpr int S = kStages, kLoads = kXParts * X::kLoads + kWParts * W::kLoads;
+    auto load = [&](int t, int slot) {
+      aim(t);
+#pragma unroll
+      for (int p = 0; p < kWParts; p++) load_w(slot, p);
+#pragma unroll
+      for (int h = 0; h < kXParts; h++) load_x(slot, h);
+    };
     for (int i = 0; i < S - 1; i++)
       if (t0 + i < t1) load(t0 + i, i);
     int slot = 0;
@@ -480,117 +509,135 @@ __global__ __launch_bounds__(Shape::kThreads) void k_gemm(GemmArgs a) {
         wait_loads<0>();
       __syncthreads();  // this tile has arrived; everyone is done with the one before
       if (t + S - 1 < t1) load(t + S - 1, slot == 0 ? S - 1 : slot - 1);
-      const int buf = slot;
+      lds_char* at = lds + slot * kBuf;
       slot = slot == S - 1 ? 0 : slot + 1;
-      lds_char* at = lds + buf * kBuf;
 #pragma unroll
-      for (int kk = 0; kk < BK / 32; kk++) {
-        Frag<E> wf[P][F];
+      for (int kk = 0; kk < KK; kk++) {
+        Frag<E> wf[kWParts][FW];
 #pragma unroll
-        for (int p = 0; p < P; p++)
+        for (int p = 0; p < kWParts; p++)
 #pragma unroll
-          for (int j = 0; j < F; j++) wf[p][j] = read_frag<W, E>(at + X::kBytes + p * W::kBytes, wbase, j, kk);
+          for (int j = 0; j < FW; j++)
+            wf[p][j] = read_frag<W, E>(at + kXParts * X::kBytes + p * W::kBytes, wbase, j, kk);
 #pragma unroll
-        for (int f = 0; f < FM; f++) {
+        for (int f = 0; f < FX; f++) {
           const Frag<E> xf = read_frag<X, E>(at, xbase, f, kk);
 #pragma unroll
-          for (int p = 0; p < P; p++)
+          for (int p = 0; p < kWParts; p++)
 #pragma unroll
-            for (int j = 0; j < F; j++) acc[p][f][j] = mma<E>(wf[p][j], xf, acc[p][f][j]);
+            for (int j = 0; j < FW; j++) acc[0][p][f][j] = mma<E>(wf[p][j], xf, acc[0][p][f][j]);
         }
       }
     }
   }
 
-  // ---- results: of fragment (f, j) lane l holds row l % 16 and 4 neighbouring
+  // ---- results: of fragments (f, j) lane l holds row l % 16 and 4 neighbouring
   // columns.  Bare sums (a gradient, a partial plane, a product without
   // epilogue) are stored from there; everything else goes through LDS, where a
   // lane takes 8 columns of one row, so that the epilogue is one piece of code
   // and its accesses are whole lines.
   const int lane = threadIdx.x & 63, q = lane >> 4;
+  const int mwave = m0 + wm * 16 * FX, nwave = n0 + wn * 16 * FW;
   bool bare = !kGated && (a.splits > 1 || (a.vec_out && !a.bias && !a.resid && !a.z[0] && a.act == kActNone));
   bool nan = false;
   if constexpr (E::kind == 0) {
 #pragma unroll
-    for (int p = 0; p < P; p++)
+    for (int h = 0; h < kXParts; h++)
 #pragma unroll
-      for (int f = 0; f < FM; f++)
+      for (int p = 0; p < kWParts; p++)
 #pragma unroll
-        for (int j = 0; j < F; j++) {
-          const f32x4 c = acc[p][f][j];
-          const float s = (c[0] + c[1]) + (c[2] + c[3]);
-          nan = nan || s != s;
-        }
+        for (int f = 0; f < FX; f++)
+#pragma unroll
+          for (int j = 0; j < FW; j++) {
+            const f32x4 c = acc[h][p][f][j];
+            const float s = (c[0] + c[1]) + (c[2] + c[3]);
+            nan = nan || s != s;
+          }
     nan = __any(nan);
     bare = bare && !nan;
   }
   if (bare) {
-    constexpr int kRunLen = kSpread ? (4 * F < 8 ? 4 * F : 8) : 4;
+    constexpr int kRunLen = kSpread ? (4 * FW < 8 ? 4 * FW : 8) : 4;
 #pragma unroll
-    for (int f = 0; f < FM; f++) {
-      const int m = m0 + (wm * FM + f) * 16 + (lane & 15);
+    for (int h = 0; h < kXParts; h++)
 #pragma unroll
-      for (int j = 0; j < F; j += kRunLen / 4) {
-        const int col = n0 + wn * 16 * F + (kSpread ? q * 4 * F + 4 * j : 16 * j + 4 * q);
-        if (m < a.M && col < a.N) {
-          if (a.splits > 1) {
-            float* d = a.partial + (((int64_t)split * a.batch + b) * a.M + m) * a.npad + col;
+      for (int f = 0; f < FX; f++) {
+        const int m = mwave + h * kXRowsPart + f * 16 + (lane & 15);
 #pragma unroll
-            for (int i = 0; i < kRunLen / 4; i++)
-              if (col + 4 * i < a.npad) *(f32x4*)(d + 4 * i) = acc[0][f][j + i];
-          } else {
-            float v[kRunLen];
+        for (int p = 0; p < kWParts; p++)
 #pragma unroll
-            for (int i = 0; i < kRunLen; i++) v[i] = acc[0][f][j + i / 4][i % 4];
-            store_vals<E, kRunLen>((T*)a.out[b] + m * a.outld + col, v, a.N - col, true);
+          for (int j = 0; j < FW; j += kRunLen / 4) {
+            const int col = nwave + p * kWStep + (kSpread ? q * 4 * FW + 4 * j : 16 * j + 4 * q);
+            if (m < a.M && col < a.N) {
+              if (a.splits > 1) {
+                float* d = a.partial + (((int64_t)split * a.batch + b) * a.M + m) * a.npad + col;
+#pragma unroll
+                for (int i = 0; i < kRunLen / 4; i++)
+                  if (col + 4 * i < a.npad) *(f32x4*)(d + 4 * i) = acc[h][p][f][j + i];
+              } else {
+                float v[kRunLen];
+#pragma unroll
+                for (int i = 0; i < kRunLen; i++) v[i] = acc[h][p][f][j + i / 4][i % 4];
+                store_vals<E, kRunLen>((T*)a.out[b] + m * a.outld + col, v, a.N - col, true);
+              }
+            }
           }
-        }
       }
-    }
     return;
   }
-  // half of the wave's rows at a time; 16-byte chunk c of a row lies at c ^ row % 16
-  constexpr int kCols = 16 * F * P, kRows = FM * 16 / 2;
-  static_assert(Shape::kWaves * kRows * kCols * 4 <= Shape::kStages * kBuf, "the waves' sums fit the tile buffers");
+  // half of the wave's rows at a time (a part of x, or half of its one);
+  // 16-byte chunk c of a row lies at c ^ row % 16
+  constexpr int kCols = 16 * FW * kWParts, kHalf = kXParts * FX / 2, kRows = kHalf * 16;
+  static_assert(Shape::kWaves * kRows * kCols * 4 <= kStages * kBuf, "the waves' sums fit the tile buffers");
   lds_char* mine = lds + wave * (kRows * kCols * 4);
-  auto chunk = [&](int row, int c) { return (LLAR_LDS f32x4*)(mine + (row * (kCols / 4) + (c ^ (row % 16 % (kCols / 4)))) * 16); };
+  auto chunk = [&](int row, int c) {
+    return (LLAR_LDS f32x4*)(mine + (row * (kCols / 4) + (c ^ (row % 16 % (kCols / 4)))) * 16);
+  };
   auto k_of = [&](int t) { return (int64_t)(t / ktiles) * a.K + min((t % ktiles) * BK, a.K); };
+  auto settle = [] {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+  };
   __syncthreads();  // everyone is done with the tiles
 #pragma unroll
   for (int h = 0; h < 2; h++) {
+    const int mhalf = mwave + (kXParts == 2 ? h * kXRowsPart : h * kRows);
 #pragma unroll
-    for (int f = 0; f < FM / 2; f++)
+    for (int i = 0; i < kHalf; i++)
 #pragma unroll
-      for (int p = 0; p < P; p++)
+      for (int p = 0; p < kWParts; p++)
 #pragma unroll
-        for (int j = 0; j < F; j++)
-          *chunk(f * 16 + (lane & 15), p * 4 * F + (kSpread ? q * F + j : 4 * j + q)) = acc[p][h * (FM / 2) + f][j];
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
+        for (int j = 0; j < FW; j++) {
+          constexpr int kPer = kXParts == 2 ? 0 : kHalf;  // fragments of x before this half's in its part
+          *chunk(i * 16 + (lane & 15), p * 4 * FW + (kSpread ? q * FW + j : 4 * j + q)) =
+              acc[kXParts == 2 ? h : 0][p][i + h * kPer][j];
+        }
+    settle();
     if constexpr (E::kind == 0) {
       // most calls have no NaN: the wave looks before it goes through them
       if (nan) {
 #pragma clang loop unroll(disable)
         for (int i = lane; i < kRows * kCols; i += 64) {
-          const int row = i / kCols, c = i % kCols, p = c / (16 * F);
-          const int m = m0 + (wm * FM + h * (FM / 2)) * 16 + row, col = n0 + wn * 16 * F + c % (16 * F);
+          const int row = i / kCols, c = i % kCols, p = c / (16 * FW);
+          const int m = mhalf + row, col = nwave + p * kWStep + c % (16 * FW);
           LLAR_LDS float* v = (LLAR_LDS float*)chunk(row, c / 4) + c % 4;
-          if (*v != *v && m < a.M && col < a.N) *v = sum_again<kXRows, kWRows>(a, b, p, m, col, k_of(t0), k_of(t1));
+          if (*v != *v && m < a.M && col < a.N)
+            *v = sum_again<kXRows, kWRows>(a, b, kGated ? p : 0, m, col, k_of(t0), k_of(t1));
         }
-        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-        __builtin_amdgcn_wave_barrier();
+        settle();
       }
     }
-    constexpr int kRuns = 2 * F;  // pieces of 8 columns of one projection
+    // gated: a lane takes the same 8 columns of both parts
+    constexpr int kRuns = 2 * FW * (kGated ? 1 : kWParts);
 #pragma clang loop unroll(disable)
     for (int i = lane; i < kRows * kRuns; i += 64) {
       const int row = i / kRuns, c = i % kRuns;
-      const int m = m0 + (wm * FM + h * (FM / 2)) * 16 + row, col = n0 + wn * 16 * F + 8 * c;
+      const int m = mhalf + row, col = nwave + c / (2 * FW) * kWStep + 8 * (c % (2 * FW));
       if (m >= a.M || col >= a.N) continue;
       float v[P][8];
 #pragma unroll
       for (int p = 0; p < P; p++) {
-        const f32x4 lo = *chunk(row, p * 4 * F + 2 * c), hi = *chunk(row, p * 4 * F + 2 * c + 1);
+        const f32x4 lo = *chunk(row, p * 4 * FW + 2 * c), hi = *chunk(row, p * 4 * FW + 2 * c + 1);
 #pragma unroll
         for (int e = 0; e < 4; e++) {
           v[p][e] = lo[e];
@@ -608,8 +655,7 @@ __global__ __launch_bounds__(Shape::kThreads) void k_gemm(GemmArgs a) {
         finish<E, kGated, 8>(a, b, m, col, v[0], v[P - 1]);
       }
     }
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
+    settle();
   }
 }
 
