@@ -52,17 +52,16 @@ __device__ __forceinline__ f32x4 mma<F16>(const Frag<F16>& a, const Frag<F16>& b
 }
 // Of the nine products of parts the six above 2^-23 of the whole, small ones
 // first: 6 bfloat16 products at 16 times the binary32 unit's rate.
+__device__ __forceinline__ f32x4 mma_part(int s, const Frag<F32>& a, const Frag<F32>& b, f32x4 c) {
+  const s16x8 p = s == 0 || s == 3 ? a.mid : s == 1 ? a.lo : a.hi;
+  const s16x8 q = s == 0 || s == 4 ? b.mid : s == 2 ? b.lo : b.hi;
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, p), __builtin_bit_cast(bf16x8, q), c, 0, 0,
+                                                 0);
+}
 template <>
 __device__ __forceinline__ f32x4 mma<F32>(const Frag<F32>& a, const Frag<F32>& b, f32x4 c) {
-#define LLAR_MMA(p, q) \
-  c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, p), __builtin_bit_cast(bf16x8, q), c, 0, 0, 0)
-  LLAR_MMA(a.mid, b.mid);
-  LLAR_MMA(a.lo, b.hi);
-  LLAR_MMA(a.hi, b.lo);
-  LLAR_MMA(a.mid, b.hi);
-  LLAR_MMA(a.hi, b.mid);
-  LLAR_MMA(a.hi, b.hi);
-#undef LLAR_MMA
+#pragma unroll
+  for (int s = 0; s < 6; s++) c = mma_part(s, a, b, c);
   return c;
 }
 
@@ -93,15 +92,15 @@ __device__ __forceinline__ Frag<F32> split3(const float (&x)[8]) {
   return f;
 }
 
-// ---- one operand's tile in LDS --------------------------------------------------------
-// R rows by 128 bytes of k, in one of two orders.
+// ---- one 16-bit operand's tile in LDS -------------------------------------------------
+// R rows by 64 k, in one of two orders.
 //
 // k-contiguous source: [row][8 chunks of 16 bytes], chunk c of a row stored at
 // position c ^ key(row), so that the 16 rows of a fragment read the same chunk
 // from different banks.
 // Row-contiguous source: [k][row], chunk c of a k line stored at c ^ key(k);
-// 16-bit fragments come out through the transposing LDS read, which gathers
-// four k of one row into a lane.
+// fragments come out through the transposing LDS read, which gathers four k of
+// one row into a lane.
 //
 // perm: fragment j's 16 rows are spread over the wave's rows as
 // n = 4 F b + 4 j + i (b, i = 0..3, F fragments in a run), so that a lane's
@@ -125,11 +124,7 @@ struct Operand {
     return kPerm ? (row & 3) | (((row / (4 * F)) & 1) << 2) : row & 7;
   }
   static __device__ __forceinline__ int key_k(int k) {
-    if constexpr (ES == 2) {
-      return 2 * (((k & 3) | (((k >> 3) & 1) << 2)) & (kLine / 2 - 1));
-    } else {
-      return (4 * ((k >> 3) & 3)) & (kLine - 1);
-    }
+    return 2 * (((k & 3) | (((k >> 3) & 1) << 2)) & (kLine / 2 - 1));
   }
 
   // chunk number of load i of this thread, in LDS order
@@ -197,16 +192,11 @@ template <class Op>
 __device__ __forceinline__ uint32_t frag_base(int row0) {
   const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
   if constexpr (Op::kByRows) {
-    if constexpr (Op::ES == 2) {
-      const int k = q * 8 + (r >> 2), col = row0 + (r & 3) * 4;
-      return (k * Op::kLine + ((col / 8) ^ Op::key_k(k))) * 16 + (col % 8) * 2;
-    } else {
-      const int k = q * 8, col = row0 + r;
-      return (k * Op::kLine + ((col / 4) ^ Op::key_k(k))) * 16 + (col % 4) * 4;
-    }
+    const int k = q * 8 + (r >> 2), col = row0 + (r & 3) * 4;
+    return (k * Op::kLine + ((col / 8) ^ Op::key_k(k))) * 16 + (col % 8) * 2;
   } else {
     const int row = row0 + (Op::kSpread ? (r >> 2) * 4 * Op::kRun + (r & 3) : r);
-    return row * 128 + ((Op::ES == 2 ? q : 2 * q) ^ Op::key_row(row)) * 16;
+    return row * 128 + (q ^ Op::key_row(row)) * 16;
   }
 }
 
@@ -215,29 +205,14 @@ template <class Op, class E>
 __device__ __forceinline__ Frag<E> read_frag(lds_char* lds, uint32_t base, int f, int kk) {
   Frag<E> out;
   if constexpr (Op::kByRows) {
-    if constexpr (Op::ES == 2) {
-      // lane i of 16 hands in row i / 4 of a 4 x 16 block and takes column i
-      const uint32_t at = (base ^ (f * 32)) + kk * 32 * Op::kLine * 16;
-      const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LLAR_LDS s16x4*)(lds + at));
-      const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LLAR_LDS s16x4*)(lds + at + 4 * Op::kLine * 16));
-      out.v = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
-    } else {
-      float x[8];
-      const uint32_t at = base ^ (f * 64);
-#pragma unroll
-      for (int t = 0; t < 8; t++) x[t] = *(LLAR_LDS float*)(lds + at + t * Op::kLine * 16);
-      out = split3(x);
-    }
+    // lane i of 16 hands in row i / 4 of a 4 x 16 block and takes column i
+    const uint32_t at = (base ^ (f * 32)) + kk * 32 * Op::kLine * 16;
+    const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LLAR_LDS s16x4*)(lds + at));
+    const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LLAR_LDS s16x4*)(lds + at + 4 * Op::kLine * 16));
+    out.v = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
   } else {
     const uint32_t step = Op::kSpread ? 4 * 128 : 16 * 128;
-    if constexpr (Op::ES == 2) {
-      out.v = *(LLAR_LDS s16x8*)(lds + ((base ^ (kk * 64)) + f * step));
-    } else {
-      const f32x4 a = *(LLAR_LDS f32x4*)(lds + (base + f * step));
-      const f32x4 b = *(LLAR_LDS f32x4*)(lds + ((base ^ 16) + f * step));
-      const float x[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
-      out = split3(x);
-    }
+    out.v = *(LLAR_LDS s16x8*)(lds + ((base ^ (kk * 64)) + f * step));
   }
   return out;
 }
@@ -297,6 +272,175 @@ __device__ __forceinline__ float sum_again(const GemmArgs& a, int b, int p, int 
   return s;
 }
 
+// ---- results -------------------------------------------------------------------------
+// The tile (m0, n0) of plane b: acc[part of x][part of w][fragment of x][of w].
+template <class E, bool kXRows, bool kWRows, bool kGated, class Shape, int kXParts, int kWParts, bool kSpread, int kLds,
+          int FX, int FW>
+__device__ __forceinline__ void store_results(const GemmArgs& a, f32x4 (&acc)[kXParts][kWParts][FX][FW], lds_char* lds,
+                                              int m0, int n0, int b, int split, int ktiles, int t0, int t1, int bk) {
+  // of fragments (f, j) lane l holds row l % 16 and 4 neighbouring
+  // columns.  Bare sums (a gradient, a partial plane, a product without
+  // epilogue) are stored from there; everything else goes through LDS, where a
+  // lane takes 8 columns of one row, so that the epilogue is one piece of code
+  // and its accesses are whole lines.
+  typedef typename E::T T;
+  constexpr int P = kGated ? 2 : 1;
+  constexpr int kXRowsPart = Shape::TM / kXParts, kWRowsPart = Shape::TN / kWParts;
+  constexpr int kWStep = kGated ? 0 : kWRowsPart;
+  const int lane = threadIdx.x & 63, q = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave / Shape::WN, wn = wave % Shape::WN;
+  const int mwave = m0 + wm * 16 * FX, nwave = n0 + wn * 16 * FW;
+  bool bare = !kGated && (a.splits > 1 || (a.vec_out && !a.bias && !a.resid && !a.z[0] && a.act == kActNone));
+  bool nan = false;
+  if constexpr (E::kind == 0) {
+#pragma unroll
+    for (int h = 0; h < kXParts; h++)
+#pragma unroll
+      for (int p = 0; p < kWParts; p++)
+#pragma unroll
+        for (int f = 0; f < FX; f++)
+#pragma unroll
+          for (int j = 0; j < FW; j++) {
+            const f32x4 c = acc[h][p][f][j];
+            const float s = (c[0] + c[1]) + (c[2] + c[3]);
+            nan = nan || s != s;
+          }
+    nan = __any(nan);
+    bare = bare && !nan;
+  }
+  if (bare) {
+    constexpr int kRunLen = kSpread ? (4 * FW < 8 ? 4 * FW : 8) : 4;
+#pragma unroll
+    for (int h = 0; h < kXParts; h++)
+#pragma unroll
+      for (int f = 0; f < FX; f++) {
+        const int m = mwave + h * kXRowsPart + f * 16 + (lane & 15);
+#pragma unroll
+        for (int p = 0; p < kWParts; p++)
+#pragma unroll
+          for (int j = 0; j < FW; j += kRunLen / 4) {
+            const int col = nwave + p * kWStep + (kSpread ? q * 4 * FW + 4 * j : 16 * j + 4 * q);
+            if (m < a.M && col < a.N) {
+              if (a.splits > 1) {
+                float* d = a.partial + (((int64_t)split * a.batch + b) * a.M + m) * a.npad + col;
+#pragma unroll
+                for (int i = 0; i < kRunLen / 4; i++)
+                  if (col + 4 * i < a.npad) *(f32x4*)(d + 4 * i) = acc[h][p][f][j + i];
+              } else {
+                float v[kRunLen];
+#pragma unroll
+                for (int i = 0; i < kRunLen; i++) v[i] = acc[h][p][f][j + i / 4][i % 4];
+                store_vals<E, kRunLen>((T*)a.out[b] + m * a.outld + col, v, a.N - col, true);
+              }
+            }
+          }
+      }
+    return;
+  }
+  // half of the wave's rows at a time (a part of x, or half of its one);
+  // 16-byte chunk c of a row lies at c ^ row % 16
+  constexpr int kCols = 16 * FW * kWParts, kHalf = kXParts * FX / 2, kRows = kHalf * 16;
+  static_assert(Shape::kWaves * kRows * kCols * 4 <= kLds, "the waves' sums fit the tile buffers");
+  lds_char* mine = lds + wave * (kRows * kCols * 4);
+  auto chunk = [&](int row, int c) {
+    return (LLAR_LDS f32x4*)(mine + (row * (kCols / 4) + (c ^ (row % 16 % (kCols / 4)))) * 16);
+  };
+  auto k_of = [&](int t) { return (int64_t)(t / ktiles) * a.K + min((t % ktiles) * bk, a.K); };
+  auto settle = [] {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+  };
+  __syncthreads();  // everyone is done with the tiles
+#pragma unroll
+  for (int h = 0; h < 2; h++) {
+    const int mhalf = mwave + (kXParts == 2 ? h * kXRowsPart : h * kRows);
+#pragma unroll
+    for (int i = 0; i < kHalf; i++)
+#pragma unroll
+      for (int p = 0; p < kWParts; p++)
+#pragma unroll
+        for (int j = 0; j < FW; j++) {
+          constexpr int kPer = kXParts == 2 ? 0 : kHalf;  // fragments of x before this half's in its part
+          *chunk(i * 16 + (lane & 15), p * 4 * FW + (kSpread ? q * FW + j : 4 * j + q)) =
+              acc[kXParts == 2 ? h : 0][p][i + h * kPer][j];
+        }
+    settle();
+    if constexpr (E::kind == 0) {
+      // most calls have no NaN: the wave looks before it goes through them
+      if (nan) {
+#pragma clang loop unroll(disable)
+        for (int i = lane; i < kRows * kCols; i += 64) {
+          const int row = i / kCols, c = i % kCols, p = c / (16 * FW);
+          const int m = mhalf + row, col = nwave + p * kWStep + c % (16 * FW);
+          LLAR_LDS float* v = (LLAR_LDS float*)chunk(row, c / 4) + c % 4;
+          if (*v != *v && m < a.M && col < a.N)
+            *v = sum_again<kXRows, kWRows>(a, b, kGated ? p : 0, m, col, k_of(t0), k_of(t1));
+        }
+        settle();
+      }
+    }
+    // gated: a lane takes the same 8 columns of both parts
+    constexpr int kRuns = 2 * FW * (kGated ? 1 : kWParts);
+#pragma clang loop unroll(disable)
+    for (int i = lane; i < kRows * kRuns; i += 64) {
+      const int row = i / kRuns, c = i % kRuns;
+      const int m = mhalf + row, col = nwave + c / (2 * FW) * kWStep + 8 * (c % (2 * FW));
+      if (m >= a.M || col >= a.N) continue;
+      float v[P][8];
+#pragma unroll
+      for (int p = 0; p < P; p++) {
+        const f32x4 lo = *chunk(row, p * 4 * FW + 2 * c), hi = *chunk(row, p * 4 * FW + 2 * c + 1);
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+          v[p][e] = lo[e];
+          v[p][4 + e] = hi[e];
+        }
+      }
+      if (a.splits > 1) {
+#pragma unroll
+        for (int p = 0; p < P; p++) {
+          float* d = a.partial + (((int64_t)split * (kGated ? 2 : a.batch) + (kGated ? p : b)) * a.M + m) * a.npad + col;
+          *(f32x4*)d = f32x4{v[p][0], v[p][1], v[p][2], v[p][3]};
+          *(f32x4*)(d + 4) = f32x4{v[p][4], v[p][5], v[p][6], v[p][7]};
+        }
+      } else {
+        finish<E, kGated, 8>(a, b, m, col, v[0], v[P - 1]);
+      }
+    }
+    settle();
+  }
+}
+
+// Which tile, plane and share of the k tiles this workgroup takes: workgroup b
+// runs on XCD b % 8; each XCD takes a run of neighbouring tiles, in groups of 8
+// along m, so that its L2 holds what they share.
+struct Place {
+  int m0, n0, b, split, ktiles, t0, t1;
+};
+template <int TM, int TN>
+__device__ __forceinline__ Place place(const GemmArgs& a, int BK) {
+  Place o;
+  const int tm = (a.M + TM - 1) / TM, tn = (a.N + TN - 1) / TN;
+  const int total = gridDim.x;
+  const int wg = blockIdx.x, xcd = wg & 7, share = total >> 3, extra = total & 7;
+  int id = xcd * share + (xcd < extra ? xcd : extra) + (wg >> 3);
+  const int tiles = tm * tn;
+  const int plane = id / tiles;
+  id -= plane * tiles;
+  o.b = plane % a.batch;
+  o.split = plane / a.batch;
+  const int group = id / (8 * tn), in = id - group * 8 * tn;
+  const int gm = min(tm - group * 8, 8);
+  o.m0 = (group * 8 + in % gm) * TM;
+  o.n0 = in / gm * TN;
+  o.ktiles = (a.K + BK - 1) / BK;
+  const int64_t all = (int64_t)o.ktiles * a.segs;
+  o.t0 = (int)(all * o.split / a.splits);
+  o.t1 = (int)(all * (o.split + 1) / a.splits);
+  return o;
+}
+
 // One workgroup computes a TM x TN tile of the output (gated: TM x TN/2 of both
 // projections) over its share of the k tiles.  While a tile is multiplied the
 // next ones' loads are on their way to the other LDS buffers.
@@ -324,29 +468,8 @@ __global__ __launch_bounds__(Shape::kThreads) void k_gemm(GemmArgs a) {
   __shared__ __attribute__((aligned(1024))) char smem[kStages * kBuf];
   lds_char* lds = (lds_char*)smem;
 
-  // ---- which tile: workgroup b runs on XCD b % 8; each XCD takes a run of
-  // neighbouring tiles, in groups of 8 along m, so that its L2 holds what they share
-  const int tm = (a.M + TM - 1) / TM, tn = (a.N + TN - 1) / TN;
-  const int total = gridDim.x;
-  int id;
-  {
-    const int b = blockIdx.x, xcd = b & 7, q = total >> 3, r = total & 7;
-    id = xcd * q + (xcd < r ? xcd : r) + (b >> 3);
-  }
-  const int tiles = tm * tn;
-  const int plane = id / tiles;
-  id -= plane * tiles;
-  const int b = plane % a.batch, split = plane / a.batch;
-  int m0, n0;
-  {
-    const int group = id / (8 * tn), in = id - group * 8 * tn;
-    const int gm = min(tm - group * 8, 8);
-    m0 = (group * 8 + in % gm) * TM;
-    n0 = in / gm * TN;
-  }
-  const int ktiles = (a.K + BK - 1) / BK;
-  const int all = ktiles * a.segs;
-  const int t0 = (int)((int64_t)all * split / a.splits), t1 = (int)((int64_t)all * (split + 1) / a.splits);
+  const Place at = place<TM, TN>(a, BK);
+  const int m0 = at.m0, n0 = at.n0, b = at.b, split = at.split, ktiles = at.ktiles, t0 = at.t0, t1 = at.t1;
 
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / Shape::WN, wn = wave % Shape::WN;
@@ -509,7 +632,7 @@ __global__ __launch_bounds__(Shape::kThreads) void k_gemm(GemmArgs a) {
         wait_loads<0>();
       __syncthreads();  // this tile has arrived; everyone is done with the one before
       if (t + S - 1 < t1) load(t + S - 1, slot == 0 ? S - 1 : slot - 1);
-      lds_char* at = lds + slot * kBuf;
+      lds_char* tile = lds + slot * kBuf;
       slot = slot == S - 1 ? 0 : slot + 1;
 #pragma unroll
       for (int kk = 0; kk < KK; kk++) {
@@ -518,10 +641,10 @@ __global__ __launch_bounds__(Shape::kThreads) void k_gemm(GemmArgs a) {
         for (int p = 0; p < kWParts; p++)
 #pragma unroll
           for (int j = 0; j < FW; j++)
-            wf[p][j] = read_frag<W, E>(at + kXParts * X::kBytes + p * W::kBytes, wbase, j, kk);
+            wf[p][j] = read_frag<W, E>(tile + kXParts * X::kBytes + p * W::kBytes, wbase, j, kk);
 #pragma unroll
         for (int f = 0; f < FX; f++) {
-          const Frag<E> xf = read_frag<X, E>(at, xbase, f, kk);
+          const Frag<E> xf = read_frag<X, E>(tile, xbase, f, kk);
 #pragma unroll
           for (int p = 0; p < kWParts; p++)
 #pragma unroll
@@ -531,132 +654,174 @@ __global__ __launch_bounds__(Shape::kThreads) void k_gemm(GemmArgs a) {
     }
   }
 
-  // ---- results: of fragments (f, j) lane l holds row l % 16 and 4 neighbouring
-  // columns.  Bare sums (a gradient, a partial plane, a product without
-  // epilogue) are stored from there; everything else goes through LDS, where a
-  // lane takes 8 columns of one row, so that the epilogue is one piece of code
-  // and its accesses are whole lines.
-  const int lane = threadIdx.x & 63, q = lane >> 4;
-  const int mwave = m0 + wm * 16 * FX, nwave = n0 + wn * 16 * FW;
-  bool bare = !kGated && (a.splits > 1 || (a.vec_out && !a.bias && !a.resid && !a.z[0] && a.act == kActNone));
-  bool nan = false;
-  if constexpr (E::kind == 0) {
-#pragma unroll
-    for (int h = 0; h < kXParts; h++)
-#pragma unroll
-      for (int p = 0; p < kWParts; p++)
-#pragma unroll
-        for (int f = 0; f < FX; f++)
-#pragma unroll
-          for (int j = 0; j < FW; j++) {
-            const f32x4 c = acc[h][p][f][j];
-            const float s = (c[0] + c[1]) + (c[2] + c[3]);
-            nan = nan || s != s;
-          }
-    nan = __any(nan);
-    bare = bare && !nan;
+  store_results<E, kXRows, kWRows, kGated, Shape, kXParts, kWParts, kSpread, kStages * kBuf>(
+      a, acc, lds, m0, n0, b, split, ktiles, t0, t1, BK);
+}
+
+// ---- binary32 ----------------------------------------------------------------------
+// R rows by 32 k of one operand, as three planes of bfloat16 parts in LDS:
+// [plane][row][4 chunks of 8 k], chunk c of a row at c ^ key(row).  A thread
+// fetches its share of the tile into registers one tile ahead, and cuts it into
+// parts when it writes it, once for all the waves that multiply it.
+template <bool kRows, int R, int NT, int F, bool kPerm>
+struct Parts {
+  static constexpr bool kAll = R * 4 >= NT;  // else threads from R * 4 on have no share
+  static constexpr int C = kAll ? R * 4 / NT : 1;  // 8-k chunks of a thread (row-contiguous: of neighbouring rows)
+  static constexpr int kPlane = R * 64, kBytes = 3 * kPlane;
+  static_assert(C == 1 || C == 2 || C == 4, "whole chunks");
+  float raw[C][8];
+
+  static __device__ __forceinline__ int key(int row) {
+    return kPerm ? ((row >> 1) & 1) | (((row / (4 * F)) & 1) << 1) : (row >> 1) & 3;
   }
-  if (bare) {
-    constexpr int kRunLen = kSpread ? (4 * FW < 8 ? 4 * FW : 8) : 4;
+  static __device__ __forceinline__ void where(int c, int& row, int& kc) {
+    const int t = threadIdx.x;
+    if constexpr (kRows) {
+      row = t % (R / C) * C + c;
+      kc = t / (R / C);
+    } else {
+      row = (c * NT + t) / 4;
+      kc = (c * NT + t) % 4;
+    }
+  }
+  // rows and k that exist, counted from the tile's first
+  __device__ __forceinline__ void fetch(int64_t base, int64_t ld, int rows_left, int krem) {
+    if (!kAll && threadIdx.x >= R * 4) krem = 0;
+    const uint64_t first = (uint32_t)__builtin_amdgcn_readfirstlane((int)base) |
+                           (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(base >> 32)) << 32;
+    const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void*)first, (short)0, 0x7fffffff, 0x00020000);
+    if constexpr (kRows) {
+      int row, kc;
+      where(0, row, kc);
 #pragma unroll
-    for (int h = 0; h < kXParts; h++)
+      for (int e = 0; e < 8; e++) {
+        const int k = kc * 8 + e;
+        const uint32_t off = row < rows_left && k < krem ? (uint32_t)((k * ld + row) * 4) : kNoLoad;
+        if constexpr (C == 1) {
+          raw[0][e] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, (int)off, 0, 0));
+        } else if constexpr (C == 2) {
+          const auto v = __builtin_amdgcn_raw_buffer_load_b64(r, (int)off, 0, 0);
+          raw[0][e] = __uint_as_float(v[0]);
+          raw[1][e] = __uint_as_float(v[1]);
+        } else {
+          const auto v = __builtin_amdgcn_raw_buffer_load_b128(r, (int)off, 0, 0);
 #pragma unroll
-      for (int f = 0; f < FX; f++) {
-        const int m = mwave + h * kXRowsPart + f * 16 + (lane & 15);
-#pragma unroll
-        for (int p = 0; p < kWParts; p++)
-#pragma unroll
-          for (int j = 0; j < FW; j += kRunLen / 4) {
-            const int col = nwave + p * kWStep + (kSpread ? q * 4 * FW + 4 * j : 16 * j + 4 * q);
-            if (m < a.M && col < a.N) {
-              if (a.splits > 1) {
-                float* d = a.partial + (((int64_t)split * a.batch + b) * a.M + m) * a.npad + col;
-#pragma unroll
-                for (int i = 0; i < kRunLen / 4; i++)
-                  if (col + 4 * i < a.npad) *(f32x4*)(d + 4 * i) = acc[h][p][f][j + i];
-              } else {
-                float v[kRunLen];
-#pragma unroll
-                for (int i = 0; i < kRunLen; i++) v[i] = acc[h][p][f][j + i / 4][i % 4];
-                store_vals<E, kRunLen>((T*)a.out[b] + m * a.outld + col, v, a.N - col, true);
-              }
-            }
-          }
+          for (int c = 0; c < 4; c++) raw[c][e] = __uint_as_float(v[c]);
+        }
       }
-    return;
-  }
-  // half of the wave's rows at a time (a part of x, or half of its one);
-  // 16-byte chunk c of a row lies at c ^ row % 16
-  constexpr int kCols = 16 * FW * kWParts, kHalf = kXParts * FX / 2, kRows = kHalf * 16;
-  static_assert(Shape::kWaves * kRows * kCols * 4 <= kStages * kBuf, "the waves' sums fit the tile buffers");
-  lds_char* mine = lds + wave * (kRows * kCols * 4);
-  auto chunk = [&](int row, int c) {
-    return (LLAR_LDS f32x4*)(mine + (row * (kCols / 4) + (c ^ (row % 16 % (kCols / 4)))) * 16);
-  };
-  auto k_of = [&](int t) { return (int64_t)(t / ktiles) * a.K + min((t % ktiles) * BK, a.K); };
-  auto settle = [] {
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-  };
-  __syncthreads();  // everyone is done with the tiles
+    } else {
 #pragma unroll
-  for (int h = 0; h < 2; h++) {
-    const int mhalf = mwave + (kXParts == 2 ? h * kXRowsPart : h * kRows);
+      for (int c = 0; c < C; c++) {
+        int row, kc;
+        where(c, row, kc);
 #pragma unroll
-    for (int i = 0; i < kHalf; i++)
+        for (int h = 0; h < 2; h++) {
+          const int k = kc * 8 + 4 * h;
+          const uint32_t off = row < rows_left && k < krem ? (uint32_t)((row * ld + k) * 4) : kNoLoad;
+          const auto v = __builtin_amdgcn_raw_buffer_load_b128(r, (int)off, 0, 0);
 #pragma unroll
-      for (int p = 0; p < kWParts; p++)
-#pragma unroll
-        for (int j = 0; j < FW; j++) {
-          constexpr int kPer = kXParts == 2 ? 0 : kHalf;  // fragments of x before this half's in its part
-          *chunk(i * 16 + (lane & 15), p * 4 * FW + (kSpread ? q * FW + j : 4 * j + q)) =
-              acc[kXParts == 2 ? h : 0][p][i + h * kPer][j];
+          for (int e = 0; e < 4; e++) raw[c][4 * h + e] = __uint_as_float(v[e]);
         }
-    settle();
-    if constexpr (E::kind == 0) {
-      // most calls have no NaN: the wave looks before it goes through them
-      if (nan) {
-#pragma clang loop unroll(disable)
-        for (int i = lane; i < kRows * kCols; i += 64) {
-          const int row = i / kCols, c = i % kCols, p = c / (16 * FW);
-          const int m = mhalf + row, col = nwave + p * kWStep + c % (16 * FW);
-          LLAR_LDS float* v = (LLAR_LDS float*)chunk(row, c / 4) + c % 4;
-          if (*v != *v && m < a.M && col < a.N)
-            *v = sum_again<kXRows, kWRows>(a, b, kGated ? p : 0, m, col, k_of(t0), k_of(t1));
-        }
-        settle();
       }
     }
-    // gated: a lane takes the same 8 columns of both parts
-    constexpr int kRuns = 2 * FW * (kGated ? 1 : kWParts);
-#pragma clang loop unroll(disable)
-    for (int i = lane; i < kRows * kRuns; i += 64) {
-      const int row = i / kRuns, c = i % kRuns;
-      const int m = mhalf + row, col = nwave + c / (2 * FW) * kWStep + 8 * (c % (2 * FW));
-      if (m >= a.M || col >= a.N) continue;
-      float v[P][8];
-#pragma unroll
-      for (int p = 0; p < P; p++) {
-        const f32x4 lo = *chunk(row, p * 4 * FW + 2 * c), hi = *chunk(row, p * 4 * FW + 2 * c + 1);
-#pragma unroll
-        for (int e = 0; e < 4; e++) {
-          v[p][e] = lo[e];
-          v[p][4 + e] = hi[e];
-        }
-      }
-      if (a.splits > 1) {
-#pragma unroll
-        for (int p = 0; p < P; p++) {
-          float* d = a.partial + (((int64_t)split * (kGated ? 2 : a.batch) + (kGated ? p : b)) * a.M + m) * a.npad + col;
-          *(f32x4*)d = f32x4{v[p][0], v[p][1], v[p][2], v[p][3]};
-          *(f32x4*)(d + 4) = f32x4{v[p][4], v[p][5], v[p][6], v[p][7]};
-        }
-      } else {
-        finish<E, kGated, 8>(a, b, m, col, v[0], v[P - 1]);
-      }
-    }
-    settle();
   }
+  __device__ __forceinline__ void write(lds_char* lds) const {
+    if (!kAll && threadIdx.x >= R * 4) return;
+#pragma unroll
+    for (int c = 0; c < C; c++) {
+      int row, kc;
+      where(c, row, kc);
+      const Frag<F32> f = split3(raw[c]);
+      lds_char* at = lds + row * 64 + (kc ^ key(row)) * 16;
+      *(LLAR_LDS s16x8*)at = f.hi;
+      *(LLAR_LDS s16x8*)(at + kPlane) = f.mid;
+      *(LLAR_LDS s16x8*)(at + 2 * kPlane) = f.lo;
+    }
+  }
+  static __device__ __forceinline__ uint32_t frag_at(int row0) {
+    const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+    const int row = row0 + (kPerm ? (r >> 2) * 4 * F + (r & 3) : r);
+    return row * 64 + (q ^ key(row)) * 16;
+  }
+  static __device__ __forceinline__ Frag<F32> read(lds_char* lds, uint32_t base, int f) {
+    lds_char* at = lds + base + f * (kPerm ? 4 * 64 : 16 * 64);
+    Frag<F32> o;
+    o.hi = *(LLAR_LDS s16x8*)at;
+    o.mid = *(LLAR_LDS s16x8*)(at + kPlane);
+    o.lo = *(LLAR_LDS s16x8*)(at + 2 * kPlane);
+    return o;
+  }
+};
+
+// The same product for binary32: one LDS buffer, registers one tile ahead; the
+// other workgroups of the CU multiply while this one writes.
+template <bool kXRows, bool kWRows, class Shape, bool kGated>
+__global__ __launch_bounds__(Shape::kThreads) void k_gemm32(GemmArgs a) {
+  constexpr int TM = Shape::TM, NT = Shape::kThreads, BK = 32;
+  constexpr int P = kGated ? 2 : 1;
+  constexpr int TN = Shape::TN / P;
+  constexpr int FX = Shape::FM, FW = Shape::FN / P;
+  typedef Parts<kXRows, TM, NT, FX, false> X;
+  typedef Parts<kWRows, TN, NT, FW, true> W;
+  constexpr int kBuf = X::kBytes + P * W::kBytes;
+  __shared__ __attribute__((aligned(1024))) char smem[kBuf];
+  lds_char* lds = (lds_char*)smem;
+  const Place at = place<TM, TN>(a, BK);
+  const int m0 = at.m0, n0 = at.n0, b = at.b, ktiles = at.ktiles, t0 = at.t0, t1 = at.t1;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave / Shape::WN, wn = wave % Shape::WN;
+
+  f32x4 acc[1][P][FX][FW];
+#pragma unroll
+  for (int p = 0; p < P; p++)
+#pragma unroll
+    for (int f = 0; f < FX; f++)
+#pragma unroll
+      for (int j = 0; j < FW; j++) acc[0][p][f][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const int64_t x1 = (int64_t)a.x[1], w1 = (int64_t)a.w[1];
+  const int64_t x0 = b ? x1 : (int64_t)a.x[0], w0 = b ? w1 : (int64_t)a.w[0];
+  const int64_t xnext = x1 - x0, wnext = w1 - w0;
+  const int64_t xfirst = kXRows ? m0 : m0 * a.xld, xstep = kXRows ? BK * a.xld : BK;
+  const int64_t wfirst = kWRows ? n0 : n0 * a.wld, wstep = kWRows ? BK * a.wld : BK;
+  X xr;
+  W wr[P];
+  auto fetch = [&](int t) {
+    const bool second = a.segs == 2 && t >= ktiles;
+    const int kt = second ? t - ktiles : t;
+    const int krem = t < t1 ? a.K - kt * BK : 0;
+    xr.fetch(x0 + (second ? xnext : 0) + (xfirst + kt * xstep) * 4, a.xld, a.M - m0, krem);
+#pragma unroll
+    for (int p = 0; p < P; p++)
+      wr[p].fetch(w0 + (second || p ? wnext : 0) + (wfirst + kt * wstep) * 4, a.wld, a.N - n0, krem);
+  };
+  const uint32_t xbase = X::frag_at(wm * 16 * FX), wbase = W::frag_at(wn * 16 * FW);
+  fetch(t0);
+  for (int t = t0; t < t1; t++) {
+    __syncthreads();  // everyone is done with the tile before
+    xr.write(lds);
+#pragma unroll
+    for (int p = 0; p < P; p++) wr[p].write(lds + X::kBytes + p * W::kBytes);
+    fetch(t + 1);
+    __syncthreads();
+    Frag<F32> wf[P][FW];
+#pragma unroll
+    for (int p = 0; p < P; p++)
+#pragma unroll
+      for (int j = 0; j < FW; j++) wf[p][j] = W::read(lds + X::kBytes + p * W::kBytes, wbase, j);
+#pragma unroll
+    for (int f = 0; f < FX; f++) {
+      const Frag<F32> xf = X::read(lds, xbase, f);
+      // small products first; neighbours in the sequence have different sums
+#pragma unroll
+      for (int s = 0; s < 6; s++)
+#pragma unroll
+        for (int p = 0; p < P; p++)
+#pragma unroll
+          for (int j = 0; j < FW; j++) acc[0][p][f][j] = mma_part(s, wf[p][j], xf, acc[0][p][f][j]);
+    }
+  }
+  store_results<F32, kXRows, kWRows, kGated, Shape, 1, P, true, kBuf>(a, acc, lds, m0, n0, b, at.split, ktiles, t0, t1,
+                                                                    BK);
 }
 
 template <class E, bool kXRows, bool kWRows, class Shape, bool kGated>
@@ -666,7 +831,10 @@ hipError_t launch_one(const GemmArgs& a, hipStream_t s) {
   const int64_t grid = tiles * a.batch * a.splits;
   if (grid <= 0) return hipSuccess;
   if (grid > 0x7fffffff) return hipErrorInvalidValue;
-  k_gemm<E, kXRows, kWRows, Shape, kGated><<<dim3((uint32_t)grid), dim3(Shape::kThreads), 0, s>>>(a);
+  if constexpr (E::kind == 0)
+    k_gemm32<kXRows, kWRows, Shape, kGated><<<dim3((uint32_t)grid), dim3(Shape::kThreads), 0, s>>>(a);
+  else
+    k_gemm<E, kXRows, kWRows, Shape, kGated><<<dim3((uint32_t)grid), dim3(Shape::kThreads), 0, s>>>(a);
   return hipGetLastError();
 }
 
