@@ -45,7 +45,7 @@ constexpr int kTileKBytes = 128;  // k extent of a tile in bytes of one row
 
 struct GemmPlan {
   int kind;        // llar_dtype
-  int tile;
+  int tile, groups;
   bool x_rows;     // x is row-contiguous
   bool w_rows;
   bool gated;

@@ -83,13 +83,13 @@ bool vec8(const void* p, int64_t ld, int es) { return !p || (((uintptr_t)p & 15)
 // How a product runs: the kernel for few rows, or tiles; and its split over k.
 struct Shape {
   bool few;
-  int tile, splits;
+  int tile, groups, splits;
 };
 
 // `kt`: k tiles of a plane in all, `segs` products added; `outs`: output planes;
 // `few`: x is k-contiguous, so that few rows of it may go the direct way.
 Shape choose(int64_t M, int64_t N, int64_t K, int segs, int outs, bool gated, int es, bool few, bool w_rows) {
-  Shape s{false, kTile64, 1};
+  Shape s{false, kTile64, 1, 1};
   if (M == 0 || N == 0) return s;  // nothing to launch
   if (few && M <= kFewRows && outs == 1) {
     s.few = true;
@@ -99,14 +99,47 @@ Shape choose(int64_t M, int64_t N, int64_t K, int segs, int outs, bool gated, in
     }
     return s;
   }
-  const int64_t kt = cdiv(K * es, kTileKBytes) * segs;
-  auto tiles = [&](int t) { return cdiv(M, kTileM[t]) * cdiv(N, kTileN[t] / (gated ? 2 : 1)) * outs; };
-  if (es == 2 && tiles(kTile256) >= 192)
-    s.tile = kTile256;
-  else if (tiles(kTile128) >= 256)
-    s.tile = kTile128;
-  const int64_t n = tiles(s.tile);
-  while (n * s.splits < 256 && s.splits < 16 && kt / (2 * s.splits) >= 4) s.splits *= 2;
+  // The cheapest way by measured costs (us): `one` is what a k tile takes a
+  // workgroup alone on its CU, `full` what it takes `occ` of them together,
+  // `turn` the first loads and the results.  Measured on MI355X at 32 .. 4096
+  // rows, 600 .. 8192 columns, k 336 .. 8192.
+  struct Way {
+    int tile, groups, occ;
+    double one, full, turn;
+  };
+  static const Way ways16[] = {{kTile256, 1, 1, 1.42, 1.42, 4},   {kTile128, 2, 1, 0.55, 0.55, 2.5},
+                               {kTile128, 1, 2, 0.78, 1.08, 2.5}, {kTile64, 1, 2, 0.37, 0.50, 1.5},
+                               {kTile64, 2, 1, 0.24, 0.24, 1.7},  {kTile64, 4, 1, 0.26, 0.26, 2}};
+  static const Way ways32[] = {{kTile128, 2, 1, 1.36, 1.36, 2.5}, {kTile128, 1, 2, 1.75, 2.57, 2.5},
+                               {kTile64, 1, 4, 0.78, 1.70, 1.5},  {kTile64, 2, 2, 0.50, 0.82, 1.7},
+                               {kTile64, 4, 1, 0.43, 0.43, 2}};
+  constexpr double kLaunch = 2;
+  constexpr double kJoin = 4;          // a second launch
+  constexpr double kBytesPerUs = 4e6;  // and its planes, written and read
+  const int64_t kt = es == 2 ? cdiv(K, 64) * segs : cdiv(K, 32) * segs;
+  const int planes = gated ? 2 : outs;
+  double best = 0;
+  auto look = [&](const Way& w) {
+    const int64_t tiles = cdiv(M, kTileM[w.tile]) * cdiv(N, kTileN[w.tile] / (gated ? 2 : 1)) * outs;
+    for (int splits = 1; splits <= 16 && (splits == 1 || kt / splits >= 2 * w.groups); splits *= 2) {
+      const int64_t wgs = tiles * splits, all = 256 * w.occ, rest = wgs % all;
+      double tile = (double)(wgs / all) * w.full;
+      if (rest > 0) tile += w.one + (rest > 256 ? (w.full - w.one) * (rest - 256) / (all - 256) : 0);
+      double t = kLaunch + cdiv(wgs, all) * w.turn + tile * w.groups * cdiv(cdiv(kt, splits), w.groups);
+      if (splits > 1) t += kJoin + (double)splits * planes * M * N * 8 / kBytesPerUs;
+      if (best == 0 || t < best) {
+        best = t;
+        s.tile = w.tile;
+        s.groups = w.groups;
+        s.splits = splits;
+      }
+    }
+  };
+  if (es == 2) {
+    for (const Way& w : ways16) look(w);
+  } else {
+    for (const Way& w : ways32) look(w);
+  }
   return s;
 }
 size_t partial_bytes(const Shape& s, int64_t M, int64_t N, int planes) {
@@ -240,6 +273,7 @@ int run_product(const Product& p, int dtype, const Carve& space, hipStream_t s) 
     GemmPlan plan;
     plan.kind = dtype;
     plan.tile = sh.tile;
+    plan.groups = sh.groups;
     plan.x_rows = p.x[0].by_rows;
     plan.w_rows = p.w[0].by_rows;
     plan.gated = p.gated;

@@ -11,18 +11,24 @@ typedef LLAR_LDS char lds_char;
 
 constexpr uint32_t kNoLoad = 0x80000000u;  // beyond every descriptor: the load writes zeros
 
-template <int TM_, int TN_, int WM_, int WN_>
+// A TM x TN tile by WM x WN waves; kGroups such groups of waves take the k
+// tiles in turn, each with its own buffers, and their sums are joined in LDS:
+// more waves where there are few tiles, without a second kernel.
+template <int TM_, int TN_, int WM_, int WN_, int G_>
 struct TileShape {
-  static constexpr int TM = TM_, TN = TN_, WM = WM_, WN = WN_;
-  static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
+  static constexpr int TM = TM_, TN = TN_, WM = WM_, WN = WN_, kGroups = G_;
+  static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;  // of a group
+  static constexpr int kAllThreads = kThreads * kGroups;
   static constexpr int FM = TM / WM / 16;  // 16-row fragments of a wave along m
   static constexpr int FN = TN / WN / 16;  // and along n
   static constexpr bool kPaired = WM == 2 && WN == 4;
-  static constexpr int kStages = kPaired || TM > 64 ? 2 : 4;  // tile buffers
+  static constexpr int kStages = kPaired || TM > 64 || G_ == 4 ? 2 : 4;  // tile buffers of a group
 };
-typedef TileShape<256, 256, 2, 4> Shape256;
-typedef TileShape<128, 128, 2, 2> Shape128;
-typedef TileShape<64, 64, 2, 2> Shape64;
+typedef TileShape<256, 256, 2, 4, 1> Shape256;
+template <int G>
+using Shape128 = TileShape<128, 128, 2, 2, G>;
+template <int G>
+using Shape64 = TileShape<64, 64, 2, 2, G>;
 
 // ---- fragments -------------------------------------------------------------------
 // A 16 x 32 operand fragment: lane l holds row l % 16, k = 8 (l / 16) .. + 7.
@@ -30,9 +36,11 @@ template <class E>
 struct Frag {
   s16x8 v;
 };
-// binary32 as three bfloat16 whose sum is the value: each part is what the
-// parts before it leave, rounded to bfloat16's 8 bits.  Every remainder is
-// exact, and 8 bits at most are left for the third part.
+// binary32 as three bfloat16 whose sum is the value: each part is the leading 8
+// bits of what the parts before it leave.  Every remainder is exact, and 8 bits
+// at most are left for the third part.  Cut, not rounded: the rounding
+// conversion measured four times an ordinary instruction, and the cut costs
+// nothing that counts (below).
 template <>
 struct Frag<F32> {
   s16x8 hi, mid, lo;
@@ -50,8 +58,9 @@ __device__ __forceinline__ f32x4 mma<F16>(const Frag<F16>& a, const Frag<F16>& b
   return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a.v), __builtin_bit_cast(f16x8, b.v), c, 0,
                                                 0, 0);
 }
-// Of the nine products of parts the six above 2^-23 of the whole, small ones
-// first: 6 bfloat16 products at 16 times the binary32 unit's rate.
+// Six of the nine products of parts, small ones first: 6 bfloat16 products at 16
+// times the binary32 unit's rate.  The three left out are at most 2^-20 of the
+// whole, and 2^-24 on average (mid is 2^-8.6 of a value on average, lo 2^-16.6).
 __device__ __forceinline__ f32x4 mma_part(int s, const Frag<F32>& a, const Frag<F32>& b, f32x4 c) {
   const s16x8 p = s == 0 || s == 3 ? a.mid : s == 1 ? a.lo : a.hi;
   const s16x8 q = s == 0 || s == 4 ? b.mid : s == 2 ? b.lo : b.hi;
@@ -65,10 +74,9 @@ __device__ __forceinline__ f32x4 mma<F32>(const Frag<F32>& a, const Frag<F32>& b
   return c;
 }
 
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {  // both rounded to nearest even
-  typedef __bf16 pair __attribute__((ext_vector_type(2)));
-  const pair p = {(__bf16)a, (__bf16)b};
-  return __builtin_bit_cast(uint32_t, p);
+// The upper halves of two words, a's lower.
+__device__ __forceinline__ uint32_t upper_halves(uint32_t a, uint32_t b) {
+  return __builtin_amdgcn_perm(b, a, 0x07060302);
 }
 __device__ __forceinline__ Frag<F32> split3(const float (&x)[8]) {
   union {
@@ -77,13 +85,14 @@ __device__ __forceinline__ Frag<F32> split3(const float (&x)[8]) {
   } hi, mid, lo;
 #pragma unroll
   for (int i = 0; i < 4; i++) {
-    const uint32_t h = pack_bf16(x[2 * i], x[2 * i + 1]);
-    const float r0 = x[2 * i] - __uint_as_float(h << 16), r1 = x[2 * i + 1] - __uint_as_float(h & 0xffff0000u);
-    const uint32_t m = pack_bf16(r0, r1);
-    const float q0 = r0 - __uint_as_float(m << 16), q1 = r1 - __uint_as_float(m & 0xffff0000u);
-    hi.u[i] = h;
-    mid.u[i] = m;
-    lo.u[i] = pack_bf16(q0, q1);
+    const uint32_t x0 = __float_as_uint(x[2 * i]), x1 = __float_as_uint(x[2 * i + 1]);
+    const float r0 = x[2 * i] - __uint_as_float(x0 & 0xffff0000u);
+    const float r1 = x[2 * i + 1] - __uint_as_float(x1 & 0xffff0000u);
+    const uint32_t m0 = __float_as_uint(r0), m1 = __float_as_uint(r1);
+    const float q0 = r0 - __uint_as_float(m0 & 0xffff0000u), q1 = r1 - __uint_as_float(m1 & 0xffff0000u);
+    hi.u[i] = upper_halves(x0, x1);
+    mid.u[i] = upper_halves(m0, m1);
+    lo.u[i] = upper_halves(__float_as_uint(q0), __float_as_uint(q1));
   }
   Frag<F32> f;
   f.hi = hi.v;
@@ -128,7 +137,7 @@ struct Operand {
   }
 
   // chunk number of load i of this thread, in LDS order
-  static __device__ __forceinline__ int slot(int i) { return i * NT + (int)threadIdx.x; }
+  static __device__ __forceinline__ int slot(int i) { return i * NT + (int)(threadIdx.x % NT); }
   // its row (or first row) and its k (or first k) within the tile
   static __device__ __forceinline__ void where(int i, int& row, int& k) {
     const int s = slot(i);
@@ -169,7 +178,7 @@ __device__ __forceinline__ void direct_offsets(uint32_t (&voff)[Op::kLoads], int
 template <class Op>
 __device__ __forceinline__ void load_direct(lds_char* lds, int64_t base, const uint32_t (&voff)[Op::kLoads],
                                             int krem) {
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x % Op::kThreads >> 6);
   const u32x4 desc = {(uint32_t)__builtin_amdgcn_readfirstlane((int)base),
                       (uint32_t)__builtin_amdgcn_readfirstlane((int)(base >> 32)) & 0xffffu, 0x7fffffffu, 0x00020000u};
   const uint32_t at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)lds + wave * 1024);
@@ -256,9 +265,8 @@ __device__ __forceinline__ void finish(const GemmArgs& a, int b, int m, int col,
 }
 
 // The product of parts turns an infinity into a NaN (infinity times a zero
-// part, or infinity less infinity in a remainder; a value that rounds to
-// bfloat16's infinity does the same), so a NaN sum of binary32 inputs is taken
-// again from the inputs, in k order, up to the first true NaN.
+// part, or infinity less infinity in a remainder), so a NaN sum of binary32
+// inputs is taken again from the inputs, in k order, up to the first true NaN.
 template <bool kXRows, bool kWRows>
 __device__ __forceinline__ float sum_again(const GemmArgs& a, int b, int p, int m, int col, int64_t k0, int64_t k1) {
   float s = 0.f;
@@ -412,6 +420,34 @@ __device__ __forceinline__ void store_results(const GemmArgs& a, f32x4 (&acc)[kX
   }
 }
 
+// Adds the groups' sums, in their order, into the first group's; false for the
+// others, which are done.
+template <class Shape, int kLds, int A, int B, int FX, int FW>
+__device__ __forceinline__ bool join_groups(f32x4 (&acc)[A][B][FX][FW], lds_char* lds) {
+  constexpr int G = Shape::kGroups, kFrags = A * B * FX * FW;
+  if constexpr (G == 1) return true;
+  static_assert((G - 1) * kFrags * Shape::kThreads * 16 <= kLds, "the groups' sums fit the tile buffers");
+  const int group = __builtin_amdgcn_readfirstlane(threadIdx.x / Shape::kThreads), t = threadIdx.x % Shape::kThreads;
+  f32x4(&flat)[kFrags] = reinterpret_cast<f32x4(&)[kFrags]>(acc);
+  __syncthreads();
+  if (group > 0) {
+#pragma unroll
+    for (int i = 0; i < kFrags; i++)
+      *(LLAR_LDS f32x4*)(lds + (((group - 1) * kFrags + i) * Shape::kThreads + t) * 16) = flat[i];
+  }
+  __syncthreads();
+  if (group > 0) return false;
+#pragma unroll
+  for (int g = 0; g < G - 1; g++)
+#pragma unroll
+    for (int i = 0; i < kFrags; i++) {
+      const f32x4 v = *(LLAR_LDS f32x4*)(lds + ((g * kFrags + i) * Shape::kThreads + t) * 16);
+#pragma unroll
+      for (int e = 0; e < 4; e++) flat[i][e] += v[e];
+    }
+  return true;
+}
+
 // Which tile, plane and share of the k tiles this workgroup takes: workgroup b
 // runs on XCD b % 8; each XCD takes a run of neighbouring tiles, in groups of 8
 // along m, so that its L2 holds what they share.
@@ -449,7 +485,7 @@ __device__ __forceinline__ Place place(const GemmArgs& a, int BK) {
 // projection), those of x as kXParts; a wave owns FX fragments of every part
 // of x and FW of every part of w.
 template <class E, bool kXRows, bool kWRows, class Shape, bool kGated>
-__global__ __launch_bounds__(Shape::kThreads) void k_gemm(GemmArgs a) {
+__global__ __launch_bounds__(Shape::kAllThreads) void k_gemm(GemmArgs a) {
   typedef typename E::T T;
   constexpr bool kPaired = Shape::kPaired;
   constexpr int TM = Shape::TM, NT = Shape::kThreads;
@@ -465,13 +501,15 @@ __global__ __launch_bounds__(Shape::kThreads) void k_gemm(GemmArgs a) {
   constexpr int BK = X::BK, ES = X::ES;
   constexpr int kBuf = kXParts * X::kBytes + kWParts * W::kBytes;
   constexpr int kStages = Shape::kStages;
-  __shared__ __attribute__((aligned(1024))) char smem[kStages * kBuf];
-  lds_char* lds = (lds_char*)smem;
+  constexpr int G = Shape::kGroups;
+  __shared__ __attribute__((aligned(1024))) char smem[G * kStages * kBuf];
+  const int group = __builtin_amdgcn_readfirstlane(threadIdx.x / NT);
+  lds_char* lds = (lds_char*)smem + group * kStages * kBuf;
 
   const Place at = place<TM, TN>(a, BK);
   const int m0 = at.m0, n0 = at.n0, b = at.b, split = at.split, ktiles = at.ktiles, t0 = at.t0, t1 = at.t1;
 
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x % NT >> 6);
   const int wm = wave / Shape::WN, wn = wave % Shape::WN;
 
   f32x4 acc[kXParts][kWParts][FX][FW];
@@ -496,13 +534,20 @@ __global__ __launch_bounds__(Shape::kThreads) void k_gemm(GemmArgs a) {
   const int64_t wpart = kGated ? wnext : (kWRows ? kWStep : kWStep * a.wld) * ES;
   const int64_t xfirst = kXRows ? m0 : m0 * a.xld, xstep = kXRows ? BK * a.xld : BK;
   const int64_t wfirst = kWRows ? n0 : n0 * a.wld, wstep = kWRows ? BK * a.wld : BK;
+  // Neighbouring workgroups start up to three k tiles apart: the rows of a tile
+  // can lie so that a k tile of all of them is in a few memory channels (8192 x
+  // 8192 x 3584 bf16: 400 -> 333 us, other shapes within 2 %).
+  const int shift = (n0 / TN % 4) % max(t1 - t0, 1);
   // k tile t's first elements and how many of its k exist (none beyond the last tile)
   int64_t xat, wat;
   int krem;
   auto aim = [&](int t) {
+    const bool exists = t < t1;
+    t += shift;
+    if (t >= t1) t -= t1 - t0;
     const bool second = a.segs == 2 && t >= ktiles;
     const int kt = second ? t - ktiles : t;
-    krem = t < t1 ? a.K - kt * BK : 0;
+    krem = exists ? a.K - kt * BK : 0;
     xat = x0 + (second ? xnext : 0) + (xfirst + kt * xstep) * ES;
     wat = w0 + (second ? wnext : 0) + (wfirst + kt * wstep) * ES;
   };
@@ -622,16 +667,15 @@ __global__ __launch_bounds__(Shape::kThreads) void k_gemm(GemmArgs a) {
 #pragma unroll
       for (int h = 0; h < kXParts; h++) load_x(slot, h);
     };
-    for (int i = 0; i < S - 1; i++)
-      if (t0 + i < t1) load(t0 + i, i);
+    // group g takes the tiles t0 + g, t0 + g + G, ...; all groups go round
+    // equally often, loading nothing beyond the last tile
+    const int rounds = (t1 - t0 + G - 1) / G;
+    for (int i = 0; i < S - 1; i++) load(t0 + group + i * G, i);
     int slot = 0;
-    for (int t = t0; t < t1; t++) {
-      if (t + S - 2 < t1)
-        wait_loads<(S - 2) * kLoads>();
-      else
-        wait_loads<0>();
+    for (int r = 0; r < rounds; r++) {
+      wait_loads<(S - 2) * kLoads>();
       __syncthreads();  // this tile has arrived; everyone is done with the one before
-      if (t + S - 1 < t1) load(t + S - 1, slot == 0 ? S - 1 : slot - 1);
+      load(t0 + group + (r + S - 1) * G, slot == 0 ? S - 1 : slot - 1);
       lds_char* tile = lds + slot * kBuf;
       slot = slot == S - 1 ? 0 : slot + 1;
 #pragma unroll
@@ -652,10 +696,12 @@ __global__ __launch_bounds__(Shape::kThreads) void k_gemm(GemmArgs a) {
         }
       }
     }
+    wait_loads<0>();
   }
 
-  store_results<E, kXRows, kWRows, kGated, Shape, kXParts, kWParts, kSpread, kStages * kBuf>(
-      a, acc, lds, m0, n0, b, split, ktiles, t0, t1, BK);
+  if (!join_groups<Shape, G * kStages * kBuf>(acc, (lds_char*)smem)) return;
+  store_results<E, kXRows, kWRows, kGated, Shape, kXParts, kWParts, kSpread, G * kStages * kBuf>(
+      a, acc, (lds_char*)smem, m0, n0, b, split, ktiles, t0, t1, BK);
 }
 
 // ---- binary32 ----------------------------------------------------------------------
@@ -675,7 +721,7 @@ struct Parts {
     return kPerm ? ((row >> 1) & 1) | (((row / (4 * F)) & 1) << 1) : (row >> 1) & 3;
   }
   static __device__ __forceinline__ void where(int c, int& row, int& kc) {
-    const int t = threadIdx.x;
+    const int t = threadIdx.x % NT;
     if constexpr (kRows) {
       row = t % (R / C) * C + c;
       kc = t / (R / C);
@@ -686,7 +732,7 @@ struct Parts {
   }
   // rows and k that exist, counted from the tile's first
   __device__ __forceinline__ void fetch(int64_t base, int64_t ld, int rows_left, int krem) {
-    if (!kAll && threadIdx.x >= R * 4) krem = 0;
+    if (!kAll && threadIdx.x % NT >= R * 4) krem = 0;
     const uint64_t first = (uint32_t)__builtin_amdgcn_readfirstlane((int)base) |
                            (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(base >> 32)) << 32;
     const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void*)first, (short)0, 0x7fffffff, 0x00020000);
@@ -726,7 +772,7 @@ struct Parts {
     }
   }
   __device__ __forceinline__ void write(lds_char* lds) const {
-    if (!kAll && threadIdx.x >= R * 4) return;
+    if (!kAll && threadIdx.x % NT >= R * 4) return;
 #pragma unroll
     for (int c = 0; c < C; c++) {
       int row, kc;
@@ -756,7 +802,7 @@ struct Parts {
 // The same product for binary32: one LDS buffer, registers one tile ahead; the
 // other workgroups of the CU multiply while this one writes.
 template <bool kXRows, bool kWRows, class Shape, bool kGated>
-__global__ __launch_bounds__(Shape::kThreads) void k_gemm32(GemmArgs a) {
+__global__ __launch_bounds__(Shape::kAllThreads) void k_gemm32(GemmArgs a) {
   constexpr int TM = Shape::TM, NT = Shape::kThreads, BK = 32;
   constexpr int P = kGated ? 2 : 1;
   constexpr int TN = Shape::TN / P;
@@ -764,11 +810,13 @@ __global__ __launch_bounds__(Shape::kThreads) void k_gemm32(GemmArgs a) {
   typedef Parts<kXRows, TM, NT, FX, false> X;
   typedef Parts<kWRows, TN, NT, FW, true> W;
   constexpr int kBuf = X::kBytes + P * W::kBytes;
-  __shared__ __attribute__((aligned(1024))) char smem[kBuf];
-  lds_char* lds = (lds_char*)smem;
+  constexpr int G = Shape::kGroups;
+  __shared__ __attribute__((aligned(1024))) char smem[G * kBuf];
+  const int group = __builtin_amdgcn_readfirstlane(threadIdx.x / NT);
+  lds_char* lds = (lds_char*)smem + group * kBuf;
   const Place at = place<TM, TN>(a, BK);
   const int m0 = at.m0, n0 = at.n0, b = at.b, ktiles = at.ktiles, t0 = at.t0, t1 = at.t1;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x % NT >> 6);
   const int wm = wave / Shape::WN, wn = wave % Shape::WN;
 
   f32x4 acc[1][P][FX][FW];
@@ -795,13 +843,18 @@ __global__ __launch_bounds__(Shape::kThreads) void k_gemm32(GemmArgs a) {
       wr[p].fetch(w0 + (second || p ? wnext : 0) + (wfirst + kt * wstep) * 4, a.wld, a.N - n0, krem);
   };
   const uint32_t xbase = X::frag_at(wm * 16 * FX), wbase = W::frag_at(wn * 16 * FW);
-  fetch(t0);
-  for (int t = t0; t < t1; t++) {
+  // group g takes the tiles t0 + g, t0 + g + G, ...; the second half of the
+  // groups runs half a round behind, cutting while the first half multiplies
+  const int rounds = (t1 - t0 + G - 1) / G;
+  const bool late = group >= (G + 1) / 2;
+  fetch(t0 + group);
+  if (late) __syncthreads();
+  for (int r = 0; r < rounds; r++) {
     __syncthreads();  // everyone is done with the tile before
     xr.write(lds);
 #pragma unroll
     for (int p = 0; p < P; p++) wr[p].write(lds + X::kBytes + p * W::kBytes);
-    fetch(t + 1);
+    fetch(t0 + group + (r + 1) * G);
     __syncthreads();
     Frag<F32> wf[P][FW];
 #pragma unroll
@@ -820,30 +873,10 @@ __global__ __launch_bounds__(Shape::kThreads) void k_gemm32(GemmArgs a) {
           for (int j = 0; j < FW; j++) acc[0][p][f][j] = mma_part(s, wf[p][j], xf, acc[0][p][f][j]);
     }
   }
-  store_results<F32, kXRows, kWRows, kGated, Shape, 1, P, true, kBuf>(a, acc, lds, m0, n0, b, at.split, ktiles, t0, t1,
-                                                                    BK);
-}
-
-template <class E, bool kXRows, bool kWRows, class Shape, bool kGated>
-hipError_t launch_one(const GemmArgs& a, hipStream_t s) {
-  const int tn_cols = Shape::TN / (kGated ? 2 : 1);
-  const int64_t tiles = ((int64_t)a.M + Shape::TM - 1) / Shape::TM * (((int64_t)a.N + tn_cols - 1) / tn_cols);
-  const int64_t grid = tiles * a.batch * a.splits;
-  if (grid <= 0) return hipSuccess;
-  if (grid > 0x7fffffff) return hipErrorInvalidValue;
-  if constexpr (E::kind == 0)
-    k_gemm32<kXRows, kWRows, Shape, kGated><<<dim3((uint32_t)grid), dim3(Shape::kThreads), 0, s>>>(a);
-  else
-    k_gemm<E, kXRows, kWRows, Shape, kGated><<<dim3((uint32_t)grid), dim3(Shape::kThreads), 0, s>>>(a);
-  return hipGetLastError();
-}
-
-template <class E, bool kXRows, bool kWRows, bool kGated>
-hipError_t launch_shape(const GemmPlan& p, const GemmArgs& a, hipStream_t s) {
-  if constexpr (E::kind != 0)
-    if (p.tile == kTile256) return launch_one<E, kXRows, kWRows, Shape256, kGated>(a, s);
-  if (p.tile == kTile128) return launch_one<E, kXRows, kWRows, Shape128, kGated>(a, s);
-  return launch_one<E, kXRows, kWRows, Shape64, kGated>(a, s);
+  if (G > 1 && !late) __syncthreads();
+  if (!join_groups<Shape, G * kBuf>(acc, (lds_char*)smem)) return;
+  store_results<F32, kXRows, kWRows, kGated, Shape, 1, P, true, G * kBuf>(a, acc, (lds_char*)smem, m0, n0, b, at.split,
+                                                                        ktiles, t0, t1, BK);
 }
 
 }  // namespace llar_ffn
