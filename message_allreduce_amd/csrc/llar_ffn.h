@@ -33,7 +33,6 @@ struct GemmArgs {
   int segs, batch, splits;
   int act;
   int npad;             // row length of a partial plane
-  int vec_out;          // every output row piece of 8 elements may be accessed as one vector
 };
 
 // Tile shapes of the product kernel (rows of x by rows of w by workgroup);
@@ -80,7 +79,6 @@ struct GateGradArgs {
   int64_t dhld, gld, uld, dld;
   int M, N;
   int act;
-  int vec;
 };
 hipError_t launch_gate_grad(int kind, const GateGradArgs& a, hipStream_t s);
 
@@ -96,7 +94,6 @@ struct ActGradArgs {
   int M, N;
   int act;
   int chunks;
-  int vec;
 };
 hipError_t launch_act_grad(int kind, const ActGradArgs& a, hipStream_t s);
 

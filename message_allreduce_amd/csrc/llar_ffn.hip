@@ -78,7 +78,6 @@ bool chunks_whole(const Operand& o, int es) {
   if (!o.padded && (o.by_rows ? o.rows : o.k) % ce) return false;
   return o.ld * es < (1ll << 31) / 256;
 }
-bool vec8(const void* p, int64_t ld, int es) { return !p || (((uintptr_t)p & 15) == 0 && ld * es % 16 == 0); }
 
 // How a product runs: the kernel for few rows, or tiles; and its split over k.
 struct Shape {
@@ -241,17 +240,14 @@ int run_product(const Product& p, int dtype, const Carve& space, hipStream_t s) 
   a.N = (int)p.N();
   a.K = (int)p.x[0].k;
   if (a.M == 0 || a.N == 0) return LLAR_OK;
-  bool vec_out = true;
   for (int i = 0; i < 2; i++) {
     a.x[i] = p.x[std::min(i, p.n_x - 1)].p;
     a.w[i] = p.w[std::min(i, p.n_w - 1)].p;
     a.out[i] = p.out[i];
     a.z[i] = p.z[i];
-    vec_out = vec_out && vec8(p.out[i], p.outld, es) && vec8(p.z[i], p.zld, es);
   }
   a.bias = p.bias;
   a.resid = p.resid;
-  a.vec_out = vec_out && vec8(p.resid, p.rld, es) && vec8(p.bias, 0, es);
   a.xld = p.x[0].ld;
   a.wld = p.w[0].ld;
   a.outld = p.outld;
@@ -294,12 +290,15 @@ int pack_and_run(Product& p, int dtype, void* space, size_t bytes, hipStream_t s
 
 bool dtype_ok(int t) { return t == LLAR_FP32 || t == LLAR_FP16 || t == LLAR_BF16; }
 bool act_ok(int a) { return a >= LLAR_ACT_NONE && a <= LLAR_ACT_SILU; }
-int row_chunks(int64_t M, int64_t N) {
-  // about 1024 workgroups of 256 columns, at least 32 rows each
+// Row chunks of the activation's gradient, of which each needs 32 rows at a
+// time: about 512 workgroups of 256 columns.  Up to 512 rows with a bias
+// gradient one chunk does without a second launch (333 x 1480 fp16: 26 us with
+// it, of which the two launches are 8); without one nothing is added up.
+int row_chunks(int64_t M, int64_t N, bool sums) {
+  if (sums && M <= 512) return 1;
   const int64_t cols = std::max<int64_t>(cdiv(N, 256), 1);
-  return (int)std::max<int64_t>(1, std::min(cdiv(1024, cols), M / 32));
+  return (int)std::max<int64_t>(1, std::min(cdiv(512, cols), M / 32));
 }
-
 bool space_ok(void* w, size_t n) { return n == 0 || (w && ((uintptr_t)w & 255) == 0); }
 
 // Whether the workspace holds what a call on these inputs needs.
@@ -336,7 +335,7 @@ size_t llar_ffn_workspace(llar_ffn_op op, int64_t m, int64_t n, int64_t k, llar_
     case LLAR_OP_LINEAR: return x + w + product_space(m, n, k, 1, 1, false, es, xr, wr);
     case LLAR_OP_GATED_FFN: return x + 2 * w + product_space(m, n, k, 1, 1, true, es, xr, wr);
     case LLAR_OP_LINEAR_BACKWARD:
-      return x + w + (copies ? copy_bytes(m, n, es) : dz) + align256((size_t)row_chunks(m, n) * n * 4) +
+      return x + w + (copies ? copy_bytes(m, n, es) : dz) + align256((size_t)row_chunks(m, n, true) * n * 4) +
              std::max(product_space(m, k, n, 1, 1, false, es, yr, !wr),
                       product_space(n, k, m, 1, 1, false, es, !yr, !xr));
     case LLAR_OP_GATED_FFN_BACKWARD:
@@ -419,14 +418,12 @@ int llar_linear_backward(const llar_matrix* dy, const llar_matrix* x, const llar
     a.act = act;
     a.dy = dy->data;
     a.dyld = row_ld(dy);
-    a.chunks = row_chunks(M, N);
-    bool vec = vec8(dy->data, a.dyld, es);
+    a.chunks = row_chunks(M, N, db != nullptr);
     if (with_act) {
       a.z = pre->data;
       a.zld = row_ld(pre);
       a.dzld = cdiv(N, 8) * 8;
       a.dz = c.take((size_t)M * a.dzld * es);
-      vec = vec && vec8(a.z, a.zld, es);
       dz.p = a.dz;
       dz.ld = a.dzld;
       dz.padded = true;
@@ -435,7 +432,6 @@ int llar_linear_backward(const llar_matrix* dy, const llar_matrix* x, const llar
       a.db = db;
       a.part = (float*)c.take((size_t)a.chunks * N * 4);
     }
-    a.vec = vec;
     if (!c.ok) return llar::fail(LLAR_ERR_ARG);
     if (launch_act_grad(dtype, a, (hipStream_t)stream) != hipSuccess) return llar::fail(LLAR_ERR_HIP);
   }
@@ -548,7 +544,6 @@ int llar_gated_ffn_backward(const llar_matrix* dh, const llar_matrix* x, const l
   a.dld = cdiv(N, 8) * 8;
   a.dg = c.take((size_t)M * a.dld * es);
   a.du = c.take((size_t)M * a.dld * es);
-  a.vec = vec8(a.dh, a.dhld, es) && vec8(a.g, a.gld, es) && vec8(a.u, a.uld, es);
   if (!c.ok) return llar::fail(LLAR_ERR_ARG);
   if (launch_gate_grad(dtype, a, (hipStream_t)stream) != hipSuccess) return llar::fail(LLAR_ERR_HIP);
   Operand dg, du;

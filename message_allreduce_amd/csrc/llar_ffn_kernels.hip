@@ -125,23 +125,22 @@ __global__ __launch_bounds__(256) void k_gate_grad(GateGradArgs a) {
   const int col = (int)(id - m * groups) * 8;
   if (m >= a.M) return;
   const int cnt = a.N - col;
-  const bool vec = a.vec != 0;
-  const Vals<E, 8> dh = load_vals<E, 8>((const T*)a.dh + m * a.dhld + col, cnt, vec);
-  const Vals<E, 8> g = load_vals<E, 8>((const T*)a.g + m * a.gld + col, cnt, vec);
-  const Vals<E, 8> u = load_vals<E, 8>((const T*)a.u + m * a.uld + col, cnt, vec);
+  const Vals<E, 8> dh = load_vals<E, 8>((const T*)a.dh + m * a.dhld + col, cnt);
+  const Vals<E, 8> g = load_vals<E, 8>((const T*)a.g + m * a.gld + col, cnt);
+  const Vals<E, 8> u = load_vals<E, 8>((const T*)a.u + m * a.uld + col, cnt);
   float dg[8], du[8];
   with_act(a.act, [&](auto c) {
 #pragma unroll
     for (int i = 0; i < 8; i++) {
       float value, slope;
-      act_two<decltype(c)::value>(g.v[i], value, slope);
+      act_two<decltype(c)::value, E>(g.v[i], value, slope);
       dg[i] = dh.v[i] * u.v[i] * slope;
       du[i] = dh.v[i] * value;
     }
   });
   // what is loaded beyond column N is 0, and so is its gradient
-  store_vals<E, 8>((T*)a.dg + m * a.dld + col, dg, 8, true);
-  store_vals<E, 8>((T*)a.du + m * a.dld + col, du, 8, true);
+  store_vals<E, 8>((T*)a.dg + m * a.dld + col, dg, 8);
+  store_vals<E, 8>((T*)a.du + m * a.dld + col, du, 8);
 }
 
 hipError_t launch_gate_grad(int kind, const GateGradArgs& a, hipStream_t s) {
@@ -158,33 +157,36 @@ hipError_t launch_gate_grad(int kind, const GateGradArgs& a, hipStream_t s) {
 }
 
 // ---- dz = dy act'(z), and column sums of dz ----------------------------------------
-// A workgroup takes 256 columns of one row chunk: 32 lanes of 8 columns by 8
-// rows at a time; its sums go to part[chunk], and a second kernel adds the
-// chunks in order, so the bias gradient does not depend on timing.
+// A workgroup takes 256 columns of one row chunk: 32 lanes of 8 columns by 32
+// rows at a time.  One chunk: its sums are the bias gradient.  More: they go to
+// part[chunk], and a second kernel adds the chunks in order, so the result does
+// not depend on timing.  Bound by memory: 4096 x 8192 bf16 with the erf form of
+// GELU reads and writes 201 MB.
+constexpr int kSumRows = 32;
 template <class E>
-__global__ __launch_bounds__(256) void k_act_grad(ActGradArgs a) {
+__global__ __launch_bounds__(32 * kSumRows) void k_act_grad(ActGradArgs a) {
   typedef typename E::T T;
-  __shared__ float sums[8][256];
+  __shared__ float sums[kSumRows][256];
   const int lane = threadIdx.x & 31, r = threadIdx.x >> 5;
   const int col = (blockIdx.x * 32 + lane) * 8;
   const int cnt = a.N - col;
-  const bool vec = a.vec != 0;
   const int64_t m0 = (int64_t)a.M * blockIdx.y / a.chunks, m1 = (int64_t)a.M * (blockIdx.y + 1) / a.chunks;
   float acc[8] = {};
   if (cnt > 0) {
-    for (int64_t m = m0 + r; m < m1; m += 8) {
-      Vals<E, 8> d = load_vals<E, 8>((const T*)a.dy + m * a.dyld + col, cnt, vec);
+#pragma unroll 2
+    for (int64_t m = m0 + r; m < m1; m += kSumRows) {
+      Vals<E, 8> d = load_vals<E, 8>((const T*)a.dy + m * a.dyld + col, cnt);
       if (a.z) {
-        const Vals<E, 8> z = load_vals<E, 8>((const T*)a.z + m * a.zld + col, cnt, vec);
+        const Vals<E, 8> z = load_vals<E, 8>((const T*)a.z + m * a.zld + col, cnt);
         with_act(a.act, [&](auto c) {
 #pragma unroll
           for (int i = 0; i < 8; i++) {
             float value, slope;
-            act_two<decltype(c)::value>(z.v[i], value, slope);
+            act_two<decltype(c)::value, E>(z.v[i], value, slope);
             d.v[i] *= slope;
           }
         });
-        store_vals<E, 8>((T*)a.dz + m * a.dzld + col, d.v, 8, true);  // zeros beyond column N
+        store_vals<E, 8>((T*)a.dz + m * a.dzld + col, d.v, 8);  // zeros beyond column N
       }
 #pragma unroll
       for (int i = 0; i < 8; i++) acc[i] += d.v[i];
@@ -195,10 +197,14 @@ __global__ __launch_bounds__(256) void k_act_grad(ActGradArgs a) {
   for (int i = 0; i < 8; i++) sums[r][lane * 8 + i] = acc[i];
   __syncthreads();
   const int c = blockIdx.x * 256 + threadIdx.x;
+  if (threadIdx.x >= 256 || c >= a.N) return;
   float s = 0.f;
 #pragma unroll
-  for (int i = 0; i < 8; i++) s += sums[i][threadIdx.x];
-  if (c < a.N) a.part[(int64_t)blockIdx.y * a.N + c] = s;
+  for (int i = 0; i < kSumRows; i++) s += sums[i][threadIdx.x];
+  if (a.chunks == 1)
+    ((T*)a.db)[c] = E::from(s);
+  else
+    a.part[(int64_t)blockIdx.y * a.N + c] = s;
 }
 
 template <class E>
@@ -206,6 +212,7 @@ __global__ __launch_bounds__(256) void k_bias_grad(ActGradArgs a) {
   const int c = blockIdx.x * 256 + threadIdx.x;
   if (c >= a.N) return;
   float s = 0.f;
+#pragma unroll 8
   for (int i = 0; i < a.chunks; i++) s += a.part[(int64_t)i * a.N + c];
   ((typename E::T*)a.db)[c] = E::from(s);
 }
@@ -214,9 +221,9 @@ template <class E>
 hipError_t act_grad(const ActGradArgs& a, hipStream_t s) {
   if (a.N == 0) return hipSuccess;
   const uint32_t cols = (uint32_t)((a.N + 255) / 256);
-  k_act_grad<E><<<dim3(cols, (uint32_t)a.chunks), dim3(256), 0, s>>>(a);
+  k_act_grad<E><<<dim3(cols, (uint32_t)a.chunks), dim3(32 * kSumRows), 0, s>>>(a);
   hipError_t e = hipGetLastError();
-  if (e != hipSuccess || !a.db) return e;
+  if (e != hipSuccess || !a.db || a.chunks == 1) return e;
   k_bias_grad<E><<<dim3(cols), dim3(256), 0, s>>>(a);
   return hipGetLastError();
 }

@@ -38,20 +38,25 @@ struct BF16 {
   static __device__ __forceinline__ __bf16 from(float v) { return (__bf16)v; }
 };
 
-// n values held in registers moved to or from memory: one wide access where
-// the caller says the address allows it, else element by element up to `cnt`.
+// n neighbouring values moved to or from memory: one access at the element's
+// alignment (which the memory pipeline takes for any width), or at a row's end
+// the `cnt` that exist one by one.
 template <class E, int n>
 struct Vals {
   float v[n];
 };
 
 template <class E, int n>
-__device__ __forceinline__ Vals<E, n> load_vals(const typename E::T* p, int cnt, bool vec) {
-  typedef typename E::T T;
-  typedef T Vec __attribute__((ext_vector_type(n)));
+struct Wide {
+  typedef typename E::T vec __attribute__((ext_vector_type(n)));
+  typedef vec loose __attribute__((aligned(2)));
+};
+
+template <class E, int n>
+__device__ __forceinline__ Vals<E, n> load_vals(const typename E::T* p, int cnt) {
   Vals<E, n> r;
-  if (vec && cnt >= n) {
-    Vec q = *(const Vec*)p;
+  if (cnt >= n) {
+    const typename Wide<E, n>::vec q = *(const typename Wide<E, n>::loose*)p;
 #pragma unroll
     for (int i = 0; i < n; i++) r.v[i] = E::to(q[i]);
   } else {
@@ -62,14 +67,12 @@ __device__ __forceinline__ Vals<E, n> load_vals(const typename E::T* p, int cnt,
 }
 
 template <class E, int n>
-__device__ __forceinline__ void store_vals(typename E::T* p, const float* v, int cnt, bool vec) {
-  typedef typename E::T T;
-  typedef T Vec __attribute__((ext_vector_type(n)));
-  if (vec && cnt >= n) {
-    Vec q;
+__device__ __forceinline__ void store_vals(typename E::T* p, const float* v, int cnt) {
+  if (cnt >= n) {
+    typename Wide<E, n>::vec q;
 #pragma unroll
     for (int i = 0; i < n; i++) q[i] = E::from(v[i]);
-    *(Vec*)p = q;
+    *(typename Wide<E, n>::loose*)p = q;
   } else {
 #pragma unroll
     for (int i = 0; i < n; i++)
@@ -77,30 +80,72 @@ __device__ __forceinline__ void store_vals(typename E::T* p, const float* v, int
   }
 }
 
-// tanh(t) = 2 s(2t) - 1, so the tanh form of GELU is z s(2 w) with
-// w = sqrt(2/pi) (z + 0.044715 z^3): no cancellation for negative z.
-__device__ __forceinline__ float sigmoid(float t) { return 1.f / (1.f + expf(-t)); }
+// ---- activations ---------------------------------------------------------------------
+// For 16-bit results the hardware's exponential and reciprocal do (off by 2^-20
+// at most where the result counts); binary32 takes the library's.
+template <class E>
+__device__ __forceinline__ float exp_of(float x) {
+  if constexpr (E::kind == 0) return expf(x);
+  return __builtin_amdgcn_exp2f(x * 1.44269504f);
+}
+template <class E>
+__device__ __forceinline__ float inverse(float x) {
+  if constexpr (E::kind == 0) return 1.f / x;
+  return __builtin_amdgcn_rcpf(x);
+}
+template <class E>
+__device__ __forceinline__ float sigmoid(float t) {
+  return inverse<E>(1.f + exp_of<E>(-t));
+}
 
 constexpr float kSqrt2OverPi = 0.7978845608028654f;
 constexpr float kGeluCubic = 0.044715f;
-constexpr float kSqrtHalf = 0.7071067811865476f;
 constexpr float kInvSqrt2Pi = 0.3989422804014327f;
 
 // z s for a factor s that reaches 0 at z = -inf faster than z grows: the limit
 // there is 0, where the plain product would be a NaN.
 __device__ __forceinline__ float fading(float z, float s) { return s == 0.f ? 0.f : z * s; }
 
-template <int act>
+// Phi(z) and e = exp(-z^2 / 2), which the density shares.  For t = |z|,
+// Phi(-t) exp(t^2 / 2) is a smooth function of s = 1 / (1 + 0.36 t): a minimax
+// polynomial of degree 9 in s (fitted for this file over t = 0 .. 40) is within
+// 9e-8 of it, relatively, so the tail keeps its digits.
+template <class E>
+__device__ __forceinline__ float normal(float z, float& e) {
+  const float zz = z * z;
+  const float rest = zz < 1e4f ? fmaf(z, z, -zz) : 0.f;  // what the square's rounding lost
+  e = exp_of<E>(-0.5f * zz);
+  e = fmaf(-0.5f * rest, e, e);
+  const float s = inverse<E>(fmaf(0.36f, fabsf(z), 1.f));
+  float p = -0.0302381665f;
+  p = fmaf(p, s, 0.139508024f);
+  p = fmaf(p, s, -0.223599017f);
+  p = fmaf(p, s, 0.107368767f);
+  p = fmaf(p, s, -0.000386219239f);
+  p = fmaf(p, s, 0.0960373282f);
+  p = fmaf(p, s, 0.124009758f);
+  p = fmaf(p, s, 0.143681884f);
+  p = fmaf(p, s, 0.14361766f);
+  const float tail = e * (p * s);
+  return z > 0.f ? 1.f - tail : tail;
+}
+
+// tanh(t) = 2 s(2t) - 1, so the tanh form of GELU is z s(2 w) with
+// w = sqrt(2/pi) (z + 0.044715 z^3): no cancellation for negative z.
+template <int act, class E>
 __device__ __forceinline__ float act_one(float z) {
   if constexpr (act == kActRelu) return z < 0.f ? 0.f : z;  // keeps a NaN
-  if constexpr (act == kActGelu) return fading(z, 0.5f * erfcf(-z * kSqrtHalf));
-  if constexpr (act == kActGeluTanh) return fading(z, sigmoid(2.f * kSqrt2OverPi * (z + kGeluCubic * z * z * z)));
-  if constexpr (act == kActSilu) return fading(z, sigmoid(z));
+  if constexpr (act == kActGelu) {
+    float e;
+    return fading(z, normal<E>(z, e));
+  }
+  if constexpr (act == kActGeluTanh) return fading(z, sigmoid<E>(2.f * kSqrt2OverPi * (z + kGeluCubic * z * z * z)));
+  if constexpr (act == kActSilu) return fading(z, sigmoid<E>(z));
   return z;
 }
 
 // The value and the derivative together: they share the exponential.
-template <int act>
+template <int act, class E>
 __device__ __forceinline__ void act_two(float z, float& value, float& slope) {
   value = z;
   slope = 1.f;
@@ -108,17 +153,18 @@ __device__ __forceinline__ void act_two(float z, float& value, float& slope) {
     value = z < 0.f ? 0.f : z;
     slope = z > 0.f ? 1.f : (z <= 0.f ? 0.f : z);
   } else if constexpr (act == kActGelu) {
-    const float p = 0.5f * erfcf(-z * kSqrtHalf);
+    float e;
+    const float p = normal<E>(z, e);
     value = fading(z, p);
-    slope = p + fading(z, kInvSqrt2Pi * expf(-0.5f * z * z));
+    slope = p + fading(z, kInvSqrt2Pi * e);
   } else if constexpr (act == kActGeluTanh) {
-    const float s = sigmoid(2.f * kSqrt2OverPi * (z + kGeluCubic * z * z * z));
+    const float s = sigmoid<E>(2.f * kSqrt2OverPi * (z + kGeluCubic * z * z * z));
     value = fading(z, s);
     // s (1 - s) is 0 long before the square would overflow
     const float d = s * (1.f - s);
     slope = d == 0.f ? s : s + z * d * 2.f * kSqrt2OverPi * (1.f + 3.f * kGeluCubic * z * z);
   } else if constexpr (act == kActSilu) {
-    const float s = sigmoid(z);
+    const float s = sigmoid<E>(z);
     value = fading(z, s);
     slope = s + fading(z, s * (1.f - s));
   }
@@ -135,11 +181,11 @@ __device__ __forceinline__ void with_act(int act, F f) {
     default: return f(std::integral_constant<int, kActNone>());
   }
 }
-template <int n>
+template <class E, int n>
 __device__ __forceinline__ void act_values(float (&y)[n], int act) {
   with_act(act, [&](auto c) {
 #pragma unroll
-    for (int i = 0; i < n; i++) y[i] = act_one<decltype(c)::value>(y[i]);
+    for (int i = 0; i < n; i++) y[i] = act_one<decltype(c)::value, E>(y[i]);
   });
 }
 

@@ -228,40 +228,40 @@ __device__ __forceinline__ Frag<E> read_frag(lds_char* lds, uint32_t base, int f
 
 // Applies the epilogue to n neighbours of one output row and stores them.
 // acc0: the sums (gated: of the first projection), acc1: of the second.
-template <class E, bool kGated, int n>
-__device__ __forceinline__ void finish(const GemmArgs& a, int b, int m, int col, const float* acc0,
-                                       const float* acc1) {
+// kResid: the caller has loaded the residual's piece (if there is a residual).
+template <class E, bool kGated, int n, bool kResid = false>
+__device__ __forceinline__ void finish(const GemmArgs& a, int b, int m, int col, const float* acc0, const float* acc1,
+                                       Vals<E, n> resid = {}) {
   typedef typename E::T T;
   const int cnt = a.N - col;
-  const bool vec = a.vec_out != 0;
   float y[n];
   if constexpr (kGated) {
     if (a.z[0]) {
-      store_vals<E, n>((T*)a.z[0] + m * a.zld + col, acc0, cnt, vec);
-      store_vals<E, n>((T*)a.z[1] + m * a.zld + col, acc1, cnt, vec);
+      store_vals<E, n>((T*)a.z[0] + m * a.zld + col, acc0, cnt);
+      store_vals<E, n>((T*)a.z[1] + m * a.zld + col, acc1, cnt);
     }
 #pragma unroll
     for (int i = 0; i < n; i++) y[i] = acc0[i];
-    act_values<n>(y, a.act);
+    act_values<E, n>(y, a.act);
 #pragma unroll
     for (int i = 0; i < n; i++) y[i] *= acc1[i];
   } else {
 #pragma unroll
     for (int i = 0; i < n; i++) y[i] = acc0[i];
     if (a.bias) {
-      const Vals<E, n> v = load_vals<E, n>((const T*)a.bias + col, cnt, vec);
+      const Vals<E, n> v = load_vals<E, n>((const T*)a.bias + col, cnt);
 #pragma unroll
       for (int i = 0; i < n; i++) y[i] += v.v[i];
     }
-    if (a.z[0]) store_vals<E, n>((T*)a.z[0] + m * a.zld + col, y, cnt, vec);
-    act_values<n>(y, a.act);
+    if (a.z[0]) store_vals<E, n>((T*)a.z[0] + m * a.zld + col, y, cnt);
+    act_values<E, n>(y, a.act);
     if (a.resid) {
-      const Vals<E, n> v = load_vals<E, n>((const T*)a.resid + m * a.rld + col, cnt, vec);
+      if constexpr (!kResid) resid = load_vals<E, n>((const T*)a.resid + m * a.rld + col, cnt);
 #pragma unroll
-      for (int i = 0; i < n; i++) y[i] += v.v[i];
+      for (int i = 0; i < n; i++) y[i] += resid.v[i];
     }
   }
-  store_vals<E, n>((T*)a.out[b] + m * a.outld + col, y, cnt, vec);
+  store_vals<E, n>((T*)a.out[b] + m * a.outld + col, y, cnt);
 }
 
 // The product of parts turns an infinity into a NaN (infinity times a zero
@@ -299,7 +299,7 @@ __device__ __forceinline__ void store_results(const GemmArgs& a, f32x4 (&acc)[kX
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / Shape::WN, wn = wave % Shape::WN;
   const int mwave = m0 + wm * 16 * FX, nwave = n0 + wn * 16 * FW;
-  bool bare = !kGated && (a.splits > 1 || (a.vec_out && !a.bias && !a.resid && !a.z[0] && a.act == kActNone));
+  bool bare = !kGated && (a.splits > 1 || (!a.bias && !a.resid && !a.z[0] && a.act == kActNone));
   bool nan = false;
   if constexpr (E::kind == 0) {
 #pragma unroll
@@ -339,7 +339,7 @@ __device__ __forceinline__ void store_results(const GemmArgs& a, f32x4 (&acc)[kX
                 float v[kRunLen];
 #pragma unroll
                 for (int i = 0; i < kRunLen; i++) v[i] = acc[h][p][f][j + i / 4][i % 4];
-                store_vals<E, kRunLen>((T*)a.out[b] + m * a.outld + col, v, a.N - col, true);
+                store_vals<E, kRunLen>((T*)a.out[b] + m * a.outld + col, v, a.N - col);
               }
             }
           }
@@ -389,11 +389,40 @@ __device__ __forceinline__ void store_results(const GemmArgs& a, f32x4 (&acc)[kX
       }
     }
     // gated: a lane takes the same 8 columns of both parts
-    constexpr int kRuns = 2 * FW * (kGated ? 1 : kWParts);
+    constexpr int kRuns = 2 * FW * (kGated ? 1 : kWParts), kPieces = kRows * kRuns;
+    // The residual comes from memory: three pieces ahead of their use, or a
+    // tile pays that latency for each (8192 x 8192 x 3584 bf16: 60 us in all).
+    typedef typename Wide<E, 8>::vec piece;
+    const bool queue = !kGated && kPieces > 64 && a.resid && a.splits == 1 && n0 + Shape::TN / P <= a.N;
+    auto where = [&](int i, int& m, int& col) {
+      const int c = i % kRuns;
+      m = mhalf + i / kRuns;
+      col = nwave + c / (2 * FW) * kWStep + 8 * (c % (2 * FW));
+    };
+    auto peek = [&](int i) {
+      int m, col;
+      where(i, m, col);
+      piece v = {};
+      if (i < kPieces && m < a.M) v = *(const typename Wide<E, 8>::loose*)((const T*)a.resid + m * a.rld + col);
+      return v;
+    };
+    piece q0 = {}, q1 = {}, q2 = {};
+    if (queue) {
+      q0 = peek(lane);
+      q1 = peek(lane + 64);
+      q2 = peek(lane + 128);
+    }
 #pragma clang loop unroll(disable)
-    for (int i = lane; i < kRows * kRuns; i += 64) {
+    for (int i = lane; i < kPieces; i += 64) {
       const int row = i / kRuns, c = i % kRuns;
-      const int m = mhalf + row, col = nwave + c / (2 * FW) * kWStep + 8 * (c % (2 * FW));
+      int m, col;
+      where(i, m, col);
+      const piece now = q0;
+      if (queue) {
+        q0 = q1;
+        q1 = q2;
+        q2 = peek(i + 192);
+      }
       if (m >= a.M || col >= a.N) continue;
       float v[P][8];
 #pragma unroll
@@ -413,7 +442,12 @@ __device__ __forceinline__ void store_results(const GemmArgs& a, f32x4 (&acc)[kX
           *(f32x4*)(d + 4) = f32x4{v[p][4], v[p][5], v[p][6], v[p][7]};
         }
       } else {
-        finish<E, kGated, 8>(a, b, m, col, v[0], v[P - 1]);
+        Vals<E, 8> r;
+#pragma unroll
+        for (int e = 0; e < 8; e++) r.v[e] = E::to(now[e]);
+        if (!kGated && a.resid && !queue)
+          r = load_vals<E, 8>((const T*)a.resid + m * a.rld + col, a.N - col);
+        finish<E, kGated, 8, true>(a, b, m, col, v[0], v[P - 1], r);
       }
     }
     settle();
