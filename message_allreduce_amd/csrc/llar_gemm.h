@@ -228,10 +228,9 @@ __device__ __forceinline__ Frag<E> read_frag(lds_char* lds, uint32_t base, int f
 
 // Applies the epilogue to n neighbours of one output row and stores them.
 // acc0: the sums (gated: of the first projection), acc1: of the second.
-// kResid: the caller has loaded the residual's piece (if there is a residual).
-template <class E, bool kGated, int n, bool kResid = false>
-__device__ __forceinline__ void finish(const GemmArgs& a, int b, int m, int col, const float* acc0, const float* acc1,
-                                       Vals<E, n> resid = {}) {
+template <class E, bool kGated, int n>
+__device__ __forceinline__ void finish(const GemmArgs& a, int b, int m, int col, const float* acc0,
+                                       const float* acc1) {
   typedef typename E::T T;
   const int cnt = a.N - col;
   float y[n];
@@ -256,9 +255,9 @@ __device__ __forceinline__ void finish(const GemmArgs& a, int b, int m, int col,
     if (a.z[0]) store_vals<E, n>((T*)a.z[0] + m * a.zld + col, y, cnt);
     act_values<E, n>(y, a.act);
     if (a.resid) {
-      if constexpr (!kResid) resid = load_vals<E, n>((const T*)a.resid + m * a.rld + col, cnt);
+      const Vals<E, n> v = load_vals<E, n>((const T*)a.resid + m * a.rld + col, cnt);
 #pragma unroll
-      for (int i = 0; i < n; i++) y[i] += resid.v[i];
+      for (int i = 0; i < n; i++) y[i] += v.v[i];
     }
   }
   store_vals<E, n>((T*)a.out[b] + m * a.outld + col, y, cnt);
@@ -280,10 +279,17 @@ __device__ __forceinline__ float sum_again(const GemmArgs& a, int b, int p, int 
   return s;
 }
 
+// Whether the residual can be in a sum from its start.
+__device__ __forceinline__ bool starts_with_resid(const GemmArgs& a) {
+  return a.resid && a.splits == 1 && !a.z[0] && a.act == kActNone;
+}
+
 // ---- results -------------------------------------------------------------------------
 // The tile (m0, n0) of plane b: acc[part of x][part of w][fragment of x][of w].
+// kSumsHaveBias: they began with the bias, and with the residual where nothing
+// comes between (starts_with_resid).
 template <class E, bool kXRows, bool kWRows, bool kGated, class Shape, int kXParts, int kWParts, bool kSpread, int kLds,
-          int FX, int FW>
+          bool kSumsHaveBias, int FX, int FW>
 __device__ __forceinline__ void store_results(const GemmArgs& a, f32x4 (&acc)[kXParts][kWParts][FX][FW], lds_char* lds,
                                               int m0, int n0, int b, int split, int ktiles, int t0, int t1, int bk) {
   // of fragments (f, j) lane l holds row l % 16 and 4 neighbouring
@@ -299,7 +305,8 @@ __device__ __forceinline__ void store_results(const GemmArgs& a, f32x4 (&acc)[kX
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / Shape::WN, wn = wave % Shape::WN;
   const int mwave = m0 + wm * 16 * FX, nwave = n0 + wn * 16 * FW;
-  bool bare = !kGated && (a.splits > 1 || (!a.bias && !a.resid && !a.z[0] && a.act == kActNone));
+  bool bare = !kGated && (a.splits > 1 || (!a.z[0] && a.act == kActNone &&
+                                           (kSumsHaveBias || (!a.bias && !a.resid))));
   bool nan = false;
   if constexpr (E::kind == 0) {
 #pragma unroll
@@ -388,67 +395,99 @@ __device__ __forceinline__ void store_results(const GemmArgs& a, f32x4 (&acc)[kX
         settle();
       }
     }
-    // gated: a lane takes the same 8 columns of both parts
-    constexpr int kRuns = 2 * FW * (kGated ? 1 : kWParts), kPieces = kRows * kRuns;
-    // The residual comes from memory: three pieces ahead of their use, or a
-    // tile pays that latency for each (8192 x 8192 x 3584 bf16: 60 us in all).
+    // A lane takes the same 8 columns of every row it comes to (gated: of both
+    // projections), two rows at a time so that their chains overlap.
+    constexpr int kRuns = 2 * FW * (kGated ? 1 : kWParts), kPieces = kRows * kRuns, kStride = 64 / kRuns;
+    constexpr int U = kPieces >= 128 && E::kind != 0 ? 2 : 1;  // binary32: a second workgroup must fit the registers
+    static_assert(64 % kRuns == 0, "whole rows a wave");
+    const int c = lane % kRuns, col = nwave + c / (2 * FW) * kWStep + 8 * (c % (2 * FW));
+    const int cnt = a.N - col;
+    auto row_of = [&](int i) { return lane / kRuns + i * kStride; };
+    // The residual comes from memory: pieces ahead of their use, or a tile pays
+    // that latency for each.
     typedef typename Wide<E, 8>::vec piece;
-    const bool queue = !kGated && kPieces > 64 && a.resid && a.splits == 1 && n0 + Shape::TN / P <= a.N;
-    auto where = [&](int i, int& m, int& col) {
-      const int c = i % kRuns;
-      m = mhalf + i / kRuns;
-      col = nwave + c / (2 * FW) * kWStep + 8 * (c % (2 * FW));
-    };
+    const bool queue = !kGated && a.resid && a.splits == 1 && cnt >= 8;
     auto peek = [&](int i) {
-      int m, col;
-      where(i, m, col);
       piece v = {};
-      if (i < kPieces && m < a.M) v = *(const typename Wide<E, 8>::loose*)((const T*)a.resid + m * a.rld + col);
+      if (queue && row_of(i) < kRows && mhalf + row_of(i) < a.M)
+        v = *(const typename Wide<E, 8>::loose*)((const T*)a.resid + (mhalf + row_of(i)) * a.rld + col);
       return v;
     };
-    piece q0 = {}, q1 = {}, q2 = {};
-    if (queue) {
-      q0 = peek(lane);
-      q1 = peek(lane + 64);
-      q2 = peek(lane + 128);
-    }
+    piece next[U];
+#pragma unroll
+    for (int u = 0; u < U; u++) next[u] = peek(u);
+    Vals<E, 8> bias = {};
+    if (!kSumsHaveBias && !kGated && a.bias && cnt > 0) bias = load_vals<E, 8>((const T*)a.bias + col, cnt);
 #pragma clang loop unroll(disable)
-    for (int i = lane; i < kPieces; i += 64) {
-      const int row = i / kRuns, c = i % kRuns;
-      int m, col;
-      where(i, m, col);
-      const piece now = q0;
-      if (queue) {
-        q0 = q1;
-        q1 = q2;
-        q2 = peek(i + 192);
+    for (int i = 0; i * kStride < kRows; i += U) {
+      piece now[U];
+#pragma unroll
+      for (int u = 0; u < U; u++) {
+        now[u] = next[u];
+        next[u] = peek(i + U + u);
       }
-      if (m >= a.M || col >= a.N) continue;
-      float v[P][8];
+      float v[P][8 * U];
 #pragma unroll
-      for (int p = 0; p < P; p++) {
-        const f32x4 lo = *chunk(row, p * 4 * FW + 2 * c), hi = *chunk(row, p * 4 * FW + 2 * c + 1);
+      for (int u = 0; u < U; u++)
 #pragma unroll
-        for (int e = 0; e < 4; e++) {
-          v[p][e] = lo[e];
-          v[p][4 + e] = hi[e];
+        for (int p = 0; p < P; p++) {
+          const int row = row_of(i + u) % kRows;  // a wave with fewer pieces than lanes comes back to the first
+          const f32x4 lo = *chunk(row, p * 4 * FW + 2 * c), hi = *chunk(row, p * 4 * FW + 2 * c + 1);
+#pragma unroll
+          for (int e = 0; e < 4; e++) {
+            v[p][8 * u + e] = lo[e];
+            v[p][8 * u + 4 + e] = hi[e];
+          }
         }
+      bool live[U];
+      int64_t m[U];
+#pragma unroll
+      for (int u = 0; u < U; u++) {
+        m[u] = mhalf + row_of(i + u);
+        live[u] = row_of(i + u) < kRows && m[u] < a.M && cnt > 0;
       }
       if (a.splits > 1) {
 #pragma unroll
-        for (int p = 0; p < P; p++) {
-          float* d = a.partial + (((int64_t)split * (kGated ? 2 : a.batch) + (kGated ? p : b)) * a.M + m) * a.npad + col;
-          *(f32x4*)d = f32x4{v[p][0], v[p][1], v[p][2], v[p][3]};
-          *(f32x4*)(d + 4) = f32x4{v[p][4], v[p][5], v[p][6], v[p][7]};
-        }
-      } else {
-        Vals<E, 8> r;
+        for (int u = 0; u < U; u++)
 #pragma unroll
-        for (int e = 0; e < 8; e++) r.v[e] = E::to(now[e]);
-        if (!kGated && a.resid && !queue)
-          r = load_vals<E, 8>((const T*)a.resid + m * a.rld + col, a.N - col);
-        finish<E, kGated, 8, true>(a, b, m, col, v[0], v[P - 1], r);
+          for (int p = 0; p < P; p++) {
+            if (!live[u]) continue;
+            float* d = a.partial + (((int64_t)split * (kGated ? 2 : a.batch) + (kGated ? p : b)) * a.M + m[u]) * a.npad + col;
+            const float* s = &v[p][8 * u];
+            *(f32x4*)d = f32x4{s[0], s[1], s[2], s[3]};
+            *(f32x4*)(d + 4) = f32x4{s[4], s[5], s[6], s[7]};
+          }
+        continue;
       }
+      if constexpr (!kSumsHaveBias && !kGated) {
+#pragma unroll
+        for (int e = 0; e < 8 * U; e++) v[0][e] += bias.v[e % 8];
+      }
+      if (a.z[0]) {
+#pragma unroll
+        for (int u = 0; u < U; u++)
+#pragma unroll
+          for (int p = 0; p < P; p++)
+            if (live[u]) store_vals<E, 8>((T*)a.z[p] + m[u] * a.zld + col, &v[p][8 * u], cnt);
+      }
+      act_values<E, 8 * U>(v[0], a.act);
+      if constexpr (kGated) {
+#pragma unroll
+        for (int e = 0; e < 8 * U; e++) v[0][e] *= v[P - 1][e];
+      } else if (a.resid) {
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+          Vals<E, 8> r;
+#pragma unroll
+          for (int e = 0; e < 8; e++) r.v[e] = E::to(now[u][e]);
+          if (!queue && live[u]) r = load_vals<E, 8>((const T*)a.resid + m[u] * a.rld + col, cnt);
+#pragma unroll
+          for (int e = 0; e < 8; e++) v[0][8 * u + e] += r.v[e];
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; u++)
+        if (live[u]) store_vals<E, 8>((T*)a.out[b] + m[u] * a.outld + col, &v[0][8 * u], cnt);
     }
     settle();
   }
@@ -592,6 +631,35 @@ __global__ __launch_bounds__(Shape::kAllThreads) void k_gemm(GemmArgs a) {
     load_direct<W>(lds + slot * kBuf + kXParts * X::kBytes + p * W::kBytes, wat + p * wpart, woff[p], krem);
   };
 
+  // The first group's sums start with the bias, and with the residual if only
+  // sums follow: its loads then overlap the first tiles', and the results need
+  // no pass through LDS (8192 x 8192 x 3584 bf16 with a bias 361 us, RESULT).
+  auto begin = [&] {
+    if (kGated || a.splits > 1 || group > 0) return;
+    const int lane = threadIdx.x & 63, q = lane >> 4;
+    constexpr int kRunLen = kSpread ? (4 * FW < 8 ? 4 * FW : 8) : 4;
+    const bool resid = starts_with_resid(a);
+#pragma unroll
+    for (int p = 0; p < kWParts; p++)
+#pragma unroll
+      for (int j = 0; j < FW; j += kRunLen / 4) {
+        const int col = n0 + wn * 16 * FW + p * kWStep + (kSpread ? q * 4 * FW + 4 * j : 16 * j + 4 * q);
+        const int cnt = a.N - col;
+        Vals<E, kRunLen> bias = {};
+        if (a.bias && cnt > 0) bias = load_vals<E, kRunLen>((const T*)a.bias + col, cnt);
+#pragma unroll
+        for (int h = 0; h < kXParts; h++)
+#pragma unroll
+          for (int f = 0; f < FX; f++) {
+            const int m = m0 + wm * 16 * FX + h * kXRowsPart + f * 16 + (lane & 15);
+            Vals<E, kRunLen> r = {};
+            if (resid && m < a.M && cnt > 0) r = load_vals<E, kRunLen>((const T*)a.resid + m * a.rld + col, cnt);
+#pragma unroll
+            for (int i = 0; i < kRunLen; i++) acc[h][p][f][j + i / 4][i % 4] = bias.v[i] + r.v[i];
+          }
+      }
+  };
+
   const uint32_t xbase = frag_base<X>(wm * 16 * FX), wbase = frag_base<W>(wn * 16 * FW);
   constexpr int KK = BK / 32;
   if constexpr (kPaired) {
@@ -647,6 +715,7 @@ __global__ __launch_bounds__(Shape::kAllThreads) void k_gemm(GemmArgs a) {
         load_w(i, 1 - i);
         load_x(i, 1);
       }
+      begin();
       wait_loads<kAhead>();
       turn();
       read_w(0, 0);
@@ -690,6 +759,8 @@ __global__ __launch_bounds__(Shape::kAllThreads) void k_gemm(GemmArgs a) {
       if (t < t1) tile(t, std::integral_constant<int, 0>());
       if (wm == 0) turn();
       wait_loads<0>();
+    } else {
+      begin();
     }
   } else {
     // a ring of buffers: all but one are on their way while one is multiplied
@@ -705,6 +776,7 @@ __global__ __launch_bounds__(Shape::kAllThreads) void k_gemm(GemmArgs a) {
     // equally often, loading nothing beyond the last tile
     const int rounds = (t1 - t0 + G - 1) / G;
     for (int i = 0; i < S - 1; i++) load(t0 + group + i * G, i);
+    begin();
     int slot = 0;
     for (int r = 0; r < rounds; r++) {
       wait_loads<(S - 2) * kLoads>();
@@ -734,7 +806,7 @@ __global__ __launch_bounds__(Shape::kAllThreads) void k_gemm(GemmArgs a) {
   }
 
   if (!join_groups<Shape, G * kStages * kBuf>(acc, (lds_char*)smem)) return;
-  store_results<E, kXRows, kWRows, kGated, Shape, kXParts, kWParts, kSpread, G * kStages * kBuf>(
+  store_results<E, kXRows, kWRows, kGated, Shape, kXParts, kWParts, kSpread, G * kStages * kBuf, true>(
       a, acc, (lds_char*)smem, m0, n0, b, split, ktiles, t0, t1, BK);
 }
 
@@ -909,7 +981,7 @@ __global__ __launch_bounds__(Shape::kAllThreads) void k_gemm32(GemmArgs a) {
   }
   if (G > 1 && !late) __syncthreads();
   if (!join_groups<Shape, G * kBuf>(acc, (lds_char*)smem)) return;
-  store_results<F32, kXRows, kWRows, kGated, Shape, 1, P, true, G * kBuf>(a, acc, (lds_char*)smem, m0, n0, b, at.split,
+  store_results<F32, kXRows, kWRows, kGated, Shape, 1, P, true, G * kBuf, false>(a, acc, (lds_char*)smem, m0, n0, b, at.split,
                                                                         ktiles, t0, t1, BK);
 }
 
