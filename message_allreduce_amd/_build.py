@@ -11,12 +11,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libllar.so")
+BINDING = os.path.join(HERE, "_llar_py.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 SOURCES = ["llar_kernels.hip", "llar_multi.hip", "llar_host.hip", "llar_floor.hip", "llar_ffn.hip",
            "llar_ffn_kernels.hip"]
@@ -68,9 +70,22 @@ def build(verbose: bool = False) -> str:
     if res.returncode != 0:
         raise RuntimeError("link failed:\n%s\n%s" % (" ".join(cmd), res.stderr[-4000:]))
     os.replace(tmp, LIB)
+    _build_binding()
     if verbose:
         print("built", LIB, file=sys.stderr)
     return LIB
+
+
+def _build_binding() -> None:
+    """The feed-forward operators' Python entry points (plain C against libllar.so and the CPython API)."""
+    tmp = BINDING + ".tmp%d" % os.getpid()
+    cmd = [shutil.which("gcc") or "gcc", "-O2", "-std=c11", "-Wall", "-fPIC", "-shared", "-I", INCLUDE,
+           "-I", sysconfig.get_paths()["include"], os.path.join(CSRC, "llar_py.c"), "-o", tmp,
+           "-L", HERE, "-l:libllar.so", "-Wl,-rpath,$ORIGIN"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError("building the binding failed:\n%s\n%s" % (" ".join(cmd), res.stderr[-4000:]))
+    os.replace(tmp, BINDING)
 
 
 if __name__ == "__main__":
