@@ -290,14 +290,13 @@ int pack_and_run(Product& p, int dtype, void* space, size_t bytes, hipStream_t s
 
 bool dtype_ok(int t) { return t == LLAR_FP32 || t == LLAR_FP16 || t == LLAR_BF16; }
 bool act_ok(int a) { return a >= LLAR_ACT_NONE && a <= LLAR_ACT_SILU; }
-// Row chunks of the activation's gradient, of which each needs 32 rows at a
-// time: about 512 workgroups of 256 columns.  Up to 512 rows with a bias
-// gradient one chunk does without a second launch (333 x 1480 fp16: 26 us with
-// it, of which the two launches are 8); without one nothing is added up.
-int row_chunks(int64_t M, int64_t N, bool sums) {
-  if (sums && M <= 512) return 1;
-  const int64_t cols = std::max<int64_t>(cdiv(N, 256), 1);
-  return (int)std::max<int64_t>(1, std::min(cdiv(512, cols), M / 32));
+// Row chunks of the bias gradient's sums, 128 rows at a time: about 512
+// workgroups of 64 columns.  Up to 512 rows one chunk does without a second
+// launch (333 x 1480 fp16: 4 us of 25).
+int row_chunks(int64_t M, int64_t N) {
+  if (M <= 512) return 1;
+  const int64_t cols = std::max<int64_t>(cdiv(N, 64), 1);
+  return (int)std::max<int64_t>(1, std::min(cdiv(512, cols), cdiv(M, 128)));
 }
 bool space_ok(void* w, size_t n) { return n == 0 || (w && ((uintptr_t)w & 255) == 0); }
 
@@ -335,7 +334,7 @@ size_t llar_ffn_workspace(llar_ffn_op op, int64_t m, int64_t n, int64_t k, llar_
     case LLAR_OP_LINEAR: return x + w + product_space(m, n, k, 1, 1, false, es, xr, wr);
     case LLAR_OP_GATED_FFN: return x + 2 * w + product_space(m, n, k, 1, 1, true, es, xr, wr);
     case LLAR_OP_LINEAR_BACKWARD:
-      return x + w + (copies ? copy_bytes(m, n, es) : dz) + align256((size_t)row_chunks(m, n, true) * n * 4) +
+      return x + w + (copies ? copy_bytes(m, n, es) : dz) + align256((size_t)row_chunks(m, n) * n * 4) +
              std::max(product_space(m, k, n, 1, 1, false, es, yr, !wr),
                       product_space(n, k, m, 1, 1, false, es, !yr, !xr));
     case LLAR_OP_GATED_FFN_BACKWARD:
@@ -418,7 +417,7 @@ int llar_linear_backward(const llar_matrix* dy, const llar_matrix* x, const llar
     a.act = act;
     a.dy = dy->data;
     a.dyld = row_ld(dy);
-    a.chunks = row_chunks(M, N, db != nullptr);
+    a.chunks = row_chunks(M, N);
     if (with_act) {
       a.z = pre->data;
       a.zld = row_ld(pre);

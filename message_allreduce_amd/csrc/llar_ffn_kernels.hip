@@ -157,54 +157,77 @@ hipError_t launch_gate_grad(int kind, const GateGradArgs& a, hipStream_t s) {
 }
 
 // ---- dz = dy act'(z), and column sums of dz ----------------------------------------
-// A workgroup takes 256 columns of one row chunk: 32 lanes of 8 columns by 32
-// rows at a time.  One chunk: its sums are the bias gradient.  More: they go to
-// part[chunk], and a second kernel adds the chunks in order, so the result does
-// not depend on timing.  Bound by memory: 4096 x 8192 bf16 with the erf form of
-// GELU reads and writes 201 MB.
-constexpr int kSumRows = 32;
+// Eight elements of a row; the sum's share is returned unrounded.
 template <class E>
-__global__ __launch_bounds__(32 * kSumRows) void k_act_grad(ActGradArgs a) {
+__device__ __forceinline__ Vals<E, 8> act_grad_piece(const ActGradArgs& a, int64_t m, int col) {
   typedef typename E::T T;
-  __shared__ float sums[kSumRows][256];
-  const int lane = threadIdx.x & 31, r = threadIdx.x >> 5;
-  const int col = (blockIdx.x * 32 + lane) * 8;
   const int cnt = a.N - col;
+  Vals<E, 8> d = load_vals<E, 8>((const T*)a.dy + m * a.dyld + col, cnt);
+  if (a.z) {
+    const Vals<E, 8> z = load_vals<E, 8>((const T*)a.z + m * a.zld + col, cnt);
+    with_act(a.act, [&](auto c) {
+#pragma unroll
+      for (int i = 0; i < 8; i++) {
+        float value, slope;
+        act_two<decltype(c)::value, E>(z.v[i], value, slope);
+        d.v[i] *= slope;
+      }
+    });
+    store_vals<E, 8>((T*)a.dz + m * a.dzld + col, d.v, 8);  // zeros beyond column N
+  }
+  return d;
+}
+
+// Without a bias gradient: a piece a thread.
+template <class E>
+__global__ __launch_bounds__(256) void k_act_grad(ActGradArgs a) {
+  const int groups = (a.N + 7) / 8;
+  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t m = id / groups;
+  if (m < a.M) act_grad_piece<E>(a, m, (int)(id - m * groups) * 8);
+}
+
+// With it: a workgroup takes 64 columns of one row chunk, 128 rows at a time
+// (a line of memory a row).  One chunk: its sums are the bias gradient.  More:
+// they go to part[chunk], and a second kernel adds the chunks in order, so the
+// result does not depend on timing.  Bound by memory: 4096 x 8192 bf16 with the
+// erf form of GELU reads and writes 201 MB, RESULT.
+constexpr int kSumCols = 64, kSumRows = 128, kSumThreads = kSumRows * kSumCols / 8;
+template <class E>
+__global__ __launch_bounds__(kSumThreads) void k_act_grad_sum(ActGradArgs a) {
+  __shared__ float sums[kSumRows][kSumCols + 4];
+  const int lane = threadIdx.x % (kSumCols / 8), r = threadIdx.x / (kSumCols / 8);
+  const int col = blockIdx.x * kSumCols + lane * 8;
   const int64_t m0 = (int64_t)a.M * blockIdx.y / a.chunks, m1 = (int64_t)a.M * (blockIdx.y + 1) / a.chunks;
   float acc[8] = {};
-  if (cnt > 0) {
+  if (col < a.N) {
 #pragma unroll 2
     for (int64_t m = m0 + r; m < m1; m += kSumRows) {
-      Vals<E, 8> d = load_vals<E, 8>((const T*)a.dy + m * a.dyld + col, cnt);
-      if (a.z) {
-        const Vals<E, 8> z = load_vals<E, 8>((const T*)a.z + m * a.zld + col, cnt);
-        with_act(a.act, [&](auto c) {
-#pragma unroll
-          for (int i = 0; i < 8; i++) {
-            float value, slope;
-            act_two<decltype(c)::value, E>(z.v[i], value, slope);
-            d.v[i] *= slope;
-          }
-        });
-        store_vals<E, 8>((T*)a.dz + m * a.dzld + col, d.v, 8);  // zeros beyond column N
-      }
+      const Vals<E, 8> d = act_grad_piece<E>(a, m, col);
 #pragma unroll
       for (int i = 0; i < 8; i++) acc[i] += d.v[i];
     }
   }
-  if (!a.db) return;
 #pragma unroll
   for (int i = 0; i < 8; i++) sums[r][lane * 8 + i] = acc[i];
+  // 16 threads a column, 8 rows each, then the 16
   __syncthreads();
-  const int c = blockIdx.x * 256 + threadIdx.x;
-  if (threadIdx.x >= 256 || c >= a.N) return;
+  const int c = threadIdx.x % kSumCols, part = threadIdx.x / kSumCols;
   float s = 0.f;
 #pragma unroll
-  for (int i = 0; i < kSumRows; i++) s += sums[i][threadIdx.x];
+  for (int i = 0; i < kSumRows * kSumCols / kSumThreads; i++) s += sums[part + i * (kSumThreads / kSumCols)][c];
+  __syncthreads();
+  sums[part][c] = s;
+  __syncthreads();
+  const int out = blockIdx.x * kSumCols + c;
+  if (part > 0 || out >= a.N) return;
+  s = 0.f;
+#pragma unroll
+  for (int i = 0; i < kSumThreads / kSumCols; i++) s += sums[i][c];
   if (a.chunks == 1)
-    ((T*)a.db)[c] = E::from(s);
+    ((typename E::T*)a.db)[out] = E::from(s);
   else
-    a.part[(int64_t)blockIdx.y * a.N + c] = s;
+    a.part[(int64_t)blockIdx.y * a.N + out] = s;
 }
 
 template <class E>
@@ -220,11 +243,16 @@ __global__ __launch_bounds__(256) void k_bias_grad(ActGradArgs a) {
 template <class E>
 hipError_t act_grad(const ActGradArgs& a, hipStream_t s) {
   if (a.N == 0) return hipSuccess;
-  const uint32_t cols = (uint32_t)((a.N + 255) / 256);
-  k_act_grad<E><<<dim3(cols, (uint32_t)a.chunks), dim3(32 * kSumRows), 0, s>>>(a);
+  if (!a.db) {
+    const int64_t n = (int64_t)a.M * ((a.N + 7) / 8);
+    if (n > 0) k_act_grad<E><<<dim3((uint32_t)((n + 255) / 256)), dim3(256), 0, s>>>(a);
+    return hipGetLastError();
+  }
+  const uint32_t cols = (uint32_t)((a.N + kSumCols - 1) / kSumCols);
+  k_act_grad_sum<E><<<dim3(cols, (uint32_t)a.chunks), dim3(kSumThreads), 0, s>>>(a);
   hipError_t e = hipGetLastError();
-  if (e != hipSuccess || !a.db || a.chunks == 1) return e;
-  k_bias_grad<E><<<dim3(cols), dim3(256), 0, s>>>(a);
+  if (e != hipSuccess || a.chunks == 1) return e;
+  k_bias_grad<E><<<dim3((uint32_t)((a.N + 255) / 256)), dim3(256), 0, s>>>(a);
   return hipGetLastError();
 }
 hipError_t launch_act_grad(int kind, const ActGradArgs& a, hipStream_t s) {

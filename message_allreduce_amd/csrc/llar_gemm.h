@@ -305,7 +305,7 @@ __device__ __forceinline__ void store_results(const GemmArgs& a, f32x4 (&acc)[kX
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / Shape::WN, wn = wave % Shape::WN;
   const int mwave = m0 + wm * 16 * FX, nwave = n0 + wn * 16 * FW;
-  bool bare = !kGated && (a.splits > 1 || (!a.z[0] && a.act == kActNone &&
+  bool bare = !kGated && kSpread && (a.splits > 1 || (!a.z[0] && a.act == kActNone &&
                                            (kSumsHaveBias || (!a.bias && !a.resid))));
   bool nan = false;
   if constexpr (E::kind == 0) {
