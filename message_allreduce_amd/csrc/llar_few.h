@@ -39,6 +39,16 @@ struct Eight {
     for (int i = 0; i < (int)sizeof(T) / 2; i++) v[i] = u.q[i];
   }
   __device__ __forceinline__ Frag<E> frag() const;
+  __device__ __forceinline__ void values(float (&f)[8]) const {
+    union {
+      T t[8];
+      u32x4 q[sizeof(T) / 2];
+    } u;
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; i++) u.q[i] = v[i];
+#pragma unroll
+    for (int i = 0; i < 8; i++) f[i] = E::to(u.t[i]);
+  }
 };
 template <>
 __device__ __forceinline__ Frag<F16> Eight<F16>::frag() const {
@@ -88,14 +98,16 @@ __device__ __forceinline__ void few_finish(const GemmArgs& a, const float* part,
 
 // Weights contiguous along k.  A wave multiplies 16 weight rows (gated: 8 of
 // each projection) by all rows of x; a row's four lanes read 128 consecutive
-// bytes a step, and the workgroup's waves take the steps in turn.
+// bytes a step, and the workgroup's waves take the steps in turn.  16 waves of
+// two steps in flight: 8192 x 3584 bf16 with cold weights 19.4 us at 16 rows (3.0
+// TB/s) and 14.8 at 4; 8 waves of four steps took 20.1 and 16.
 template <class E, bool kGated, int kWaves>
 __global__ __launch_bounds__(kWaves * 64) void k_few_k(GemmArgs a) {
   typedef typename E::T T;
   constexpr int kN = kGated ? 8 : 16;
   constexpr int G = sizeof(T) == 2 ? 2 : 1;  // fragments of a step
   constexpr int kStep = 32 * G;
-  constexpr int U = 4;                       // steps in flight
+  constexpr int U = 2;                       // steps in flight
   __shared__ float part[kWaves * 16 * 16];
   const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -150,6 +162,82 @@ __global__ __launch_bounds__(kWaves * 64) void k_few_k(GemmArgs a) {
       part[(wave * 16 + r) * 16 + n] = acc[i];
   }
   few_finish<E, false, false, kGated, kWaves, kN>(a, part, n0, 0, 0, (int64_t)a.K * a.segs);
+}
+
+// One or two rows of x and weights contiguous along k: a wave takes two weight
+// rows (gated: one of each projection) over all of k, a step of 512 consecutive
+// k at a time; no other wave is needed for its sums.  Whole lines a load: cold
+// weights at one row, bf16, against the kernel above: gated 2 x 3584 x 8192 24.0
+// against 25.5 us (4.9 TB/s), 8192 x 3584 13.5 against 14.1, 28672 x 8192 82
+// against 85 (5.7 TB/s); two rows 14.0 against 14.2, four 19.1 against 14.8.
+template <class E, bool kGated, int kRows>
+__global__ __launch_bounds__(256) void k_few_dot(GemmArgs a) {
+  typedef typename E::T T;
+  constexpr int R = 2, kN = kGated ? 1 : 2;
+  const int lane = threadIdx.x & 63;
+  const int64_t n0 = ((int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6)) * kN;
+  if (n0 >= a.N) return;
+  float acc[R][kRows] = {};
+  for (int seg = 0; seg < a.segs; seg++) {
+    const T* w[R];
+#pragma unroll
+    for (int r = 0; r < R; r++)
+      w[r] = (const T*)a.w[kGated ? r / kN : seg] + min(n0 + r % kN, (int64_t)a.N - 1) * a.wld;
+    const T* x = (const T*)a.x[seg];
+    auto step = [&](int64_t k, auto whole) {
+      Eight<E> wv[R], xv[kRows];
+      const int64_t left = a.K - k;
+#pragma unroll
+      for (int r = 0; r < R; r++) {
+        if constexpr (decltype(whole)::value)
+          wv[r].load(w[r] + k);
+        else
+          wv[r].load(w[r] + k, left);
+      }
+#pragma unroll
+      for (int m = 0; m < kRows; m++) {
+        xv[m].zero();
+        if (m < a.M) {
+          if constexpr (decltype(whole)::value)
+            xv[m].load(x + m * a.xld + k);
+          else
+            xv[m].load(x + m * a.xld + k, left);
+        }
+      }
+      float xf[kRows][8];
+#pragma unroll
+      for (int m = 0; m < kRows; m++) xv[m].values(xf[m]);
+#pragma unroll
+      for (int r = 0; r < R; r++) {
+        float wf[8];
+        wv[r].values(wf);
+#pragma unroll
+        for (int m = 0; m < kRows; m++)
+#pragma unroll
+          for (int e = 0; e < 8; e++) acc[r][m] = fmaf(wf[e], xf[m][e], acc[r][m]);
+      }
+    };
+    int64_t k = lane * 8;
+#pragma unroll 4
+    for (; k + 512 <= a.K + lane * 8; k += 512) step(k, std::integral_constant<bool, true>());
+    if (k < a.K) step(k, std::integral_constant<bool, false>());
+  }
+#pragma unroll
+  for (int r = 0; r < R; r++)
+#pragma unroll
+    for (int m = 0; m < kRows; m++)
+#pragma unroll
+      for (int d = 32; d > 0; d >>= 1) acc[r][m] += __shfl_xor(acc[r][m], d);
+  // every lane has every sum: lane n + kN m finishes output (m, n)
+  const int n = lane % kN, mine = lane / kN;
+  if (mine >= a.M || n0 + n >= a.N) return;
+  float v[2] = {};
+#pragma unroll
+  for (int r = 0; r < R; r++)
+#pragma unroll
+    for (int m = 0; m < kRows; m++)
+      if (r % kN == n && m == mine) v[r / kN] = acc[r][m];
+  finish<E, kGated, 1>(a, 0, mine, (int)n0 + n, &v[0], &v[1]);
 }
 
 // Weights contiguous along n.  Lane (r, q) reads kC neighbouring columns of

@@ -26,8 +26,15 @@ hipError_t few(bool w_rows, const GemmArgs& a, hipStream_t s) {
     constexpr int kC = 4, kWaves = kGated ? 8 : 16;
     const int64_t grid = ((int64_t)a.N + 16 * kC - 1) / (16 * kC) * a.splits;
     k_few_n<E, kGated, kC, kWaves><<<dim3((uint32_t)grid), dim3(kWaves * 64), 0, s>>>(a);
+  } else if (a.M <= 2) {
+    constexpr int kN = 4 * (kGated ? 1 : 2);  // columns of a workgroup's four waves
+    const dim3 grid((uint32_t)(((int64_t)a.N + kN - 1) / kN));
+    if (a.M == 1)
+      k_few_dot<E, kGated, 1><<<grid, dim3(256), 0, s>>>(a);
+    else
+      k_few_dot<E, kGated, 2><<<grid, dim3(256), 0, s>>>(a);
   } else {
-    constexpr int kN = kGated ? 8 : 16, kWaves = 8;
+    constexpr int kN = kGated ? 8 : 16, kWaves = 16;
     k_few_k<E, kGated, kWaves><<<dim3((uint32_t)((a.N + kN - 1) / kN)), dim3(kWaves * 64), 0, s>>>(a);
   }
   return hipGetLastError();
