@@ -242,7 +242,10 @@ __global__ __launch_bounds__(256) void k_few_dot(GemmArgs a) {
 
 // Weights contiguous along n.  Lane (r, q) reads kC neighbouring columns of
 // the 8 lines k = 8 q + t, which are 8 k of each of its columns: column j of
-// every lane makes fragment j without leaving the lane's registers.
+// every lane makes fragment j without leaving the lane's registers.  Eight waves
+// and k split over up to 512 workgroups: cold weights bf16, 2 x 3584 x 8192 gated
+// 34 us (3.4 TB/s), 8192 x 3584 20 us, 16 x 4096 x 4096 14 us, joins included;
+// 16 waves on 256 workgroups took 42, 21 and 19.
 template <class E, int kC>
 struct Lines {
   typedef typename E::T T;

@@ -93,8 +93,9 @@ Shape choose(int64_t M, int64_t N, int64_t K, int segs, int outs, bool gated, in
   if (few && M <= kFewRows && outs == 1) {
     s.few = true;
     if (w_rows) {
-      const int64_t groups = cdiv(N, 64), steps = cdiv(K, 32) * segs / ((gated ? 8 : 16) * 4);
-      if (groups < 128) s.splits = (int)std::max<int64_t>(1, std::min<int64_t>({cdiv(256, groups), steps, 16}));
+      // two workgroups a CU want 512; a split leaves every wave four steps
+      const int64_t groups = cdiv(N, 64), steps = cdiv(K, 32) * segs / (8 * 4);
+      if (groups < 256) s.splits = (int)std::max<int64_t>(1, std::min<int64_t>({cdiv(512, groups), steps, 16}));
     }
     return s;
   }

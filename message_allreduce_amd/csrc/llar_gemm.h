@@ -633,7 +633,7 @@ __global__ __launch_bounds__(Shape::kAllThreads) void k_gemm(GemmArgs a) {
 
   // The first group's sums start with the bias, and with the residual if only
   // sums follow: its loads then overlap the first tiles', and the results need
-  // no pass through LDS (8192 x 8192 x 3584 bf16 with a bias 361 us, RESULT).
+  // no pass through LDS (8192 x 8192 x 3584 bf16 with a bias: 361 us, now 334).
   auto begin = [&] {
     if (kGated || a.splits > 1 || group > 0) return;
     const int lane = threadIdx.x & 63, q = lane >> 4;

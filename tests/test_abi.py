@@ -233,6 +233,9 @@ def test_feed_forward_calls_check_their_arguments_without_a_gpu(L):
     assert linear(*ok[:2], mat(4, 32, 1, 4)) == -2                # output columns not contiguous
     assert linear(*ok[:2], mat(4, 32, 16)) == -1                  # output rows overlap
     assert linear(mat(4, (1 << 30) + 8), mat(32, (1 << 30) + 8), ok[2]) == -2
+    line = 1 << 21                                                # longest contiguous axis: 2^21 - 8
+    assert linear(mat(4, line), mat(32, line), ok[2]) == -2
+    assert linear(mat(line, 64, 1, line), ok[1], mat(line, 32)) == -2
     assert linear(mat(-1, 64), *ok[1:]) == -1
     assert linear(*ok, residual=mat(4, 32, 1, 4)) == -2 and linear(*ok, pre=mat(3, 32)) == -1
     assert linear(*ok, ws=4096 + 8, n=1 << 20) == -1              # misaligned workspace
