@@ -37,10 +37,9 @@ struct GemmArgs {
 
 // Tile shapes of the product kernel (rows of x by rows of w by workgroup);
 // see llar_gemm.h.
-enum Tile : int { kTile256 = 0, kTile128 = 1, kTile64 = 2, kTileCount = 3 };
-constexpr int kTileM[kTileCount] = {256, 128, 64};
-constexpr int kTileN[kTileCount] = {256, 128, 64};
-constexpr int kTileKBytes = 128;  // k extent of a tile in bytes of one row
+enum Tile : int { kTile256 = 0, kTile128 = 1, kTile64 = 2, kTile128x64 = 3, kTileCount = 4 };
+constexpr int kTileM[kTileCount] = {256, 128, 64, 128};
+constexpr int kTileN[kTileCount] = {256, 128, 64, 64};
 
 struct GemmPlan {
   int kind;        // llar_dtype

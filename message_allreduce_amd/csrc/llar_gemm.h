@@ -22,11 +22,13 @@ struct TileShape {
   static constexpr int FM = TM / WM / 16;  // 16-row fragments of a wave along m
   static constexpr int FN = TN / WN / 16;  // and along n
   static constexpr bool kPaired = WM == 2 && WN == 4;
-  static constexpr int kStages = kPaired || TM > 64 || G_ == 4 ? 2 : 4;  // tile buffers of a group
+  // tile buffers of a group: what the CU's LDS holds, four at most
+  static constexpr int kStages = kPaired || (TM > 64 && TN > 64) || G_ == 4 ? 2 : TM > 64 ? 3 : 4;
 };
 typedef TileShape<256, 256, 2, 4, 1> Shape256;
 template <int G>
 using Shape128 = TileShape<128, 128, 2, 2, G>;
+typedef TileShape<128, 64, 2, 2, 2> Shape128x64;
 template <int G>
 using Shape64 = TileShape<64, 64, 2, 2, G>;
 

@@ -21,8 +21,10 @@ hipError_t launch_one(const GemmArgs& a, hipStream_t s) {
 
 template <class E, bool kXRows, bool kWRows, bool kGated>
 hipError_t launch_shape(const GemmPlan& p, const GemmArgs& a, hipStream_t s) {
-  if constexpr (E::kind != 0)
+  if constexpr (E::kind != 0) {
     if (p.tile == kTile256) return launch_one<E, kXRows, kWRows, Shape256, kGated>(a, s);
+    if (p.tile == kTile128x64) return launch_one<E, kXRows, kWRows, Shape128x64, kGated>(a, s);
+  }
   if (p.tile == kTile128) {
     if (p.groups == 1) return launch_one<E, kXRows, kWRows, Shape128<1>, kGated>(a, s);
     return launch_one<E, kXRows, kWRows, Shape128<2>, kGated>(a, s);
