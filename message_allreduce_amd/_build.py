@@ -26,6 +26,9 @@ SOURCES = ["llar_kernels.hip", "llar_multi.hip", "llar_host.hip", "llar_floor.hi
 INSTANCES = [("llar_gemm_inst.hip", "llar_gemm_%s_%d%d" % (e.lower(), x, w),
               ["-DLLAR_ELEM=" + e, "-DLLAR_XR=%d" % x, "-DLLAR_WR=%d" % w])
              for e in ("F32", "F16", "BF16") for x in (0, 1) for w in (0, 1)]
+# and both products of a backward pass in one launch
+INSTANCES += [("llar_gemm_pair.hip", "llar_gemm_pair_%s_%d" % (e.lower(), w), ["-DLLAR_ELEM=" + e, "-DLLAR_WR=%d" % w])
+              for e in ("F32", "F16", "BF16") for w in (0, 1)]
 ARCH = "gfx950"
 
 CFLAGS = [

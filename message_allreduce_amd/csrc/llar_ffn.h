@@ -51,6 +51,15 @@ struct GemmPlan {
 
 hipError_t launch_gemm(const GemmPlan& p, const GemmArgs& a, hipStream_t s);
 
+// The products of a backward pass together: dx from k-contiguous rows of dz, dw
+// from dz and x both row-contiguous.
+struct PairArgs {
+  GemmArgs dx, dw;
+  int first;  // workgroups of the one that goes first
+  bool dw_first;
+};
+hipError_t launch_pair(int kind, int tile, int groups, bool w_rows, PairArgs a, hipStream_t s);
+
 // A product with M <= kFewRows rows of k-contiguous x, any alignment; a.batch is 1.
 constexpr int kFewRows = 16;
 hipError_t launch_few(int kind, bool w_rows, bool gated, const GemmArgs& a, hipStream_t s);

@@ -83,14 +83,46 @@ bool chunks_whole(const Operand& o, int es) {
 struct Shape {
   bool few;
   int tile, groups, splits;
+  double cost;  // us, by the measured costs below; 0 where there is no choice
 };
+
+// What the tiles cost (us): `one` is what a k tile takes a workgroup alone on
+// its CU, `full` what it takes `occ` of them together, `turn` the first loads and
+// the results.  Measured on MI355X at 32 .. 4096 rows, 600 .. 8192 columns,
+// k 336 .. 8192.
+struct Way {
+  int tile, groups, occ;
+  double one, full, turn;
+};
+template <class F>
+void each_way(int es, F f) {
+  static constexpr Way ways16[] = {{kTile256, 1, 1, 1.42, 1.42, 4},       {kTile128, 2, 1, 0.55, 0.55, 2.5},
+                                   {kTile128, 1, 2, 0.78, 1.08, 2.5},     {kTile64, 1, 2, 0.37, 0.50, 1.5},
+                                   {kTile128x64, 2, 1, 0.38, 0.38, 2.3}, {kTile64, 2, 1, 0.24, 0.24, 1.7},
+                                   {kTile64, 4, 1, 0.26, 0.26, 2}};
+  static constexpr Way ways32[] = {{kTile128, 2, 1, 1.36, 1.36, 2.5}, {kTile128, 1, 2, 1.75, 2.57, 2.5},
+                                   {kTile64, 1, 4, 0.78, 1.70, 1.5},  {kTile64, 2, 2, 0.50, 0.82, 1.7},
+                                   {kTile64, 4, 1, 0.43, 0.43, 2}};
+  if (es == 2) {
+    for (const Way& w : ways16) f(w);
+  } else {
+    for (const Way& w : ways32) f(w);
+  }
+}
+constexpr int kCus = 256;
+constexpr double kLaunch = 2;
+// a second launch, and the planes it joins, written and read at 4 TB/s
+double join_cost(int splits, int planes, int64_t M, int64_t N) {
+  return splits > 1 ? 4 + (double)splits * planes * M * N * 8 / 4e6 : 0;
+}
+int64_t k_tiles(int64_t K, int es) { return cdiv(K, 128 / es); }
 
 // `segs`: products added; `outs`: output planes; `few`: x is k-contiguous, so
 // that few rows of it, one matrix fragment, may go the direct way.  Both ways at
 // 16 and 17 rows, cold weights, bf16: 2048 x 2048 6.8 and 10.9 us, 8192 x 3584
 // 17.2 and 17.0, contiguous along n 10.7 and 10.8, 20.3 and 19.1.
 Shape choose(int64_t M, int64_t N, int64_t K, int segs, int outs, bool gated, int es, bool few, bool w_rows) {
-  Shape s{false, kTile64, 1, 1};
+  Shape s{false, kTile64, 1, 1, 0};
   if (M == 0 || N == 0) return s;  // nothing to launch
   if (few && M <= kFewRows && outs == 1) {
     s.few = true;
@@ -101,57 +133,93 @@ Shape choose(int64_t M, int64_t N, int64_t K, int segs, int outs, bool gated, in
     }
     return s;
   }
-  // The cheapest way by measured costs (us): `one` is what a k tile takes a
-  // workgroup alone on its CU, `full` what it takes `occ` of them together,
-  // `turn` the first loads and the results.  Measured on MI355X at 32 .. 4096
-  // rows, 600 .. 8192 columns, k 336 .. 8192.
-  struct Way {
-    int tile, groups, occ;
-    double one, full, turn;
-  };
-  static const Way ways16[] = {{kTile256, 1, 1, 1.42, 1.42, 4},   {kTile128, 2, 1, 0.55, 0.55, 2.5},
-                               {kTile128, 1, 2, 0.78, 1.08, 2.5}, {kTile64, 1, 2, 0.37, 0.50, 1.5},
-                               {kTile128x64, 2, 1, 0.38, 0.38, 2.3}, {kTile64, 2, 1, 0.24, 0.24, 1.7},
-                               {kTile64, 4, 1, 0.26, 0.26, 2}};
-  static const Way ways32[] = {{kTile128, 2, 1, 1.36, 1.36, 2.5}, {kTile128, 1, 2, 1.75, 2.57, 2.5},
-                               {kTile64, 1, 4, 0.78, 1.70, 1.5},  {kTile64, 2, 2, 0.50, 0.82, 1.7},
-                               {kTile64, 4, 1, 0.43, 0.43, 2}};
-  constexpr double kLaunch = 2;
-  constexpr double kJoin = 4;          // a second launch
-  constexpr double kBytesPerUs = 4e6;  // and its planes, written and read
-  const int64_t kt = es == 2 ? cdiv(K, 64) * segs : cdiv(K, 32) * segs;
-  const int planes = gated ? 2 : outs;
-  double best = 0;
-  auto look = [&](const Way& w) {
+  s.cost = -1;
+  each_way(es, [&](const Way& w) {
     const int64_t tiles = cdiv(M, kTileM[w.tile]) * cdiv(N, kTileN[w.tile] / (gated ? 2 : 1)) * outs;
+    const int64_t kt = k_tiles(K, es) * segs;
     for (int splits = 1; splits <= 16 && (splits == 1 || kt / splits >= 2 * w.groups); splits *= 2) {
-      const int64_t wgs = tiles * splits, all = 256 * w.occ, rest = wgs % all;
+      const int64_t wgs = tiles * splits, all = kCus * w.occ, rest = wgs % all;
       double tile = (double)(wgs / all) * w.full;
-      if (rest > 0) tile += w.one + (rest > 256 ? (w.full - w.one) * (rest - 256) / (all - 256) : 0);
-      double t = kLaunch + cdiv(wgs, all) * w.turn + tile * w.groups * cdiv(cdiv(kt, splits), w.groups);
-      if (splits > 1) t += kJoin + (double)splits * planes * M * N * 8 / kBytesPerUs;
-      if (best == 0 || t < best) {
-        best = t;
-        s.tile = w.tile;
-        s.groups = w.groups;
-        s.splits = splits;
-      }
+      if (rest > 0) tile += w.one + (rest > kCus ? (w.full - w.one) * (rest - kCus) / (all - kCus) : 0);
+      const double t = kLaunch + cdiv(wgs, all) * w.turn + tile * w.groups * cdiv(cdiv(kt, splits), w.groups) +
+                       join_cost(splits, gated ? 2 : outs, M, N);
+      if (s.cost < 0 || t < s.cost) s = {false, w.tile, w.groups, splits, t};
     }
-  };
-  if (es == 2) {
-    for (const Way& w : ways16) look(w);
-  } else {
-    for (const Way& w : ways32) look(w);
-  }
+  });
   return s;
 }
-size_t partial_bytes(const Shape& s, int64_t M, int64_t N, int planes) {
-  return s.splits <= 1 ? 0 : align256((size_t)s.splits * planes * M * (size_t)(cdiv(N, 8) * 8) * 4);
+
+// Both products of a backward pass of M x N gradients and M x K inputs in one
+// launch: the same tile for both, the one with more k first, and only that one
+// split.  `on`: it costs less than two launches.
+struct PairShape {
+  bool on, dw_first;
+  int tile, groups, splits;  // of the first
+};
+
+// The time n0 workgroups of d0 each and then n1 of d1 take, each of them as one
+// of the slots comes free.
+double list_time(int64_t n0, double d0, int64_t n1, double d1, int64_t slots) {
+  const int64_t late = n0 % slots, early = slots - late;  // slots with a workgroup more, and without
+  double t_early = n0 / slots * d0, t_late = t_early + d0, end = late ? t_late : t_early;
+  const int64_t skip = std::max<int64_t>(0, n1 / slots - (int64_t)(d0 / d1) - 2);  // rounds that all slots take
+  n1 -= skip * slots;
+  t_early += skip * d1;
+  t_late += skip * d1;
+  while (n1 > 0) {
+    if (late == 0 || t_early <= t_late) {
+      n1 -= early;
+      t_early += d1;
+      end = std::max(end, t_early);
+    } else {
+      n1 -= late;
+      t_late += d1;
+      end = std::max(end, t_late);
+    }
+  }
+  return end;
+}
+
+PairShape choose_pair(int64_t M, int64_t N, int64_t K, int segs, int batch, int es) {
+  PairShape p{false, false, 0, 1, 1};
+  if (M <= kFewRows || N == 0 || K == 0) return p;
+  const int64_t ktx = k_tiles(N, es) * segs, ktw = k_tiles(M, es);
+  p.dw_first = ktw > ktx;
+  const int64_t kt0 = std::max(ktx, ktw), kt1 = std::min(ktx, ktw);
+  if (kt0 > 64 * kt1) return p;  // nothing to fill in
+  double best = choose(M, K, N, segs, 1, false, es, true, false).cost +
+                choose(N, K, M, 1, batch, false, es, false, false).cost;
+  each_way(es, [&](const Way& w) {
+    const int64_t tm = kTileM[w.tile], tn = kTileN[w.tile];
+    const int64_t nx = cdiv(M, tm) * cdiv(K, tn), nw = cdiv(N, tm) * cdiv(K, tn) * batch;
+    const int64_t n0 = p.dw_first ? nw : nx, n1 = p.dw_first ? nx : nw;
+    for (int splits = 1; splits <= 8 && (splits == 1 || kt0 / splits >= 2 * w.groups); splits *= 2) {
+      const double step = (n0 * splits + n1 <= kCus ? w.one : w.full) * w.groups;
+      const double t = kLaunch +
+                       list_time(n0 * splits, w.turn + step * cdiv(cdiv(kt0, splits), w.groups), n1,
+                                 w.turn + step * cdiv(kt1, w.groups), kCus * w.occ) +
+                       (p.dw_first ? join_cost(splits, batch, N, K) : join_cost(splits, 1, M, K));
+      if (t < best) {
+        best = t;
+        p = {true, p.dw_first, w.tile, w.groups, splits};
+      }
+    }
+  });
+  return p;
+}
+
+size_t partial_bytes(int splits, int64_t M, int64_t N, int planes) {
+  return splits <= 1 ? 0 : align256((size_t)splits * planes * M * (size_t)(cdiv(N, 8) * 8) * 4);
 }
 
 size_t product_space(int64_t M, int64_t N, int64_t K, int segs, int outs, bool gated, int es, bool x_rows,
                      bool w_rows) {
-  return partial_bytes(choose(M, N, K, segs, outs, gated, es, !x_rows, w_rows), M, N, gated ? 2 : outs);
+  return partial_bytes(choose(M, N, K, segs, outs, gated, es, !x_rows, w_rows).splits, M, N, gated ? 2 : outs);
+}
+size_t pair_space(int64_t M, int64_t N, int64_t K, int segs, int batch, int es) {
+  const PairShape p = choose_pair(M, N, K, segs, batch, es);
+  if (!p.on) return 0;
+  return p.dw_first ? partial_bytes(p.splits, N, K, batch) : partial_bytes(p.splits, M, K, 1);
 }
 
 struct Carve {
@@ -237,13 +305,11 @@ void pack(Product& p, int es, Packer& k) {
   for (int i = 0; w && i < p.n_w; i++) k.add(p.w[i], true);
 }
 
-int run_product(const Product& p, int dtype, const Carve& space, hipStream_t s) {
-  const int es = elem_size(dtype);
+GemmArgs args_of(const Product& p, int splits, float* partial) {
   GemmArgs a = {};
   a.M = (int)p.M();
   a.N = (int)p.N();
   a.K = (int)p.x[0].k;
-  if (a.M == 0 || a.N == 0) return LLAR_OK;
   for (int i = 0; i < 2; i++) {
     a.x[i] = p.x[std::min(i, p.n_x - 1)].p;
     a.w[i] = p.w[std::min(i, p.n_w - 1)].p;
@@ -261,12 +327,16 @@ int run_product(const Product& p, int dtype, const Carve& space, hipStream_t s) 
   a.batch = p.batch;
   a.act = p.act;
   a.npad = (int)(cdiv(a.N, 8) * 8);
-  const Shape sh = p.shape(es);
-  a.splits = sh.splits;
-  if (sh.splits > 1) {
-    if (partial_bytes(sh, a.M, a.N, p.gated ? 2 : p.batch) > space.left) return LLAR_ERR_ARG;
-    a.partial = (float*)space.p;
-  }
+  a.splits = splits;
+  if (splits > 1) a.partial = partial;
+  return a;
+}
+
+int run_product(const Product& p, int dtype, const Carve& space, hipStream_t s) {
+  if (p.M() == 0 || p.N() == 0) return LLAR_OK;
+  const Shape sh = p.shape(elem_size(dtype));
+  if (partial_bytes(sh.splits, p.M(), p.N(), p.gated ? 2 : p.batch) > space.left) return LLAR_ERR_ARG;
+  const GemmArgs a = args_of(p, sh.splits, (float*)space.p);
   if (sh.few) {
     if (launch_few(dtype, p.w[0].by_rows, p.gated, a, s) != hipSuccess) return LLAR_ERR_HIP;
   } else {
@@ -280,6 +350,30 @@ int run_product(const Product& p, int dtype, const Carve& space, hipStream_t s) 
     if (launch_gemm(plan, a, s) != hipSuccess) return LLAR_ERR_HIP;
   }
   if (sh.splits > 1 && launch_join(dtype, p.gated, a, s) != hipSuccess) return LLAR_ERR_HIP;
+  return LLAR_OK;
+}
+
+// The products of a backward pass: px (dx) and pw (dw), or one of them.
+int run_backward(const Product* px, const Product* pw, int dtype, const Carve& space, hipStream_t s) {
+  if (px && pw && !px->x[0].by_rows && pw->w[0].by_rows) {
+    const PairShape sh =
+        choose_pair(px->M(), px->x[0].k, px->N(), px->segs, pw->batch, elem_size(dtype));
+    if (sh.on) {
+      const Product& first = sh.dw_first ? *pw : *px;
+      if (partial_bytes(sh.splits, first.M(), first.N(), first.batch) > space.left) return LLAR_ERR_ARG;
+      PairArgs a = {};
+      a.dx = args_of(*px, sh.dw_first ? 1 : sh.splits, (float*)space.p);
+      a.dw = args_of(*pw, sh.dw_first ? sh.splits : 1, (float*)space.p);
+      a.dw_first = sh.dw_first;
+      if (launch_pair(dtype, sh.tile, sh.groups, px->w[0].by_rows, a, s) != hipSuccess) return LLAR_ERR_HIP;
+      if (sh.splits > 1 && launch_join(dtype, false, sh.dw_first ? a.dw : a.dx, s) != hipSuccess) return LLAR_ERR_HIP;
+      return LLAR_OK;
+    }
+  }
+  for (const Product* p : {px, pw}) {
+    const int st = p ? run_product(*p, dtype, space, s) : LLAR_OK;
+    if (st != LLAR_OK) return st;
+  }
   return LLAR_OK;
 }
 
@@ -339,12 +433,14 @@ size_t llar_ffn_workspace(llar_ffn_op op, int64_t m, int64_t n, int64_t k, llar_
     case LLAR_OP_GATED_FFN: return x + 2 * w + product_space(m, n, k, 1, 1, true, es, xr, wr);
     case LLAR_OP_LINEAR_BACKWARD:
       return x + w + (copies ? copy_bytes(m, n, es) : dz) + align256((size_t)row_chunks(m, n) * n * 4) +
-             std::max(product_space(m, k, n, 1, 1, false, es, yr, !wr),
-                      product_space(n, k, m, 1, 1, false, es, !yr, !xr));
+             std::max({product_space(m, k, n, 1, 1, false, es, yr, !wr),
+                       product_space(n, k, m, 1, 1, false, es, !yr, !xr),
+                       yr || xr ? 0 : pair_space(m, n, k, 1, 1, es)});
     case LLAR_OP_GATED_FFN_BACKWARD:
       return x + 2 * w + 2 * dz +
-             std::max(product_space(m, k, n, 2, 1, false, es, false, !wr),
-                      product_space(n, k, m, 1, 2, false, es, true, !xr));
+             std::max({product_space(m, k, n, 2, 1, false, es, false, !wr),
+                       product_space(n, k, m, 1, 2, false, es, true, !xr),
+                       xr ? 0 : pair_space(m, n, k, 2, 2, es)});
   }
   return 0;
 }
@@ -453,13 +549,12 @@ int llar_linear_backward(const llar_matrix* dy, const llar_matrix* x, const llar
   if (dx) {
     px.out[0] = dx->data;
     px.outld = row_ld(dx);
-    LLAR_TRY(run_product(px, dtype, c, (hipStream_t)stream));
   }
   if (dw) {
     pw.out[0] = dw->data;
     pw.outld = row_ld(dw);
-    LLAR_TRY(run_product(pw, dtype, c, (hipStream_t)stream));
   }
+  LLAR_TRY(run_backward(dx ? &px : nullptr, dw ? &pw : nullptr, dtype, c, (hipStream_t)stream));
   return LLAR_OK;
 }
 
@@ -574,14 +669,13 @@ int llar_gated_ffn_backward(const llar_matrix* dh, const llar_matrix* x, const l
   if (dx) {
     px.out[0] = dx->data;
     px.outld = row_ld(dx);
-    LLAR_TRY(run_product(px, dtype, c, (hipStream_t)stream));
   }
   if (dw_gate) {
     pw.out[0] = dw_gate->data;
     pw.out[1] = dw_up->data;
     pw.outld = row_ld(dw_gate);
-    LLAR_TRY(run_product(pw, dtype, c, (hipStream_t)stream));
   }
+  LLAR_TRY(run_backward(dx ? &px : nullptr, dw_gate ? &pw : nullptr, dtype, c, (hipStream_t)stream));
   return LLAR_OK;
 }
 

@@ -19,6 +19,19 @@ hipError_t launch_gemm(const GemmPlan& p, const GemmArgs& a, hipStream_t s) {
   return table[p.kind][p.x_rows][p.w_rows](p, a, s);
 }
 
+#define LLAR_PAIR(E) \
+  hipError_t launch_pair_##E##_0(int, int, PairArgs&, hipStream_t); \
+  hipError_t launch_pair_##E##_1(int, int, PairArgs&, hipStream_t);
+LLAR_PAIR(F32) LLAR_PAIR(F16) LLAR_PAIR(BF16)
+
+hipError_t launch_pair(int kind, int tile, int groups, bool w_rows, PairArgs a, hipStream_t s) {
+  typedef hipError_t (*Fn)(int, int, PairArgs&, hipStream_t);
+  static const Fn table[3][2] = {{launch_pair_F32_0, launch_pair_F32_1},
+                                 {launch_pair_F16_0, launch_pair_F16_1},
+                                 {launch_pair_BF16_0, launch_pair_BF16_1}};
+  return table[kind][w_rows](tile, groups, a, s);
+}
+
 // ---- few rows ------------------------------------------------------------------------
 template <class E, bool kGated>
 hipError_t few(bool w_rows, const GemmArgs& a, hipStream_t s) {
