@@ -172,29 +172,35 @@ __device__ __forceinline__ void direct_offsets(uint32_t (&voff)[Op::kLoads], int
   }
 }
 
-// Loads a tile straight into LDS, 16 bytes a lane; the wave's 64 chunks land
-// back to back.  krem: how many k of the tile exist.  The compiler would count
-// these loads against every later LDS read and wait for all of them; written
-// as assembly they are this code's own to wait for (wait_loads).  They have no
-// result registers.
+// Loads 16 bytes a lane from base + off straight into LDS, the wave's 64 chunks
+// back to back from `at`.  The compiler would count these loads against every
+// later LDS read and wait for all of them; written as assembly they are this
+// code's own to wait for (wait_loads).  They have no result registers.
+__device__ __forceinline__ u32x4 describe(int64_t base) {
+  return u32x4{(uint32_t)__builtin_amdgcn_readfirstlane((int)base),
+               (uint32_t)__builtin_amdgcn_readfirstlane((int)(base >> 32)) & 0xffffu, 0x7fffffffu, 0x00020000u};
+}
+__device__ __forceinline__ void load_chunks(uint32_t at, uint32_t off, u32x4 desc) {
+  asm volatile(
+      "s_mov_b32 m0, %0\n\t"
+      "s_nop 0\n\t"
+      "buffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(at),
+      "v"(off), "s"(desc)
+      : "memory");
+}
+
+// A whole tile that way.  krem: how many k of it exist.
 template <class Op>
 __device__ __forceinline__ void load_direct(lds_char* lds, int64_t base, const uint32_t (&voff)[Op::kLoads],
                                             int krem) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x % Op::kThreads >> 6);
-  const u32x4 desc = {(uint32_t)__builtin_amdgcn_readfirstlane((int)base),
-                      (uint32_t)__builtin_amdgcn_readfirstlane((int)(base >> 32)) & 0xffffu, 0x7fffffffu, 0x00020000u};
+  const u32x4 desc = describe(base);
   const uint32_t at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)lds + wave * 1024);
 #pragma unroll
   for (int i = 0; i < Op::kLoads; i++) {
     int row, k;
     Op::where(i, row, k);
-    const uint32_t off = k < krem ? voff[i] : kNoLoad;
-    asm volatile(
-        "s_mov_b32 m0, %0\n\t"
-        "s_nop 0\n\t"
-        "buffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(at + i * (Op::kThreads * 16)),
-        "v"(off), "s"(desc)
-        : "memory");
+    load_chunks(at + i * (Op::kThreads * 16), k < krem ? voff[i] : kNoLoad, desc);
   }
 }
 
@@ -558,10 +564,20 @@ __device__ __forceinline__ Place place(const GemmArgs& a, int BK, int wg, int to
 // The tile's rows of w lie in LDS as kWParts operands (gated: one for each
 // projection), those of x as kXParts; a wave owns FX fragments of every part
 // of x and FW of every part of w.
+//
+// Which tile: a 256 x 256 one reads 12 KB of fragments a wave for 32 matrix
+// instructions and keeps them 80 % busy at the clock that power leaves (8192^3
+// bf16 1480 TF, of 1850 there), but 256 CUs want 256 tiles.  The smaller ones are
+// bound by LDS reads (64 x 64: 4 KB for 4), then by their first loads; the
+// groups of waves bring the waves that few tiles lack.  bf16, us, 256 / 128 /
+// 128 x 64 / 64, best groups: 4096 x 2048 x 8192 119 / 130 / 171 / -, 2048 x 2048 x 2048
+// 40 / 24 / 26 / 33, 1024 x 2048 x 2048 - / 21 / 16 / 18, 128 x 2048 x 2048 - / - / 13 / 10.5.
 template <class Shape>
 constexpr int kGemmLds = Shape::kGroups * Shape::kStages * (Shape::TM + Shape::TN) * 128;
+// The large tile's room for a quarter of every wave's residual (kLater).
+constexpr int kResidLds = 8 * 64 * 32 * 2;
 
-template <class E, bool kXRows, bool kWRows, class Shape, bool kGated>
+template <class E, bool kXRows, bool kWRows, class Shape, bool kGated, bool kLater>
 __device__ __forceinline__ void gemm_body(const GemmArgs& a, char* smem, int wg, int total) {
   typedef typename E::T T;
   constexpr bool kPaired = Shape::kPaired;
@@ -635,6 +651,13 @@ __device__ __forceinline__ void gemm_body(const GemmArgs& a, char* smem, int wg,
     load_direct<W>(lds + slot * kBuf + kXParts * X::kBytes + p * W::kBytes, wat + p * wpart, woff[p], krem);
   };
 
+  // The large tile takes the residual in quarters while it multiplies, if every
+  // 8 columns of it are an aligned chunk and there are tiles enough (8192 x 8192 x
+  // 3584 bf16 398 -> 384 us, x 1024 178 -> 147; without a residual 340 and 122).
+  bool later = false;
+  if constexpr (kLater)
+    later = starts_with_resid(a) && t1 - t0 > 8 && ((a.N | a.rld | ((int64_t)a.resid / 2)) & 7) == 0 && a.rld < 1 << 23;
+
   // The first group's sums start with the bias, and with the residual if only
   // sums follow: its loads then overlap the first tiles', and the results need
   // no pass through LDS (8192 x 8192 x 3584 bf16 with a bias: 361 us, now 334).
@@ -642,7 +665,7 @@ __device__ __forceinline__ void gemm_body(const GemmArgs& a, char* smem, int wg,
     if (kGated || a.splits > 1 || group > 0) return;
     const int lane = threadIdx.x & 63, q = lane >> 4;
     constexpr int kRunLen = kSpread ? (4 * FW < 8 ? 4 * FW : 8) : 4;
-    const bool resid = starts_with_resid(a);
+    const bool resid = starts_with_resid(a) && !later;
 #pragma unroll
     for (int p = 0; p < kWParts; p++)
 #pragma unroll
@@ -726,8 +749,52 @@ __device__ __forceinline__ void gemm_body(const GemmArgs& a, char* smem, int wg,
       read_done();
       turn();
       if (wm == 1) turn();
+      // Quarter i of the residual is sent for at tile 2 i, into this wave's own
+      // LDS, and added at tile 2 i + 2: eight turns' loads are behind it then, and
+      // the waits for those have covered it.  Row r's chunk c lies at c ^ r / 2 % 4.
+      auto quarter = [&](auto number) {
+        constexpr int i = decltype(number)::value;
+        if constexpr (kLater) {
+          static_assert(FX == 4 && FW == 2, "a quarter is 64 rows of 4 chunks");
+          // kept here: what depends on them would wait in registers through the loop
+          int lane = threadIdx.x & 63, my = wave;
+          asm volatile("" : "+v"(lane), "+s"(my));
+          const int r = lane & 15, q = lane >> 4, wm = my / Shape::WN, wn = my % Shape::WN;
+          lds_char* mine = (lds_char*)smem + kGemmLds<Shape> + my * (kResidLds / 8);
+          if constexpr (i > 0) {
+#pragma unroll
+            for (int f = 0; f < FX; f++) {
+              const auto v =
+                  *(LLAR_LDS typename Wide<E, 8>::vec*)(mine + (f * 16 + r) * 64 + (q ^ (r / 2 % 4)) * 16);
+#pragma unroll
+              for (int e = 0; e < 8; e++) acc[(i - 1) / 2][(i - 1) % 2][f][e / 4][e % 4] += E::to(v[e]);
+            }
+            read_done();
+          }
+          if constexpr (i < 4) {
+            const int m = m0 + wm * 16 * FX + i / 2 * kXRowsPart, n = n0 + wn * 16 * FW + i % 2 * kWStep;
+            const u32x4 desc = describe((int64_t)a.resid + (m * a.rld + n) * ES);
+            const uint32_t to = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)mine);
+#pragma unroll
+            for (int g = 0; g < 4; g++) {
+              const int row = g * 16 + lane / 4, c = (lane & 3) ^ (row / 2 % 4);
+              load_chunks(to + g * 1024, m + row < a.M && n + c * 8 < a.N ? (row * (uint32_t)a.rld + c * 8) * ES : kNoLoad,
+                          desc);
+            }
+          }
+        }
+      };
       auto tile = [&](int t, auto first) {
         constexpr int wa = decltype(first)::value, wb = 1 - wa, slot = wa;
+        if constexpr (kLater && wa == 0) {
+          if (later) {
+            if (t == t0) quarter(std::integral_constant<int, 0>());
+            if (t == t0 + 2) quarter(std::integral_constant<int, 1>());
+            if (t == t0 + 4) quarter(std::integral_constant<int, 2>());
+            if (t == t0 + 6) quarter(std::integral_constant<int, 3>());
+            if (t == t0 + 8) quarter(std::integral_constant<int, 4>());
+          }
+        }
         auto ready = [&] {
           wait_loads<kAhead>();
           read_done();
@@ -816,8 +883,9 @@ __device__ __forceinline__ void gemm_body(const GemmArgs& a, char* smem, int wg,
 
 template <class E, bool kXRows, bool kWRows, class Shape, bool kGated>
 __global__ __launch_bounds__(Shape::kAllThreads) void k_gemm(GemmArgs a) {
-  __shared__ __attribute__((aligned(1024))) char smem[kGemmLds<Shape>];
-  gemm_body<E, kXRows, kWRows, Shape, kGated>(a, smem, blockIdx.x, gridDim.x);
+  constexpr bool kLater = Shape::kPaired && !kGated && !kWRows;
+  __shared__ __attribute__((aligned(1024))) char smem[kGemmLds<Shape> + (kLater ? kResidLds : 0)];
+  gemm_body<E, kXRows, kWRows, Shape, kGated, kLater>(a, smem, blockIdx.x, gridDim.x);
 }
 
 // ---- binary32 ----------------------------------------------------------------------
@@ -916,7 +984,10 @@ struct Parts {
 };
 
 // The same product for binary32: one LDS buffer, registers one tile ahead; the
-// other workgroups of the CU multiply while this one writes.
+// other workgroups of the CU multiply while this one writes.  Bound by the six
+// products (matrix units 63 % busy) and the cutting beside them: 4096^3 660 us (208
+// TF), 512 x 2048 x 2048 33 us.  us, 128 / 64, best groups: 2048 x 2048 x 2048 90 / 110,
+// 512 x 4096 x 2048 56 / 57, 128 x 2048 x 2048 - / 16.
 template <class Shape>
 constexpr int kGemm32Lds = Shape::kGroups * (Shape::TM + Shape::TN) * 192;
 
@@ -1019,12 +1090,12 @@ __global__ __launch_bounds__(Shape::kAllThreads) void k_gemm_pair(PairArgs a) {
     if constexpr (k32)
       gemm32_body<false, kWRows, Shape, false>(a.dx, smem, wg, total);
     else
-      gemm_body<E, false, kWRows, Shape, false>(a.dx, smem, wg, total);
+      gemm_body<E, false, kWRows, Shape, false, false>(a.dx, smem, wg, total);
   } else {
     if constexpr (k32)
       gemm32_body<true, true, Shape, false>(a.dw, smem, wg, total);
     else
-      gemm_body<E, true, true, Shape, false>(a.dw, smem, wg, total);
+      gemm_body<E, true, true, Shape, false, false>(a.dw, smem, wg, total);
   }
 }
 

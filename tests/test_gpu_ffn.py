@@ -486,3 +486,47 @@ def test_refusals():
             bad()
     with pytest.raises(TypeError):
         llar.linear(x.double(), w.double())
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16], ids=ids)
+@pytest.mark.parametrize("k", [500, 512, 576, 640, 1160])
+def test_residual_of_large_tiles(k, dtype):
+    """The residual taken while the sums grow (nine k tiles or more) and before them (fewer); rows and columns
+    that end inside a tile; residuals whose rows are apart, unaligned, repeated, or the output itself."""
+    m, n = 3000, 4104
+    d = Draw(k, dtype)
+    w, b = d(n, k, "row", k ** -0.5), d(1, n)[0]
+    for xl in ("row", "col"):
+        x = d(m, k, xl)
+        X, W = x.double(), w.double()
+        want, A = mm64(X, W.t()), mm64(X.abs(), W.t().abs())
+        for rl in ("row", "pad", "off", "one", "out"):
+            r = d(1, n).expand(m, n) if rl == "one" else d(m, n, "row" if rl == "out" else rl)
+            bias = b if rl in ("row", "off") else None
+            w64, a64 = want + r.double(), A + r.double().abs()
+            if bias is not None:
+                w64, a64 = w64 + b.double(), a64 + b.double().abs()
+            y = llar.linear(x, w, bias, r, out=r if rl == "out" else None)
+            check(y, w64, (k + 16) * EPS * a64, "residual %s, x %s" % (rl, xl))
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=ids)
+@pytest.mark.parametrize("size", [(48, 2560, 1280), (90, 64, 1500), (2400, 320, 290), (515, 500, 1410), (1030, 2048, 520)],
+                         ids=str)
+def test_both_gradients_of_one_launch(size, dtype):
+    """They are what each of them is alone, up to the order of the sums; and the same bits every time."""
+    m, n, k = size
+    d = Draw(m, dtype)
+    x, w, dy = d(m, k), d(n, k, "row", k ** -0.5), d(m, n)
+    dx, dw, _ = llar.linear_backward(dy, x, w)
+    X, W, Y = x.double(), w.double(), dy.double()
+    check(dx, mm64(Y, W), (n + 16) * EPS * mm64(Y.abs(), W.abs()), "dx")
+    check(dw, mm64(Y.t(), X), (m + 16) * EPS * mm64(Y.t().abs(), X.abs()), "dw")
+    for _ in range(3):
+        again = llar.linear_backward(dy, x, w)
+        assert torch.equal(again[0], dx) and torch.equal(again[1], dw)
+    only_dx = llar.linear_backward(dy, x, w, weight_grad=False)
+    only_dw = llar.linear_backward(dy, x, w, input_grad=False)
+    assert only_dx[1] is None and only_dw[0] is None
+    check(only_dx[0], mm64(Y, W), (n + 16) * EPS * mm64(Y.abs(), W.abs()), "dx alone")
+    check(only_dw[1], mm64(Y.t(), X), (m + 16) * EPS * mm64(Y.t().abs(), X.abs()), "dw alone")
