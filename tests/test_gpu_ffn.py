@@ -530,3 +530,31 @@ def test_both_gradients_of_one_launch(size, dtype):
     assert only_dx[1] is None and only_dw[0] is None
     check(only_dx[0], mm64(Y, W), (n + 16) * EPS * mm64(Y.abs(), W.abs()), "dx alone")
     check(only_dw[1], mm64(Y.t(), X), (m + 16) * EPS * mm64(Y.t().abs(), X.abs()), "dw alone")
+
+
+def test_lines_far_apart():
+    """Rows 8 MiB and more apart (copied above 16 rows, read in place below), offsets beyond 2^32 elements, and an
+    output and a residual whose rows are as far apart."""
+    dtype, n, k, ld = torch.bfloat16, 40, 72, (1 << 27) + 8
+    big = torch.empty(n * ld, dtype=dtype, device="cuda")
+
+    def far(rows, cols, start):
+        return big[start:].as_strided((rows, cols), (ld, 1))
+    w = far(n, k, 0)
+    d = Draw(5, dtype)
+    w.copy_(d(n, k))
+    assert (n - 1) * ld > 1 << 32
+    for m in (1, 4, 40):
+        x = d(m, k)
+        assert torch.equal(llar.linear(x, w), llar.linear(x, w.contiguous()))
+        xf, rf, out = far(m, k, 1024), far(m, n, 2048), far(m, n, 4096)
+        xf.copy_(x)
+        rf.copy_(d(m, n))
+        want = llar.linear(x, w.contiguous(), residual=rf.contiguous())
+        assert llar.linear(xf, w, residual=rf, out=out) is out
+        assert torch.equal(out, want)
+        dy = far(m, n, 8192)
+        dy.copy_(d(m, n))
+        for a, b in zip(llar.linear_backward(dy, xf, w, bias_grad=True),
+                        llar.linear_backward(dy.contiguous(), x, w.contiguous(), bias_grad=True)):
+            assert torch.equal(a, b)
