@@ -287,17 +287,18 @@ __device__ __forceinline__ float sum_again(const GemmArgs& a, int b, int p, int 
   return s;
 }
 
-// Whether the residual can be in a sum from its start.
+// Whether the residual can be in a sum from its start: begin (or the quarters)
+// and store_results both ask here, so that exactly one of them adds it.
 __device__ __forceinline__ bool starts_with_resid(const GemmArgs& a) {
   return a.resid && a.splits == 1 && !a.z[0] && a.act == kActNone;
 }
 
 // ---- results -------------------------------------------------------------------------
 // The tile (m0, n0) of plane b: acc[part of x][part of w][fragment of x][of w].
-// kSumsHaveBias: they began with the bias, and with the residual where nothing
-// comes between (starts_with_resid).
+// kSumsBegun: they began with the bias, and with the residual where nothing
+// comes between (starts_with_resid), for either order of w.
 template <class E, bool kXRows, bool kWRows, bool kGated, class Shape, int kXParts, int kWParts, bool kSpread, int kLds,
-          bool kSumsHaveBias, int FX, int FW>
+          bool kSumsBegun, int FX, int FW>
 __device__ __forceinline__ void store_results(const GemmArgs& a, f32x4 (&acc)[kXParts][kWParts][FX][FW], lds_char* lds,
                                               int m0, int n0, int b, int split, int ktiles, int t0, int t1, int bk) {
   // of fragments (f, j) lane l holds row l % 16 and 4 neighbouring
@@ -313,8 +314,10 @@ __device__ __forceinline__ void store_results(const GemmArgs& a, f32x4 (&acc)[kX
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / Shape::WN, wn = wave % Shape::WN;
   const int mwave = m0 + wm * 16 * FX, nwave = n0 + wn * 16 * FW;
-  bool bare = !kGated && kSpread && (a.splits > 1 || (!a.z[0] && a.act == kActNone &&
-                                           (kSumsHaveBias || (!a.bias && !a.resid))));
+  const bool add_bias = !kGated && !kSumsBegun && a.bias;
+  const bool add_resid = !kGated && a.resid && a.splits == 1 && !(kSumsBegun && starts_with_resid(a));
+  bool bare = !kGated && kSpread &&
+              (a.splits > 1 || (!a.z[0] && a.act == kActNone && !add_bias && !add_resid));
   bool nan = false;
   if constexpr (E::kind == 0) {
 #pragma unroll
@@ -414,7 +417,7 @@ __device__ __forceinline__ void store_results(const GemmArgs& a, f32x4 (&acc)[kX
     // The residual comes from memory: pieces ahead of their use, or a tile pays
     // that latency for each.
     typedef typename Wide<E, 8>::vec piece;
-    const bool queue = !kGated && a.resid && a.splits == 1 && cnt >= 8;
+    const bool queue = add_resid && cnt >= 8;
     auto peek = [&](int i) {
       piece v = {};
       if (queue && row_of(i) < kRows && mhalf + row_of(i) < a.M)
@@ -425,7 +428,7 @@ __device__ __forceinline__ void store_results(const GemmArgs& a, f32x4 (&acc)[kX
 #pragma unroll
     for (int u = 0; u < U; u++) next[u] = peek(u);
     Vals<E, 8> bias = {};
-    if (!kSumsHaveBias && !kGated && a.bias && cnt > 0) bias = load_vals<E, 8>((const T*)a.bias + col, cnt);
+    if (add_bias && cnt > 0) bias = load_vals<E, 8>((const T*)a.bias + col, cnt);
 #pragma clang loop unroll(disable)
     for (int i = 0; i * kStride < kRows; i += U) {
       piece now[U];
@@ -467,7 +470,7 @@ __device__ __forceinline__ void store_results(const GemmArgs& a, f32x4 (&acc)[kX
           }
         continue;
       }
-      if constexpr (!kSumsHaveBias && !kGated) {
+      if constexpr (!kSumsBegun && !kGated) {
 #pragma unroll
         for (int e = 0; e < 8 * U; e++) v[0][e] += bias.v[e % 8];
       }
@@ -482,7 +485,7 @@ __device__ __forceinline__ void store_results(const GemmArgs& a, f32x4 (&acc)[kX
       if constexpr (kGated) {
 #pragma unroll
         for (int e = 0; e < 8 * U; e++) v[0][e] *= v[P - 1][e];
-      } else if (a.resid) {
+      } else if (add_resid) {
 #pragma unroll
         for (int u = 0; u < U; u++) {
           Vals<E, 8> r;
