@@ -180,13 +180,18 @@ __device__ __forceinline__ u32x4 describe(int64_t base) {
   return u32x4{(uint32_t)__builtin_amdgcn_readfirstlane((int)base),
                (uint32_t)__builtin_amdgcn_readfirstlane((int)(base >> 32)) & 0xffffu, 0x7fffffffu, 0x00020000u};
 }
+// m0 is declared, so that a value that the compiler keeps there for a use of its
+// own is set again (it warns that it does not save it across the statement).
 __device__ __forceinline__ void load_chunks(uint32_t at, uint32_t off, u32x4 desc) {
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
   asm volatile(
       "s_mov_b32 m0, %0\n\t"
       "s_nop 0\n\t"
       "buffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(at),
       "v"(off), "s"(desc)
-      : "memory");
+      : "memory", "m0");
+#pragma clang diagnostic pop
 }
 
 // A whole tile that way.  krem: how many k of it exist.
