@@ -220,7 +220,8 @@ int llar_all_gather(llar_comm* h, const void* const* inputs, void* const* outs, 
  * with its epilogue, and their backward passes.
  *
  * Arithmetic: products of the I/O type summed in binary32 by the matrix units
- * (binary32 inputs: as three bfloat16 parts, which keeps 24 bits), the
+ * (binary32 inputs: as three bfloat16 parts each, a product off by 2^-24 of
+ * itself at most; of inputs below 2^-110 up to 2^-133 is lost), the
  * epilogue in binary32, each output rounded once.  The backward passes round
  * the gradient that both of their products read (dz, or dg and du) to the I/O
  * type once.  No atomics: the same inputs and shapes give the same bits.

@@ -82,7 +82,7 @@ __device__ __forceinline__ void few_finish(const GemmArgs& a, const float* part,
 #pragma unroll
       for (int w = 0; w < kWaves; w++) s += part[((w * P + p) * 16 + m) * kN + n];
       if constexpr (E::kind == 0) {
-        if (s != s) s = sum_again<kXRows, kWRows>(a, 0, p, m, n0 + n, k0, k1);
+        if (not_finite(s)) s = sum_again<kXRows, kWRows>(a, 0, p, m, n0 + n, k0, k1);
       }
       v[p] = s;
     }
