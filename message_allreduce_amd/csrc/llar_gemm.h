@@ -289,16 +289,35 @@ __device__ __forceinline__ void finish(const GemmArgs& a, int b, int m, int col,
 // part, or infinity less infinity in a remainder), and a part rounded up may
 // overflow where its value does not.  So a sum of binary32 inputs that is not
 // finite is taken again from the inputs, in k order, up to the first true NaN.
+// One lane a sum, 16 terms fetched together, which is slow next to the matrix
+// units: with an infinity in one row of x, 512 x 2048 x 2048 takes 73 us instead of
+// 33 (one term at a time 380), 4096^3 880 instead of 645.
 __device__ __forceinline__ bool not_finite(float s) { return !(fabsf(s) < __builtin_inff()); }
 template <bool kXRows, bool kWRows>
 __device__ __forceinline__ float sum_again(const GemmArgs& a, int b, int p, int m, int col, int64_t k0, int64_t k1) {
+  constexpr int U = 16;
+  const int64_t xstep = kXRows ? a.xld : 1, wstep = kWRows ? a.wld : 1;
+  const bool two = a.segs == 2;
   float s = 0.f;
-  for (int64_t k = k0; k < k1 && s == s; k++) {
-    const int seg = a.segs == 2 ? (int)(k / a.K) : b;
-    const int64_t kk = a.segs == 2 ? k % a.K : k;
-    const float* x = (const float*)a.x[seg];
-    const float* w = (const float*)a.w[a.segs == 2 || a.batch == 2 ? seg : p];
-    s = fmaf(x[kXRows ? kk * a.xld + m : m * a.xld + kk], w[kWRows ? kk * a.wld + col : col * a.wld + kk], s);
+  for (int seg = two ? 0 : b; seg <= (two ? 1 : b); seg++) {
+    const int64_t before = two ? (int64_t)seg * a.K : 0;  // terms of the pairs before this one
+    const int64_t end = two ? min(k1 - before, (int64_t)a.K) : k1;
+    int64_t k = max(k0 - before, (int64_t)0);
+    const float* x = (const float*)a.x[seg] + (kXRows ? m : m * a.xld);
+    const float* w = (const float*)a.w[two || a.batch == 2 ? seg : p] + (kWRows ? col : col * a.wld);
+#pragma clang loop unroll(disable)
+    for (; k + U <= end && s == s; k += U) {
+      float xv[U], wv[U];
+#pragma unroll
+      for (int i = 0; i < U; i++) {
+        xv[i] = x[(k + i) * xstep];
+        wv[i] = w[(k + i) * wstep];
+      }
+#pragma unroll
+      for (int i = 0; i < U; i++) s = fmaf(xv[i], wv[i], s);
+    }
+#pragma clang loop unroll(disable)
+    for (; k < end && s == s; k++) s = fmaf(x[k * xstep], w[k * wstep], s);
   }
   return s;
 }

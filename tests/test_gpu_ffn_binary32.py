@@ -120,3 +120,45 @@ def test_small_values_keep_what_the_parts_can_hold(m):
     want = v.double()[:, None] * 2.0 ** 40
     off = (llar.linear(x, w).double() - want).abs()
     assert (off <= TOL * want.abs() + 2.0 ** (40 - 133)).all()
+
+
+def same_kind(got, want, what):
+    """Infinities, with their signs, and NaNs are where binary64 has them; the rest is near."""
+    assert torch.equal(got.isnan(), want.isnan()), what
+    assert torch.equal(got == float("inf"), want == float("inf")), what
+    assert torch.equal(got == -float("inf"), want == -float("inf")), what
+    ok = want.isfinite()
+    assert torch.allclose(got[ok].double(), want[ok], rtol=1e-4, atol=1e-4), what
+
+
+@pytest.mark.parametrize("wl", ["row", "col"])
+@pytest.mark.parametrize("size", [(5, 48, 64), (16, 72, 1000), (40, 56, 72), (17, 40, 4000), (300, 264, 136)], ids=str)
+def test_infinities_go_through_both_products_and_splits(size, wl):
+    """An infinity, two of opposite weight, and a NaN, in either of the pairs that are added, in the first, a
+    middle and the last k: the sums taken again run over the same products."""
+    m, n, k = size
+    g = torch.Generator(device="cuda")
+    g.manual_seed(m * n)
+    def t(r, c):
+        return torch.empty(r, c, device="cuda").normal_(generator=g)
+    inf, nan = float("inf"), float("nan")
+    wg, wu, x = t(n, k), t(n, k), t(m, k)
+    wgo, wuo = ordered(wg, wl), ordered(wu, wl)
+    xi = x.clone()
+    xi[0, k - 1], xi[1, k // 2], xi[2, 0], xi[2, k - 1], xi[3, k // 2] = inf, -inf, inf, inf, nan
+    for got, w in zip(llar.gated_ffn(xi, wgo, wuo, activation="none", save=True)[1:], (wg, wu)):
+        same_kind(got, torch.mm(xi.double(), w.double().t()), "forward")
+    same_kind(llar.linear(xi, wgo), torch.mm(xi.double(), wg.double().t()), "linear")
+    one = torch.ones(m, n, device="cuda")
+    for pair in (0, 1):
+        for at in (0, n // 2, n - 1):
+            # activation none: dg = dh up, du = dh gate
+            gate, up = one.clone(), one.clone()
+            (up if pair == 0 else gate)[1, at] = inf
+            (up if pair == 0 else gate)[2, at] = nan
+            dh = t(m, n)
+            dx, dwg, dwu = llar.gated_ffn_backward(dh, x, wgo, wuo, gate, up, activation="none")
+            dg, du = dh.double() * up.double(), dh.double() * gate.double()
+            same_kind(dx, torch.mm(dg, wg.double()) + torch.mm(du, wu.double()), "dx")
+            same_kind(dwg, torch.mm(dg.t().contiguous(), x.double()), "dw_gate")
+            same_kind(dwu, torch.mm(du.t().contiguous(), x.double()), "dw_up")
