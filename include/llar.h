@@ -249,7 +249,8 @@ typedef enum {
 /* rows x cols elements, element (i, j) at data + i*row_stride + j*col_stride
  * (strides in elements, not negative; 0 repeats a row or column of an input).
  * An input needs a stride of 1 along one axis (any layout when that axis has
- * one element); where stated, and for every output, col_stride must be 1.
+ * one element), but for the incoming gradients dy and dh, which may have any;
+ * where stated, and for every output, col_stride must be 1.
  * Output rows must not overlap.  Any alignment is accepted; above 16
  * tokens, LLAR_LAYOUT_UNALIGNED operands are copied into
  * the workspace first. */
@@ -265,7 +266,7 @@ enum {
                                   more apart: adds room for copies */
   LLAR_LAYOUT_X_COLUMNS = 2,   /* x's columns are contiguous, not its rows (a transposed view) */
   LLAR_LAYOUT_W_COLUMNS = 4,   /* so are the weights' */
-  LLAR_LAYOUT_DY_COLUMNS = 8   /* so are linear_backward's dy's */
+  LLAR_LAYOUT_DY_COLUMNS = 8   /* linear_backward's dy's rows are not contiguous */
 };
 
 /* Bytes of workspace a call needs for m tokens, n outputs and k inputs (0 is
@@ -290,8 +291,10 @@ int llar_linear(const llar_matrix* x, const llar_matrix* w, const void* bias, co
 /* Backward pass of llar_linear:  dz = dy act'(pre);  dx = dz w,  dw = dz^T x,
  * db = sum of dz over the rows (the residual's gradient is dy itself).
  * dx (m x k), dw (n x k) and db (n contiguous elements) may each be NULL.
- * pre (contiguous rows) is needed unless act is LLAR_ACT_NONE; dy then needs
- * contiguous rows, and so it does when db is asked for. */
+ * pre (contiguous rows) is needed unless act is LLAR_ACT_NONE.  dy whose rows
+ * are not contiguous is read fastest as one of contiguous columns, without an
+ * activation and without db; with either, or with neither axis contiguous, it is
+ * laid out in the workspace first, and n is at most 2^21 - 8. */
 int llar_linear_backward(const llar_matrix* dy, const llar_matrix* x, const llar_matrix* w, const llar_matrix* pre,
                          const llar_matrix* dx, const llar_matrix* dw, void* db, llar_dtype dtype, llar_act act,
                          void* workspace, size_t workspace_bytes, void* stream);
@@ -308,7 +311,7 @@ int llar_gated_ffn(const llar_matrix* x, const llar_matrix* w_gate, const llar_m
 /* Backward pass of llar_gated_ffn:  dg = dh up act'(gate), du = dh act(gate);
  * dx = dg w_gate + du w_up,  dw_gate = dg^T x,  dw_up = du^T x.  dx may be
  * NULL, and so may dw_gate and dw_up together (they have the same strides).
- * dh, gate and up have contiguous rows. */
+ * gate and up have contiguous rows. */
 int llar_gated_ffn_backward(const llar_matrix* dh, const llar_matrix* x, const llar_matrix* w_gate,
                             const llar_matrix* w_up, const llar_matrix* gate, const llar_matrix* up,
                             const llar_matrix* dx, const llar_matrix* dw_gate, const llar_matrix* dw_up,

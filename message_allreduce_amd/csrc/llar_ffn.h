@@ -79,26 +79,27 @@ hipError_t launch_repack(int kind, const RepackArgs& a, hipStream_t s);
 // Sums the partial planes of a product split over k and applies its epilogue.
 hipError_t launch_join(int kind, bool gated, const GemmArgs& a, hipStream_t s);
 
-// dg = dh u act'(g), du = dh act(g), element by element (rows contiguous; those
-// of dg and du `dld` apart, a multiple of 8, with zeros behind column N).
+// dg = dh u act'(g), du = dh act(g), element by element (rows contiguous, but for
+// dh's, whose columns are `dhcs` apart; rows of dg and du `dld` apart, a multiple
+// of 8, with zeros behind column N).
 struct GateGradArgs {
   const void *dh, *g, *u;
   void *dg, *du;
-  int64_t dhld, gld, uld, dld;
+  int64_t dhld, dhcs, gld, uld, dld;
   int M, N;
   int act;
 };
 hipError_t launch_gate_grad(int kind, const GateGradArgs& a, hipStream_t s);
 
-// dz = dy act'(z) (dz and z null: no activation) and the sum of dz over the
-// rows: part[c][j] = sum over row chunk c, then db[j] = sum over c in order.
-// dz rows as for the gated block.
+// dz = dy act'(z) (z null: no activation; dz null: not written) and the sum of dz
+// over the rows: part[c][j] = sum over row chunk c, then db[j] = sum over c in
+// order.  dz rows as for the gated block, dy's columns `dycs` apart.
 struct ActGradArgs {
   const void *dy, *z;
   void* dz;
   void* db;
   float* part;
-  int64_t dyld, zld, dzld;
+  int64_t dyld, dycs, zld, dzld;
   int M, N;
   int act;
   int chunks;

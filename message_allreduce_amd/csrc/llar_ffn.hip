@@ -39,19 +39,24 @@ struct Operand {
 
 bool row_major(const llar_matrix* m) { return m->cols <= 1 || m->col_stride == 1; }
 
-int check(const llar_matrix* m, bool output = false) {
+bool unit_axis(const llar_matrix* m) {
+  return m->cols <= 1 || m->col_stride == 1 || m->rows <= 1 || m->row_stride == 1;
+}
+
+enum Use { kInput, kGradient, kOutput };  // a gradient may have any strides
+int check(const llar_matrix* m, Use use = kInput) {
   if (!m) return LLAR_ERR_ARG;
   if (m->rows < 0 || m->cols < 0) return LLAR_ERR_ARG;
   if (m->rows > kMaxDim || m->cols > kMaxDim) return LLAR_ERR_UNSUPPORTED;
   if (m->rows == 0 || m->cols == 0) return LLAR_OK;
   if (!m->data || m->row_stride < 0 || m->col_stride < 0) return LLAR_ERR_ARG;
-  if (output) {
+  if (use == kOutput) {
     if (m->cols > 1 && m->col_stride != 1) return LLAR_ERR_UNSUPPORTED;
     if (m->rows > 1 && m->row_stride < m->cols) return LLAR_ERR_ARG;
-  } else if (m->cols > 1 && m->col_stride != 1 && m->rows > 1 && m->row_stride != 1) {
+  } else if (use == kInput && !unit_axis(m)) {
     return LLAR_ERR_UNSUPPORTED;
   }
-  if (!output && (row_major(m) ? m->cols : m->rows) > kMaxLine) return LLAR_ERR_UNSUPPORTED;
+  if (use != kOutput && (row_major(m) ? m->cols : m->rows) > kMaxLine) return LLAR_ERR_UNSUPPORTED;
   return LLAR_OK;
 }
 
@@ -431,11 +436,15 @@ size_t llar_ffn_workspace(llar_ffn_op op, int64_t m, int64_t n, int64_t k, llar_
   switch (op) {
     case LLAR_OP_LINEAR: return x + w + product_space(m, n, k, 1, 1, false, es, xr, wr);
     case LLAR_OP_GATED_FFN: return x + 2 * w + product_space(m, n, k, 1, 1, true, es, xr, wr);
-    case LLAR_OP_LINEAR_BACKWARD:
-      return x + w + (copies ? copy_bytes(m, n, es) : dz) + align256((size_t)row_chunks(m, n) * n * 4) +
-             std::max({product_space(m, k, n, 1, 1, false, es, yr, !wr),
-                       product_space(n, k, m, 1, 1, false, es, !yr, !xr),
-                       yr || xr ? 0 : pair_space(m, n, k, 1, 1, es)});
+    case LLAR_OP_LINEAR_BACKWARD: {
+      // the products read dy, or dz, whose rows are contiguous
+      size_t products = 0;
+      for (const bool by_columns : {false, yr})
+        products = std::max({products, product_space(m, k, n, 1, 1, false, es, by_columns, !wr),
+                             product_space(n, k, m, 1, 1, false, es, !by_columns, !xr),
+                             by_columns || xr ? 0 : pair_space(m, n, k, 1, 1, es)});
+      return x + w + (copies ? copy_bytes(m, n, es) : dz) + align256((size_t)row_chunks(m, n) * n * 4) + products;
+    }
     case LLAR_OP_GATED_FFN_BACKWARD:
       return x + 2 * w + 2 * dz +
              std::max({product_space(m, k, n, 2, 1, false, es, false, !wr),
@@ -451,7 +460,7 @@ int llar_linear(const llar_matrix* x, const llar_matrix* w, const void* bias, co
   if (!dtype_ok(dtype) || !act_ok(act) || !space_ok(workspace, workspace_bytes)) return llar::fail(LLAR_ERR_ARG);
   LLAR_TRY(check(x));
   LLAR_TRY(check(w));
-  LLAR_TRY(check(out, true));
+  LLAR_TRY(check(out, kOutput));
   if (x->cols != w->cols || out->rows != x->rows || out->cols != w->rows) return llar::fail(LLAR_ERR_ARG);
   if (residual) {
     LLAR_TRY(check(residual));
@@ -459,7 +468,7 @@ int llar_linear(const llar_matrix* x, const llar_matrix* w, const void* bias, co
     if (!row_major(residual)) return llar::fail(LLAR_ERR_UNSUPPORTED);
   }
   if (pre) {
-    LLAR_TRY(check(pre, true));
+    LLAR_TRY(check(pre, kOutput));
     if (!same_shape(pre, out)) return llar::fail(LLAR_ERR_ARG);
   }
   if (!enough(workspace_bytes, LLAR_OP_LINEAR, x, w, nullptr, nullptr, dtype)) return llar::fail(LLAR_ERR_ARG);
@@ -486,7 +495,7 @@ int llar_linear_backward(const llar_matrix* dy, const llar_matrix* x, const llar
                          const llar_matrix* dx, const llar_matrix* dw, void* db, llar_dtype dtype, llar_act act,
                          void* workspace, size_t workspace_bytes, void* stream) {
   if (!dtype_ok(dtype) || !act_ok(act) || !space_ok(workspace, workspace_bytes)) return llar::fail(LLAR_ERR_ARG);
-  LLAR_TRY(check(dy));
+  LLAR_TRY(check(dy, kGradient));
   LLAR_TRY(check(x));
   LLAR_TRY(check(w));
   if (x->cols != w->cols || dy->rows != x->rows || dy->cols != w->rows) return llar::fail(LLAR_ERR_ARG);
@@ -496,13 +505,15 @@ int llar_linear_backward(const llar_matrix* dy, const llar_matrix* x, const llar
     if (!same_shape(pre, dy)) return llar::fail(LLAR_ERR_ARG);
     if (!row_major(pre)) return llar::fail(LLAR_ERR_UNSUPPORTED);
   }
-  if ((with_act || db) && !row_major(dy)) return llar::fail(LLAR_ERR_UNSUPPORTED);
+  // dz is a matrix of its own with an activation, or where dy cannot be read as it is
+  const bool own = with_act || (!row_major(dy) && (db || !unit_axis(dy)));
+  if (own && dy->cols > kMaxLine) return llar::fail(LLAR_ERR_UNSUPPORTED);  // dz's rows
   if (dx) {
-    LLAR_TRY(check(dx, true));
+    LLAR_TRY(check(dx, kOutput));
     if (!same_shape(dx, x)) return llar::fail(LLAR_ERR_ARG);
   }
   if (dw) {
-    LLAR_TRY(check(dw, true));
+    LLAR_TRY(check(dw, kOutput));
     if (!same_shape(dw, w)) return llar::fail(LLAR_ERR_ARG);
   }
   if (!enough(workspace_bytes, LLAR_OP_LINEAR_BACKWARD, x, w, nullptr, dy, dtype)) return llar::fail(LLAR_ERR_ARG);
@@ -510,21 +521,25 @@ int llar_linear_backward(const llar_matrix* dy, const llar_matrix* x, const llar
   const int es = elem_size(dtype);
   Carve c{(uint8_t*)workspace, workspace_bytes};
   Operand dz = operand(dy);
-  if (with_act || db) {
+  if (own || db) {
     ActGradArgs a = {};
     a.M = (int)M;
     a.N = (int)N;
     a.act = act;
     a.dy = dy->data;
     a.dyld = row_ld(dy);
+    a.dycs = row_major(dy) ? 1 : dy->col_stride;
     a.chunks = row_chunks(M, N);
     if (with_act) {
       a.z = pre->data;
       a.zld = row_ld(pre);
+    }
+    if (own) {
       a.dzld = cdiv(N, 8) * 8;
       a.dz = c.take((size_t)M * a.dzld * es);
       dz.p = a.dz;
       dz.ld = a.dzld;
+      dz.by_rows = false;
       dz.padded = true;
     }
     if (db) {
@@ -565,13 +580,13 @@ int llar_gated_ffn(const llar_matrix* x, const llar_matrix* w_gate, const llar_m
   LLAR_TRY(check(x));
   LLAR_TRY(check(w_gate));
   LLAR_TRY(check(w_up));
-  LLAR_TRY(check(out, true));
+  LLAR_TRY(check(out, kOutput));
   if (!same_shape(w_gate, w_up) || x->cols != w_gate->cols || out->rows != x->rows || out->cols != w_gate->rows)
     return llar::fail(LLAR_ERR_ARG);
   if (!gate != !up) return llar::fail(LLAR_ERR_ARG);
   if (gate) {
-    LLAR_TRY(check(gate, true));
-    LLAR_TRY(check(up, true));
+    LLAR_TRY(check(gate, kOutput));
+    LLAR_TRY(check(up, kOutput));
     if (!same_shape(gate, out) || !same_shape(up, out)) return llar::fail(LLAR_ERR_ARG);
     if (gate->rows > 1 && gate->row_stride != up->row_stride) return llar::fail(LLAR_ERR_UNSUPPORTED);
   }
@@ -601,7 +616,7 @@ int llar_gated_ffn_backward(const llar_matrix* dh, const llar_matrix* x, const l
                             const llar_matrix* dx, const llar_matrix* dw_gate, const llar_matrix* dw_up,
                             llar_dtype dtype, llar_act act, void* workspace, size_t workspace_bytes, void* stream) {
   if (!dtype_ok(dtype) || !act_ok(act) || !space_ok(workspace, workspace_bytes)) return llar::fail(LLAR_ERR_ARG);
-  LLAR_TRY(check(dh));
+  LLAR_TRY(check(dh, kGradient));
   LLAR_TRY(check(x));
   LLAR_TRY(check(w_gate));
   LLAR_TRY(check(w_up));
@@ -610,15 +625,15 @@ int llar_gated_ffn_backward(const llar_matrix* dh, const llar_matrix* x, const l
   if (!same_shape(w_gate, w_up) || x->cols != w_gate->cols || dh->rows != x->rows || dh->cols != w_gate->rows ||
       !same_shape(gate, dh) || !same_shape(up, dh))
     return llar::fail(LLAR_ERR_ARG);
-  if (!row_major(dh) || !row_major(gate) || !row_major(up)) return llar::fail(LLAR_ERR_UNSUPPORTED);
+  if (!row_major(gate) || !row_major(up)) return llar::fail(LLAR_ERR_UNSUPPORTED);
   if (!dw_gate != !dw_up) return llar::fail(LLAR_ERR_ARG);
   if (dx) {
-    LLAR_TRY(check(dx, true));
+    LLAR_TRY(check(dx, kOutput));
     if (!same_shape(dx, x)) return llar::fail(LLAR_ERR_ARG);
   }
   if (dw_gate) {
-    LLAR_TRY(check(dw_gate, true));
-    LLAR_TRY(check(dw_up, true));
+    LLAR_TRY(check(dw_gate, kOutput));
+    LLAR_TRY(check(dw_up, kOutput));
     if (!same_shape(dw_gate, w_gate) || !same_shape(dw_up, w_gate)) return llar::fail(LLAR_ERR_ARG);
     if (dw_gate->rows > 1 && dw_gate->row_stride != dw_up->row_stride) return llar::fail(LLAR_ERR_UNSUPPORTED);
   }
@@ -635,6 +650,7 @@ int llar_gated_ffn_backward(const llar_matrix* dh, const llar_matrix* x, const l
   a.act = act;
   a.dh = dh->data;
   a.dhld = row_ld(dh);
+  a.dhcs = row_major(dh) ? 1 : dh->col_stride;
   a.g = gate->data;
   a.gld = row_ld(gate);
   a.u = up->data;

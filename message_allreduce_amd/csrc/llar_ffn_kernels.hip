@@ -140,19 +140,39 @@ hipError_t launch_join(int kind, bool gated, const GemmArgs& a, hipStream_t s) {
   return kind == 0 ? join<F32>(gated, a, s) : kind == 1 ? join<F16>(gated, a, s) : join<BF16>(gated, a, s);
 }
 
+// Eight elements of a row of an incoming gradient; kAny: `cs` apart.
+template <class E, bool kAny>
+__device__ __forceinline__ Vals<E, 8> load_grad(const void* p, int64_t m, int64_t ld, int64_t cs, int col, int cnt) {
+  const typename E::T* row = (const typename E::T*)p + m * ld;
+  if constexpr (!kAny) return load_vals<E, 8>(row + col, cnt);
+  Vals<E, 8> r;
+#pragma unroll
+  for (int i = 0; i < 8; i++) r.v[i] = i < cnt ? E::to(row[(col + i) * cs]) : 0.f;
+  return r;
+}
+// The row and the first column of an element-wise pass's piece `id`; kAny: the
+// rows first, neighbours in memory where the columns are not (a transposed view:
+// 4096 x 8192 bf16 GELU slopes 56 us against 41 for contiguous rows, 43 for one
+// value repeated; the gated block's 4096 x 3584 39 against 24).
+template <bool kAny>
+__device__ __forceinline__ int64_t piece_of(int64_t id, int M, int N, int& col) {
+  const int groups = (N + 7) / 8;
+  const int64_t m = kAny ? id % M : id / groups;
+  col = (int)(kAny ? id / M : id - m * groups) * 8;
+  return m;
+}
+
 // ---- the gated block's element-wise gradient: 3 reads, 2 writes --------------------
 // Eight elements a thread, the exponential shared by value and slope.  Bound by
 // memory: 4096 x 3584 bf16 moves 147 MB in 29 us (5.1 TB/s).
-template <class E>
+template <class E, bool kAny>
 __global__ __launch_bounds__(256) void k_gate_grad(GateGradArgs a) {
   typedef typename E::T T;
-  const int groups = (a.N + 7) / 8;
-  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t m = id / groups;
-  const int col = (int)(id - m * groups) * 8;
-  if (m >= a.M) return;
+  int col;
+  const int64_t m = piece_of<kAny>((int64_t)blockIdx.x * 256 + threadIdx.x, a.M, a.N, col);
+  if (m >= a.M || col >= a.N) return;
   const int cnt = a.N - col;
-  const Vals<E, 8> dh = load_vals<E, 8>((const T*)a.dh + m * a.dhld + col, cnt);
+  const Vals<E, 8> dh = load_grad<E, kAny>(a.dh, m, a.dhld, a.dhcs, col, cnt);
   const Vals<E, 8> g = load_vals<E, 8>((const T*)a.g + m * a.gld + col, cnt);
   const Vals<E, 8> u = load_vals<E, 8>((const T*)a.u + m * a.uld + col, cnt);
   float dg[8], du[8];
@@ -170,26 +190,28 @@ __global__ __launch_bounds__(256) void k_gate_grad(GateGradArgs a) {
   store_vals<E, 8>((T*)a.du + m * a.dld + col, du, 8);
 }
 
-hipError_t launch_gate_grad(int kind, const GateGradArgs& a, hipStream_t s) {
+template <class E>
+hipError_t gate_grad(const GateGradArgs& a, hipStream_t s) {
   const int64_t n = (int64_t)a.M * ((a.N + 7) / 8);
   if (n == 0) return hipSuccess;
   const dim3 grid((uint32_t)((n + 255) / 256)), block(256);
-  if (kind == 0)
-    k_gate_grad<F32><<<grid, block, 0, s>>>(a);
-  else if (kind == 1)
-    k_gate_grad<F16><<<grid, block, 0, s>>>(a);
+  if (a.dhcs == 1)
+    k_gate_grad<E, false><<<grid, block, 0, s>>>(a);
   else
-    k_gate_grad<BF16><<<grid, block, 0, s>>>(a);
+    k_gate_grad<E, true><<<grid, block, 0, s>>>(a);
   return hipGetLastError();
+}
+hipError_t launch_gate_grad(int kind, const GateGradArgs& a, hipStream_t s) {
+  return kind == 0 ? gate_grad<F32>(a, s) : kind == 1 ? gate_grad<F16>(a, s) : gate_grad<BF16>(a, s);
 }
 
 // ---- dz = dy act'(z), and column sums of dz ----------------------------------------
 // Eight elements of a row; the sum's share is returned unrounded.
-template <class E>
+template <class E, bool kAny>
 __device__ __forceinline__ Vals<E, 8> act_grad_piece(const ActGradArgs& a, int64_t m, int col) {
   typedef typename E::T T;
   const int cnt = a.N - col;
-  Vals<E, 8> d = load_vals<E, 8>((const T*)a.dy + m * a.dyld + col, cnt);
+  Vals<E, 8> d = load_grad<E, kAny>(a.dy, m, a.dyld, a.dycs, col, cnt);
   if (a.z) {
     const Vals<E, 8> z = load_vals<E, 8>((const T*)a.z + m * a.zld + col, cnt);
     with_act(a.act, [&](auto c) {
@@ -200,19 +222,18 @@ __device__ __forceinline__ Vals<E, 8> act_grad_piece(const ActGradArgs& a, int64
         d.v[i] *= slope;
       }
     });
-    store_vals<E, 8>((T*)a.dz + m * a.dzld + col, d.v, 8);  // zeros beyond column N
   }
+  if (a.dz) store_vals<E, 8>((T*)a.dz + m * a.dzld + col, d.v, 8);  // zeros beyond column N
   return d;
 }
 
 // Without a bias gradient: a piece a thread (4096 x 4096 bf16, erf form of GELU: 101
 // MB in 27 us, 3.7 TB/s; the arithmetic counts).
-template <class E>
+template <class E, bool kAny>
 __global__ __launch_bounds__(256) void k_act_grad(ActGradArgs a) {
-  const int groups = (a.N + 7) / 8;
-  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t m = id / groups;
-  if (m < a.M) act_grad_piece<E>(a, m, (int)(id - m * groups) * 8);
+  int col;
+  const int64_t m = piece_of<kAny>((int64_t)blockIdx.x * 256 + threadIdx.x, a.M, a.N, col);
+  if (m < a.M && col < a.N) act_grad_piece<E, kAny>(a, m, col);
 }
 
 // With it: a workgroup takes 64 columns of one row chunk, 128 rows at a time
@@ -221,7 +242,7 @@ __global__ __launch_bounds__(256) void k_act_grad(ActGradArgs a) {
 // result does not depend on timing.  Bound by memory: 4096 x 8192 bf16 with the
 // erf form of GELU moves 201 MB in 51 us (3.9 TB/s), 256 x 3008 takes 9 us.
 constexpr int kSumCols = 64, kSumRows = 128, kSumThreads = kSumRows * kSumCols / 8;
-template <class E>
+template <class E, bool kAny>
 __global__ __launch_bounds__(kSumThreads) void k_act_grad_sum(ActGradArgs a) {
   __shared__ float sums[kSumRows][kSumCols + 4];
   const int lane = threadIdx.x % (kSumCols / 8), r = threadIdx.x / (kSumCols / 8);
@@ -231,7 +252,7 @@ __global__ __launch_bounds__(kSumThreads) void k_act_grad_sum(ActGradArgs a) {
   if (col < a.N) {
 #pragma unroll 2
     for (int64_t m = m0 + r; m < m1; m += kSumRows) {
-      const Vals<E, 8> d = act_grad_piece<E>(a, m, col);
+      const Vals<E, 8> d = act_grad_piece<E, kAny>(a, m, col);
 #pragma unroll
       for (int i = 0; i < 8; i++) acc[i] += d.v[i];
     }
@@ -268,23 +289,25 @@ __global__ __launch_bounds__(256) void k_bias_grad(ActGradArgs a) {
   ((typename E::T*)a.db)[c] = E::from(s);
 }
 
-template <class E>
+template <class E, bool kAny>
 hipError_t act_grad(const ActGradArgs& a, hipStream_t s) {
   if (a.N == 0) return hipSuccess;
   if (!a.db) {
     const int64_t n = (int64_t)a.M * ((a.N + 7) / 8);
-    if (n > 0) k_act_grad<E><<<dim3((uint32_t)((n + 255) / 256)), dim3(256), 0, s>>>(a);
+    if (n > 0) k_act_grad<E, kAny><<<dim3((uint32_t)((n + 255) / 256)), dim3(256), 0, s>>>(a);
     return hipGetLastError();
   }
   const uint32_t cols = (uint32_t)((a.N + kSumCols - 1) / kSumCols);
-  k_act_grad_sum<E><<<dim3(cols, (uint32_t)a.chunks), dim3(kSumThreads), 0, s>>>(a);
+  k_act_grad_sum<E, kAny><<<dim3(cols, (uint32_t)a.chunks), dim3(kSumThreads), 0, s>>>(a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.chunks == 1) return e;
   k_bias_grad<E><<<dim3((uint32_t)((a.N + 255) / 256)), dim3(256), 0, s>>>(a);
   return hipGetLastError();
 }
 hipError_t launch_act_grad(int kind, const ActGradArgs& a, hipStream_t s) {
-  return kind == 0 ? act_grad<F32>(a, s) : kind == 1 ? act_grad<F16>(a, s) : act_grad<BF16>(a, s);
+  if (a.dycs == 1)
+    return kind == 0 ? act_grad<F32, false>(a, s) : kind == 1 ? act_grad<F16, false>(a, s) : act_grad<BF16, false>(a, s);
+  return kind == 0 ? act_grad<F32, true>(a, s) : kind == 1 ? act_grad<F16, true>(a, s) : act_grad<BF16, true>(a, s);
 }
 
 }  // namespace llar_ffn

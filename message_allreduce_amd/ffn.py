@@ -6,7 +6,8 @@ the library's (``include/llar.h``); this module checks and marshals arguments.
 Tensors are fp32, fp16 or bf16 device tensors of one type.  ``x`` and the other
 activations have shape (..., width), with leading dimensions that can be viewed
 as one; weights are (n, k).  A matrix may be strided along one axis (a slice of
-a wider buffer, a transposed view, an expanded row).  Nothing is recorded for
+a wider buffer, a transposed view, an expanded row), the incoming gradients
+``dy`` and ``dh`` along both (the gradient of a sum).  Nothing is recorded for
 autograd: ``linear_backward`` and ``gated_ffn_backward`` are the gradients.
 
 ``stream`` is a torch stream (default: the current one of x's device).  Outputs
