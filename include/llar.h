@@ -279,11 +279,13 @@ size_t llar_ffn_workspace(llar_ffn_op op, int64_t m, int64_t n, int64_t k, llar_
  * rows, or NULL.  pre: m x n output that receives x w^T + bias (what the
  * backward pass needs), or NULL.  k == 0 sums nothing; m or n == 0: no-op.
  *
- * Errors of all four calls, with nothing enqueued: LLAR_ERR_ARG for a bad
+ * Errors of all four calls: with nothing enqueued LLAR_ERR_ARG for a bad
  * type, activation, shape or stride, a missing matrix, a misaligned or too
  * small workspace; LLAR_ERR_UNSUPPORTED for a layout other than those above
  * or a dimension above 2^30, or above 2^21 - 8 along an input's contiguous
- * axis; LLAR_ERR_HIP if a launch failed. */
+ * axis.  LLAR_ERR_HIP if a launch failed, after those before it: a launch has
+ * less than 2^32 threads, so that a copied operand and an element-wise gradient
+ * have at most 2^34 elements, and a product 2^33 results in whole 64 x 64 tiles. */
 int llar_linear(const llar_matrix* x, const llar_matrix* w, const void* bias, const llar_matrix* residual,
                 const llar_matrix* out, const llar_matrix* pre, llar_dtype dtype, llar_act act, void* workspace,
                 size_t workspace_bytes, void* stream);

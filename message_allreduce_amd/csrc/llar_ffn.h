@@ -35,6 +35,10 @@ struct GemmArgs {
   int npad;             // row length of a partial plane
 };
 
+// Whether a launch stays below 2^32 threads.  The runtime counts them in 32 bits,
+// and what is beyond would be left out without an error, so every launcher asks.
+inline bool launchable(int64_t groups, int threads) { return groups * threads < (1ll << 32); }
+
 // Tile shapes of the product kernel (rows of x by rows of w by workgroup);
 // see llar_gemm.h.
 enum Tile : int { kTile256 = 0, kTile128 = 1, kTile64 = 2, kTile128x64 = 3, kTileCount = 4 };
@@ -60,8 +64,10 @@ struct PairArgs {
 };
 hipError_t launch_pair(int kind, int tile, int groups, bool w_rows, PairArgs a, hipStream_t s);
 
-// A product with M <= kFewRows rows of k-contiguous x, any alignment; a.batch is 1.
+// A product with M <= kFewRows rows of k-contiguous x and N <= kFewColumns (up to
+// 128 threads a column: 2^31), any alignment; a.batch is 1.
 constexpr int kFewRows = 16;
+constexpr int64_t kFewColumns = 1 << 24;
 hipError_t launch_few(int kind, bool w_rows, bool gated, const GemmArgs& a, hipStream_t s);
 
 // Copies of matrices in whole chunks: lines of `width` elements, `ld` apart,

@@ -129,7 +129,7 @@ int64_t k_tiles(int64_t K, int es) { return cdiv(K, 128 / es); }
 Shape choose(int64_t M, int64_t N, int64_t K, int segs, int outs, bool gated, int es, bool few, bool w_rows) {
   Shape s{false, kTile64, 1, 1, 0};
   if (M == 0 || N == 0) return s;  // nothing to launch
-  if (few && M <= kFewRows && outs == 1) {
+  if (few && M <= kFewRows && N <= kFewColumns && outs == 1) {
     s.few = true;
     if (w_rows) {
       // two workgroups a CU want 512; a split leaves every wave four steps

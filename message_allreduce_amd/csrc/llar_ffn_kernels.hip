@@ -35,6 +35,7 @@ hipError_t launch_pair(int kind, int tile, int groups, bool w_rows, PairArgs a, 
 // ---- few rows ------------------------------------------------------------------------
 template <class E, bool kGated>
 hipError_t few(bool w_rows, const GemmArgs& a, hipStream_t s) {
+  if (a.N > kFewColumns) return hipErrorInvalidConfiguration;
   if (w_rows) {
     constexpr int kC = 4, kWaves = 8;
     const int64_t grid = ((int64_t)a.N + 16 * kC - 1) / (16 * kC) * a.splits;
@@ -87,6 +88,7 @@ __global__ __launch_bounds__(256) void k_repack(RepackArgs a) {
 hipError_t launch_repack(int kind, const RepackArgs& a, hipStream_t s) {
   const dim3 grid((uint32_t)a.first[a.count]), block(256);
   if (a.first[a.count] == 0) return hipSuccess;
+  if (!launchable(a.first[a.count], 256)) return hipErrorInvalidConfiguration;
   if (kind == 0)
     k_repack<F32><<<grid, block, 0, s>>>(a);
   else if (kind == 1)
@@ -127,9 +129,10 @@ __global__ __launch_bounds__(256) void k_join(GemmArgs a) {
 
 template <class E>
 hipError_t join(bool gated, const GemmArgs& a, hipStream_t s) {
-  const int64_t n = (int64_t)a.batch * a.M * ((a.N + 3) / 4);
+  const int64_t n = (int64_t)a.batch * a.M * ((a.N + 3) / 4), groups = (n + 255) / 256;
   if (n == 0) return hipSuccess;
-  const dim3 grid((uint32_t)((n + 255) / 256));
+  if (!launchable(groups, 256)) return hipErrorInvalidConfiguration;
+  const dim3 grid((uint32_t)groups);
   if (gated)
     k_join<E, true><<<grid, dim3(256), 0, s>>>(a);
   else
@@ -192,9 +195,10 @@ __global__ __launch_bounds__(256) void k_gate_grad(GateGradArgs a) {
 
 template <class E>
 hipError_t gate_grad(const GateGradArgs& a, hipStream_t s) {
-  const int64_t n = (int64_t)a.M * ((a.N + 7) / 8);
+  const int64_t n = (int64_t)a.M * ((a.N + 7) / 8), groups = (n + 255) / 256;
   if (n == 0) return hipSuccess;
-  const dim3 grid((uint32_t)((n + 255) / 256)), block(256);
+  if (!launchable(groups, 256)) return hipErrorInvalidConfiguration;
+  const dim3 grid((uint32_t)groups), block(256);
   if (a.dhcs == 1)
     k_gate_grad<E, false><<<grid, block, 0, s>>>(a);
   else
@@ -293,11 +297,13 @@ template <class E, bool kAny>
 hipError_t act_grad(const ActGradArgs& a, hipStream_t s) {
   if (a.N == 0) return hipSuccess;
   if (!a.db) {
-    const int64_t n = (int64_t)a.M * ((a.N + 7) / 8);
-    if (n > 0) k_act_grad<E, kAny><<<dim3((uint32_t)((n + 255) / 256)), dim3(256), 0, s>>>(a);
+    const int64_t groups = ((int64_t)a.M * ((a.N + 7) / 8) + 255) / 256;
+    if (!launchable(groups, 256)) return hipErrorInvalidConfiguration;
+    if (groups > 0) k_act_grad<E, kAny><<<dim3((uint32_t)groups), dim3(256), 0, s>>>(a);
     return hipGetLastError();
   }
   const uint32_t cols = (uint32_t)((a.N + kSumCols - 1) / kSumCols);
+  if (!launchable((int64_t)cols * a.chunks, kSumThreads)) return hipErrorInvalidConfiguration;
   k_act_grad_sum<E, kAny><<<dim3(cols, (uint32_t)a.chunks), dim3(kSumThreads), 0, s>>>(a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.chunks == 1) return e;

@@ -11,7 +11,7 @@ hipError_t launch_one(const GemmArgs& a, hipStream_t s) {
   const int64_t tiles = ((int64_t)a.M + Shape::TM - 1) / Shape::TM * (((int64_t)a.N + tn_cols - 1) / tn_cols);
   const int64_t grid = tiles * a.batch * a.splits;
   if (grid <= 0) return hipSuccess;
-  if (grid > 0x7fffffff) return hipErrorInvalidValue;
+  if (!launchable(grid, Shape::kAllThreads)) return hipErrorInvalidConfiguration;
   if constexpr (E::kind == 0)
     k_gemm32<kXRows, kWRows, Shape, kGated><<<dim3((uint32_t)grid), dim3(Shape::kAllThreads), 0, s>>>(a);
   else

@@ -15,7 +15,7 @@ template <class E, bool kWRows, class Shape>
 hipError_t launch_one(PairArgs& a, hipStream_t s) {
   const int64_t first = workgroups<Shape>(a.dw_first ? a.dw : a.dx);
   const int64_t grid = first + workgroups<Shape>(a.dw_first ? a.dx : a.dw);
-  if (grid > 0x7fffffff) return hipErrorInvalidValue;
+  if (!launchable(grid, Shape::kAllThreads)) return hipErrorInvalidConfiguration;
   a.first = (int)first;
   k_gemm_pair<E, kWRows, Shape><<<dim3((uint32_t)grid), dim3(Shape::kAllThreads), 0, s>>>(a);
   return hipGetLastError();
