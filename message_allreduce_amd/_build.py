@@ -79,16 +79,38 @@ def build(verbose: bool = False) -> str:
     return LIB
 
 
-def _build_binding() -> None:
-    """The feed-forward operators' Python entry points (plain C against libllar.so and the CPython API)."""
+def _c_compiler():
+    """gcc, or the clang that comes with hipcc."""
+    for name in ("gcc", "cc", "clang", "amdclang", "/opt/rocm/llvm/bin/clang"):
+        path = shutil.which(name)
+        if path:
+            return path
+    return None
+
+
+def _build_binding() -> bool:
+    """The feed-forward operators' Python entry points (plain C against libllar.so and the CPython API).
+
+    Only they need a C compiler and Python's headers.  Where those are missing the rest stays usable: no binding
+    is left (an older one would not fit the library), a line says so, and the operators raise when called."""
+    python = sysconfig.get_paths()["include"]
+    compiler = _c_compiler()
+    if compiler is None or not os.path.exists(os.path.join(python, "Python.h")):
+        if os.path.exists(BINDING):
+            os.remove(BINDING)
+        print("not built: %s (no %s), so linear, gated_ffn and their backward passes are not available from Python"
+              % (os.path.basename(BINDING), "C compiler" if compiler is None else "Python.h in " + python),
+              file=sys.stderr)
+        return False
     tmp = BINDING + ".tmp%d" % os.getpid()
-    cmd = [shutil.which("gcc") or "gcc", "-O2", "-std=c11", "-Wall", "-fPIC", "-shared", "-I", INCLUDE,
-           "-I", sysconfig.get_paths()["include"], os.path.join(CSRC, "llar_py.c"), "-o", tmp,
+    cmd = [compiler, "-O2", "-std=c11", "-Wall", "-fPIC", "-shared", "-I", INCLUDE,
+           "-I", python, os.path.join(CSRC, "llar_py.c"), "-o", tmp,
            "-L", HERE, "-l:libllar.so", "-Wl,-rpath,$ORIGIN"]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError("building the binding failed:\n%s\n%s" % (" ".join(cmd), res.stderr[-4000:]))
     os.replace(tmp, BINDING)
+    return True
 
 
 if __name__ == "__main__":

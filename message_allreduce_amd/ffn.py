@@ -33,7 +33,8 @@ def _setup():
     try:
         from . import _llar_py as native
     except ImportError as e:
-        raise LlarError(-4, "_llar_py is not built (run __graft_entry__.build()): %s" % e) from None
+        raise LlarError(-4, "_llar_py is not built (run __graft_entry__.build(); it needs a C compiler and "
+                        "Python.h): %s" % e) from None
     # the current device and stream's handle, without building objects where torch offers that
     device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
     stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
