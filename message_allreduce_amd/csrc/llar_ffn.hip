@@ -256,9 +256,7 @@ struct Packer {
   int es;
   Carve* c;
   Packer(int es_, Carve* c_) : es(es_), c(c_) {}
-  // a copy that another product of the call has made already is taken again
-  void add(Operand& o, bool force = false) {
-    if (!force && chunks_whole(o, es)) return;
+  void add(Operand& o) {
     const int i = a.count++;
     const int64_t lines = o.by_rows ? o.k : o.rows, width = o.by_rows ? o.rows : o.k;
     a.src[i] = o.p;
@@ -306,8 +304,8 @@ void pack(Product& p, int es, Packer& k) {
   bool x = false, w = false;
   for (int i = 0; i < p.n_x; i++) x = x || !chunks_whole(p.x[i], es);
   for (int i = 0; i < p.n_w; i++) w = w || !chunks_whole(p.w[i], es);
-  for (int i = 0; x && i < p.n_x; i++) k.add(p.x[i], true);
-  for (int i = 0; w && i < p.n_w; i++) k.add(p.w[i], true);
+  for (int i = 0; x && i < p.n_x; i++) k.add(p.x[i]);
+  for (int i = 0; w && i < p.n_w; i++) k.add(p.w[i]);
 }
 
 GemmArgs args_of(const Product& p, int splits, float* partial) {
@@ -557,7 +555,7 @@ int llar_linear_backward(const llar_matrix* dy, const llar_matrix* x, const llar
   Packer k(es, &c);
   if (dx) pack(px, es, k);
   if (dw) {
-    if (px.x[0].p != dz.p) pw.x[0] = px.x[0].t();
+    if (px.x[0].p != dz.p) pw.x[0] = px.x[0].t();  // the copy that dx's product reads
     pack(pw, es, k);
   }
   LLAR_TRY(k.run(dtype, (hipStream_t)stream));
