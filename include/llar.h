@@ -224,7 +224,8 @@ int llar_all_gather(llar_comm* h, const void* const* inputs, void* const* outs, 
  * itself at most; of inputs below 2^-110 up to 2^-133 is lost), the
  * epilogue in binary32, each output rounded once.  The backward passes round
  * the gradient that both of their products read (dz, or dg and du) to the I/O
- * type once.  No atomics: the same inputs and shapes give the same bits.
+ * type once, as the matrix units take 16-bit operands (in binary16 it has that
+ * type's range: infinite from 65520, zero below 2^-25); db sums it unrounded.  No atomics: the same inputs and shapes give the same bits.
  *
  * These calls need no communicator, allocate nothing and only enqueue kernels
  * on `stream` (they may be captured into graphs).  All pointers are on the

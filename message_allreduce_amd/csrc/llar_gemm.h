@@ -929,7 +929,7 @@ __global__ __launch_bounds__(Shape::kAllThreads) void k_gemm(GemmArgs a) {
 // ---- binary32 ----------------------------------------------------------------------
 // R rows by 32 k of one operand, as three planes of bfloat16 parts in LDS:
 // [plane][row][4 chunks of 8 k], chunk c of a row at c ^ key(row).  A thread
-// fetches its share of the tile into registers one tile ahead, and cuts it into
+// fetches its share of the tile into registers one tile ahead, and splits it into
 // parts when it writes it, once for all the waves that multiply it.
 template <bool kRows, int R, int NT, int F, bool kPerm>
 struct Parts {
@@ -1023,9 +1023,9 @@ struct Parts {
 
 // The same product for binary32: one LDS buffer, registers one tile ahead; the
 // other workgroups of the CU multiply while this one writes.  Bound by the six
-// products (matrix units 63 % busy) and the cutting beside them: 4096^3 660 us (208
-// TF), 512 x 2048 x 2048 33 us.  us, 128 / 64, best groups: 2048 x 2048 x 2048 90 / 110,
-// 512 x 4096 x 2048 56 / 57, 128 x 2048 x 2048 - / 16.
+// products (matrix units 61 % busy) and the splitting beside them: 4096^3 647 us (212
+// TF), 512 x 2048 x 2048 33 us, 2048^3 89, 128 x 2048 x 2048 17.  us, 128 / 64, best
+// groups (with parts cut): 2048 x 2048 x 2048 90 / 110, 512 x 4096 x 2048 56 / 57.
 template <class Shape>
 constexpr int kGemm32Lds = Shape::kGroups * (Shape::TM + Shape::TN) * 192;
 
@@ -1072,7 +1072,7 @@ __device__ __forceinline__ void gemm32_body(const GemmArgs& a, char* smem, int w
   };
   const uint32_t xbase = X::frag_at(wm * 16 * FX), wbase = W::frag_at(wn * 16 * FW);
   // group g takes the tiles t0 + g, t0 + g + G, ...; the second half of the
-  // groups runs half a round behind, cutting while the first half multiplies
+  // groups runs half a round behind, splitting while the first half multiplies
   const int rounds = (t1 - t0 + G - 1) / G;
   const bool late = group >= (G + 1) / 2;
   fetch(t0 + group);
