@@ -267,7 +267,8 @@ enum {
                                   more apart: adds room for copies */
   LLAR_LAYOUT_X_COLUMNS = 2,   /* x's columns are contiguous, not its rows (a transposed view) */
   LLAR_LAYOUT_W_COLUMNS = 4,   /* so are the weights' */
-  LLAR_LAYOUT_DY_COLUMNS = 8   /* linear_backward's dy's rows are not contiguous */
+  LLAR_LAYOUT_DY_COLUMNS = 8,  /* linear_backward's dy's rows are not contiguous */
+  LLAR_LAYOUT_X_VALUES = 16    /* llar_int8_workspace: x is given as values, without scales */
 };
 
 /* Bytes of workspace a call needs for m tokens, n outputs and k inputs (0 is
@@ -319,6 +320,40 @@ int llar_gated_ffn_backward(const llar_matrix* dh, const llar_matrix* x, const l
                             const llar_matrix* w_up, const llar_matrix* gate, const llar_matrix* up,
                             const llar_matrix* dx, const llar_matrix* dw_gate, const llar_matrix* dw_up,
                             llar_dtype dtype, llar_act act, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---- products of 8-bit whole numbers ------------------------------------ *
+ * The same two products for decoding with weights of half the bytes: tokens
+ * and output channels are rows of whole numbers -127 .. 127 with one binary32
+ * scale each.  Sums are whole numbers and exact (k up to 2^17 - 1); a sum times
+ * both scales, the epilogue in binary32, one rounding to `dtype`.  Streams,
+ * workspaces, overlap, errors and sizes as for the calls above. */
+
+/* scale[i] = max over j of |x[i][j]| / 127, rounded to binary32, and q[i][j] = the
+ * whole number nearest to x[i][j] / scale[i], ties to even, at most 127 in
+ * magnitude.  A row of zeros has scale 0 and zeros; a row with an infinity or
+ * a NaN has scale NaN and zeros, so that what it is multiplied into is NaN.
+ * x: any strides, of type dtype; q: int8, contiguous rows; scale: m contiguous. */
+int llar_quantize_rows(const llar_matrix* x, const llar_matrix* q, float* scale, llar_dtype dtype, void* stream);
+
+/* Bytes of workspace of llar_linear_int8 (op LLAR_OP_LINEAR) or
+ * llar_gated_ffn_int8 (LLAR_OP_GATED_FFN); layout: LLAR_LAYOUT_X_VALUES and, for
+ * 8-bit matrices, LLAR_LAYOUT_UNALIGNED. */
+size_t llar_int8_workspace(llar_ffn_op op, int64_t m, int64_t n, int64_t k, int layout);
+
+/* out = act(s_x s_w (x w^T) + bias) + residual.  x: int8 rows with x_scale (m
+ * elements), or, with x_scale NULL, values of type dtype in any strides, which
+ * the call quantises as llar_quantize_rows does.  w: n x k, int8; w_scale: n
+ * elements.  8-bit matrices have contiguous rows.  bias, residual and out are
+ * of type dtype, as for llar_linear. */
+int llar_linear_int8(const llar_matrix* x, const float* x_scale, const llar_matrix* w, const float* w_scale,
+                     const void* bias, const llar_matrix* residual, const llar_matrix* out, llar_dtype dtype,
+                     llar_act act, void* workspace, size_t workspace_bytes, void* stream);
+
+/* out = act(s_x s_gate (x w_gate^T)) * (s_x s_up (x w_up^T)); the weights have the
+ * same row stride. */
+int llar_gated_ffn_int8(const llar_matrix* x, const float* x_scale, const llar_matrix* w_gate, const llar_matrix* w_up,
+                        const float* gate_scale, const float* up_scale, const llar_matrix* out, llar_dtype dtype,
+                        llar_act act, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Free all resources (synchronises the device first).  NULL is a no-op. */
 int llar_destroy(llar_comm* h);

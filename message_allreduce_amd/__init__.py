@@ -32,6 +32,7 @@ __all__ = [
     "llar_get_timing", "llar_wallclock_hz", "llar_launch_geometry", "llar_floor_measure",
     "llar_status_string", "llar_last_error", "llar_get_trace", "llar_get_pipeline_trace", "Communicator", "EXPORTED_SYMBOLS",
     "ACTIVATIONS", "linear", "linear_backward", "gated_ffn", "gated_ffn_backward",
+    "quantize_rows", "linear_int8", "gated_ffn_int8",
 ]
 
 FP32, FP16, BF16 = 0, 1, 2
@@ -49,7 +50,7 @@ EXPORTED_SYMBOLS = (
     "llar_get_timing", "llar_wallclock_hz", "llar_launch_geometry", "llar_floor_measure",
     "llar_get_trace", "llar_get_pipeline_trace", "llar_send_recv", "llar_reduce_scatter", "llar_all_gather",
     "llar_allreduce_noalloc", "llar_ffn_workspace", "llar_linear", "llar_linear_backward", "llar_gated_ffn",
-    "llar_gated_ffn_backward",
+    "llar_gated_ffn_backward", "llar_quantize_rows", "llar_int8_workspace", "llar_linear_int8", "llar_gated_ffn_int8",
 )
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -104,6 +105,10 @@ def lib() -> ctypes.CDLL:
         "llar_linear_backward": (i32, [vp] * 7 + [i32, i32, vp, sz, vp]),
         "llar_gated_ffn": (i32, [vp] * 6 + [i32, i32, vp, sz, vp]),
         "llar_gated_ffn_backward": (i32, [vp] * 9 + [i32, i32, vp, sz, vp]),
+        "llar_quantize_rows": (i32, [vp] * 3 + [i32, vp]),
+        "llar_int8_workspace": (sz, [i32, i64, i64, i64, i32]),
+        "llar_linear_int8": (i32, [vp] * 7 + [i32, i32, vp, sz, vp]),
+        "llar_gated_ffn_int8": (i32, [vp] * 7 + [i32, i32, vp, sz, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)
@@ -430,4 +435,5 @@ class Communicator:
             pass
 
 
-from .ffn import ACTIVATIONS, gated_ffn, gated_ffn_backward, linear, linear_backward  # noqa: E402
+from .ffn import (ACTIVATIONS, gated_ffn, gated_ffn_backward, gated_ffn_int8, linear, linear_backward,  # noqa: E402
+                  linear_int8, quantize_rows)

@@ -21,7 +21,7 @@ LIB = os.path.join(HERE, "libllar.so")
 BINDING = os.path.join(HERE, "_llar_py.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 SOURCES = ["llar_kernels.hip", "llar_multi.hip", "llar_host.hip", "llar_floor.hip", "llar_ffn.hip",
-           "llar_ffn_kernels.hip"]
+           "llar_ffn_kernels.hip", "llar_int8.hip", "llar_int8_kernels.hip"]
 # the matrix product, compiled once for each element type and operand order
 INSTANCES = [("llar_gemm_inst.hip", "llar_gemm_%s_%d%d" % (e.lower(), x, w),
               ["-DLLAR_ELEM=" + e, "-DLLAR_XR=%d" % x, "-DLLAR_WR=%d" % w])
@@ -29,6 +29,7 @@ INSTANCES = [("llar_gemm_inst.hip", "llar_gemm_%s_%d%d" % (e.lower(), x, w),
 # and both products of a backward pass in one launch
 INSTANCES += [("llar_gemm_pair.hip", "llar_gemm_pair_%s_%d" % (e.lower(), w), ["-DLLAR_ELEM=" + e, "-DLLAR_WR=%d" % w])
               for e in ("F32", "F16", "BF16") for w in (0, 1)]
+INSTANCES += [("llar_gemm_int8.hip", "llar_gemm_int8_" + e.lower(), ["-DLLAR_ELEM=" + e]) for e in ("F32", "F16", "BF16")]
 ARCH = "gfx950"
 
 CFLAGS = [

@@ -1,0 +1,171 @@
+// llar_chunk.h -- 16-row products whose weights go from memory straight to the
+// matrix units' operand registers, for any type of operand: what the 8-bit and the
+// experts' kernels for few tokens share.
+//
+// A chunk is a lane's 16 bytes of a fragment: 16 rows of 64 bytes, lane l holds
+// bytes 16 (l / 16) .. + 15 of row l % 16.  That is a whole matrix instruction's
+// operand for 8- and 16-bit numbers and four of them for binary32, whose own
+// instruction keeps infinities where they are; the order of k within 64 bytes is
+// the same for both operands and so does not matter.
+#pragma once
+#include "llar_gemm.h"
+
+namespace llar_ffn {
+
+typedef u32x4 __attribute__((aligned(1))) any_u32x4;
+
+template <class E>
+struct Chunk {
+  static constexpr int ES = sizeof(typename E::X), CE = 16 / ES;
+  u32x4 v;
+  __device__ __forceinline__ void zero() { v = u32x4{0u, 0u, 0u, 0u}; }
+  __device__ __forceinline__ void load(const char* p) { v = *(const any_u32x4*)p; }
+  // `left` elements exist, none if it is not positive
+  __device__ __forceinline__ void load(const char* p, int64_t left) {
+    if (left >= CE) {
+      load(p);
+      return;
+    }
+    union {
+      typename E::X t[CE];
+      u32x4 q;
+    } u;
+    u.q = u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int i = 0; i < CE; i++)
+      if (i < left) u.t[i] = ((const typename E::X*)p)[i];
+    v = u.q;
+  }
+};
+
+template <class E>
+__device__ __forceinline__ f32x4 mma_chunk(const Chunk<E>& a, const Chunk<E>& b, f32x4 c) {
+  if constexpr (E::kParts) {
+#pragma unroll
+    for (int i = 0; i < 4; i++)
+      c = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(a.v[i]), __uint_as_float(b.v[i]), c, 0, 0, 0);
+    return c;
+  } else {
+    return mma<E>(Frag<E>{__builtin_bit_cast(s16x8, a.v)}, Frag<E>{__builtin_bit_cast(s16x8, b.v)}, c);
+  }
+}
+
+// A sum's bits, of an integer for 8-bit operands, added to another's.
+template <class E>
+__device__ __forceinline__ float add_sums(float a, float b) {
+  if constexpr (E::kInt8) return __int_as_float(__float_as_int(a) + __float_as_int(b));
+  return a + b;
+}
+
+// P planes of 16 weight rows times NB blocks of 16 rows of x, over the steps
+// i0, i0 + stride, ... below i1 of k: a step is 64 G bytes of a row, G chunks a
+// lane.  w and x point at the lane's first chunk of step 0 (16 G q bytes into the
+// row); a row of x that is not live counts as zeros and is not read.  U steps'
+// loads are in flight.  acc[p][b], lane (r, q): row 16 b + r of x, weight rows 4 q
+// .. 4 q + 3 of plane p.
+template <class E, int P, int NB, int G, int U>
+__device__ __forceinline__ void multiply_steps(f32x4 (&acc)[P][NB], const char* const (&w)[P], const char* const (&x)[NB],
+                                               const bool (&live)[NB], int K, int i0, int i1, int stride) {
+  typedef Chunk<E> C;
+  constexpr int kStep = 4 * C::CE * G;  // elements
+  const int q = (threadIdx.x & 63) >> 4;
+  const int full = min(i1, K / kStep);
+  int i = i0;
+  for (; i + (U - 1) * stride < full; i += U * stride) {
+    C wv[U][P][G], xv[U][NB][G];
+#pragma unroll
+    for (int s = 0; s < U; s++)
+#pragma unroll
+      for (int p = 0; p < P; p++)
+#pragma unroll
+        for (int g = 0; g < G; g++) wv[s][p][g].load(w[p] + (int64_t)(i + s * stride) * (64 * G) + g * 16);
+#pragma unroll
+    for (int s = 0; s < U; s++)
+#pragma unroll
+      for (int b = 0; b < NB; b++)
+#pragma unroll
+        for (int g = 0; g < G; g++) {
+          xv[s][b][g].zero();
+          if (live[b]) xv[s][b][g].load(x[b] + (int64_t)(i + s * stride) * (64 * G) + g * 16);
+        }
+#pragma unroll
+    for (int s = 0; s < U; s++)
+#pragma unroll
+      for (int g = 0; g < G; g++)
+#pragma unroll
+        for (int p = 0; p < P; p++)
+#pragma unroll
+          for (int b = 0; b < NB; b++) acc[p][b] = mma_chunk<E>(wv[s][p][g], xv[s][b][g], acc[p][b]);
+  }
+  for (; i < i1; i += stride) {
+    C wv[P][G], xv[NB][G];
+#pragma unroll
+    for (int g = 0; g < G; g++) {
+      const int64_t left = K - (int64_t)i * kStep - (q * G + g) * C::CE;
+#pragma unroll
+      for (int p = 0; p < P; p++) wv[p][g].load(w[p] + (int64_t)i * (64 * G) + g * 16, left);
+#pragma unroll
+      for (int b = 0; b < NB; b++) {
+        xv[b][g].zero();
+        if (live[b]) xv[b][g].load(x[b] + (int64_t)i * (64 * G) + g * 16, left);
+      }
+    }
+#pragma unroll
+    for (int g = 0; g < G; g++)
+#pragma unroll
+      for (int p = 0; p < P; p++)
+#pragma unroll
+        for (int b = 0; b < NB; b++) acc[p][b] = mma_chunk<E>(wv[p][g], xv[b][g], acc[p][b]);
+  }
+}
+
+template <class E, int P, int NB>
+__device__ __forceinline__ void clear(f32x4 (&acc)[P][NB]) {
+#pragma unroll
+  for (int p = 0; p < P; p++)
+#pragma unroll
+    for (int b = 0; b < NB; b++) acc[p][b] = f32x4{0.f, 0.f, 0.f, 0.f};  // an integer's zeros too
+}
+
+// ---- rows of whole numbers -----------------------------------------------------------
+// q = x / scale rounded to the nearest, ties to even, where scale is the row's
+// largest magnitude / 127.  The product with the reciprocal can be off by one next
+// to a half; the remainder x - q scale is exact in binary32 (it is a multiple of
+// half of scale's last bit and at most about half of scale), and decides.
+struct Quantizer {
+  float scale, inv, half, lift;
+  // top: the largest magnitude's bits, a NaN above infinity
+  __device__ __forceinline__ explicit Quantizer(uint32_t top) {
+    const float t = __uint_as_float(top);
+    scale = top >= 0x7f800000u ? __builtin_nanf("") : t / 127.f;
+    // tiny rows are lifted, so that the reciprocal exists
+    lift = scale < 0x1p-90f ? 0x1p60f : 1.f;
+    const float s = scale * lift;
+    inv = s > 0.f ? 1.f / s : 0.f;  // a row of zeros, or with a NaN: zeros
+    half = 0.5f * s;
+  }
+  __device__ __forceinline__ int operator()(float x) const {
+    if (!(inv > 0.f)) return 0;
+    x *= lift;
+    float r = rintf(x * inv);
+    const float d = fmaf(-r, half + half, x), m = fabsf(d);
+    const bool odd = (int)r & 1;
+    if (m > half || (m == half && odd)) r += d > 0.f ? 1.f : -1.f;
+    return (int)fminf(fmaxf(r, -127.f), 127.f);
+  }
+};
+__device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+
+// Four whole numbers in a word.
+__device__ __forceinline__ uint32_t pack4(int a, int b, int c, int d) {
+  return (uint32_t)(a & 255) | (uint32_t)(b & 255) << 8 | (uint32_t)(c & 255) << 16 | (uint32_t)d << 24;
+}
+
+template <int n>
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+#pragma unroll
+  for (int d = n / 2; d > 0; d >>= 1) v = max(v, (uint32_t)__shfl_xor((int)v, d));
+  return v;
+}
+
+}  // namespace llar_ffn

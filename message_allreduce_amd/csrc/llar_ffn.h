@@ -33,6 +33,8 @@ struct GemmArgs {
   int segs, batch, splits;
   int act;
   int npad;             // row length of a partial plane
+  const float* xscale;  // 8-bit operands: of every row of x, and of w[0] and w[1]
+  const float* wscale[2];
 };
 
 // Whether a launch stays below 2^32 threads.  The runtime counts them in 32 bits,
@@ -54,6 +56,8 @@ struct GemmPlan {
 };
 
 hipError_t launch_gemm(const GemmPlan& p, const GemmArgs& a, hipStream_t s);
+// The same with 8-bit operands, both k-contiguous, and outputs of type p.kind.
+hipError_t launch_gemm_int8(const GemmPlan& p, const GemmArgs& a, hipStream_t s);
 
 // The products of a backward pass together: dx from k-contiguous rows of dz, dw
 // from dz and x both row-contiguous.

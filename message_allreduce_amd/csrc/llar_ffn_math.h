@@ -13,29 +13,46 @@ namespace llar_ffn {
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
+// T: the type of results, X: of a product's operands.  kParts: operands are
+// multiplied as three bfloat16 parts.
 struct F32 {
   typedef float T;
+  typedef float X;
   static constexpr int kind = 0;
+  static constexpr bool kParts = true, kInt8 = false;
   static __device__ __forceinline__ float to(float v) { return v; }
   static __device__ __forceinline__ float from(float v) { return v; }
 };
 struct F16 {
   typedef _Float16 T;
+  typedef _Float16 X;
   static constexpr int kind = 1;
+  static constexpr bool kParts = false, kInt8 = false;
   static __device__ __forceinline__ float to(_Float16 v) { return (float)v; }
   static __device__ __forceinline__ _Float16 from(float v) { return (_Float16)v; }
 };
 struct BF16 {
   typedef __bf16 T;
+  typedef __bf16 X;
   static constexpr int kind = 2;
+  static constexpr bool kParts = false, kInt8 = false;
   static __device__ __forceinline__ float to(__bf16 v) {
     return __builtin_bit_cast(float, (uint32_t)__builtin_bit_cast(uint16_t, v) << 16);
   }
   static __device__ __forceinline__ __bf16 from(float v) { return (__bf16)v; }
+};
+
+// Products of 8-bit whole numbers, summed in 32 bits (the accumulator's bits are
+// those of an int until they are scaled), with results of Out's type.
+template <class Out>
+struct Int8 : Out {
+  typedef int8_t X;
+  static constexpr bool kParts = false, kInt8 = true;
 };
 
 // n neighbouring values moved to or from memory: one access at the element's

@@ -61,6 +61,22 @@ __device__ __forceinline__ f32x4 mma<F16>(const Frag<F16>& a, const Frag<F16>& b
   return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a.v), __builtin_bit_cast(f16x8, b.v), c, 0,
                                                 0, 0);
 }
+// 16 x 64 fragments of 8-bit numbers: lane l holds row l % 16, k = 16 (l / 16) ..
+// + 15, the same bytes of a row as 16-bit lanes hold.  c's bits are integers'.
+#define LLAR_MMA_INT8(Out) \
+  template <> \
+  __device__ __forceinline__ f32x4 mma<Int8<Out>>(const Frag<Int8<Out>>& a, const Frag<Int8<Out>>& b, f32x4 c) { \
+    return mma_int8(a.v, b.v, c); \
+  }
+__device__ __forceinline__ f32x4 mma_int8(s16x8 a, s16x8 b, f32x4 c) {
+  return __builtin_bit_cast(f32x4, __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, a),
+                                                                         __builtin_bit_cast(i32x4, b),
+                                                                         __builtin_bit_cast(i32x4, c), 0, 0, 0));
+}
+LLAR_MMA_INT8(F32)
+LLAR_MMA_INT8(F16)
+LLAR_MMA_INT8(BF16)
+
 // Six of the nine products of parts, small ones first: 6 bfloat16 products at 16
 // times the binary32 unit's rate.  mid is at most 2^-8 of its value and lo 2^-17,
 // so the three left out are at most 2^-24 of the whole, as much as binary32
@@ -112,8 +128,8 @@ __device__ __forceinline__ Frag<F32> split3(const float (&x)[8]) {
   return f;
 }
 
-// ---- one 16-bit operand's tile in LDS -------------------------------------------------
-// R rows by 64 k, in one of two orders.
+// ---- one 16-bit (or 8-bit) operand's tile in LDS ----------------------------------------
+// R rows by 64 k (128), in one of two orders.
 //
 // k-contiguous source: [row][8 chunks of 16 bytes], chunk c of a row stored at
 // position c ^ key(row), so that the 16 rows of a fragment read the same chunk
@@ -130,9 +146,8 @@ template <class E, bool kRows, int R, int NT, int F, bool kPerm>
 struct Operand {
   static constexpr bool kByRows = kRows, kSpread = kPerm;
   static constexpr int kRun = F;
-  typedef typename E::T T;
   static constexpr int kThreads = NT;
-  static constexpr int ES = sizeof(T);
+  static constexpr int ES = sizeof(typename E::X);
   static constexpr int CE = 16 / ES;          // elements of a chunk
   static constexpr int BK = 128 / ES;         // k of a tile
   static constexpr int kBytes = R * 128;
@@ -248,6 +263,10 @@ __device__ __forceinline__ Frag<E> read_frag(lds_char* lds, uint32_t base, int f
   return out;
 }
 
+// What a whole sum stands for: three roundings of binary32, in an order that
+// neither overflows nor vanishes where the value does not.
+__device__ __forceinline__ float scaled(int sum, float xs, float ws) { return (float)sum * xs * ws; }
+
 // Applies the epilogue to n neighbours of one output row and stores them.
 // acc0: the sums (gated: of the first projection), acc1: of the second.
 template <class E, bool kGated, int n>
@@ -354,7 +373,7 @@ __device__ __forceinline__ void store_results(const GemmArgs& a, f32x4 (&acc)[kX
   bool bare = !kGated && kSpread &&
               (a.splits > 1 || (!a.z[0] && a.act == kActNone && !add_bias && !add_resid));
   bool again = false;
-  if constexpr (E::kind == 0) {
+  if constexpr (E::kParts) {
 #pragma unroll
     for (int h = 0; h < kXParts; h++)
 #pragma unroll
@@ -427,7 +446,7 @@ __device__ __forceinline__ void store_results(const GemmArgs& a, f32x4 (&acc)[kX
               acc[kXParts == 2 ? h : 0][p][i + h * kPer][j];
         }
     settle();
-    if constexpr (E::kind == 0) {
+    if constexpr (E::kParts) {
       // most calls have no such sum: the wave looks before it goes through them
       if (again) {
 #pragma clang loop unroll(disable)
@@ -541,7 +560,7 @@ __device__ __forceinline__ void store_results(const GemmArgs& a, f32x4 (&acc)[kX
 
 // Adds the groups' sums, in their order, into the first group's; false for the
 // others, which are done.
-template <class Shape, int kLds, int A, int B, int FX, int FW>
+template <class E, class Shape, int kLds, int A, int B, int FX, int FW>
 __device__ __forceinline__ bool join_groups(f32x4 (&acc)[A][B][FX][FW], lds_char* lds) {
   constexpr int G = Shape::kGroups, kFrags = A * B * FX * FW;
   if constexpr (G == 1) return true;
@@ -562,7 +581,12 @@ __device__ __forceinline__ bool join_groups(f32x4 (&acc)[A][B][FX][FW], lds_char
     for (int i = 0; i < kFrags; i++) {
       const f32x4 v = *(LLAR_LDS f32x4*)(lds + ((g * kFrags + i) * Shape::kThreads + t) * 16);
 #pragma unroll
-      for (int e = 0; e < 4; e++) flat[i][e] += v[e];
+      for (int e = 0; e < 4; e++) {
+        if constexpr (E::kInt8)
+          flat[i][e] = __int_as_float(__float_as_int(flat[i][e]) + __float_as_int(v[e]));
+        else
+          flat[i][e] += v[e];
+      }
     }
   return true;
 }
@@ -700,7 +724,7 @@ __device__ __forceinline__ void gemm_body(const GemmArgs& a, char* smem, int wg,
   // sums follow: its loads then overlap the first tiles', and the results need
   // no pass through LDS (8192 x 8192 x 3584 bf16 with a bias: 361 us, now 334).
   auto begin = [&] {
-    if (kGated || a.splits > 1 || group > 0) return;
+    if (E::kInt8 || kGated || a.splits > 1 || group > 0) return;
     const int lane = threadIdx.x & 63, q = lane >> 4;
     constexpr int kRunLen = kSpread ? (4 * FW < 8 ? 4 * FW : 8) : 4;
     const bool resid = starts_with_resid(a) && !later;
@@ -726,7 +750,7 @@ __device__ __forceinline__ void gemm_body(const GemmArgs& a, char* smem, int wg,
   };
 
   const uint32_t xbase = frag_base<X>(wm * 16 * FX), wbase = frag_base<W>(wn * 16 * FW);
-  constexpr int KK = BK / 32;
+  constexpr int KK = BK * ES / 64;
   if constexpr (kPaired) {
     // Two groups of four waves (one a SIMD) take turns: while one multiplies a
     // quarter of its wave tiles (one part of x by one of w), the other reads its
@@ -914,14 +938,42 @@ __device__ __forceinline__ void gemm_body(const GemmArgs& a, char* smem, int wg,
     wait_loads<0>();
   }
 
-  if (!join_groups<Shape, G * kStages * kBuf>(acc, (lds_char*)smem)) return;
-  store_results<E, kXRows, kWRows, kGated, Shape, kXParts, kWParts, kSpread, G * kStages * kBuf, true>(
+  if (!join_groups<E, Shape, G * kStages * kBuf>(acc, (lds_char*)smem)) return;
+  if constexpr (E::kInt8) {
+    // whole sums become values; a share of them is joined with the others' first
+    int lane = threadIdx.x & 63;
+    asm volatile("" : "+v"(lane));  // what depends on it would wait in registers through the loop
+    const int q = lane >> 4;
+#pragma unroll
+    for (int p = 0; p < kWParts; p++)
+#pragma unroll
+      for (int j = 0; j < FW; j++) {
+        const int col = n0 + wn * 16 * FW + p * kWStep + (kSpread ? q * 4 * FW + 4 * j : 16 * j + 4 * q);
+        const float* ws = a.wscale[kGated ? p : 0];
+        float scale[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++) scale[i] = a.splits == 1 && col + i < a.N ? ws[col + i] : 0.f;
+#pragma unroll
+        for (int h = 0; h < kXParts; h++)
+#pragma unroll
+          for (int f = 0; f < FX; f++) {
+            const int m = m0 + wm * 16 * FX + h * kXRowsPart + f * 16 + (lane & 15);
+            const float xs = a.splits == 1 && m < a.M ? a.xscale[m] : 0.f;
+            if (a.splits == 1) {
+#pragma unroll
+              for (int i = 0; i < 4; i++)
+                acc[h][p][f][j][i] = scaled(__float_as_int(acc[h][p][f][j][i]), xs, scale[i]);
+            }
+          }
+      }
+  }
+  store_results<E, kXRows, kWRows, kGated, Shape, kXParts, kWParts, kSpread, G * kStages * kBuf, !E::kInt8>(
       a, acc, (lds_char*)smem, m0, n0, b, split, ktiles, t0, t1, BK);
 }
 
 template <class E, bool kXRows, bool kWRows, class Shape, bool kGated>
 __global__ __launch_bounds__(Shape::kAllThreads) void k_gemm(GemmArgs a) {
-  constexpr bool kLater = Shape::kPaired && !kGated && !kWRows;
+  constexpr bool kLater = Shape::kPaired && !kGated && !kWRows && !E::kInt8;
   __shared__ __attribute__((aligned(1024))) char smem[kGemmLds<Shape> + (kLater ? kResidLds : 0)];
   gemm_body<E, kXRows, kWRows, Shape, kGated, kLater>(a, smem, blockIdx.x, gridDim.x);
 }
@@ -1102,7 +1154,7 @@ __device__ __forceinline__ void gemm32_body(const GemmArgs& a, char* smem, int w
     }
   }
   if (G > 1 && !late) __syncthreads();
-  if (!join_groups<Shape, G * kBuf>(acc, (lds_char*)smem)) return;
+  if (!join_groups<F32, Shape, G * kBuf>(acc, (lds_char*)smem)) return;
   store_results<F32, kXRows, kWRows, kGated, Shape, 1, P, true, G * kBuf, false>(a, acc, (lds_char*)smem, m0, n0, b, at.split,
                                                                         ktiles, t0, t1, BK);
 }

@@ -23,7 +23,7 @@ typedef struct {
 } tensor;
 
 static PyObject *s_dtype, *s_get_device, *s_data_ptr, *s_shape, *s_stride, *s_new_empty, *kw_dtype;
-static PyObject *t_types[3], *t_uint8, *f_current_device, *f_raw_stream, *e_llar;
+static PyObject *t_types[3], *t_uint8, *t_int8, *t_int32, *t_int64, *f_current_device, *f_raw_stream, *e_llar;
 
 static const char* const kActs[] = {"none", "relu", "gelu", "gelu_tanh", "silu"};
 
@@ -139,16 +139,18 @@ typedef struct {
   void* stream;
 } call;
 
-static int begin(PyObject* x, PyObject* act, call* c) {
-  if (read_tensor(x, &c->x) < 0) return -1;
+/* The library's number of a torch type, -1 with an error if it has none. */
+static int type_of(PyObject* dtype) {
   int i;
-  for (i = 0; i < 3 && c->x.dtype != t_types[i]; i++) {
+  for (i = 0; i < 3 && dtype != t_types[i]; i++) {
   }
-  if (i == 3) {
-    PyErr_Format(PyExc_TypeError, "unsupported dtype %R (fp32, fp16, bf16 only)", c->x.dtype);
-    return -1;
-  }
-  c->type = (llar_dtype)i;
+  if (i < 3) return i;
+  PyErr_Format(PyExc_TypeError, "unsupported dtype %R (fp32, fp16, bf16 only)", dtype);
+  return -1;
+}
+
+static int activation(PyObject* act, call* c) {
+  int i;
   const char* name = PyUnicode_Check(act) ? PyUnicode_AsUTF8(act) : NULL;
   for (i = 0; name && i < 5 && strcmp(name, kActs[i]); i++) {
   }
@@ -157,6 +159,11 @@ static int begin(PyObject* x, PyObject* act, call* c) {
     return -1;
   }
   c->act = (llar_act)i;
+  return 0;
+}
+
+/* The device's current stream, and x as a matrix. */
+static int begin_on_device(call* c) {
   if (c->x.device < 0) {
     PyObject* v = PyObject_CallFunction(e_llar, "is", LLAR_ERR_HIP, "no GPU tensor: the operators run only on the HIP device");
     if (v) PyErr_SetObject(e_llar, v);
@@ -178,13 +185,21 @@ static int begin(PyObject* x, PyObject* act, call* c) {
   return as_matrix(&c->x, &c->xm, "x");
 }
 
-/* A new contiguous tensor of x's type; its address goes to *data. */
-static PyObject* new_tensor(const tensor* x, const int64_t* size, int nd, void** data) {
+static int begin(PyObject* x, PyObject* act, call* c) {
+  if (read_tensor(x, &c->x) < 0) return -1;
+  const int i = type_of(c->x.dtype);
+  if (i < 0) return -1;
+  c->type = (llar_dtype)i;
+  return activation(act, c) < 0 ? -1 : begin_on_device(c);
+}
+
+/* A new contiguous tensor of x's type, or the type given, on x's device; its address goes to *data. */
+static PyObject* new_typed(const tensor* x, const int64_t* size, int nd, PyObject* dtype, void** data) {
   PyObject* shape = PyTuple_New(nd);
   if (!shape) return NULL;
   for (int i = 0; i < nd; i++) PyTuple_SET_ITEM(shape, i, PyLong_FromLongLong(size[i]));
-  PyObject* args[2] = {x->obj, shape};
-  PyObject* t = PyObject_VectorcallMethod(s_new_empty, args, 2 | PY_VECTORCALL_ARGUMENTS_OFFSET, NULL);
+  PyObject* args[3] = {x->obj, shape, dtype};
+  PyObject* t = PyObject_VectorcallMethod(s_new_empty, args, 2 | PY_VECTORCALL_ARGUMENTS_OFFSET, dtype ? kw_dtype : NULL);
   Py_DECREF(shape);
   if (!t) return NULL;
   PyObject* v = PyObject_CallMethodNoArgs(t, s_data_ptr);
@@ -195,6 +210,9 @@ static PyObject* new_tensor(const tensor* x, const int64_t* size, int nd, void**
   *data = PyLong_AsVoidPtr(v);
   Py_DECREF(v);
   return t;
+}
+static PyObject* new_tensor(const tensor* x, const int64_t* size, int nd, void** data) {
+  return new_typed(x, size, nd, NULL, data);
 }
 
 static llar_matrix dense(void* data, int64_t rows, int64_t cols) {
@@ -227,6 +245,14 @@ static int loose(const llar_matrix* m, int es) {
   return (((intptr_t)m->data | (width | line) * es) & 15) != 0 || line * es >= 1 << 23;
 }
 
+/* Device memory for a call's workspace (None: it needs none). */
+static PyObject* room(const call* c, size_t bytes, void** data) {
+  *data = NULL;
+  if (bytes == 0) Py_RETURN_NONE;
+  const int64_t n = (int64_t)bytes;
+  return new_typed(&c->x, &n, 1, t_uint8, data);
+}
+
 /* The workspace of a call (None: it needs none). */
 static PyObject* workspace(const call* c, llar_ffn_op op, const llar_matrix* w, const llar_matrix* w2,
                            const llar_matrix* dy, void** data, size_t* bytes) {
@@ -237,23 +263,8 @@ static PyObject* workspace(const call* c, llar_ffn_op op, const llar_matrix* w, 
   if (!by_rows(&c->xm)) layout |= LLAR_LAYOUT_X_COLUMNS;
   if (!by_rows(w)) layout |= LLAR_LAYOUT_W_COLUMNS;
   if (dy && !by_rows(dy)) layout |= LLAR_LAYOUT_DY_COLUMNS;
-  *data = NULL;
   *bytes = llar_ffn_workspace(op, c->xm.rows, w->rows, c->xm.cols, c->type, layout);
-  if (*bytes == 0) Py_RETURN_NONE;
-  PyObject* n = PyLong_FromSize_t(*bytes);
-  if (!n) return NULL;
-  PyObject* args[3] = {c->x.obj, n, t_uint8};
-  PyObject* t = PyObject_VectorcallMethod(s_new_empty, args, 2 | PY_VECTORCALL_ARGUMENTS_OFFSET, kw_dtype);
-  Py_DECREF(n);
-  if (!t) return NULL;
-  PyObject* v = PyObject_CallMethodNoArgs(t, s_data_ptr);
-  if (!v) {
-    Py_DECREF(t);
-    return NULL;
-  }
-  *data = PyLong_AsVoidPtr(v);
-  Py_DECREF(v);
-  return t;
+  return room(c, *bytes, data);
 }
 
 static int done(int status, const char* what) {
@@ -437,11 +448,204 @@ end:
   return result;
 }
 
-/* (float32, float16, bfloat16, uint8, current_device(), raw_stream(device), LlarError): once, before any call */
+/* ---- 8-bit products ---------------------------------------------------------------- */
+
+/* A contiguous binary32 tensor of `count` scales, its leading dimensions x's (lead) or one dimension. */
+static const float* scales(const call* c, PyObject* obj, int64_t count, int lead, const char* what) {
+  tensor t;
+  if (read_tensor(obj, &t) < 0) return NULL;
+  if (t.dtype != t_types[0] || t.device != c->x.device) {
+    PyErr_Format(PyExc_ValueError, "%s must be float32 and on x's device", what);
+    return NULL;
+  }
+  const int nd = lead ? c->x.nd - 1 : 1;
+  int ok = t.nd == nd;
+  for (int i = 0; ok && i < nd; i++) ok = t.size[i] == (lead ? c->x.size[i] : count);
+  int64_t step = 1;
+  for (int i = nd - 1; ok && i >= 0; i--) {
+    ok = t.size[i] <= 1 || t.stride[i] == step || count == 0;
+    step *= t.size[i];
+  }
+  if (!ok) {
+    PyErr_Format(PyExc_ValueError, lead ? "%s must be contiguous and have x's shape without its width"
+                                        : "%s must be contiguous and of shape (%lld,)", what, (long long)count);
+    return NULL;
+  }
+  static const float none = 0.f;
+  return t.data ? (const float*)t.data : &none; /* an empty tensor's: never read */
+}
+
+static int int8_weight(const call* c, PyObject* obj, int64_t n, llar_matrix* m, const char* what) {
+  tensor x = c->x;
+  x.dtype = t_int8;
+  tensor t;
+  if (read_tensor(obj, &t) < 0) return -1;
+  if (t.dtype != t_int8 || t.device != c->x.device) {
+    PyErr_Format(PyExc_ValueError, "%s must be int8 and on x's device", what);
+    return -1;
+  }
+  return weight_shaped(&x, obj, n, c->xm.cols, m, what);
+}
+
+/* x of a call that takes whole numbers with scales, or values: sets c->type to the results' and *xs. */
+static int begin_int8(PyObject* x, PyObject* x_scale, PyObject* act, PyObject* dtype, call* c, const float** xs) {
+  if (read_tensor(x, &c->x) < 0) return -1;
+  int i;
+  if (x_scale != Py_None) {
+    if (c->x.dtype != t_int8) {
+      PyErr_Format(PyExc_TypeError, "x with x_scale must be int8, not %R", c->x.dtype);
+      return -1;
+    }
+    i = dtype == Py_None ? LLAR_BF16 : type_of(dtype);
+  } else {
+    i = type_of(c->x.dtype);
+    if (i >= 0 && dtype != Py_None && dtype != c->x.dtype) {
+      PyErr_SetString(PyExc_ValueError, "dtype is x's own where x is not int8");
+      return -1;
+    }
+  }
+  if (i < 0) return -1;
+  c->type = (llar_dtype)i;
+  if (activation(act, c) < 0) return -1;
+  const int st = begin_on_device(c);
+  if (st != 0) return st;
+  *xs = NULL;
+  if (x_scale != Py_None && !(*xs = scales(c, x_scale, c->xm.rows, 1, "x_scale"))) return -1;
+  return 0;
+}
+
+/* The output, given or new, and the workspace. */
+static PyObject* int8_out(const call* c, PyObject* given, int64_t width, llar_matrix* m) {
+  tensor like_out = c->x;
+  like_out.dtype = t_types[c->type];
+  if (given != Py_None) {
+    if (activation_shaped(&like_out, given, width, m, "out") < 0) return NULL;
+    Py_INCREF(given);
+    return given;
+  }
+  int64_t size[kMaxDims];
+  memcpy(size, c->x.size, sizeof(size));
+  size[c->x.nd - 1] = width;
+  void* data = NULL;
+  PyObject* t = new_typed(&c->x, size, c->x.nd, t_types[c->type], &data);
+  *m = dense(data, c->xm.rows, width);
+  return t;
+}
+static int loose8(const llar_matrix* m) {
+  return (((intptr_t)m->data | m->cols | (m->rows > 1 ? m->row_stride : 0)) & 15) != 0 ||
+         (m->rows > 1 && m->row_stride >= 1 << 23);
+}
+static PyObject* int8_room(const call* c, llar_ffn_op op, const float* xs, const llar_matrix* w, const llar_matrix* w2,
+                           void** data, size_t* bytes) {
+  int layout = xs ? 0 : LLAR_LAYOUT_X_VALUES;
+  if ((xs && loose8(&c->xm)) || loose8(w) || (w2 && loose8(w2))) layout |= LLAR_LAYOUT_UNALIGNED;
+  *bytes = llar_int8_workspace(op, c->xm.rows, w->rows, c->xm.cols, layout);
+  return room(c, *bytes, data);
+}
+
+/* (x) -> (q, scale) */
+static PyObject* py_quantize_rows(PyObject* self, PyObject* const* a, Py_ssize_t n_args) {
+  call c;
+  if (arity(n_args, 1) < 0) return NULL;
+  if (read_tensor(a[0], &c.x) < 0) return NULL;
+  const int i = type_of(c.x.dtype);
+  if (i < 0) return NULL;
+  c.type = (llar_dtype)i;
+  const int st = begin_on_device(&c);
+  if (st < 0) return NULL;
+  if (st > 0) Py_RETURN_NOTIMPLEMENTED;
+  void *qd = NULL, *sd = NULL;
+  PyObject *q = NULL, *s = NULL, *result = NULL;
+  if (!(q = new_typed(&c.x, c.x.size, c.x.nd, t_int8, &qd))) goto end;
+  if (!(s = new_typed(&c.x, c.x.size, c.x.nd - 1, t_types[0], &sd))) goto end;
+  const llar_matrix qm = dense(qd, c.xm.rows, c.xm.cols);
+  if (done(llar_quantize_rows(&c.xm, &qm, (float*)sd, c.type, c.stream), "llar_quantize_rows") < 0) goto end;
+  result = PyTuple_Pack(2, q, s);
+end:
+  Py_XDECREF(q);
+  Py_XDECREF(s);
+  return result;
+}
+
+/* (x, weight, w_scale, x_scale, bias, residual, activation, dtype, out) */
+static PyObject* py_linear_int8(PyObject* self, PyObject* const* a, Py_ssize_t n_args) {
+  call c;
+  const float *xs, *ws;
+  if (arity(n_args, 9) < 0) return NULL;
+  const int st = begin_int8(a[0], a[3], a[6], a[7], &c, &xs);
+  if (st < 0) return NULL;
+  if (st > 0) Py_RETURN_NOTIMPLEMENTED;
+  llar_matrix w, r, y;
+  if (int8_weight(&c, a[1], -1, &w, "weight") < 0) return NULL;
+  if (!(ws = scales(&c, a[2], w.rows, 0, "w_scale"))) return NULL;
+  tensor like_out = c.x;
+  like_out.dtype = t_types[c.type];
+  const void* bias = NULL;
+  if (a[4] != Py_None) {
+    tensor b;
+    if (read_tensor(a[4], &b) < 0) return NULL;
+    if (b.dtype != like_out.dtype || b.device != c.x.device || b.nd != 1 || b.size[0] != w.rows ||
+        (w.rows > 1 && b.stride[0] != 1)) {
+      PyErr_Format(PyExc_ValueError, "bias must be contiguous, of shape (%lld,), the output's type and x's device",
+                   (long long)w.rows);
+      return NULL;
+    }
+    bias = b.data;
+  }
+  const int has_r = a[5] != Py_None;
+  if (has_r && activation_shaped(&like_out, a[5], w.rows, &r, "residual") < 0) return NULL;
+  PyObject *ws_room = NULL, *result = NULL, *out = int8_out(&c, a[8], w.rows, &y);
+  void* space;
+  size_t bytes;
+  if (!out) return NULL;
+  if (!(ws_room = int8_room(&c, LLAR_OP_LINEAR, xs, &w, NULL, &space, &bytes))) goto end;
+  if (done(llar_linear_int8(&c.xm, xs, &w, ws, bias, has_r ? &r : NULL, &y, c.type, c.act, space, bytes, c.stream),
+           "llar_linear_int8") < 0)
+    goto end;
+  result = out;
+  out = NULL;
+end:
+  Py_XDECREF(out);
+  Py_XDECREF(ws_room);
+  return result;
+}
+
+/* (x, w_gate, w_up, gate_scale, up_scale, x_scale, activation, dtype, out) */
+static PyObject* py_gated_ffn_int8(PyObject* self, PyObject* const* a, Py_ssize_t n_args) {
+  call c;
+  const float *xs, *gs, *us;
+  if (arity(n_args, 9) < 0) return NULL;
+  const int st = begin_int8(a[0], a[5], a[6], a[7], &c, &xs);
+  if (st < 0) return NULL;
+  if (st > 0) Py_RETURN_NOTIMPLEMENTED;
+  llar_matrix wg, wu, h;
+  if (int8_weight(&c, a[1], -1, &wg, "w_gate") < 0) return NULL;
+  if (int8_weight(&c, a[2], wg.rows, &wu, "w_up") < 0) return NULL;
+  if (!(gs = scales(&c, a[3], wg.rows, 0, "gate_scale"))) return NULL;
+  if (!(us = scales(&c, a[4], wg.rows, 0, "up_scale"))) return NULL;
+  PyObject *ws_room = NULL, *result = NULL, *out = int8_out(&c, a[8], wg.rows, &h);
+  void* space;
+  size_t bytes;
+  if (!out) return NULL;
+  if (!(ws_room = int8_room(&c, LLAR_OP_GATED_FFN, xs, &wg, &wu, &space, &bytes))) goto end;
+  if (done(llar_gated_ffn_int8(&c.xm, xs, &wg, &wu, gs, us, &h, c.type, c.act, space, bytes, c.stream),
+           "llar_gated_ffn_int8") < 0)
+    goto end;
+  result = out;
+  out = NULL;
+end:
+  Py_XDECREF(out);
+  Py_XDECREF(ws_room);
+  return result;
+}
+
+/* (float32, float16, bfloat16, uint8, int8, int32, int64, current_device(), raw_stream(device), LlarError): once,
+ * before any call */
 static PyObject* py_setup(PyObject* self, PyObject* const* a, Py_ssize_t n_args) {
-  if (arity(n_args, 7) < 0) return NULL;
-  PyObject** const to[7] = {&t_types[0], &t_types[1], &t_types[2], &t_uint8, &f_current_device, &f_raw_stream, &e_llar};
-  for (int i = 0; i < 7; i++) {
+  PyObject** const to[10] = {&t_types[0], &t_types[1], &t_types[2], &t_uint8,          &t_int8,
+                             &t_int32,    &t_int64,    &f_current_device, &f_raw_stream, &e_llar};
+  if (arity(n_args, 10) < 0) return NULL;
+  for (int i = 0; i < 10; i++) {
     Py_INCREF(a[i]);
     Py_XSETREF(*to[i], a[i]);
   }
@@ -454,6 +658,9 @@ static PyMethodDef methods[] = {
     {"linear_backward", (PyCFunction)(void (*)(void))py_linear_backward, METH_FASTCALL, NULL},
     {"gated_ffn", (PyCFunction)(void (*)(void))py_gated_ffn, METH_FASTCALL, NULL},
     {"gated_ffn_backward", (PyCFunction)(void (*)(void))py_gated_ffn_backward, METH_FASTCALL, NULL},
+    {"quantize_rows", (PyCFunction)(void (*)(void))py_quantize_rows, METH_FASTCALL, NULL},
+    {"linear_int8", (PyCFunction)(void (*)(void))py_linear_int8, METH_FASTCALL, NULL},
+    {"gated_ffn_int8", (PyCFunction)(void (*)(void))py_gated_ffn_int8, METH_FASTCALL, NULL},
     {NULL, NULL, 0, NULL}};
 
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_llar_py", NULL, -1, methods, NULL, NULL, NULL, NULL};

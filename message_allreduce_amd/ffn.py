@@ -18,7 +18,8 @@ from __future__ import annotations
 
 from . import LlarError, lib
 
-__all__ = ["ACTIVATIONS", "linear", "linear_backward", "gated_ffn", "gated_ffn_backward"]
+__all__ = ["ACTIVATIONS", "linear", "linear_backward", "gated_ffn", "gated_ffn_backward", "quantize_rows",
+           "linear_int8", "gated_ffn_int8"]
 
 ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 
@@ -39,7 +40,8 @@ def _setup():
     device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
     stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
         lambda index: torch.cuda.current_stream(index).cuda_stream)
-    native.setup(torch.float32, torch.float16, torch.bfloat16, torch.uint8, device, stream, LlarError)
+    native.setup(torch.float32, torch.float16, torch.bfloat16, torch.uint8, torch.int8, torch.int32, torch.int64, device,
+                 stream, LlarError)
     _native = native
     return native
 
@@ -91,5 +93,40 @@ def gated_ffn_backward(dh, x, w_gate, w_up, gate, up, activation="silu", input_g
     """Gradients (dx, dw_gate, dw_up) of ``gated_ffn`` from the products it saved; those not asked for are None."""
     f = (_native or _setup()).gated_ffn_backward
     args = (dh, x, w_gate, w_up, gate, up, activation, input_grad, weight_grad)
+    r = NotImplemented if stream is not None else f(*args)
+    return r if r is not NotImplemented else _elsewhere(x, stream, f, *args)
+
+
+# ---- products of 8-bit whole numbers -----------------------------------------------
+
+def quantize_rows(x, stream=None):
+    """(q, scale): ``scale`` (float32) the largest magnitude of each row of x (..., k) over 127, ``q`` (int8, x's
+    shape) the nearest whole numbers to ``x / scale``, ties to even.  Tokens are quantised so before
+    ``linear_int8``, and a weight's output channels, which are its rows.  A row of zeros has scale 0; one with an
+    infinity or a NaN has scale NaN, and so do the products it enters."""
+    f = (_native or _setup()).quantize_rows
+    r = NotImplemented if stream is not None else f(x)
+    return r if r is not NotImplemented else _elsewhere(x, stream, f, x)
+
+
+def linear_int8(x, weight, w_scale, x_scale=None, bias=None, residual=None, activation="none", dtype=None, out=None,
+                stream=None):
+    """``activation(x_scale * w_scale * (x @ weight.T) + bias) + residual`` with exact whole-number sums.
+
+    ``weight`` (n, k) int8 with contiguous rows and ``w_scale`` (n,) float32, as ``quantize_rows`` makes them.  x:
+    (..., k) int8 with ``x_scale`` (...,), or fp32, fp16 or bf16 without it, which the call quantises the same way.
+    ``dtype``: the output's type, bias's and residual's (x's own, or bf16 for int8 x).  k is at most 2^17 - 1."""
+    f = (_native or _setup()).linear_int8
+    args = (x, weight, w_scale, x_scale, bias, residual, activation, dtype, out)
+    r = NotImplemented if stream is not None else f(*args)
+    return r if r is not NotImplemented else _elsewhere(x, stream, f, *args)
+
+
+def gated_ffn_int8(x, w_gate, w_up, gate_scale, up_scale, x_scale=None, activation="silu", dtype=None, out=None,
+                   stream=None):
+    """``activation(g) * u`` of the two 8-bit products g and u of x with ``w_gate`` and ``w_up``, in one kernel (and
+    one that quantises x, if it is not int8).  Arguments as ``linear_int8``'s and ``gated_ffn``'s."""
+    f = (_native or _setup()).gated_ffn_int8
+    args = (x, w_gate, w_up, gate_scale, up_scale, x_scale, activation, dtype, out)
     r = NotImplemented if stream is not None else f(*args)
     return r if r is not NotImplemented else _elsewhere(x, stream, f, *args)
