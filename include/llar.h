@@ -355,6 +355,61 @@ int llar_gated_ffn_int8(const llar_matrix* x, const float* x_scale, const llar_m
                         const float* gate_scale, const float* up_scale, const llar_matrix* out, llar_dtype dtype,
                         llar_act act, void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---- mixture of experts for a few tokens --------------------------------- *
+ * What the gated block and the row-parallel product become where every token
+ * chooses some of E feed-forward blocks: the router, and the chosen experts'
+ * blocks with their weighted sum.  A rank may hold some of the experts, a part
+ * of every expert's inner width, or both; its output is a partial one that the
+ * AllReduce sums.  Made for decoding: every chosen expert's weights are read
+ * once for 64 tokens (longer batches go 64 tokens at a time).  Streams,
+ * workspaces, overlap, errors and sizes as for the calls above; E is at most
+ * 1024, top_k 32.  No atomics on results: the same inputs give the same bits. */
+typedef enum {
+  LLAR_SCORE_SOFTMAX = 0,
+  LLAR_SCORE_SIGMOID = 1
+} llar_score;
+
+/* E matrices of rows x cols elements, contiguous along cols; element (e, i, j)
+ * at data + e*expert_stride + i*row_stride + j. */
+typedef struct {
+  void* data;
+  int64_t experts, rows, cols, expert_stride, row_stride;
+} llar_experts;
+
+/* Bytes of workspace of llar_moe_route. */
+size_t llar_moe_route_workspace(int64_t m, int64_t experts);
+
+/* For each of the m tokens, rows of x (m x k), the top_k experts with the largest
+ * logits x router^T (router: E x k), in falling order, of equals the lowest
+ * number first; experts[m][top_k].  Logits are summed in binary64.
+ * weights[m][top_k]: the softmax of a token's logits over all experts, or each
+ * logit's sigmoid, at its choices; normalize != 0: divided by their sum.  A NaN
+ * logit is below all others, and makes its token's weights NaN.  x and router
+ * are of type dtype with contiguous rows. */
+int llar_moe_route(const llar_matrix* x, const llar_matrix* router, int top_k, llar_score score, int normalize,
+                   float* weights, int32_t* experts, llar_dtype dtype, void* workspace, size_t workspace_bytes,
+                   void* stream);
+
+/* Bytes of workspace of llar_moe_ffn for m tokens, inner width n and k inputs;
+ * int8 != 0: with scales. */
+size_t llar_moe_workspace(int64_t m, int64_t n, int64_t k, int top_k, llar_dtype dtype, int int8);
+
+/* out[t] = sum over j < top_k of weights[t][j] (act(x[t] wg^T) * (x[t] wu^T)) wd^T + residual[t],
+ * with the matrices of expert e = expert_ids[t][j]: w_gate and w_up E x n x k (the
+ * same strides), w_down E x outs x n, x m x k with contiguous rows, out m x outs.
+ * expert_ids: m x top_k whole numbers of id_bytes 4 or 8; one outside 0 .. E - 1
+ * (an expert of another rank, a padded token) adds nothing, and one that a token
+ * names twice has both weights.  The inner rows are rounded to dtype once.
+ *
+ * With gate_scale, up_scale (E x n) and down_scale (E x outs), all three, the
+ * weights are int8: x (any strides) and the inner rows, unrounded, are quantised
+ * as llar_quantize_rows does, one scale each; k and n are at most 2^17 - 1. */
+int llar_moe_ffn(const llar_matrix* x, const void* expert_ids, int id_bytes, const float* weights, int top_k,
+                 const llar_experts* w_gate, const llar_experts* w_up, const llar_experts* w_down,
+                 const float* gate_scale, const float* up_scale, const float* down_scale, const llar_matrix* residual,
+                 const llar_matrix* out, llar_dtype dtype, llar_act act, void* workspace, size_t workspace_bytes,
+                 void* stream);
+
 /* Free all resources (synchronises the device first).  NULL is a no-op. */
 int llar_destroy(llar_comm* h);
 

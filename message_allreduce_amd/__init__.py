@@ -32,7 +32,7 @@ __all__ = [
     "llar_get_timing", "llar_wallclock_hz", "llar_launch_geometry", "llar_floor_measure",
     "llar_status_string", "llar_last_error", "llar_get_trace", "llar_get_pipeline_trace", "Communicator", "EXPORTED_SYMBOLS",
     "ACTIVATIONS", "linear", "linear_backward", "gated_ffn", "gated_ffn_backward",
-    "quantize_rows", "linear_int8", "gated_ffn_int8",
+    "quantize_rows", "linear_int8", "gated_ffn_int8", "moe_route", "moe_ffn",
 ]
 
 FP32, FP16, BF16 = 0, 1, 2
@@ -51,6 +51,7 @@ EXPORTED_SYMBOLS = (
     "llar_get_trace", "llar_get_pipeline_trace", "llar_send_recv", "llar_reduce_scatter", "llar_all_gather",
     "llar_allreduce_noalloc", "llar_ffn_workspace", "llar_linear", "llar_linear_backward", "llar_gated_ffn",
     "llar_gated_ffn_backward", "llar_quantize_rows", "llar_int8_workspace", "llar_linear_int8", "llar_gated_ffn_int8",
+    "llar_moe_route_workspace", "llar_moe_route", "llar_moe_workspace", "llar_moe_ffn",
 )
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -109,6 +110,10 @@ def lib() -> ctypes.CDLL:
         "llar_int8_workspace": (sz, [i32, i64, i64, i64, i32]),
         "llar_linear_int8": (i32, [vp] * 7 + [i32, i32, vp, sz, vp]),
         "llar_gated_ffn_int8": (i32, [vp] * 7 + [i32, i32, vp, sz, vp]),
+        "llar_moe_route_workspace": (sz, [i64, i64]),
+        "llar_moe_route": (i32, [vp, vp, i32, i32, i32, vp, vp, i32, vp, sz, vp]),
+        "llar_moe_workspace": (sz, [i64, i64, i64, i32, i32, i32]),
+        "llar_moe_ffn": (i32, [vp, vp, i32, vp, i32] + [vp] * 8 + [i32, i32, vp, sz, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)
@@ -436,4 +441,4 @@ class Communicator:
 
 
 from .ffn import (ACTIVATIONS, gated_ffn, gated_ffn_backward, gated_ffn_int8, linear, linear_backward,  # noqa: E402
-                  linear_int8, quantize_rows)
+                  linear_int8, moe_ffn, moe_route, quantize_rows)

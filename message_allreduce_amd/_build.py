@@ -21,7 +21,8 @@ LIB = os.path.join(HERE, "libllar.so")
 BINDING = os.path.join(HERE, "_llar_py.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 SOURCES = ["llar_kernels.hip", "llar_multi.hip", "llar_host.hip", "llar_floor.hip", "llar_ffn.hip",
-           "llar_ffn_kernels.hip", "llar_int8.hip", "llar_int8_kernels.hip"]
+           "llar_ffn_kernels.hip", "llar_int8.hip", "llar_int8_kernels.hip", "llar_moe.hip",
+           "llar_moe_kernels.hip"]
 # the matrix product, compiled once for each element type and operand order
 INSTANCES = [("llar_gemm_inst.hip", "llar_gemm_%s_%d%d" % (e.lower(), x, w),
               ["-DLLAR_ELEM=" + e, "-DLLAR_XR=%d" % x, "-DLLAR_WR=%d" % w])

@@ -1,0 +1,47 @@
+// llar_moe.h -- argument blocks and launchers of the mixture-of-experts operators
+// (not public).
+#pragma once
+#include "llar_ffn.h"
+
+namespace llar_ffn {
+
+constexpr int kMoeTokens = 64;     // of one pair of launches: a lane each
+constexpr int kMoeExperts = 1024;
+constexpr int kMoeTopK = 32;
+
+// Logits of M tokens (rows of x) and E experts (rows of w), both k-contiguous.
+struct RouteArgs {
+  const void *x, *w;
+  double* logits;  // [M][E]
+  int64_t xld, wld;
+  int M, E, K, top_k;
+  bool sigmoid, normalize;
+  float* weights;
+  int32_t* experts;
+};
+hipError_t launch_route(int kind, const RouteArgs& a, hipStream_t s);
+
+// At most kMoeTokens tokens.  A choice is place j of token t's list, p = t top_k + j;
+// h holds a row for every choice that has an expert and is the first of its token
+// with that expert.
+struct MoeArgs {
+  const void* x;         // T rows of k elements: of the I/O type, or int8
+  const float* xscale;   // int8: of every token
+  const void* w[2];      // gate, up: [E][n][k]
+  const float* wscale[2];
+  const void* wd;        // [E][outs][n]
+  const float* dscale;
+  void* h;               // first kernel's output (int8: binary32); second kernel's input (int8: whole numbers)
+  const float* hscale;   // int8: of every choice
+  const void* ids;
+  const float* weights;
+  const void* resid;
+  void* out;
+  int64_t xld, w_expert, wld, d_expert, dld, hld, rld, outld;
+  int T, K, N, outs, E, top_k;
+  int id_bytes, act;
+};
+hipError_t launch_moe_up(int kind, bool int8, const MoeArgs& a, hipStream_t s);
+hipError_t launch_moe_down(int kind, bool int8, const MoeArgs& a, hipStream_t s);
+
+}  // namespace llar_ffn

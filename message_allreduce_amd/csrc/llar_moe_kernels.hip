@@ -1,0 +1,384 @@
+// llar_moe_kernels.hip -- the router, and the experts of a few tokens in two kernels.
+#include "llar_chunk.h"
+#include "llar_moe.h"
+
+namespace llar_ffn {
+
+// ---- the router's logits --------------------------------------------------------------
+// In binary64, so that which experts are chosen does not hang on the order of the
+// sums.  A workgroup takes 16 tokens by 16 experts, its waves parts of k: lane (r,
+// q) holds eight k of token r and of expert r, widened, and the matrix unit
+// multiplies four k at a time (which four is the same for both).
+typedef double f64x4 __attribute__((ext_vector_type(4)));
+
+template <class E, int kWaves>
+__global__ __launch_bounds__(kWaves * 64) void k_route_logits(RouteArgs a) {
+  typedef typename E::T T;
+  __shared__ double part[kWaves][16][16 + 1];
+  const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int groups = (a.E + 15) / 16;
+  const int e0 = (int)(blockIdx.x % groups) * 16, t0 = (int)(blockIdx.x / groups) * 16;
+  const T* x = (const T*)a.x + (int64_t)min(t0 + r, a.M - 1) * a.xld;
+  const T* w = (const T*)a.w + (int64_t)min(e0 + r, a.E - 1) * a.wld;
+  f64x4 acc = {0., 0., 0., 0.};
+  for (int i = wave; i * 32 < a.K; i += kWaves) {
+    const int k = i * 32 + q * 8;
+    const Vals<E, 8> xv = load_vals<E, 8>(x + k, a.K - k), wv = load_vals<E, 8>(w + k, a.K - k);
+#pragma unroll
+    for (int e = 0; e < 8; e++)
+      acc = __builtin_amdgcn_mfma_f64_16x16x4f64((double)wv.v[e], (double)xv.v[e], acc, 0, 0, 0);
+  }
+  // lane: token r, experts q + 4 i
+#pragma unroll
+  for (int i = 0; i < 4; i++) part[wave][r][q + 4 * i] = acc[i];
+  __syncthreads();
+  for (int i = threadIdx.x; i < 256; i += kWaves * 64) {
+    const int t = i / 16, e = i % 16;
+    if (t0 + t >= a.M || e0 + e >= a.E) continue;
+    double s = 0.;
+#pragma unroll
+    for (int j = 0; j < kWaves; j++) s += part[j][t][e];
+    a.logits[(int64_t)(t0 + t) * a.E + e0 + e] = s;
+  }
+}
+
+// ---- the choice ------------------------------------------------------------------------
+// A wave a token: lane l holds the experts l, l + 64, ...; the largest left is taken
+// top_k times, the lowest number first among equals.  A NaN counts as below
+// everything, so that the choices are distinct experts whatever the logits are.
+constexpr int kPerLane = kMoeExperts / 64;
+
+__global__ __launch_bounds__(256) void k_route_choose(RouteArgs a) {
+  const int lane = threadIdx.x & 63;
+  const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (t >= a.M) return;
+  const double* l = a.logits + t * a.E;
+  const double kNone = -__builtin_inf();
+  double v[kPerLane];
+  uint32_t left = 0;  // bit i: expert lane + 64 i is not chosen yet
+  double top = kNone;
+  bool nan = false;
+#pragma unroll
+  for (int i = 0; i < kPerLane; i++) {
+    const int e = lane + 64 * i;
+    v[i] = kNone;
+    if (e < a.E) {
+      left |= 1u << i;
+      v[i] = l[e];
+      if (v[i] != v[i]) {
+        nan = true;
+        v[i] = kNone;
+      }
+      top = fmax(top, v[i]);
+    }
+  }
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) top = fmax(top, __shfl_xor(top, d));
+  nan = __any(nan);
+  double sum = 0.;
+  if (!a.sigmoid && !a.normalize) {
+#pragma unroll
+    for (int i = 0; i < kPerLane; i++)
+      if (lane + 64 * i < a.E) sum += exp(v[i] - top);
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) sum += __shfl_xor(sum, d);
+  }
+  double mine = 0.;  // lane j: the score of choice j
+  for (int j = 0; j < a.top_k; j++) {
+    double best = kNone;
+    int e = 1 << 30;
+#pragma unroll
+    for (int i = 0; i < kPerLane; i++)
+      if ((left >> i & 1) && (e == 1 << 30 || v[i] > best)) {
+        best = v[i];
+        e = lane + 64 * i;
+      }
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) {
+      const double other = __shfl_xor(best, d);
+      const int oe = __shfl_xor(e, d);
+      // a lane without experts left has e = 2^30 and -inf: it loses to any other
+      if (other > best || (other == best && oe < e)) {
+        best = other;
+        e = oe;
+      }
+    }
+    if (e % 64 == lane) left &= ~(1u << (e / 64));
+    const double score = a.sigmoid ? 1. / (1. + exp(-best)) : exp(best - top);
+    if (a.normalize) sum += score;
+    if (lane == j) {
+      mine = score;
+      a.experts[t * a.top_k + j] = e;
+    }
+  }
+  // sigmoid scores stand by themselves unless they are normalised
+  if (a.sigmoid && !a.normalize) sum = 1.;
+  if (lane < a.top_k) a.weights[t * a.top_k + lane] = nan ? __builtin_nanf("") : (float)(mine / sum);
+}
+
+template <class E>
+hipError_t route(const RouteArgs& a, hipStream_t s) {
+  constexpr int kWaves = 16;
+  const int64_t groups = ((int64_t)a.M + 15) / 16 * ((a.E + 15) / 16);
+  if (!launchable(groups, kWaves * 64)) return hipErrorInvalidConfiguration;
+  k_route_logits<E, kWaves><<<dim3((uint32_t)groups), dim3(kWaves * 64), 0, s>>>(a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  k_route_choose<<<dim3((uint32_t)(((int64_t)a.M + 3) / 4)), dim3(256), 0, s>>>(a);
+  return hipGetLastError();
+}
+hipError_t launch_route(int kind, const RouteArgs& a, hipStream_t s) {
+  return kind == 0 ? route<F32>(a, s) : kind == 1 ? route<F16>(a, s) : route<BF16>(a, s);
+}
+
+// ---- experts ----------------------------------------------------------------------------
+__device__ __forceinline__ int expert_at(const MoeArgs& a, int p) {
+  const int64_t id = a.id_bytes == 8 ? ((const int64_t*)a.ids)[p] : (int64_t)((const int32_t*)a.ids)[p];
+  return id >= 0 && id < a.E ? (int)id : -1;
+}
+
+// First kernel: h = act(x wg^T) (x wu^T) of every choice.  A workgroup takes 16
+// inner columns (16 rows of each projection) of one expert for all the tokens that
+// chose it, up to 64: its weights are read once.  Every wave finds those tokens by
+// itself, a token a lane, without a word of shared memory.
+//
+// With fewer choices than experts the grid has a slot for each choice, and the
+// slot of an expert's first choice does its work; else a slot for each expert.
+template <class E, int NB, int kWaves>
+__device__ __forceinline__ void moe_up_rows(const MoeArgs& a, const char* const (&w)[2], int member, int count, int e,
+                                            int n0, float (*part)[2][16][16]) {
+  constexpr int G = NB == 1 ? 2 : 1, U = 2, ES = sizeof(typename E::X), kStep = 64 * G / ES;
+  const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  bool live[NB];
+  const char* x[NB];
+#pragma unroll
+  for (int b = 0; b < NB; b++) {
+    live[b] = 16 * b + r < count;
+    const int t = __shfl(member, 16 * b + r) & 255;
+    x[b] = (const char*)a.x + (live[b] ? t * a.xld * ES : 0) + q * (16 * G);
+  }
+  const char* at[2] = {w[0] + q * (16 * G), w[1] + q * (16 * G)};
+  f32x4 acc[2][NB];
+  clear<E>(acc);
+  multiply_steps<E, 2, NB, G, U>(acc, at, x, live, a.K, wave, (a.K + kStep - 1) / kStep, kWaves);
+#pragma unroll
+  for (int b = 0; b < NB; b++) {
+    if (b > 0) {
+      if (16 * b >= count) break;
+      __syncthreads();
+    }
+#pragma unroll
+    for (int p = 0; p < 2; p++) *(f32x4*)&part[wave][p][r][4 * q] = acc[p][b];
+    __syncthreads();
+    for (int i = threadIdx.x; i < 256; i += kWaves * 64) {
+      const int row = i / 16, col = i % 16;
+      const int m = __shfl(member, 16 * b + row);  // whole waves are in this loop
+      float v[2];
+#pragma unroll
+      for (int p = 0; p < 2; p++) {
+        v[p] = part[0][p][row][col];
+#pragma unroll
+        for (int k = 1; k < kWaves; k++) v[p] = add_sums<E>(v[p], part[k][p][row][col]);
+      }
+      if (16 * b + row >= count || n0 + col >= a.N) continue;
+      const int t = m & 255, j = m >> 8;
+      const int64_t to = (int64_t)(t * a.top_k + j) * a.hld + n0 + col;
+      if constexpr (E::kInt8) {
+        float g[1] = {scaled(__float_as_int(v[0]), a.xscale[t], a.wscale[0][(int64_t)e * a.N + n0 + col])};
+        const float u = scaled(__float_as_int(v[1]), a.xscale[t], a.wscale[1][(int64_t)e * a.N + n0 + col]);
+        act_values<F32, 1>(g, a.act);
+        ((float*)a.h)[to] = g[0] * u;
+      } else {
+        float g[1] = {v[0]};
+        act_values<E, 1>(g, a.act);
+        ((typename E::T*)a.h)[to] = E::from(g[0] * v[1]);
+      }
+    }
+  }
+}
+
+template <class E, int NB, int kWaves>
+__global__ __launch_bounds__(kWaves * 64) void k_moe_up(MoeArgs a, int tiles, bool by_choice) {
+  __shared__ float part[kWaves][2][16][16];
+  constexpr int ES = sizeof(typename E::X);
+  const int lane = threadIdx.x & 63, r = lane & 15;
+  const int slot = blockIdx.x / tiles, n0 = (int)(blockIdx.x % tiles) * 16;
+  const int e = by_choice ? expert_at(a, slot) : slot;
+  if (e < 0) return;
+  // the first place of this expert in the lane's token's list
+  int j = -1;
+  if (lane < a.T)
+    for (int i = a.top_k - 1; i >= 0; i--)
+      if (expert_at(a, lane * a.top_k + i) == e) j = i;
+  const uint64_t chose = __ballot(j >= 0);
+  const int count = __popcll(chose);
+  if (count == 0) return;
+  if (by_choice) {
+    const int first = __ffsll((unsigned long long)chose) - 1;
+    if (first * a.top_k + __shfl(j, first) != slot) return;
+  }
+  // lane i: the i-th of these tokens, and its place
+  const uint64_t below = (1ull << lane) - 1;
+  const int rank = j >= 0 ? __popcll(chose & below) : count + __popcll(~chose & below);
+  const int member = __builtin_amdgcn_ds_permute(rank * 4, lane | (j & 255) << 8);
+  const char* w[2];
+#pragma unroll
+  for (int p = 0; p < 2; p++)
+    w[p] = (const char*)a.w[p] + (e * a.w_expert + min(n0 + r, a.N - 1) * a.wld) * ES;
+  if constexpr (NB == 1) {
+    moe_up_rows<E, 1, kWaves>(a, w, member, count, e, n0, part);
+  } else {
+    if (count <= 16)
+      moe_up_rows<E, 1, kWaves>(a, w, member, count, e, n0, part);
+    else if (NB == 2 || count <= 32)
+      moe_up_rows<E, 2, kWaves>(a, w, member, count, e, n0, part);
+    else
+      moe_up_rows<E, NB, kWaves>(a, w, member, count, e, n0, part);
+  }
+}
+
+// Second kernel: y = sum over the choices of weight * h wd^T, + residual.  A
+// workgroup takes 16 output columns for all tokens and experts; the waves take
+// equal runs of the (expert, k step) pairs.  Row t of a fragment is token t, zeros
+// where the token did not choose the expert, so that sums of different experts
+// meet in one register; they are weighted, and left out where there is no choice,
+// when a wave leaves an expert.  No atomics: the waves' sums are added in order.
+template <class E, int NB, int kWaves>
+__global__ __launch_bounds__(kWaves * 64) void k_moe_down(MoeArgs a) {
+  constexpr int ES = sizeof(typename E::X), G = NB == 1 ? 2 : 1, U = 2, kStep = 64 * G / ES;
+  constexpr int kMost = kMoeTokens * kMoeTopK;
+  __shared__ float part[kWaves][NB * 16][16];
+  __shared__ uint32_t bits[kMoeExperts / 32];
+  __shared__ int16_t ids[kMost], act[kMoeExperts];
+  __shared__ float weights[kMost];
+  const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int n0 = blockIdx.x * 16;
+  const int choices = a.T * a.top_k;
+  // the experts that any token chose, in order
+  if (threadIdx.x < kMoeExperts / 32) bits[threadIdx.x] = 0;
+  __syncthreads();
+  for (int p = threadIdx.x; p < choices; p += kWaves * 64) {
+    const int e = expert_at(a, p);
+    ids[p] = (int16_t)e;
+    weights[p] = a.weights[p];
+    if (e >= 0) atomicOr(&bits[e >> 5], 1u << (e & 31));
+  }
+  __syncthreads();
+  int active = 0;
+  for (int e = threadIdx.x; e < kMoeExperts; e += kWaves * 64)
+    if (bits[e >> 5] >> (e & 31) & 1) {
+      int rank = __popc(bits[e >> 5] & ((1u << (e & 31)) - 1));
+      for (int i = 0; i < e >> 5; i++) rank += __popc(bits[i]);
+      act[rank] = (int16_t)e;
+    }
+  for (int i = 0; i < kMoeExperts / 32; i++) active += __popc(bits[i]);
+  active = __builtin_amdgcn_readfirstlane(active);
+  __syncthreads();
+
+  const int steps = (a.N + kStep - 1) / kStep;  // of one expert
+  const int64_t all = (int64_t)active * steps;
+  int64_t s = all * wave / kWaves;
+  const int64_t s1 = all * (wave + 1) / kWaves;
+  const int col = min(n0 + r, a.outs - 1);
+  float y[NB][4] = {};
+  while (s < s1) {
+    const int i = (int)(s / steps), k0 = (int)(s - (int64_t)i * steps);
+    const int k1 = (int)min((int64_t)steps, k0 + (s1 - s));
+    const int e = __builtin_amdgcn_readfirstlane(act[i]);
+    bool live[NB];
+    const char* h[NB];
+    float factor[NB];
+#pragma unroll
+    for (int b = 0; b < NB; b++) {
+      const int t = 16 * b + r;
+      int j = -1;
+      factor[b] = 0.f;
+      if (t < a.T)
+        for (int c = a.top_k - 1; c >= 0; c--)
+          if (ids[t * a.top_k + c] == e) {
+            j = c;
+            factor[b] += weights[t * a.top_k + c];
+          }
+      live[b] = j >= 0;
+      const int p = live[b] ? t * a.top_k + j : 0;
+      if constexpr (E::kInt8) factor[b] *= live[b] ? a.hscale[p] : 0.f;
+      h[b] = (const char*)a.h + p * a.hld * ES + q * (16 * G);
+    }
+    const char* w[1] = {(const char*)a.wd + (e * a.d_expert + col * a.dld) * ES + q * (16 * G)};
+    f32x4 acc[1][NB];
+    clear<E>(acc);
+    multiply_steps<E, 1, NB, G, U>(acc, w, h, live, a.N, k0, k1, 1);
+#pragma unroll
+    for (int v = 0; v < 4; v++) {
+      float scale = 1.f;
+      if constexpr (E::kInt8) scale = a.dscale[(int64_t)e * a.outs + min(n0 + 4 * q + v, a.outs - 1)];
+#pragma unroll
+      for (int b = 0; b < NB; b++) {
+        const float sum = E::kInt8 ? (float)__float_as_int(acc[0][b][v]) * scale : acc[0][b][v];
+        if (live[b]) y[b][v] = fmaf(factor[b], sum, y[b][v]);
+      }
+    }
+    s += k1 - k0;
+  }
+#pragma unroll
+  for (int b = 0; b < NB; b++) *(f32x4*)&part[wave][16 * b + r][4 * q] = f32x4{y[b][0], y[b][1], y[b][2], y[b][3]};
+  __syncthreads();
+  typedef typename E::T T;
+  for (int i = threadIdx.x; i < a.T * 16; i += kWaves * 64) {
+    const int t = i / 16, c = i % 16;
+    if (n0 + c >= a.outs) continue;
+    float v = 0.f;
+#pragma unroll
+    for (int k = 0; k < kWaves; k++) v += part[k][t][c];
+    if (a.resid) v += E::to(((const T*)a.resid)[t * a.rld + n0 + c]);
+    ((T*)a.out)[t * a.outld + n0 + c] = E::from(v);
+  }
+}
+
+constexpr int kMoeWaves = 16;
+
+template <class E>
+hipError_t moe_up(const MoeArgs& a, hipStream_t s) {
+  const int64_t choices = (int64_t)a.T * a.top_k;
+  const bool by_choice = choices <= a.E;
+  const int64_t tiles = ((int64_t)a.N + 15) / 16, groups = tiles * (by_choice ? choices : a.E);
+  if (groups == 0) return hipSuccess;
+  if (!launchable(groups, kMoeWaves * 64)) return hipErrorInvalidConfiguration;
+  const dim3 grid((uint32_t)groups), block(kMoeWaves * 64);
+  if (a.T <= 16)
+    k_moe_up<E, 1, kMoeWaves><<<grid, block, 0, s>>>(a, (int)tiles, by_choice);
+  else if (a.T <= 32)
+    k_moe_up<E, 2, kMoeWaves><<<grid, block, 0, s>>>(a, (int)tiles, by_choice);
+  else
+    k_moe_up<E, 4, kMoeWaves><<<grid, block, 0, s>>>(a, (int)tiles, by_choice);
+  return hipGetLastError();
+}
+template <class E>
+hipError_t moe_down(const MoeArgs& a, hipStream_t s) {
+  const int64_t groups = ((int64_t)a.outs + 15) / 16;
+  if (groups == 0 || a.T == 0) return hipSuccess;
+  if (!launchable(groups, kMoeWaves * 64)) return hipErrorInvalidConfiguration;
+  const dim3 grid((uint32_t)groups), block(kMoeWaves * 64);
+  if (a.T <= 16)
+    k_moe_down<E, 1, kMoeWaves><<<grid, block, 0, s>>>(a);
+  else if (a.T <= 32)
+    k_moe_down<E, 2, kMoeWaves><<<grid, block, 0, s>>>(a);
+  else
+    k_moe_down<E, 4, kMoeWaves><<<grid, block, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+hipError_t launch_moe_up(int kind, bool int8, const MoeArgs& a, hipStream_t s) {
+  if (int8) return kind == 0 ? moe_up<Int8<F32>>(a, s) : kind == 1 ? moe_up<Int8<F16>>(a, s) : moe_up<Int8<BF16>>(a, s);
+  return kind == 0 ? moe_up<F32>(a, s) : kind == 1 ? moe_up<F16>(a, s) : moe_up<BF16>(a, s);
+}
+hipError_t launch_moe_down(int kind, bool int8, const MoeArgs& a, hipStream_t s) {
+  if (int8)
+    return kind == 0 ? moe_down<Int8<F32>>(a, s) : kind == 1 ? moe_down<Int8<F16>>(a, s) : moe_down<Int8<BF16>>(a, s);
+  return kind == 0 ? moe_down<F32>(a, s) : kind == 1 ? moe_down<F16>(a, s) : moe_down<BF16>(a, s);
+}
+
+}  // namespace llar_ffn

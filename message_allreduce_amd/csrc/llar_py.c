@@ -639,6 +639,178 @@ end:
   return result;
 }
 
+/* ---- mixture of experts -------------------------------------------------------------- */
+
+static int contiguous(const tensor* t) {
+  int64_t step = 1, count = 1;
+  for (int i = 0; i < t->nd; i++) count *= t->size[i];
+  for (int i = t->nd - 1; count > 0 && i >= 0; i--) {
+    if (t->size[i] > 1 && t->stride[i] != step) return 0;
+    step *= t->size[i];
+  }
+  return 1;
+}
+
+/* (x, router, top_k, sigmoid, normalize) -> (weights, experts) */
+static PyObject* py_moe_route(PyObject* self, PyObject* const* a, Py_ssize_t n_args) {
+  call c;
+  if (arity(n_args, 5) < 0) return NULL;
+  if (read_tensor(a[0], &c.x) < 0) return NULL;
+  const int i = type_of(c.x.dtype);
+  if (i < 0) return NULL;
+  c.type = (llar_dtype)i;
+  const int st = begin_on_device(&c);
+  if (st < 0) return NULL;
+  if (st > 0) Py_RETURN_NOTIMPLEMENTED;
+  llar_matrix router;
+  if (weight_shaped(&c.x, a[1], -1, c.xm.cols, &router, "router") < 0) return NULL;
+  const long top_k = PyLong_AsLong(a[2]);
+  if (top_k == -1 && PyErr_Occurred()) return NULL;
+  if (top_k < 0 || top_k > router.rows) {
+    PyErr_Format(PyExc_ValueError, "top_k must be between 0 and the number of experts, %lld", (long long)router.rows);
+    return NULL;
+  }
+  const int sigmoid = PyObject_IsTrue(a[3]), normalize = PyObject_IsTrue(a[4]);
+  if (sigmoid < 0 || normalize < 0) return NULL;
+  int64_t size[kMaxDims];
+  memcpy(size, c.x.size, sizeof(size));
+  size[c.x.nd - 1] = top_k;
+  void *wd = NULL, *ed = NULL, *space;
+  PyObject *w = NULL, *e = NULL, *ws = NULL, *result = NULL;
+  const size_t bytes = llar_moe_route_workspace(c.xm.rows, router.rows);
+  if (!(w = new_typed(&c.x, size, c.x.nd, t_types[0], &wd))) goto end;
+  if (!(e = new_typed(&c.x, size, c.x.nd, t_int32, &ed))) goto end;
+  if (!(ws = room(&c, bytes, &space))) goto end;
+  if (done(llar_moe_route(&c.xm, &router, (int)top_k, sigmoid ? LLAR_SCORE_SIGMOID : LLAR_SCORE_SOFTMAX, normalize,
+                          (float*)wd, (int32_t*)ed, c.type, space, bytes, c.stream),
+           "llar_moe_route") < 0)
+    goto end;
+  result = PyTuple_Pack(2, w, e);
+end:
+  Py_XDECREF(w);
+  Py_XDECREF(e);
+  Py_XDECREF(ws);
+  return result;
+}
+
+/* E matrices of x's type or int8; sizes < 0 are any. */
+static int expert_weights(const call* c, PyObject* obj, PyObject* dtype, const int64_t* want, llar_experts* m,
+                          const char* what) {
+  tensor t;
+  if (read_tensor(obj, &t) < 0) return -1;
+  if (t.dtype != dtype || t.device != c->x.device) {
+    PyErr_Format(PyExc_ValueError, "%s must be on x's device and of %s", what,
+                 dtype == t_int8 ? "type int8 (it has scales)" : "x's type (without scales)");
+    return -1;
+  }
+  int ok = t.nd == 3;
+  for (int i = 0; ok && i < 3; i++) ok = want[i] < 0 || t.size[i] == want[i];
+  if (!ok) {
+    PyErr_Format(PyExc_ValueError, "%s has the wrong shape: w_gate and w_up are (experts, n, k), w_down (experts, outputs, n)", what);
+    return -1;
+  }
+  if (t.size[2] > 1 && t.stride[2] != 1) {
+    PyErr_Format(PyExc_ValueError, "%s: the rows of every expert's matrix must be contiguous", what);
+    return -1;
+  }
+  const llar_experts w = {t.data, t.size[0], t.size[1], t.size[2], t.size[0] > 1 ? t.stride[0] : 0,
+                          t.size[1] > 1 ? t.stride[1] : 0};
+  *m = w;
+  return 0;
+}
+
+static const float* expert_scales(const call* c, PyObject* obj, int64_t experts, int64_t rows, const char* what) {
+  tensor t;
+  if (read_tensor(obj, &t) < 0) return NULL;
+  if (t.dtype != t_types[0] || t.device != c->x.device || t.nd != 2 || t.size[0] != experts || t.size[1] != rows ||
+      !contiguous(&t)) {
+    PyErr_Format(PyExc_ValueError, "%s must be contiguous, float32, on x's device and of shape (%lld, %lld)", what,
+                 (long long)experts, (long long)rows);
+    return NULL;
+  }
+  static const float none = 0.f;
+  return t.data ? (const float*)t.data : &none;
+}
+
+/* A contiguous tensor with a token's choices: x's shape, with top_k as the width. */
+static int choices(const call* c, PyObject* obj, tensor* t, int64_t top_k, const char* what) {
+  if (read_tensor(obj, t) < 0) return -1;
+  if (t->device != c->x.device || t->nd == 0 || !contiguous(t)) {
+    PyErr_Format(PyExc_ValueError, "%s must be contiguous and on x's device", what);
+    return -1;
+  }
+  return shaped(&c->x, t, top_k < 0 ? t->size[t->nd - 1] : top_k, what);
+}
+
+/* (x, experts, weights, w_gate, w_up, w_down, gate_scale, up_scale, down_scale, activation, residual, out) */
+static PyObject* py_moe_ffn(PyObject* self, PyObject* const* a, Py_ssize_t n_args) {
+  call c;
+  if (arity(n_args, 12) < 0) return NULL;
+  const int st = begin(a[0], a[9], &c);
+  if (st < 0) return NULL;
+  if (st > 0) Py_RETURN_NOTIMPLEMENTED;
+  tensor ids, w;
+  if (choices(&c, a[1], &ids, -1, "experts") < 0) return NULL;
+  if (ids.dtype != t_int32 && ids.dtype != t_int64) {
+    PyErr_Format(PyExc_TypeError, "experts must be int32 or int64, not %R", ids.dtype);
+    return NULL;
+  }
+  const int64_t top_k = ids.size[ids.nd - 1];
+  if (choices(&c, a[2], &w, top_k, "weights") < 0) return NULL;
+  if (w.dtype != t_types[0]) {
+    PyErr_Format(PyExc_TypeError, "weights must be float32, not %R", w.dtype);
+    return NULL;
+  }
+  const int int8 = a[6] != Py_None;
+  if (int8 != (a[7] != Py_None) || int8 != (a[8] != Py_None)) {
+    PyErr_SetString(PyExc_ValueError, "gate_scale, up_scale and down_scale are given together");
+    return NULL;
+  }
+  PyObject* type = int8 ? t_int8 : t_types[c.type];
+  llar_experts wg, wu, wd;
+  int64_t want[3] = {-1, -1, c.xm.cols};
+  if (expert_weights(&c, a[3], type, want, &wg, "w_gate") < 0) return NULL;
+  want[0] = wg.experts;
+  want[1] = wg.rows;
+  if (expert_weights(&c, a[4], type, want, &wu, "w_up") < 0) return NULL;
+  want[1] = -1;
+  want[2] = wg.rows;
+  if (expert_weights(&c, a[5], type, want, &wd, "w_down") < 0) return NULL;
+  const float *gs = NULL, *us = NULL, *ds = NULL;
+  if (int8 && (!(gs = expert_scales(&c, a[6], wg.experts, wg.rows, "gate_scale")) ||
+               !(us = expert_scales(&c, a[7], wg.experts, wg.rows, "up_scale")) ||
+               !(ds = expert_scales(&c, a[8], wg.experts, wd.rows, "down_scale"))))
+    return NULL;
+  llar_matrix r, y;
+  const int has_r = a[10] != Py_None;
+  if (has_r && activation_shaped(&c.x, a[10], wd.rows, &r, "residual") < 0) return NULL;
+  if (top_k > 1 << 20) { /* the library's own limit is far lower; this keeps the number an int */
+    PyErr_SetString(PyExc_ValueError, "experts has too many choices a token");
+    return NULL;
+  }
+  PyObject *out = NULL, *ws = NULL, *result = NULL;
+  if (a[11] != Py_None) {
+    if (activation_shaped(&c.x, a[11], wd.rows, &y, "out") < 0) return NULL;
+    out = a[11];
+    Py_INCREF(out);
+  } else if (!(out = new_activation(&c, wd.rows, &y))) {
+    return NULL;
+  }
+  void* space;
+  const size_t bytes = llar_moe_workspace(c.xm.rows, wg.rows, c.xm.cols, (int)top_k, c.type, int8);
+  if (!(ws = room(&c, bytes, &space))) goto end;
+  if (done(llar_moe_ffn(&c.xm, ids.data, ids.dtype == t_int64 ? 8 : 4, (const float*)w.data, (int)top_k, &wg, &wu, &wd,
+                        gs, us, ds, has_r ? &r : NULL, &y, c.type, c.act, space, bytes, c.stream),
+           "llar_moe_ffn") < 0)
+    goto end;
+  result = out;
+  out = NULL;
+end:
+  Py_XDECREF(out);
+  Py_XDECREF(ws);
+  return result;
+}
+
 /* (float32, float16, bfloat16, uint8, int8, int32, int64, current_device(), raw_stream(device), LlarError): once,
  * before any call */
 static PyObject* py_setup(PyObject* self, PyObject* const* a, Py_ssize_t n_args) {
@@ -661,6 +833,8 @@ static PyMethodDef methods[] = {
     {"quantize_rows", (PyCFunction)(void (*)(void))py_quantize_rows, METH_FASTCALL, NULL},
     {"linear_int8", (PyCFunction)(void (*)(void))py_linear_int8, METH_FASTCALL, NULL},
     {"gated_ffn_int8", (PyCFunction)(void (*)(void))py_gated_ffn_int8, METH_FASTCALL, NULL},
+    {"moe_route", (PyCFunction)(void (*)(void))py_moe_route, METH_FASTCALL, NULL},
+    {"moe_ffn", (PyCFunction)(void (*)(void))py_moe_ffn, METH_FASTCALL, NULL},
     {NULL, NULL, 0, NULL}};
 
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_llar_py", NULL, -1, methods, NULL, NULL, NULL, NULL};

@@ -19,7 +19,7 @@ from __future__ import annotations
 from . import LlarError, lib
 
 __all__ = ["ACTIVATIONS", "linear", "linear_backward", "gated_ffn", "gated_ffn_backward", "quantize_rows",
-           "linear_int8", "gated_ffn_int8"]
+           "linear_int8", "gated_ffn_int8", "moe_route", "moe_ffn"]
 
 ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 
@@ -128,5 +128,37 @@ def gated_ffn_int8(x, w_gate, w_up, gate_scale, up_scale, x_scale=None, activati
     one that quantises x, if it is not int8).  Arguments as ``linear_int8``'s and ``gated_ffn``'s."""
     f = (_native or _setup()).gated_ffn_int8
     args = (x, w_gate, w_up, gate_scale, up_scale, x_scale, activation, dtype, out)
+    r = NotImplemented if stream is not None else f(*args)
+    return r if r is not NotImplemented else _elsewhere(x, stream, f, *args)
+
+
+# ---- mixture of experts for a few tokens --------------------------------------------
+
+def moe_route(x, router, top_k, scoring="softmax", normalize=True, stream=None):
+    """(weights, experts), (..., top_k) each: for every token of x (..., k) the ``top_k`` rows of ``router``
+    (experts, k) with the largest products, in falling order, of equals the lowest number first (int32), and their
+    ``scoring`` (float32): "softmax" over all experts, or each product's "sigmoid"; ``normalize``: divided by their
+    sum.  The products are summed in binary64."""
+    if scoring not in ("softmax", "sigmoid"):
+        raise ValueError("unknown scoring %r (softmax or sigmoid)" % (scoring,))
+    f = (_native or _setup()).moe_route
+    args = (x, router, top_k, scoring == "sigmoid", normalize)
+    r = NotImplemented if stream is not None else f(*args)
+    return r if r is not NotImplemented else _elsewhere(x, stream, f, *args)
+
+
+def moe_ffn(x, experts, weights, w_gate, w_up, w_down, activation="silu", residual=None, gate_scale=None, up_scale=None,
+            down_scale=None, out=None, stream=None):
+    """The sum over a token's experts of ``weight * (activation(x @ wg.T) * (x @ wu.T)) @ wd.T``, + ``residual``, in
+    two kernels.
+
+    x (..., k); ``experts`` (..., top_k) int32 or int64 and ``weights`` float32, contiguous, as ``moe_route`` returns
+    them; ``w_gate`` and ``w_up`` (E, n, k) with the same strides, ``w_down`` (E, outputs, n), contiguous along their
+    last axis.  A number outside 0 .. E - 1 (an expert of another rank, a padded token) adds nothing; the output is
+    then a partial one for the AllReduce.  With ``gate_scale``, ``up_scale`` (E, n) and ``down_scale`` (E, outputs),
+    float32, the weights are int8; x and the inner rows are quantised as ``quantize_rows`` does.  For a few tokens:
+    a chosen expert's weights are read once for every 64 of them."""
+    f = (_native or _setup()).moe_ffn
+    args = (x, experts, weights, w_gate, w_up, w_down, gate_scale, up_scale, down_scale, activation, residual, out)
     r = NotImplemented if stream is not None else f(*args)
     return r if r is not NotImplemented else _elsewhere(x, stream, f, *args)
