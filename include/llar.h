@@ -336,8 +336,9 @@ int llar_gated_ffn_backward(const llar_matrix* dh, const llar_matrix* x, const l
 int llar_quantize_rows(const llar_matrix* x, const llar_matrix* q, float* scale, llar_dtype dtype, void* stream);
 
 /* Bytes of workspace of llar_linear_int8 (op LLAR_OP_LINEAR) or
- * llar_gated_ffn_int8 (LLAR_OP_GATED_FFN); layout: LLAR_LAYOUT_X_VALUES and, for
- * 8-bit matrices, LLAR_LAYOUT_UNALIGNED. */
+ * llar_gated_ffn_int8 (LLAR_OP_GATED_FFN); layout: LLAR_LAYOUT_X_VALUES, with
+ * LLAR_LAYOUT_X_COLUMNS if the values' rows are not contiguous, and, for 8-bit
+ * matrices, LLAR_LAYOUT_UNALIGNED. */
 size_t llar_int8_workspace(llar_ffn_op op, int64_t m, int64_t n, int64_t k, int layout);
 
 /* out = act(s_x s_w (x w^T) + bias) + residual.  x: int8 rows with x_scale (m
@@ -376,8 +377,8 @@ typedef struct {
   int64_t experts, rows, cols, expert_stride, row_stride;
 } llar_experts;
 
-/* Bytes of workspace of llar_moe_route. */
-size_t llar_moe_route_workspace(int64_t m, int64_t experts);
+/* Bytes of workspace of llar_moe_route for m tokens of width k. */
+size_t llar_moe_route_workspace(int64_t m, int64_t experts, int64_t k);
 
 /* For each of the m tokens, rows of x (m x k), the top_k experts with the largest
  * logits x router^T (router: E x k), in falling order, of equals the lowest

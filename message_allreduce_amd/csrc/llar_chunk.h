@@ -131,40 +131,65 @@ __device__ __forceinline__ void clear(f32x4 (&acc)[P][NB]) {
 // q = x / scale rounded to the nearest, ties to even, where scale is the row's
 // largest magnitude / 127.  The product with the reciprocal can be off by one next
 // to a half; the remainder x - q scale is exact in binary32 (it is a multiple of
-// half of scale's last bit and at most about half of scale), and decides.
+// half of scale's last bit and at most about half of scale), and decides: a lane
+// with a remainder of half of scale or more among its eight looks at each of them.
 struct Quantizer {
-  float scale, inv, half, lift;
+  float scale, inv, unit, half, lift;
+  bool plain;
   // top: the largest magnitude's bits, a NaN above infinity
   __device__ __forceinline__ explicit Quantizer(uint32_t top) {
     const float t = __uint_as_float(top);
     scale = top >= 0x7f800000u ? __builtin_nanf("") : t / 127.f;
     // tiny rows are lifted, so that the reciprocal exists
-    lift = scale < 0x1p-90f ? 0x1p60f : 1.f;
-    const float s = scale * lift;
-    inv = s > 0.f ? 1.f / s : 0.f;  // a row of zeros, or with a NaN: zeros
-    half = 0.5f * s;
+    plain = scale >= 0x1p-90f;
+    lift = plain ? 1.f : 0x1p60f;
+    unit = scale * lift;
+    inv = unit > 0.f ? 1.f / unit : 0.f;  // a row of zeros, or with a NaN: zeros
+    half = 0.5f * unit;
   }
-  __device__ __forceinline__ int operator()(float x) const {
+  __device__ __forceinline__ int one(float x) const {
     if (!(inv > 0.f)) return 0;
     x *= lift;
     float r = rintf(x * inv);
-    const float d = fmaf(-r, half + half, x), m = fabsf(d);
+    const float d = fmaf(-r, unit, x), m = fabsf(d);
     const bool odd = (int)r & 1;
     if (m > half || (m == half && odd)) r += d > 0.f ? 1.f : -1.f;
-    return (int)fminf(fmaxf(r, -127.f), 127.f);
+    return (int)fminf(fmaxf(r, -127.f), 127.f);  // a tiny row's scale is not exact enough
+  }
+  // eight bytes
+  __device__ __forceinline__ uint2 eight(const float (&x)[8]) const {
+    // 1.5 x 2^23 + n has n in its low bits, rounded by the addition
+    constexpr float kShift = 12582912.f;
+    float y[8], worst = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+      y[i] = fmaf(x[i], inv, kShift);
+      worst = fmaxf(worst, fabsf(fmaf(-(y[i] - kShift), unit, x[i])));
+    }
+    if (!plain || worst >= half) {
+#pragma unroll
+      for (int i = 0; i < 8; i++) y[i] = __int_as_float(one(x[i]));
+    }
+    return make_uint2(pack4(y), pack4(y + 4));
+  }
+  // the low bytes of four words
+  static __device__ __forceinline__ uint32_t pack4(const float* y) {
+    const uint32_t lo = __builtin_amdgcn_perm(__float_as_uint(y[1]), __float_as_uint(y[0]), 0x0c0c0400);
+    const uint32_t hi = __builtin_amdgcn_perm(__float_as_uint(y[3]), __float_as_uint(y[2]), 0x04000c0c);
+    return lo | hi;
   }
 };
 __device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7fffffffu; }
-
-// Four whole numbers in a word.
-__device__ __forceinline__ uint32_t pack4(int a, int b, int c, int d) {
-  return (uint32_t)(a & 255) | (uint32_t)(b & 255) << 8 | (uint32_t)(c & 255) << 16 | (uint32_t)d << 24;
+template <class E>
+__device__ __forceinline__ uint32_t magnitude(const Vals<E, 8>& v) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 8; i++) top = max(top, magnitude(v.v[i]));
+  return top;
 }
-
-template <int n>
 __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
 #pragma unroll
-  for (int d = n / 2; d > 0; d >>= 1) v = max(v, (uint32_t)__shfl_xor((int)v, d));
+  for (int d = 32; d > 0; d >>= 1) v = max(v, (uint32_t)__shfl_xor((int)v, d));
   return v;
 }
 

@@ -14,9 +14,9 @@ struct QuantArgs {
   int64_t M;
   int K, qpad;
 };
-hipError_t launch_quantize(int kind, const QuantArgs& a, hipStream_t s);
 
 // 8-bit rows copied so that they start, and are, whole 16-byte chunks.
+constexpr int kPack8Threads = 256;
 struct Pack8Args {
   const int8_t* src[3];
   int8_t* dst[3];
@@ -26,8 +26,13 @@ struct Pack8Args {
 };
 hipError_t launch_pack8(const Pack8Args& a, hipStream_t s);
 
+// Both in one launch (copies.first is set here).
+hipError_t launch_quantize(int kind, const QuantArgs& a, const Pack8Args& copies, hipStream_t s);
+
 // Products with M <= kFewRows rows of x, any alignment.  kind: the results' type.
-hipError_t launch_few_int8(int kind, bool gated, const GemmArgs& a, hipStream_t s);
+// values: x is of that type and not quantised yet, M <= kFewValuesRows, K <= kFewValuesK.
+constexpr int kFewValuesRows = 2, kFewValuesK = 8192;
+hipError_t launch_few_int8(int kind, bool gated, bool values, const GemmArgs& a, hipStream_t s);
 
 // The join of a product split over k: whole sums, then scales and epilogue.
 hipError_t launch_join_int8(int kind, bool gated, const GemmArgs& a, hipStream_t s);

@@ -26,6 +26,9 @@ Operand operand8(const llar_matrix* m) {
 // Whether these sizes go to the kernel for few rows.
 Shape shape8(int64_t m, int64_t n, int64_t k, bool gated) { return choose(m, n, k, 1, 1, gated, 1, true, false); }
 
+// Whether the kernel for few rows quantises them itself.
+bool takes_values(const Shape& sh, int64_t m, int64_t k) { return sh.few && m <= kFewValuesRows && k <= kFewValuesK; }
+
 size_t copy8_bytes(int64_t rows, int64_t k) { return align256((size_t)rows * round16(k)); }
 
 QuantArgs quant_args(const llar_matrix* x, int8_t* q, int64_t qld, int qpad, float* scale) {
@@ -79,50 +82,54 @@ int run8(const Call8& c, Product& p) {
   if (m == 0 || p.w[0].rows == 0) return LLAR_OK;
   Carve space{(uint8_t*)c.space, c.bytes};
   const Shape sh = shape8(m, p.w[0].rows, k, p.gated);
+  // the tiles read whole aligned chunks; the weights of a pair share their strides
+  Pack8Args copies = {};
+  copies.dld = round16(k);
+  copies.width = (int)k;
+  auto copy = [&](Operand& o) {
+    const int i = copies.count++;
+    copies.src[i] = (const int8_t*)o.p;
+    copies.ld[i] = o.ld;
+    copies.lines[i] = o.rows;
+    copies.dst[i] = (int8_t*)space.take((size_t)o.rows * copies.dld);
+    copies.first[i + 1] = copies.first[i] + cdiv(o.rows * (copies.dld / 16), kPack8Threads);
+    o.p = copies.dst[i];
+    o.ld = copies.dld;
+    o.padded = true;
+  };
+  if (!sh.few && k > 0) {
+    bool loose = false;
+    for (int i = 0; i < c.n_w; i++) loose = loose || !chunks_whole(p.w[i], 1);
+    for (int i = 0; loose && i < c.n_w; i++) copy(p.w[i]);
+  }
   const float* x_scale = c.x_scale;
-  if (!c.x_scale) {
+  const bool values = !c.x_scale && row_major(c.x) && takes_values(sh, m, k);
+  if (values) {
+    p.x[0] = operand8(c.x);
+  } else if (c.x_scale) {
+    p.x[0] = operand8(c.x);
+    if (!sh.few && k > 0 && !chunks_whole(p.x[0], 1)) copy(p.x[0]);
+    if (!space.ok) return LLAR_ERR_ARG;
+    if (copies.count && launch_pack8(copies, c.stream) != hipSuccess) return LLAR_ERR_HIP;
+  } else {
     const int64_t ld = round16(k);
     float* scale = (float*)space.take((size_t)m * 4);
     int8_t* q = (int8_t*)space.take((size_t)m * ld);
     if (!space.ok) return LLAR_ERR_ARG;
-    if (launch_quantize(c.dtype, quant_args(c.x, q, ld, (int)ld, scale), c.stream) != hipSuccess) return LLAR_ERR_HIP;
+    if (launch_quantize(c.dtype, quant_args(c.x, q, ld, (int)ld, scale), copies, c.stream) != hipSuccess)
+      return LLAR_ERR_HIP;
     x_scale = scale;
     p.x[0].p = q;
     p.x[0].rows = m;
     p.x[0].k = k;
     p.x[0].ld = ld;
     p.x[0].padded = true;
-  } else {
-    p.x[0] = operand8(c.x);
-  }
-  if (!sh.few && k > 0) {
-    // the tiles read whole aligned chunks; the weights of a pair share their strides
-    Pack8Args a = {};
-    a.dld = round16(k);
-    a.width = (int)k;
-    bool copy_w = false;
-    for (int i = 0; i < c.n_w; i++) copy_w = copy_w || !chunks_whole(p.w[i], 1);
-    auto add = [&](Operand& o) {
-      const int i = a.count++;
-      a.src[i] = (const int8_t*)o.p;
-      a.ld[i] = o.ld;
-      a.lines[i] = o.rows;
-      a.dst[i] = (int8_t*)space.take((size_t)o.rows * a.dld);
-      a.first[i + 1] = a.first[i] + cdiv(o.rows * (a.dld / 16), 256);
-      o.p = a.dst[i];
-      o.ld = a.dld;
-      o.padded = true;
-    };
-    if (!chunks_whole(p.x[0], 1)) add(p.x[0]);
-    for (int i = 0; copy_w && i < c.n_w; i++) add(p.w[i]);
-    if (!space.ok) return LLAR_ERR_ARG;
-    if (a.count && launch_pack8(a, c.stream) != hipSuccess) return LLAR_ERR_HIP;
   }
   if (partial_bytes(sh.splits, m, p.N(), p.gated ? 2 : 1) > space.left) return LLAR_ERR_ARG;
   GemmArgs a = args_of(p, sh.splits, (float*)space.p);
   a.xscale = x_scale;
   for (int i = 0; i < 2; i++) a.wscale[i] = c.w_scale[std::min(i, c.n_w - 1)];
-  if (sh.few) return launch_few_int8(c.dtype, p.gated, a, c.stream) == hipSuccess ? LLAR_OK : LLAR_ERR_HIP;
+  if (sh.few) return launch_few_int8(c.dtype, p.gated, values, a, c.stream) == hipSuccess ? LLAR_OK : LLAR_ERR_HIP;
   GemmPlan plan = {};
   plan.kind = c.dtype;
   plan.tile = sh.tile;
@@ -136,6 +143,7 @@ int run8(const Call8& c, Product& p) {
 // What a call on these inputs needs of its workspace.
 size_t needed(const Call8& c, llar_ffn_op op) {
   int layout = c.x_scale ? 0 : LLAR_LAYOUT_X_VALUES;
+  if (!c.x_scale && !row_major(c.x)) layout |= LLAR_LAYOUT_X_COLUMNS;
   if (c.x_scale && !chunks_whole(operand8(c.x), 1)) layout |= LLAR_LAYOUT_UNALIGNED;
   for (int i = 0; i < c.n_w; i++)
     if (!chunks_whole(operand8(c.w[i]), 1)) layout |= LLAR_LAYOUT_UNALIGNED;
@@ -154,7 +162,7 @@ int llar_quantize_rows(const llar_matrix* x, const llar_matrix* q, float* scale,
   if (x->rows == 0) return LLAR_OK;
   if (!scale) return llar::fail(LLAR_ERR_ARG);
   const QuantArgs a = quant_args(x, (int8_t*)q->data, q->rows <= 1 ? q->cols : q->row_stride, (int)q->cols, scale);
-  LLAR_TRY(launch_quantize(dtype, a, (hipStream_t)stream) == hipSuccess ? LLAR_OK : LLAR_ERR_HIP);
+  LLAR_TRY(launch_quantize(dtype, a, Pack8Args{}, (hipStream_t)stream) == hipSuccess ? LLAR_OK : LLAR_ERR_HIP);
   return LLAR_OK;
 }
 
@@ -164,7 +172,8 @@ size_t llar_int8_workspace(llar_ffn_op op, int64_t m, int64_t n, int64_t k, int 
     return 0;
   const bool gated = op == LLAR_OP_GATED_FFN, values = layout & LLAR_LAYOUT_X_VALUES;
   const Shape sh = shape8(m, n, k, gated);
-  size_t need = values ? align256((size_t)m * 4) + copy8_bytes(m, k) : 0;
+  const bool rows = values && !((layout & LLAR_LAYOUT_X_COLUMNS) == 0 && takes_values(sh, m, k));
+  size_t need = rows ? align256((size_t)m * 4) + copy8_bytes(m, k) : 0;
   if (!sh.few && (layout & LLAR_LAYOUT_UNALIGNED))
     need += (values ? 0 : copy8_bytes(m, k)) + (gated ? 2 : 1) * copy8_bytes(n, k);
   return need + partial_bytes(sh.splits, m, n, gated ? 2 : 1);

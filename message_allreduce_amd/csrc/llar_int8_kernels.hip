@@ -5,31 +5,48 @@
 
 namespace llar_ffn {
 
-// ---- quantisation ----------------------------------------------------------------------
-// NT threads a row (a wave, or a workgroup), eight neighbours at a time; up to
-// kKeep such pieces a thread stay in registers between the maximum and the
-// rounding, longer rows are read twice.
-constexpr int kKeep = 4;
-
-template <class E, int NT>
-__device__ __forceinline__ uint32_t row_max(uint32_t top, uint32_t* shared) {
-  top = wave_max<64>(top);
-  if constexpr (NT > 64) {
-    if ((threadIdx.x & 63) == 0) shared[threadIdx.x >> 6] = top;
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < NT / 64; i++) top = max(top, shared[i]);
-  }
-  return top;
+// ---- aligned copies --------------------------------------------------------------------
+__device__ __forceinline__ void pack8_piece(const Pack8Args& a, int64_t group, int threads) {
+  int i = 0;
+  while (i + 1 < a.count && group >= a.first[i + 1]) i++;
+  const int64_t pieces = a.dld / 16;
+  const int64_t id = (group - a.first[i]) * threads + threadIdx.x;
+  const int64_t line = id / pieces;
+  const int64_t at = (id - line * pieces) * 16;
+  if (line >= a.lines[i]) return;
+  Chunk<Int8<F32>> c;
+  c.load((const char*)a.src[i] + line * a.ld[i] + at, a.width - at);
+  *(u32x4*)(a.dst[i] + line * a.dld + at) = c.v;
+}
+__global__ __launch_bounds__(kPack8Threads) void k_pack8(Pack8Args a) { pack8_piece(a, blockIdx.x, kPack8Threads); }
+hipError_t launch_pack8(const Pack8Args& a, hipStream_t s) {
+  const int64_t groups = a.first[a.count];
+  if (groups == 0) return hipSuccess;
+  if (!launchable(groups, kPack8Threads)) return hipErrorInvalidConfiguration;
+  k_pack8<<<dim3((uint32_t)groups), dim3(kPack8Threads), 0, s>>>(a);
+  return hipGetLastError();
 }
 
-template <class E, int NT, bool kStrided>
-__global__ __launch_bounds__(256) void k_quantize(QuantArgs a) {
+// ---- quantisation ----------------------------------------------------------------------
+// NT threads a row, eight neighbours at a time; up to kKeep such pieces a thread
+// stay in registers between the maximum and the rounding, longer rows are read
+// twice.  The copies that the product behind it needs go into the same launch.
+template <int NT>
+constexpr int kQuantThreads = NT < 256 ? 256 : NT;
+
+template <class E, int NT, int kKeep, bool kStrided>
+__global__ __launch_bounds__(kQuantThreads<NT>) void k_quantize(QuantArgs a, Pack8Args copies) {
   typedef typename E::T T;
-  __shared__ uint32_t shared[4];
+  constexpr int kThreads = kQuantThreads<NT>, kRows = kThreads / NT;
+  __shared__ uint32_t shared[NT / 64];
+  const int64_t groups = (a.M + kRows - 1) / kRows;
+  if (blockIdx.x >= groups) {
+    pack8_piece(copies, blockIdx.x - groups, kThreads);
+    return;
+  }
   const int t = threadIdx.x % NT;
-  const int64_t row = (int64_t)blockIdx.x * (256 / NT) + threadIdx.x / NT;
-  if (row >= a.M) return;  // NT == 256: whole workgroups
+  const int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / NT;
+  if (row >= a.M) return;  // whole waves, and none of a row that waits for others
   const T* x = (const T*)a.x + row * a.xld;
   auto fetch = [&](int col) {
     if constexpr (!kStrided) {
@@ -46,32 +63,32 @@ __global__ __launch_bounds__(256) void k_quantize(QuantArgs a) {
 #pragma unroll
   for (int p = 0; p < kKeep; p++) {
     const int col = (p * NT + t) * 8;
-    if (col < a.K) {
-      kept[p] = fetch(col);
-#pragma unroll
-      for (int i = 0; i < 8; i++) top = max(top, magnitude(kept[p].v[i]));
-    }
+    if (col < a.K) kept[p] = fetch(col);
   }
-  for (int col = (kKeep * NT + t) * 8; col < a.K; col += NT * 8) {
-    const Vals<E, 8> v = fetch(col);
 #pragma unroll
-    for (int i = 0; i < 8; i++) top = max(top, magnitude(v.v[i]));
+  for (int p = 0; p < kKeep; p++)
+    if ((p * NT + t) * 8 < a.K) top = max(top, magnitude(kept[p]));
+  for (int col = (kKeep * NT + t) * 8; col < a.K; col += NT * 8) top = max(top, magnitude(fetch(col)));
+  top = wave_max(top);
+  if constexpr (NT > 64) {
+    if ((threadIdx.x & 63) == 0) shared[threadIdx.x >> 6] = top;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < NT / 64; i++) top = max(top, shared[i]);
   }
-  const Quantizer quantize(row_max<E, NT>(top, shared));
-  if (t == 0) a.scale[row] = quantize.scale;
+  const Quantizer quantizer(top);
+  if (t == 0) a.scale[row] = quantizer.scale;
   int8_t* q = a.q + row * a.qld;
   auto put = [&](int col, const Vals<E, 8>& v) {
-    int n[8];
-#pragma unroll
-    for (int i = 0; i < 8; i++) n[i] = quantize(v.v[i]);
+    const uint2 n = quantizer.eight(v.v);
     if (col + 8 <= a.qpad) {
       typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
       typedef u32x2 __attribute__((aligned(1))) any_u32x2;
-      *(any_u32x2*)(q + col) = u32x2{pack4(n[0], n[1], n[2], n[3]), pack4(n[4], n[5], n[6], n[7])};
+      *(any_u32x2*)(q + col) = u32x2{n.x, n.y};
     } else {
 #pragma unroll
       for (int i = 0; i < 8; i++)
-        if (col + i < a.qpad) q[col + i] = (int8_t)n[i];
+        if (col + i < a.qpad) q[col + i] = (int8_t)((i < 4 ? n.x : n.y) >> 8 * (i & 3));
     }
   };
 #pragma unroll
@@ -85,43 +102,37 @@ __global__ __launch_bounds__(256) void k_quantize(QuantArgs a) {
 }
 
 template <class E, bool kStrided>
-hipError_t quantize(const QuantArgs& a, hipStream_t s) {
-  // a wave a row where its registers hold the row
-  const bool wave = a.K <= 64 * 8 * kKeep;
-  const int64_t groups = wave ? (a.M + 3) / 4 : a.M;
-  if (groups == 0) return hipSuccess;
-  if (!launchable(groups, 256)) return hipErrorInvalidConfiguration;
-  if (wave)
-    k_quantize<E, 64, kStrided><<<dim3((uint32_t)groups), dim3(256), 0, s>>>(a);
-  else
-    k_quantize<E, 256, kStrided><<<dim3((uint32_t)groups), dim3(256), 0, s>>>(a);
-  return hipGetLastError();
+hipError_t quantize(const QuantArgs& a, Pack8Args copies, hipStream_t s) {
+  auto launch = [&](auto kernel, int threads, int rows) {
+    if (copies.count) copies.first[0] = 0;
+    int64_t groups = (a.M + rows - 1) / rows;
+    for (int i = 0; i < copies.count; i++)
+      copies.first[i + 1] = copies.first[i] + (copies.lines[i] * (copies.dld / 16) + threads - 1) / threads;
+    groups += copies.first[copies.count];
+    if (groups == 0) return hipSuccess;
+    if (!launchable(groups, threads)) return hipErrorInvalidConfiguration;
+    kernel<<<dim3((uint32_t)groups), dim3(threads), 0, s>>>(a, copies);
+    return hipGetLastError();
+  };
+  // Many rows: as few threads as hold the row in their registers.  Few: one piece a
+  // thread, for the latency.
+  if (a.M >= 1024) {
+    if (a.K <= 2048) return launch(k_quantize<E, 64, 4, kStrided>, 256, 4);
+    if (a.K <= 8192) return launch(k_quantize<E, 256, 4, kStrided>, 256, 1);
+    return launch(k_quantize<E, 1024, 2, kStrided>, 1024, 1);
+  }
+  if (a.K <= 512) return launch(k_quantize<E, 64, 1, kStrided>, 256, 4);
+  if (a.K <= 2048) return launch(k_quantize<E, 256, 1, kStrided>, 256, 1);
+  return launch(k_quantize<E, 1024, 2, kStrided>, 1024, 1);
 }
-hipError_t launch_quantize(int kind, const QuantArgs& a, hipStream_t s) {
+hipError_t launch_quantize(int kind, const QuantArgs& a, const Pack8Args& copies, hipStream_t s) {
   if (a.xcs == 1)
-    return kind == 0 ? quantize<F32, false>(a, s) : kind == 1 ? quantize<F16, false>(a, s) : quantize<BF16, false>(a, s);
-  return kind == 0 ? quantize<F32, true>(a, s) : kind == 1 ? quantize<F16, true>(a, s) : quantize<BF16, true>(a, s);
-}
-
-// ---- aligned copies ----------------------------------------------------------------------
-__global__ __launch_bounds__(256) void k_pack8(Pack8Args a) {
-  int i = 0;
-  while (i + 1 < a.count && blockIdx.x >= a.first[i + 1]) i++;
-  const int64_t groups = a.dld / 16;
-  const int64_t id = (blockIdx.x - a.first[i]) * 256 + threadIdx.x;
-  const int64_t line = id / groups;
-  const int64_t at = (id - line * groups) * 16;
-  if (line >= a.lines[i]) return;
-  Chunk<Int8<F32>> c;
-  c.load((const char*)a.src[i] + line * a.ld[i] + at, a.width - at);
-  *(u32x4*)(a.dst[i] + line * a.dld + at) = c.v;
-}
-hipError_t launch_pack8(const Pack8Args& a, hipStream_t s) {
-  const int64_t groups = a.first[a.count];
-  if (groups == 0) return hipSuccess;
-  if (!launchable(groups, 256)) return hipErrorInvalidConfiguration;
-  k_pack8<<<dim3((uint32_t)groups), dim3(256), 0, s>>>(a);
-  return hipGetLastError();
+    return kind == 0   ? quantize<F32, false>(a, copies, s)
+           : kind == 1 ? quantize<F16, false>(a, copies, s)
+                       : quantize<BF16, false>(a, copies, s);
+  return kind == 0   ? quantize<F32, true>(a, copies, s)
+         : kind == 1 ? quantize<F16, true>(a, copies, s)
+                     : quantize<BF16, true>(a, copies, s);
 }
 
 // ---- few rows ------------------------------------------------------------------------
@@ -162,19 +173,108 @@ __global__ __launch_bounds__(kWaves * 64) void k_few_int8(GemmArgs a) {
   }
 }
 
+// The same for one or two rows of values, quantised by every workgroup for itself:
+// the rows' loads go first, all of the weights' loads follow, and the maximum and
+// the rounding take place while those are on their way.
+template <class Out, bool kGated, int kRows, int kWaves>
+__global__ __launch_bounds__(kWaves * 64, 8) void k_few_int8_values(GemmArgs a) {
+  typedef Int8<Out> E;
+  constexpr int kN = kGated ? 8 : 16, G = 2, kStep = 64 * G, kSteps = kFewValuesK / (kStep * kWaves);
+  static_assert(kFewValuesK == kWaves * 64 * 8 && kFewValuesK % (kStep * kWaves) == 0, "a piece a thread");
+  __shared__ int part[kWaves][16][16];
+  __shared__ __attribute__((aligned(16))) int8_t rows[kRows][kFewValuesK];
+  __shared__ uint32_t tops[kRows][kWaves];
+  const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int n0 = blockIdx.x * kN;
+  const int col = threadIdx.x * 8;
+  Vals<Out, 8> v[kRows];
+#pragma unroll
+  for (int m = 0; m < kRows; m++) {
+    v[m] = {};
+    if (col < a.K) v[m] = load_vals<Out, 8>((const typename Out::T*)a.x[0] + m * a.xld + col, a.K - col);
+  }
+  const int row = min(n0 + (kGated ? r & 7 : r), a.N - 1);
+  const char* w = (const char*)a.w[kGated ? r >> 3 : 0] + row * a.wld + q * (16 * G);
+  Chunk<E> wv[kSteps][G];
+#pragma unroll
+  for (int s = 0; s < kSteps; s++)
+#pragma unroll
+    for (int g = 0; g < G; g++) {
+      const int k = (wave + s * kWaves) * kStep;
+      wv[s][g].zero();
+      if (k < a.K) wv[s][g].load(w + k + g * 16, a.K - k - (q * G + g) * 16);
+    }
+#pragma unroll
+  for (int m = 0; m < kRows; m++) {
+    const uint32_t top = wave_max(magnitude(v[m]));
+    if (lane == 0) tops[m][wave] = top;
+  }
+  __syncthreads();
+  float scale[kRows];
+#pragma unroll
+  for (int m = 0; m < kRows; m++) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < kWaves; i++) top = max(top, tops[m][i]);
+    const Quantizer quantizer(top);
+    scale[m] = quantizer.scale;
+    if (col < (a.K + kStep - 1) / kStep * kStep) *(uint2*)&rows[m][col] = quantizer.eight(v[m].v);
+  }
+  __syncthreads();
+  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int s = 0; s < kSteps; s++)
+#pragma unroll
+    for (int g = 0; g < G; g++) {
+      const int k = (wave + s * kWaves) * kStep;
+      Chunk<E> xv;
+      xv.zero();
+      if (k < a.K && r < kRows) xv.v = *(const u32x4*)&rows[r][k + (q * G + g) * 16];
+      acc = mma_chunk<E>(wv[s][g], xv, acc);
+    }
+  if (r < kRows) {
+#pragma unroll
+    for (int i = 0; i < 4; i++) part[wave][r][4 * q + i] = __float_as_int(acc[i]);
+  }
+  __syncthreads();
+  if (threadIdx.x >= kRows * kN) return;
+  const int m = threadIdx.x / kN, n = threadIdx.x % kN;
+  if (n0 + n >= a.N) return;
+  constexpr int P = kGated ? 2 : 1;
+  float xs = scale[0];
+#pragma unroll
+  for (int i = 1; i < kRows; i++) xs = m == i ? scale[i] : xs;
+  float y[P];
+#pragma unroll
+  for (int p = 0; p < P; p++) {
+    int sum = 0;
+#pragma unroll
+    for (int k = 0; k < kWaves; k++) sum += part[k][m][p * kN + n];
+    y[p] = scaled(sum, xs, a.wscale[p][n0 + n]);
+  }
+  finish<E, kGated, 1>(a, 0, m, n0 + n, &y[0], &y[P - 1]);
+}
+
 template <class Out, bool kGated>
-hipError_t few_int8(const GemmArgs& a, hipStream_t s) {
+hipError_t few_int8(bool values, const GemmArgs& a, hipStream_t s) {
   constexpr int kN = kGated ? 8 : 16, kWaves = 16;
   const int64_t groups = ((int64_t)a.N + kN - 1) / kN;
   if (groups == 0 || a.M == 0) return hipSuccess;
   if (!launchable(groups, kWaves * 64)) return hipErrorInvalidConfiguration;
-  k_few_int8<Out, kGated, kWaves><<<dim3((uint32_t)groups), dim3(kWaves * 64), 0, s>>>(a);
+  const dim3 grid((uint32_t)groups), block(kWaves * 64);
+  if (!values)
+    k_few_int8<Out, kGated, kWaves><<<grid, block, 0, s>>>(a);
+  else if (a.M == 1)
+    k_few_int8_values<Out, kGated, 1, kWaves><<<grid, block, 0, s>>>(a);
+  else
+    k_few_int8_values<Out, kGated, 2, kWaves><<<grid, block, 0, s>>>(a);
   return hipGetLastError();
 }
-hipError_t launch_few_int8(int kind, bool gated, const GemmArgs& a, hipStream_t s) {
-  if (kind == 0) return gated ? few_int8<F32, true>(a, s) : few_int8<F32, false>(a, s);
-  if (kind == 1) return gated ? few_int8<F16, true>(a, s) : few_int8<F16, false>(a, s);
-  return gated ? few_int8<BF16, true>(a, s) : few_int8<BF16, false>(a, s);
+hipError_t launch_few_int8(int kind, bool gated, bool values, const GemmArgs& a, hipStream_t s) {
+  if (kind == 0) return gated ? few_int8<F32, true>(values, a, s) : few_int8<F32, false>(values, a, s);
+  if (kind == 1) return gated ? few_int8<F16, true>(values, a, s) : few_int8<F16, false>(values, a, s);
+  return gated ? few_int8<BF16, true>(values, a, s) : few_int8<BF16, false>(values, a, s);
 }
 
 // ---- join ----------------------------------------------------------------------------

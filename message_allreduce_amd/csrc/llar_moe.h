@@ -12,13 +12,15 @@ constexpr int kMoeTopK = 32;
 // Logits of M tokens (rows of x) and E experts (rows of w), both k-contiguous.
 struct RouteArgs {
   const void *x, *w;
-  double* logits;  // [M][E]
+  double* logits;  // [splits][M][E]
   int64_t xld, wld;
   int M, E, K, top_k;
+  int splits;  // shares of k
   bool sigmoid, normalize;
   float* weights;
   int32_t* experts;
 };
+int route_splits(int64_t m, int64_t experts, int64_t k);
 hipError_t launch_route(int kind, const RouteArgs& a, hipStream_t s);
 
 // At most kMoeTokens tokens.  A choice is place j of token t's list, p = t top_k + j;

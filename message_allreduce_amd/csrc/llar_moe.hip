@@ -49,9 +49,9 @@ Rooms rooms(int64_t m, int64_t n, int64_t k, int top_k, int es, bool int8) {
 
 extern "C" {
 
-size_t llar_moe_route_workspace(int64_t m, int64_t experts) {
-  if (m < 0 || experts < 0 || m > kMaxDim || experts > kMoeExperts) return 0;
-  return align256((size_t)m * experts * 8);
+size_t llar_moe_route_workspace(int64_t m, int64_t experts, int64_t k) {
+  if (m < 0 || experts < 0 || k < 0 || m > kMaxDim || experts > kMoeExperts || k > kMaxLine) return 0;
+  return align256((size_t)route_splits(m, experts, k) * m * experts * 8);
 }
 
 int llar_moe_route(const llar_matrix* x, const llar_matrix* router, int top_k, llar_score score, int normalize,
@@ -64,7 +64,7 @@ int llar_moe_route(const llar_matrix* x, const llar_matrix* router, int top_k, l
   if (x->cols != router->cols || top_k > router->rows) return llar::fail(LLAR_ERR_ARG);
   if (router->rows > kMoeExperts || top_k > kMoeTopK) return llar::fail(LLAR_ERR_UNSUPPORTED);
   if (x->rows == 0 || top_k == 0) return LLAR_OK;
-  if (!weights || !experts || workspace_bytes < llar_moe_route_workspace(x->rows, router->rows))
+  if (!weights || !experts || workspace_bytes < llar_moe_route_workspace(x->rows, router->rows, x->cols))
     return llar::fail(LLAR_ERR_ARG);
   RouteArgs a = {};
   a.x = x->data;
@@ -79,6 +79,7 @@ int llar_moe_route(const llar_matrix* x, const llar_matrix* router, int top_k, l
   a.normalize = normalize != 0;
   a.weights = weights;
   a.experts = experts;
+  a.splits = route_splits(a.M, a.E, a.K);
   a.logits = (double*)workspace;
   LLAR_TRY(launch_route(dtype, a, (hipStream_t)stream) == hipSuccess ? LLAR_OK : LLAR_ERR_HIP);
   return LLAR_OK;
@@ -169,7 +170,7 @@ int llar_moe_ffn(const llar_matrix* x, const void* expert_ids, int id_bytes, con
       q.q = xq;
       q.qld = q.qpad = (int)room.xld;
       q.scale = xs;
-      if (launch_quantize(dtype, q, s) != hipSuccess) return llar::fail(LLAR_ERR_HIP);
+      if (launch_quantize(dtype, q, Pack8Args{}, s) != hipSuccess) return llar::fail(LLAR_ERR_HIP);
       a.x = xq;
       a.xscale = xs;
       a.xld = room.xld;
@@ -191,7 +192,7 @@ int llar_moe_ffn(const llar_matrix* x, const void* expert_ids, int id_bytes, con
       q.q = hq;
       q.qld = q.qpad = (int)room.hqld;
       q.scale = hs;
-      if (launch_quantize(LLAR_FP32, q, s) != hipSuccess) return llar::fail(LLAR_ERR_HIP);
+      if (launch_quantize(LLAR_FP32, q, Pack8Args{}, s) != hipSuccess) return llar::fail(LLAR_ERR_HIP);
       a.h = hq;
       a.hld = room.hqld;
       a.hscale = hs;

@@ -6,126 +6,181 @@ namespace llar_ffn {
 
 // ---- the router's logits --------------------------------------------------------------
 // In binary64, so that which experts are chosen does not hang on the order of the
-// sums.  A workgroup takes 16 tokens by 16 experts, its waves parts of k: lane (r,
-// q) holds eight k of token r and of expert r, widened, and the matrix unit
-// multiplies four k at a time (which four is the same for both).
+// sums.  A workgroup takes 16 tokens by 16 experts and a share of k, its waves 128 k
+// at a time with all their loads in flight: lane (r, q) holds eight k of token r and
+// of expert r, widened, and the matrix unit multiplies four k at a time (which four
+// is the same for both).  Bound by the loads' latency: k is shared between as many
+// workgroups as the card holds.
 typedef double f64x4 __attribute__((ext_vector_type(4)));
 
-template <class E, int kWaves>
-__global__ __launch_bounds__(kWaves * 64) void k_route_logits(RouteArgs a) {
+constexpr int kRouteWaves = 4, kRouteSteps = 4, kRouteK = kRouteWaves * kRouteSteps * 32;
+
+template <class E>
+__global__ __launch_bounds__(kRouteWaves * 64) void k_route_logits(RouteArgs a) {
   typedef typename E::T T;
-  __shared__ double part[kWaves][16][16 + 1];
+  __shared__ double part[kRouteWaves][16][16 + 1];
   const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int groups = (a.E + 15) / 16;
-  const int e0 = (int)(blockIdx.x % groups) * 16, t0 = (int)(blockIdx.x / groups) * 16;
+  const int split = (int)(blockIdx.x % a.splits), tile = (int)(blockIdx.x / a.splits);
+  const int e0 = tile % groups * 16, t0 = tile / groups * 16;
   const T* x = (const T*)a.x + (int64_t)min(t0 + r, a.M - 1) * a.xld;
   const T* w = (const T*)a.w + (int64_t)min(e0 + r, a.E - 1) * a.wld;
   f64x4 acc = {0., 0., 0., 0.};
-  for (int i = wave; i * 32 < a.K; i += kWaves) {
-    const int k = i * 32 + q * 8;
-    const Vals<E, 8> xv = load_vals<E, 8>(x + k, a.K - k), wv = load_vals<E, 8>(w + k, a.K - k);
+  for (int64_t k0 = (int64_t)split * kRouteK + wave * (kRouteSteps * 32); k0 < a.K; k0 += (int64_t)a.splits * kRouteK) {
+    Vals<E, 8> xv[kRouteSteps], wv[kRouteSteps];
 #pragma unroll
-    for (int e = 0; e < 8; e++)
-      acc = __builtin_amdgcn_mfma_f64_16x16x4f64((double)wv.v[e], (double)xv.v[e], acc, 0, 0, 0);
+    for (int s = 0; s < kRouteSteps; s++) {
+      const int k = (int)k0 + s * 32 + q * 8;
+      xv[s] = load_vals<E, 8>(x + k, a.K - k);
+      wv[s] = load_vals<E, 8>(w + k, a.K - k);
+    }
+#pragma unroll
+    for (int s = 0; s < kRouteSteps; s++)
+#pragma unroll
+      for (int e = 0; e < 8; e++)
+        acc = __builtin_amdgcn_mfma_f64_16x16x4f64((double)wv[s].v[e], (double)xv[s].v[e], acc, 0, 0, 0);
   }
   // lane: token r, experts q + 4 i
 #pragma unroll
   for (int i = 0; i < 4; i++) part[wave][r][q + 4 * i] = acc[i];
   __syncthreads();
-  for (int i = threadIdx.x; i < 256; i += kWaves * 64) {
-    const int t = i / 16, e = i % 16;
-    if (t0 + t >= a.M || e0 + e >= a.E) continue;
-    double s = 0.;
+  const int t = threadIdx.x / 16, e = threadIdx.x % 16;
+  if (t0 + t >= a.M || e0 + e >= a.E) return;
+  double s = 0.;
 #pragma unroll
-    for (int j = 0; j < kWaves; j++) s += part[j][t][e];
-    a.logits[(int64_t)(t0 + t) * a.E + e0 + e] = s;
-  }
+  for (int j = 0; j < kRouteWaves; j++) s += part[j][t][e];
+  a.logits[((int64_t)split * a.M + t0 + t) * a.E + e0 + e] = s;
 }
 
 // ---- the choice ------------------------------------------------------------------------
+// The largest of the wave's values, none of them a NaN.
+__device__ __forceinline__ double wave_max(double v) {
+  union {
+    double d;
+    int i[2];
+  } u, o;
+  u.d = v;
+  auto step = [&](auto ctrl) {
+#pragma unroll
+    for (int h = 0; h < 2; h++) o.i[h] = __builtin_amdgcn_update_dpp(u.i[h], u.i[h], decltype(ctrl)::value, 0xf, 0xf, false);
+    u.d = fmax(u.d, o.d);
+  };
+  step(std::integral_constant<int, 0x111>());  // lane - 1 of 16
+  step(std::integral_constant<int, 0x112>());
+  step(std::integral_constant<int, 0x114>());
+  step(std::integral_constant<int, 0x118>());
+  step(std::integral_constant<int, 0x142>());  // lane 15 of 16 to the next 16
+  step(std::integral_constant<int, 0x143>());  // lane 31 to the upper 32
+#pragma unroll
+  for (int h = 0; h < 2; h++) u.i[h] = __builtin_amdgcn_readlane(u.i[h], 63);
+  return u.d;
+}
+__device__ __forceinline__ double wave_sum(double v) {
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d);
+  return v;
+}
+
 // A wave a token: lane l holds the experts l, l + 64, ...; the largest left is taken
 // top_k times, the lowest number first among equals.  A NaN counts as below
 // everything, so that the choices are distinct experts whatever the logits are.
-constexpr int kPerLane = kMoeExperts / 64;
-
-__global__ __launch_bounds__(256) void k_route_choose(RouteArgs a) {
-  const int lane = threadIdx.x & 63;
-  const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (t >= a.M) return;
-  const double* l = a.logits + t * a.E;
+template <int kPerLane>
+__global__ __launch_bounds__(64) void k_route_choose(RouteArgs a) {
+  const int lane = threadIdx.x;
+  const int64_t t = blockIdx.x;
   const double kNone = -__builtin_inf();
   double v[kPerLane];
-  uint32_t left = 0;  // bit i: expert lane + 64 i is not chosen yet
-  double top = kNone;
-  bool nan = false;
 #pragma unroll
   for (int i = 0; i < kPerLane; i++) {
     const int e = lane + 64 * i;
-    v[i] = kNone;
+    v[i] = 0.;
     if (e < a.E) {
-      left |= 1u << i;
-      v[i] = l[e];
-      if (v[i] != v[i]) {
-        nan = true;
-        v[i] = kNone;
-      }
-      top = fmax(top, v[i]);
+      const double* l = a.logits + t * a.E + e;
+#pragma unroll 4
+      for (int s = 0; s < a.splits; s++) v[i] += l[(int64_t)s * a.M * a.E];
     }
   }
+  uint32_t left = 0, nans = 0;  // bit i: expert lane + 64 i is not chosen yet; has a NaN
 #pragma unroll
-  for (int d = 32; d > 0; d >>= 1) top = fmax(top, __shfl_xor(top, d));
-  nan = __any(nan);
-  double sum = 0.;
-  if (!a.sigmoid && !a.normalize) {
+  for (int i = 0; i < kPerLane; i++) {
+    if (lane + 64 * i < a.E) left |= 1u << i;
+    if (v[i] != v[i]) nans |= 1u << i;
+    if (lane + 64 * i >= a.E || v[i] != v[i]) v[i] = kNone;
+  }
+  left &= ~nans;
+  const bool nan = __any(nans != 0);
+  double mine = 0., top = 0.;  // lane j: the logit of choice j
+  int chosen = 0;
+  for (int j = 0; j < a.top_k; j++) {
+    double best = kNone;
+#pragma unroll
+    for (int i = 0; i < kPerLane; i++)
+      if (left >> i & 1) best = fmax(best, v[i]);
+    best = wave_max(best);
+    int e = -1;
+#pragma unroll
+    for (int i = kPerLane - 1; i >= 0; i--) {
+      const uint64_t at = __ballot((left >> i & 1) && v[i] == best);
+      if (at) e = 64 * i + __ffsll((unsigned long long)at) - 1;
+    }
+    if (e < 0) {  // only NaNs are left
+#pragma unroll
+      for (int i = kPerLane - 1; i >= 0; i--) {
+        const uint64_t at = __ballot(nans >> i & 1);
+        if (at) e = 64 * i + __ffsll((unsigned long long)at) - 1;
+      }
+    }
+    if (e % 64 == lane) {
+      left &= ~(1u << (e / 64));
+      nans &= ~(1u << (e / 64));
+    }
+    if (j == 0) top = best;
+    if (lane == j) {
+      mine = best;
+      chosen = e;
+    }
+  }
+  const bool live = lane < a.top_k;
+  const double score = !live ? 0. : a.sigmoid ? 1. / (1. + exp(-mine)) : exp(mine - top);
+  double sum = 1.;  // sigmoid scores stand by themselves unless they are normalised
+  if (a.normalize) {
+    sum = wave_sum(score);
+  } else if (!a.sigmoid) {
+    sum = 0.;
 #pragma unroll
     for (int i = 0; i < kPerLane; i++)
       if (lane + 64 * i < a.E) sum += exp(v[i] - top);
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) sum += __shfl_xor(sum, d);
+    sum = wave_sum(sum);
   }
-  double mine = 0.;  // lane j: the score of choice j
-  for (int j = 0; j < a.top_k; j++) {
-    double best = kNone;
-    int e = 1 << 30;
-#pragma unroll
-    for (int i = 0; i < kPerLane; i++)
-      if ((left >> i & 1) && (e == 1 << 30 || v[i] > best)) {
-        best = v[i];
-        e = lane + 64 * i;
-      }
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) {
-      const double other = __shfl_xor(best, d);
-      const int oe = __shfl_xor(e, d);
-      // a lane without experts left has e = 2^30 and -inf: it loses to any other
-      if (other > best || (other == best && oe < e)) {
-        best = other;
-        e = oe;
-      }
-    }
-    if (e % 64 == lane) left &= ~(1u << (e / 64));
-    const double score = a.sigmoid ? 1. / (1. + exp(-best)) : exp(best - top);
-    if (a.normalize) sum += score;
-    if (lane == j) {
-      mine = score;
-      a.experts[t * a.top_k + j] = e;
-    }
+  if (live) {
+    a.experts[t * a.top_k + lane] = chosen;
+    a.weights[t * a.top_k + lane] = nan ? __builtin_nanf("") : (float)(score / sum);
   }
-  // sigmoid scores stand by themselves unless they are normalised
-  if (a.sigmoid && !a.normalize) sum = 1.;
-  if (lane < a.top_k) a.weights[t * a.top_k + lane] = nan ? __builtin_nanf("") : (float)(mine / sum);
+}
+
+int route_splits(int64_t m, int64_t experts, int64_t k) {
+  // up to four workgroups a CU
+  const int64_t tiles = (m + 15) / 16 * ((experts + 15) / 16), shares = (k + kRouteK - 1) / kRouteK;
+  int64_t splits = 1024 / (tiles > 0 ? tiles : 1);
+  if (splits > shares) splits = shares;
+  return splits < 1 ? 1 : (int)splits;
 }
 
 template <class E>
 hipError_t route(const RouteArgs& a, hipStream_t s) {
-  constexpr int kWaves = 16;
-  const int64_t groups = ((int64_t)a.M + 15) / 16 * ((a.E + 15) / 16);
-  if (!launchable(groups, kWaves * 64)) return hipErrorInvalidConfiguration;
-  k_route_logits<E, kWaves><<<dim3((uint32_t)groups), dim3(kWaves * 64), 0, s>>>(a);
+  const int64_t groups = ((int64_t)a.M + 15) / 16 * ((a.E + 15) / 16) * a.splits;
+  if (!launchable(groups, kRouteWaves * 64) || !launchable(a.M, 64)) return hipErrorInvalidConfiguration;
+  k_route_logits<E><<<dim3((uint32_t)groups), dim3(kRouteWaves * 64), 0, s>>>(a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  k_route_choose<<<dim3((uint32_t)(((int64_t)a.M + 3) / 4)), dim3(256), 0, s>>>(a);
+  const dim3 grid((uint32_t)a.M), block(64);
+  if (a.E <= 64)
+    k_route_choose<1><<<grid, block, 0, s>>>(a);
+  else if (a.E <= 256)
+    k_route_choose<4><<<grid, block, 0, s>>>(a);
+  else
+    k_route_choose<kMoeExperts / 64><<<grid, block, 0, s>>>(a);
   return hipGetLastError();
 }
 hipError_t launch_route(int kind, const RouteArgs& a, hipStream_t s) {

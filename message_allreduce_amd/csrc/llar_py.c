@@ -538,6 +538,7 @@ static int loose8(const llar_matrix* m) {
 static PyObject* int8_room(const call* c, llar_ffn_op op, const float* xs, const llar_matrix* w, const llar_matrix* w2,
                            void** data, size_t* bytes) {
   int layout = xs ? 0 : LLAR_LAYOUT_X_VALUES;
+  if (!xs && !by_rows(&c->xm)) layout |= LLAR_LAYOUT_X_COLUMNS;
   if ((xs && loose8(&c->xm)) || loose8(w) || (w2 && loose8(w2))) layout |= LLAR_LAYOUT_UNALIGNED;
   *bytes = llar_int8_workspace(op, c->xm.rows, w->rows, c->xm.cols, layout);
   return room(c, *bytes, data);
@@ -677,7 +678,7 @@ static PyObject* py_moe_route(PyObject* self, PyObject* const* a, Py_ssize_t n_a
   size[c.x.nd - 1] = top_k;
   void *wd = NULL, *ed = NULL, *space;
   PyObject *w = NULL, *e = NULL, *ws = NULL, *result = NULL;
-  const size_t bytes = llar_moe_route_workspace(c.xm.rows, router.rows);
+  const size_t bytes = llar_moe_route_workspace(c.xm.rows, router.rows, c.xm.cols);
   if (!(w = new_typed(&c.x, size, c.x.nd, t_types[0], &wd))) goto end;
   if (!(e = new_typed(&c.x, size, c.x.nd, t_int32, &ed))) goto end;
   if (!(ws = room(&c, bytes, &space))) goto end;

@@ -50,7 +50,8 @@ def test_linear_int8(L):
     assert call(mat(4, 1 << 17), mat(32, 1 << 17), ok[2]) == -2    # sums that may not fit 32 bits
     assert call(mat(4, 64, -64), *ok[1:]) == -1 and call(mat(-1, 64), *ok[1:]) == -1
     assert call(*ok, space=4096 + 8) == -1                         # misaligned workspace
-    assert call(*ok, xs=None, n=0) == -1                           # no room for the whole numbers
+    # no room for the whole numbers
+    assert call(*ok, xs=None, n=0) == -1 and call(mat(1, 64, 1, 8), ok[1], mat(1, 32), xs=None, n=0) == -1
     assert call(mat(0, 64), mat(32, 64), mat(0, 32)) == 0 and call(mat(4, 64), mat(0, 64), mat(4, 0), ws=None) == 0
 
 
@@ -71,7 +72,7 @@ def test_workspace(L):
     def need(m, n, k, layout, op=0):
         return L.llar_int8_workspace(op, m, n, k, layout)
 
-    assert need(1, 512, 512, 0) == 0 and need(1, 512, 512, 16) >= 512 + 4
+    assert need(1, 512, 512, 0) == 0 and need(4, 512, 512, 16) >= 4 * 512 + 16 and need(1, 512, 512, 18) >= 512 + 4
     assert need(100, 512, 512, 1) >= need(100, 512, 512, 0) + 512 * 512
     assert need(100, 512, 512, 1, 2) >= need(100, 512, 512, 0, 2) + 2 * 512 * 512
     for bad in ((-1, 8, 8), (8, -1, 8), (8, 8, -1), (8, 8, 1 << 17), ((1 << 30) + 1, 8, 8)):
