@@ -20,21 +20,48 @@ struct Chunk {
   u32x4 v;
   __device__ __forceinline__ void zero() { v = u32x4{0u, 0u, 0u, 0u}; }
   __device__ __forceinline__ void load(const char* p) { v = *(const any_u32x4*)p; }
-  // `left` elements exist, none if it is not positive
-  __device__ __forceinline__ void load(const char* p, int64_t left) {
-    if (left >= CE) {
-      load(p);
+  // `left` elements of a row of K exist from here on, none if it is not positive.
+  // The row's last chunk is read as its last 16 bytes (fetch), and moved down (settle).
+  __device__ __forceinline__ void fetch(const char* p, int64_t left, int K) {
+    if (K >= CE) {
+      load(p - (left >= CE ? 0 : (CE - left) * ES));
       return;
     }
     union {
-      typename E::X t[CE];
-      u32x4 q;
+      u32x4 v;
+      uint64_t d[2];
     } u;
-    u.q = u32x4{0u, 0u, 0u, 0u};
-#pragma unroll
-    for (int i = 0; i < CE; i++)
-      if (i < left) u.t[i] = ((const typename E::X*)p)[i];
-    v = u.q;
+    u.v = u32x4{0u, 0u, 0u, 0u};
+#pragma clang loop unroll(disable)
+    for (int i = 0; i < (int)left * ES; i++) {
+      const uint64_t byte = ((const uint8_t*)p)[i];
+      if (i < 8)
+        u.d[0] |= byte << 8 * i;
+      else
+        u.d[1] |= byte << 8 * (i - 8);
+    }
+    v = u.v;
+  }
+  __device__ __forceinline__ void settle(int64_t left, int K) {
+    if (left >= CE || K < CE) return;
+    union {
+      u32x4 v;
+      uint64_t d[2];
+    } u;
+    u.v = v;
+    const int bits = left <= 0 ? 128 : (CE - (int)left) * ES * 8;
+    if (bits >= 64) {
+      u.d[0] = bits < 128 ? u.d[1] >> (bits - 64) : 0;
+      u.d[1] = 0;
+    } else {
+      u.d[0] = u.d[0] >> bits | u.d[1] << (64 - bits);
+      u.d[1] >>= bits;
+    }
+    v = u.v;
+  }
+  __device__ __forceinline__ void load(const char* p, int64_t left, int K) {
+    fetch(p, left, K);
+    settle(left, K);
   }
 };
 
@@ -71,6 +98,7 @@ __device__ __forceinline__ void multiply_steps(f32x4 (&acc)[P][NB], const char* 
   const int q = (threadIdx.x & 63) >> 4;
   const int full = min(i1, K / kStep);
   int i = i0;
+#pragma clang loop unroll(disable)
   for (; i + (U - 1) * stride < full; i += U * stride) {
     C wv[U][P][G], xv[U][NB][G];
 #pragma unroll
@@ -97,17 +125,18 @@ __device__ __forceinline__ void multiply_steps(f32x4 (&acc)[P][NB], const char* 
 #pragma unroll
           for (int b = 0; b < NB; b++) acc[p][b] = mma_chunk<E>(wv[s][p][g], xv[s][b][g], acc[p][b]);
   }
+#pragma clang loop unroll(disable)
   for (; i < i1; i += stride) {
     C wv[P][G], xv[NB][G];
 #pragma unroll
     for (int g = 0; g < G; g++) {
       const int64_t left = K - (int64_t)i * kStep - (q * G + g) * C::CE;
 #pragma unroll
-      for (int p = 0; p < P; p++) wv[p][g].load(w[p] + (int64_t)i * (64 * G) + g * 16, left);
+      for (int p = 0; p < P; p++) wv[p][g].load(w[p] + (int64_t)i * (64 * G) + g * 16, left, K);
 #pragma unroll
       for (int b = 0; b < NB; b++) {
         xv[b][g].zero();
-        if (live[b]) xv[b][g].load(x[b] + (int64_t)i * (64 * G) + g * 16, left);
+        if (live[b]) xv[b][g].load(x[b] + (int64_t)i * (64 * G) + g * 16, left, K);
       }
     }
 #pragma unroll

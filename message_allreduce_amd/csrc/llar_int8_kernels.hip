@@ -15,7 +15,7 @@ __device__ __forceinline__ void pack8_piece(const Pack8Args& a, int64_t group, i
   const int64_t at = (id - line * pieces) * 16;
   if (line >= a.lines[i]) return;
   Chunk<Int8<F32>> c;
-  c.load((const char*)a.src[i] + line * a.ld[i] + at, a.width - at);
+  c.load((const char*)a.src[i] + line * a.ld[i] + at, a.width - at, a.width);
   *(u32x4*)(a.dst[i] + line * a.dld + at) = c.v;
 }
 __global__ __launch_bounds__(kPack8Threads) void k_pack8(Pack8Args a) { pack8_piece(a, blockIdx.x, kPack8Threads); }
@@ -136,50 +136,59 @@ hipError_t launch_quantize(int kind, const QuantArgs& a, const Pack8Args& copies
 }
 
 // ---- few rows ------------------------------------------------------------------------
-// 16 weight rows (gated: 8 of each projection) a workgroup, its waves take the
-// steps of k in turn.
-template <class Out, bool kGated, int kWaves>
+// 16 P weight rows (gated: half of them of each projection) a workgroup, its waves
+// take the steps of k in turn.
+template <class Out, bool kGated, int P, int kWaves>
 __global__ __launch_bounds__(kWaves * 64) void k_few_int8(GemmArgs a) {
   typedef Int8<Out> E;
-  constexpr int kN = kGated ? 8 : 16, G = 2;
-  __shared__ int part[kWaves][16][16];
+  constexpr int kN = kGated ? 8 * P : 16 * P, G = 2;
+  __shared__ int part[P][kWaves][16][16];
   const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n0 = blockIdx.x * kN;
-  const int row = min(n0 + (kGated ? r & 7 : r), a.N - 1);
-  const char* w[1] = {(const char*)a.w[kGated ? r >> 3 : 0] + row * a.wld + q * (16 * G)};
+  // weight row i of the workgroup: gated, the first half of one projection
+  const char* w[P];
+#pragma unroll
+  for (int p = 0; p < P; p++) {
+    const int i = 16 * p + r;
+    w[p] = (const char*)a.w[kGated ? i / kN : 0] + min(n0 + i % kN, a.N - 1) * a.wld + q * (16 * G);
+  }
   const bool live[1] = {r < a.M};
   const char* x[1] = {(const char*)a.x[0] + (live[0] ? r : 0) * a.xld + q * (16 * G)};
-  f32x4 acc[1][1];
+  f32x4 acc[P][1];
   clear<E>(acc);
   constexpr int kStep = 64 * G;
-  multiply_steps<E, 1, 1, G, 2>(acc, w, x, live, a.K, wave, (a.K + kStep - 1) / kStep, kWaves);
+  multiply_steps<E, P, 1, G, 2>(acc, w, x, live, a.K, wave, (a.K + kStep - 1) / kStep, kWaves);
 #pragma unroll
-  for (int i = 0; i < 4; i++) part[wave][r][4 * q + i] = __float_as_int(acc[0][0][i]);
+  for (int p = 0; p < P; p++)
+#pragma unroll
+    for (int i = 0; i < 4; i++) part[p][wave][r][4 * q + i] = __float_as_int(acc[p][0][i]);
   __syncthreads();
   for (int i = threadIdx.x; i < a.M * kN; i += kWaves * 64) {
     const int m = i / kN, n = i % kN;
     if (n0 + n >= a.N) continue;
-    constexpr int P = kGated ? 2 : 1;
-    float v[P];
+    constexpr int kPlanes = kGated ? 2 : 1;
+    float v[kPlanes];
 #pragma unroll
-    for (int p = 0; p < P; p++) {
+    for (int p = 0; p < kPlanes; p++) {
+      const int c = p * kN + n;
       int sum = 0;
 #pragma unroll
-      for (int k = 0; k < kWaves; k++) sum += part[k][m][p * kN + n];
+      for (int k = 0; k < kWaves; k++) sum += part[c / 16][k][m][c % 16];
       v[p] = scaled(sum, a.xscale[m], a.wscale[p][n0 + n]);
     }
-    finish<E, kGated, 1>(a, 0, m, n0 + n, &v[0], &v[P - 1]);
+    finish<E, kGated, 1>(a, 0, m, n0 + n, &v[0], &v[kPlanes - 1]);
   }
 }
 
 // The same for one or two rows of values, quantised by every workgroup for itself:
-// the rows' loads go first, all of the weights' loads follow, and the maximum and
-// the rounding take place while those are on their way.
+// the rows' loads go first, half of the weights' follow (all of them up to k = 4096),
+// and the maximum and the rounding take place while those are on their way.
 template <class Out, bool kGated, int kRows, int kWaves>
 __global__ __launch_bounds__(kWaves * 64, 8) void k_few_int8_values(GemmArgs a) {
   typedef Int8<Out> E;
   constexpr int kN = kGated ? 8 : 16, G = 2, kStep = 64 * G, kSteps = kFewValuesK / (kStep * kWaves);
+  constexpr int kEarly = kSteps / 2;  // all of them would not leave the registers for a second workgroup
   static_assert(kFewValuesK == kWaves * 64 * 8 && kFewValuesK % (kStep * kWaves) == 0, "a piece a thread");
   __shared__ int part[kWaves][16][16];
   __shared__ __attribute__((aligned(16))) int8_t rows[kRows][kFewValuesK];
@@ -197,14 +206,14 @@ __global__ __launch_bounds__(kWaves * 64, 8) void k_few_int8_values(GemmArgs a) 
   const int row = min(n0 + (kGated ? r & 7 : r), a.N - 1);
   const char* w = (const char*)a.w[kGated ? r >> 3 : 0] + row * a.wld + q * (16 * G);
   Chunk<E> wv[kSteps][G];
+  auto fetch = [&](int s) {
+    const int k = (wave + s * kWaves) * kStep;
 #pragma unroll
-  for (int s = 0; s < kSteps; s++)
+    for (int g = 0; g < G; g++)
+      if (k < a.K) wv[s][g].fetch(w + k + g * 16, a.K - k - (q * G + g) * 16, a.K);
+  };
 #pragma unroll
-    for (int g = 0; g < G; g++) {
-      const int k = (wave + s * kWaves) * kStep;
-      wv[s][g].zero();
-      if (k < a.K) wv[s][g].load(w + k + g * 16, a.K - k - (q * G + g) * 16);
-    }
+  for (int s = 0; s < kEarly; s++) fetch(s);
 #pragma unroll
   for (int m = 0; m < kRows; m++) {
     const uint32_t top = wave_max(magnitude(v[m]));
@@ -222,15 +231,19 @@ __global__ __launch_bounds__(kWaves * 64, 8) void k_few_int8_values(GemmArgs a) 
     if (col < (a.K + kStep - 1) / kStep * kStep) *(uint2*)&rows[m][col] = quantizer.eight(v[m].v);
   }
   __syncthreads();
+#pragma unroll
+  for (int s = kEarly; s < kSteps; s++) fetch(s);
   f32x4 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int s = 0; s < kSteps; s++)
 #pragma unroll
     for (int g = 0; g < G; g++) {
       const int k = (wave + s * kWaves) * kStep;
+      if (k >= a.K) continue;
       Chunk<E> xv;
       xv.zero();
-      if (k < a.K && r < kRows) xv.v = *(const u32x4*)&rows[r][k + (q * G + g) * 16];
+      if (r < kRows) xv.v = *(const u32x4*)&rows[r][k + (q * G + g) * 16];
+      if (k + kStep > a.K) wv[s][g].settle(a.K - k - (q * G + g) * 16, a.K);
       acc = mma_chunk<E>(wv[s][g], xv, acc);
     }
   if (r < kRows) {
@@ -258,13 +271,18 @@ __global__ __launch_bounds__(kWaves * 64, 8) void k_few_int8_values(GemmArgs a) 
 
 template <class Out, bool kGated>
 hipError_t few_int8(bool values, const GemmArgs& a, hipStream_t s) {
-  constexpr int kN = kGated ? 8 : 16, kWaves = 16;
-  const int64_t groups = ((int64_t)a.N + kN - 1) / kN;
+  // x is read again by every workgroup: more columns where it is large
+  const bool wide = !values && a.M > 4 && a.N >= (kGated ? 16 : 32) * 192;
+  constexpr int kWaves = 16;
+  const int cols = (kGated ? 8 : 16) * (wide ? 2 : 1);
+  const int64_t groups = ((int64_t)a.N + cols - 1) / cols;
   if (groups == 0 || a.M == 0) return hipSuccess;
   if (!launchable(groups, kWaves * 64)) return hipErrorInvalidConfiguration;
   const dim3 grid((uint32_t)groups), block(kWaves * 64);
-  if (!values)
-    k_few_int8<Out, kGated, kWaves><<<grid, block, 0, s>>>(a);
+  if (wide)
+    k_few_int8<Out, kGated, 2, kWaves><<<grid, block, 0, s>>>(a);
+  else if (!values)
+    k_few_int8<Out, kGated, 1, kWaves><<<grid, block, 0, s>>>(a);
   else if (a.M == 1)
     k_few_int8_values<Out, kGated, 1, kWaves><<<grid, block, 0, s>>>(a);
   else
