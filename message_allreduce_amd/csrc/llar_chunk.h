@@ -63,6 +63,9 @@ struct Chunk {
     fetch(p, left, K);
     settle(left, K);
   }
+  // rows in LDS are aligned, and zeros follow them up to a whole step
+  __device__ __forceinline__ void load(const lds_char* p) { v = *(const LLAR_LDS u32x4*)p; }
+  __device__ __forceinline__ void load(const lds_char* p, int64_t, int) { load(p); }
 };
 
 template <class E>
@@ -88,10 +91,10 @@ __device__ __forceinline__ float add_sums(float a, float b) {
 // i0, i0 + stride, ... below i1 of k: a step is 64 G bytes of a row, G chunks a
 // lane.  w and x point at the lane's first chunk of step 0 (16 G q bytes into the
 // row); a row of x that is not live counts as zeros and is not read.  U steps'
-// loads are in flight.  acc[p][b], lane (r, q): row 16 b + r of x, weight rows 4 q
+// loads are in flight.  x may lie in LDS.  acc[p][b], lane (r, q): row 16 b + r of x, weight rows 4 q
 // .. 4 q + 3 of plane p.
-template <class E, int P, int NB, int G, int U>
-__device__ __forceinline__ void multiply_steps(f32x4 (&acc)[P][NB], const char* const (&w)[P], const char* const (&x)[NB],
+template <class E, int P, int NB, int G, int U, class X>
+__device__ __forceinline__ void multiply_steps(f32x4 (&acc)[P][NB], const char* const (&w)[P], X* const (&x)[NB],
                                                const bool (&live)[NB], int K, int i0, int i1, int stride) {
   typedef Chunk<E> C;
   constexpr int kStep = 4 * C::CE * G;  // elements

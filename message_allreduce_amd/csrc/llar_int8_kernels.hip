@@ -82,7 +82,6 @@ __global__ __launch_bounds__(kQuantThreads<NT>) void k_quantize(QuantArgs a, Pac
   auto put = [&](int col, const Vals<E, 8>& v) {
     const uint2 n = quantizer.eight(v.v);
     if (col + 8 <= a.qpad) {
-      typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
       typedef u32x2 __attribute__((aligned(1))) any_u32x2;
       *(any_u32x2*)(q + col) = u32x2{n.x, n.y};
     } else {

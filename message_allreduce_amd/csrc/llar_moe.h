@@ -43,7 +43,11 @@ struct MoeArgs {
   int T, K, N, outs, E, top_k;
   int id_bytes, act;
 };
-hipError_t launch_moe_up(int kind, bool int8, const MoeArgs& a, hipStream_t s);
-hipError_t launch_moe_down(int kind, bool int8, const MoeArgs& a, hipStream_t s);
+// int8 with `values`: the kernel's own workgroups quantise its rows, x (up to
+// kMoeValuesTokens of kMoeValuesK) and the inner ones (up to 16 tokens and
+// kMoeValuesRows choices of kMoeValuesBytes together).
+constexpr int kMoeValuesTokens = 2, kMoeValuesK = 8192, kMoeValuesRows = 64, kMoeValuesBytes = 16384;
+hipError_t launch_moe_up(int kind, bool int8, bool values, const MoeArgs& a, hipStream_t s);
+hipError_t launch_moe_down(int kind, bool int8, bool values, const MoeArgs& a, hipStream_t s);
 
 }  // namespace llar_ffn

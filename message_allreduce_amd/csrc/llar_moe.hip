@@ -160,7 +160,11 @@ int llar_moe_ffn(const llar_matrix* x, const void* expert_ids, int id_bytes, con
     a.resid = residual ? (const uint8_t*)residual->data + t * a.rld * es : nullptr;
     a.out = (uint8_t*)out->data + t * a.outld * es;
     const void* rows = (const uint8_t*)x->data + t * xld * es;
-    if (int8) {
+    // few rows are quantised by the kernels that read them: two launches less (1 token, 8 of
+    // 64 experts 4096 x 1024)
+    const bool x_values = int8 && a.T <= kMoeValuesTokens && k <= kMoeValuesK && row_major(x);
+    const bool h_values = int8 && a.T <= 16 && a.T * top_k <= kMoeValuesRows && a.T * top_k * n <= kMoeValuesBytes;
+    if (int8 && !x_values) {
       QuantArgs q = {};
       q.x = rows;
       q.xld = xld;
@@ -180,8 +184,8 @@ int llar_moe_ffn(const llar_matrix* x, const void* expert_ids, int id_bytes, con
     }
     a.h = h;
     a.hld = room.hld;
-    if (launch_moe_up(dtype, int8, a, s) != hipSuccess) return llar::fail(LLAR_ERR_HIP);
-    if (int8) {
+    if (launch_moe_up(dtype, int8, x_values, a, s) != hipSuccess) return llar::fail(LLAR_ERR_HIP);
+    if (int8 && !h_values) {
       // rows of choices without an expert are whatever they were, and not read
       QuantArgs q = {};
       q.x = h;
@@ -197,7 +201,7 @@ int llar_moe_ffn(const llar_matrix* x, const void* expert_ids, int id_bytes, con
       a.hld = room.hqld;
       a.hscale = hs;
     }
-    if (launch_moe_down(dtype, int8, a, s) != hipSuccess) return llar::fail(LLAR_ERR_HIP);
+    if (launch_moe_down(dtype, int8, h_values, a, s) != hipSuccess) return llar::fail(LLAR_ERR_HIP);
   }
   return LLAR_OK;
 }

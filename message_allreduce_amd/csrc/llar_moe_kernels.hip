@@ -229,6 +229,36 @@ __device__ __forceinline__ int gather_tokens(uint32_t places, int& member, int& 
   return count;
 }
 
+// Rows of whole numbers in LDS lie `moe_pitch` bytes apart: whole steps, and 16 more
+// so that rows do not meet in the banks.
+__host__ __device__ inline int moe_pitch(int k) { return (k + 127) / 128 * 128 + 16; }
+
+// Quantises a row of k values into LDS, with zeros up to a whole step: NT threads, a
+// wave or the whole workgroup (which then meets at barriers, and needs tops, a word a
+// wave).
+template <class V, int NT>
+__device__ __forceinline__ void quantize_row(const typename V::T* x, int k, int pitch, lds_char* to, float* scale,
+                                             uint32_t* tops) {
+  const int t = threadIdx.x % NT;
+  uint32_t top = 0;
+  for (int col = t * 8; col < k; col += NT * 8) top = max(top, magnitude(load_vals<V, 8>(x + col, k - col)));
+  top = wave_max(top);
+  if constexpr (NT > 64) {
+    if (t % 64 == 0) tops[t / 64] = top;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < NT / 64; i++) top = max(top, tops[i]);
+  }
+  const Quantizer quantizer(top);
+  if (t == 0) *scale = quantizer.scale;
+  for (int col = t * 8; col < pitch; col += NT * 8) {
+    uint2 n = make_uint2(0, 0);
+    if (col < k) n = quantizer.eight(load_vals<V, 8>(x + col, k - col).v);
+    *(LLAR_LDS u32x2*)(to + col) = u32x2{n.x, n.y};
+  }
+  if constexpr (NT > 64) __syncthreads();
+}
+
 // First kernel: h = act(x wg^T) (x wu^T) of every choice.  A workgroup takes 16
 // inner columns (16 rows of each projection) of one expert for all the tokens that
 // chose it, up to 64: its weights are read once.  Every wave finds those tokens by
@@ -236,19 +266,24 @@ __device__ __forceinline__ int gather_tokens(uint32_t places, int& member, int& 
 //
 // With fewer choices than experts the grid has a slot for each choice, and the
 // slot of an expert's first choice does its work; else a slot for each expert.
-template <class E, int NB, int kWaves>
+template <class E, int NB, int kWaves, bool kValues>
 __device__ __forceinline__ void moe_up_rows(const MoeArgs& a, const char* const (&w)[2], int member, int count, int e,
-                                            int n0, float (*part)[2][16][16]) {
+                                            int n0, float (*part)[2][16][16], const lds_char* rows, int pitch,
+                                            const float* xscale) {
   constexpr int G = NB <= 2 ? 2 : 1, U = 2, ES = sizeof(typename E::X), kStep = 64 * G / ES;
   const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  typedef std::conditional_t<kValues, const lds_char, const char> Row;
   bool live[NB];
-  const char* x[NB];
+  Row* x[NB];
 #pragma unroll
   for (int b = 0; b < NB; b++) {
     live[b] = 16 * b + r < count;
     const int t = __shfl(member, 16 * b + r) & 255;
-    x[b] = (const char*)a.x + (live[b] ? t * a.xld * ES : 0) + q * (16 * G);
+    if constexpr (kValues)
+      x[b] = rows + (live[b] ? t * pitch : 0) + q * (16 * G);
+    else
+      x[b] = (const char*)a.x + (live[b] ? t * a.xld * ES : 0) + q * (16 * G);
   }
   const char* at[2] = {w[0] + q * (16 * G), w[1] + q * (16 * G)};
   f32x4 acc[2][NB];
@@ -277,8 +312,8 @@ __device__ __forceinline__ void moe_up_rows(const MoeArgs& a, const char* const 
       const int t = m & 255, j = m >> 8;
       const int64_t to = (int64_t)(t * a.top_k + j) * a.hld + n0 + col;
       if constexpr (E::kInt8) {
-        float g[1] = {scaled(__float_as_int(v[0]), a.xscale[t], a.wscale[0][(int64_t)e * a.N + n0 + col])};
-        const float u = scaled(__float_as_int(v[1]), a.xscale[t], a.wscale[1][(int64_t)e * a.N + n0 + col]);
+        float g[1] = {scaled(__float_as_int(v[0]), xscale[t], a.wscale[0][(int64_t)e * a.N + n0 + col])};
+        const float u = scaled(__float_as_int(v[1]), xscale[t], a.wscale[1][(int64_t)e * a.N + n0 + col]);
         act_values<F32, 1>(g, a.act);
         ((float*)a.h)[to] = g[0] * u;
       } else {
@@ -290,9 +325,10 @@ __device__ __forceinline__ void moe_up_rows(const MoeArgs& a, const char* const 
   }
 }
 
-template <class E, int NB, int kWaves>
+template <class E, int NB, int kWaves, bool kValues>
 __global__ __launch_bounds__(kWaves * 64) void k_moe_up(MoeArgs a, int tiles, bool by_choice) {
-  __shared__ float part[kWaves][2][16][16];
+  extern __shared__ __attribute__((aligned(16))) char quantized[];  // kValues: [T][pitch]
+  __shared__ float part[kWaves][2][16][16], own_scale[kMoeValuesTokens];
   constexpr int ES = sizeof(typename E::X);
   const int lane = threadIdx.x & 63, r = lane & 15;
   const int slot = blockIdx.x / tiles, n0 = (int)(blockIdx.x % tiles) * 16;
@@ -309,16 +345,23 @@ __global__ __launch_bounds__(kWaves * 64) void k_moe_up(MoeArgs a, int tiles, bo
 #pragma unroll
   for (int p = 0; p < 2; p++)
     w[p] = (const char*)a.w[p] + (e * a.w_expert + min(n0 + r, a.N - 1) * a.wld) * ES;
-  if constexpr (NB == 1) {
-    moe_up_rows<E, 1, kWaves>(a, w, member, count, e, n0, part);
-  } else {
-    if (count <= 16)
-      moe_up_rows<E, 1, kWaves>(a, w, member, count, e, n0, part);
-    else if (NB == 2 || count <= 32)
-      moe_up_rows<E, 2, kWaves>(a, w, member, count, e, n0, part);
-    else
-      moe_up_rows<E, NB, kWaves>(a, w, member, count, e, n0, part);
+  const int pitch = moe_pitch(a.K);
+  const float* xscale = kValues ? own_scale : a.xscale;
+  if constexpr (kValues) {
+    for (int t = 0; t < a.T; t++)
+      quantize_row<typename E::Values, kWaves * 64>((const typename E::T*)a.x + t * a.xld, a.K, pitch,
+                                                    (lds_char*)quantized + t * pitch, &own_scale[t], (uint32_t*)part);
   }
+  auto run = [&](auto blocks) {
+    moe_up_rows<E, decltype(blocks)::value, kWaves, kValues>(a, w, member, count, e, n0, part, (lds_char*)quantized, pitch,
+                                                             xscale);
+  };
+  if (NB == 1 || count <= 16)
+    run(std::integral_constant<int, 1>());
+  else if (NB == 2 || count <= 32)
+    run(std::integral_constant<int, (NB < 2 ? NB : 2)>());
+  else
+    run(std::integral_constant<int, NB>());
 }
 
 // Second kernel: y = sum over the choices of weight * h wd^T, + residual.  A
@@ -327,13 +370,15 @@ __global__ __launch_bounds__(kWaves * 64) void k_moe_up(MoeArgs a, int tiles, bo
 // chose the expert, as in the first kernel; when a wave leaves an expert it adds
 // their weighted sums to its own row of every such token in LDS.  No atomics: the
 // waves' rows are added in order.
-template <class E, int P, int NB>
+template <class E, int P, int NB, bool kValues>
 __device__ __forceinline__ void moe_down_rows(const MoeArgs& a, const char* const (&w)[P], int member, float factor,
-                                              int count, int e, int n0, int k0, int k1, float* mine) {
+                                              int count, int e, int n0, int k0, int k1, float* mine,
+                                              const lds_char* inner, int pitch, const float* hscale) {
   constexpr int G = NB <= 2 ? 2 : 1, U = P * NB * G > 4 ? 1 : 2, ES = sizeof(typename E::X);
   const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+  typedef std::conditional_t<kValues, const lds_char, const char> Row;
   bool live[NB];
-  const char* h[NB];
+  Row* h[NB];
   int token[NB];
   float f[NB];
 #pragma unroll
@@ -343,8 +388,11 @@ __device__ __forceinline__ void moe_down_rows(const MoeArgs& a, const char* cons
     f[b] = __shfl(factor, 16 * b + r);
     token[b] = m & 255;
     const int p = live[b] ? (m & 255) * a.top_k + (m >> 8) : 0;
-    if constexpr (E::kInt8) f[b] *= live[b] ? a.hscale[p] : 0.f;
-    h[b] = (const char*)a.h + p * a.hld * ES + q * (16 * G);
+    if constexpr (E::kInt8) f[b] *= live[b] ? hscale[p] : 0.f;
+    if constexpr (kValues)
+      h[b] = inner + p * pitch + q * (16 * G);
+    else
+      h[b] = (const char*)a.h + p * a.hld * ES + q * (16 * G);
   }
   const char* at[P];
 #pragma unroll
@@ -375,13 +423,13 @@ __device__ __forceinline__ void moe_down_rows(const MoeArgs& a, const char* cons
   }
 }
 
-template <class E, int P, int NB, int kWaves>
+template <class E, int P, int NB, int kWaves, bool kValues>
 __global__ __launch_bounds__(kWaves * 64) void k_moe_down(MoeArgs a) {
   constexpr int ES = sizeof(typename E::X), kStep = 64 / ES, kEven = 2;  // waves' shares: whole pairs of chunks
-  extern __shared__ __attribute__((aligned(16))) float part[];  // [kWaves][T][P][16]
+  extern __shared__ __attribute__((aligned(16))) float part[];  // [kWaves][T][P][16]; kValues: and [choices][pitch]
   __shared__ uint32_t bits[kMoeExperts / 32];
   __shared__ int16_t ids[kMoeTokens * kMoeTopK], act[kMoeExperts];
-  __shared__ float weights[kMoeTokens * kMoeTopK];
+  __shared__ float weights[kMoeTokens * kMoeTopK], own_scale[kValues ? kMoeValuesRows : 1];
   const int lane = threadIdx.x & 63, r = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n0 = blockIdx.x * (16 * P);
@@ -407,6 +455,14 @@ __global__ __launch_bounds__(kWaves * 64) void k_moe_down(MoeArgs a) {
     }
   for (int i = 0; i < kMoeExperts / 32; i++) active += __popc(bits[i]);
   active = __builtin_amdgcn_readfirstlane(active);
+  const int pitch = moe_pitch(a.N);
+  lds_char* inner = (lds_char*)part + kWaves * rows * 4;
+  const float* hscale = kValues ? own_scale : a.hscale;
+  if constexpr (kValues) {
+    // a row a wave; those of choices without an expert are whatever they were, and not used
+    for (int p = wave; p < choices; p += kWaves)
+      quantize_row<F32, 64>((const float*)a.h + p * a.hld, a.N, pitch, inner + p * pitch, &own_scale[p], nullptr);
+  }
   __syncthreads();
 
   const int steps = (a.N + kEven * kStep - 1) / (kEven * kStep);  // pairs of chunks of one expert
@@ -428,12 +484,16 @@ __global__ __launch_bounds__(kWaves * 64) void k_moe_down(MoeArgs a) {
 #pragma unroll
     for (int p = 0; p < P; p++)
       w[p] = (const char*)a.wd + (e * a.d_expert + min(n0 + 16 * p + r, a.outs - 1) * a.dld) * ES;
+    auto run = [&](auto blocks) {
+      moe_down_rows<E, P, decltype(blocks)::value, kValues>(a, w, member, factor, count, e, n0, kEven * k0, kEven * k1, mine,
+                                                            inner, pitch, hscale);
+    };
     if (NB == 1 || count <= 16)
-      moe_down_rows<E, P, 1>(a, w, member, factor, count, e, n0, kEven * k0, kEven * k1, mine);
+      run(std::integral_constant<int, 1>());
     else if (NB == 2 || count <= 32)
-      moe_down_rows<E, P, (NB < 2 ? NB : 2)>(a, w, member, factor, count, e, n0, kEven * k0, kEven * k1, mine);
+      run(std::integral_constant<int, (NB < 2 ? NB : 2)>());
     else
-      moe_down_rows<E, P, NB>(a, w, member, factor, count, e, n0, kEven * k0, kEven * k1, mine);
+      run(std::integral_constant<int, NB>());
   }
   __syncthreads();
   typedef typename E::T T;
@@ -455,53 +515,73 @@ __global__ __launch_bounds__(kWaves * 64) void k_moe_down(MoeArgs a) {
 constexpr int kMoeWaves = 8;
 
 template <class E>
-hipError_t moe_up(const MoeArgs& a, hipStream_t s) {
+hipError_t moe_up(const MoeArgs& a, bool values, hipStream_t s) {
   const int64_t choices = (int64_t)a.T * a.top_k;
   const bool by_choice = choices <= a.E;
   const int64_t tiles = ((int64_t)a.N + 15) / 16, groups = tiles * (by_choice ? choices : a.E);
   if (groups == 0) return hipSuccess;
   if (!launchable(groups, kMoeWaves * 64)) return hipErrorInvalidConfiguration;
   const dim3 grid((uint32_t)groups), block(kMoeWaves * 64);
+  if constexpr (E::kInt8) {
+    if (values) {
+      if (a.T > kMoeValuesTokens) return hipErrorInvalidConfiguration;
+      k_moe_up<E, 1, kMoeWaves, true><<<grid, block, a.T * moe_pitch(a.K), s>>>(a, (int)tiles, by_choice);
+      return hipGetLastError();
+    }
+  }
   if (a.T <= 16)
-    k_moe_up<E, 1, kMoeWaves><<<grid, block, 0, s>>>(a, (int)tiles, by_choice);
+    k_moe_up<E, 1, kMoeWaves, false><<<grid, block, 0, s>>>(a, (int)tiles, by_choice);
   else if (a.T <= 32)
-    k_moe_up<E, 2, kMoeWaves><<<grid, block, 0, s>>>(a, (int)tiles, by_choice);
+    k_moe_up<E, 2, kMoeWaves, false><<<grid, block, 0, s>>>(a, (int)tiles, by_choice);
   else
-    k_moe_up<E, 4, kMoeWaves><<<grid, block, 0, s>>>(a, (int)tiles, by_choice);
+    k_moe_up<E, 4, kMoeWaves, false><<<grid, block, 0, s>>>(a, (int)tiles, by_choice);
   return hipGetLastError();
 }
 
 template <class E, int P>
-hipError_t moe_down(const MoeArgs& a, hipStream_t s) {
+hipError_t moe_down(const MoeArgs& a, bool values, hipStream_t s) {
   const int64_t groups = ((int64_t)a.outs + 16 * P - 1) / (16 * P);
   if (groups == 0 || a.T == 0) return hipSuccess;
   if (!launchable(groups, kMoeWaves * 64)) return hipErrorInvalidConfiguration;
   const dim3 grid((uint32_t)groups), block(kMoeWaves * 64);
   const uint32_t lds = kMoeWaves * a.T * P * 16 * 4;
+  if constexpr (E::kInt8) {
+    if (values) {
+      const int choices = a.T * a.top_k;
+      if (a.T > 16 || choices > kMoeValuesRows) return hipErrorInvalidConfiguration;
+      k_moe_down<E, P, 1, kMoeWaves, true><<<grid, block, lds + choices * moe_pitch(a.N), s>>>(a);
+      return hipGetLastError();
+    }
+  }
   if (a.T <= 16)
-    k_moe_down<E, P, 1, kMoeWaves><<<grid, block, lds, s>>>(a);
+    k_moe_down<E, P, 1, kMoeWaves, false><<<grid, block, lds, s>>>(a);
   else if (a.T <= 32)
-    k_moe_down<E, P, 2, kMoeWaves><<<grid, block, lds, s>>>(a);
+    k_moe_down<E, P, 2, kMoeWaves, false><<<grid, block, lds, s>>>(a);
   else
-    k_moe_down<E, P, 4, kMoeWaves><<<grid, block, lds, s>>>(a);
+    k_moe_down<E, P, 4, kMoeWaves, false><<<grid, block, lds, s>>>(a);
   return hipGetLastError();
 }
 // Every workgroup reads the inner rows again, so it takes 32 columns where that
 // leaves enough workgroups (48 tokens, 8 experts, 8192 outputs int8: 48 us against 58;
 // 8 tokens bf16 94 against 100; but 24 tokens with 4096 outputs 78 against 55).
 template <class E>
-hipError_t moe_down(const MoeArgs& a, hipStream_t s) {
-  return a.T > 4 && a.outs >= 32 * 192 ? moe_down<E, 2>(a, s) : moe_down<E, 1>(a, s);
+hipError_t moe_down(const MoeArgs& a, bool values, hipStream_t s) {
+  return a.T > 4 && a.outs >= 32 * 192 ? moe_down<E, 2>(a, values, s) : moe_down<E, 1>(a, values, s);
 }
 
-hipError_t launch_moe_up(int kind, bool int8, const MoeArgs& a, hipStream_t s) {
-  if (int8) return kind == 0 ? moe_up<Int8<F32>>(a, s) : kind == 1 ? moe_up<Int8<F16>>(a, s) : moe_up<Int8<BF16>>(a, s);
-  return kind == 0 ? moe_up<F32>(a, s) : kind == 1 ? moe_up<F16>(a, s) : moe_up<BF16>(a, s);
-}
-hipError_t launch_moe_down(int kind, bool int8, const MoeArgs& a, hipStream_t s) {
+hipError_t launch_moe_up(int kind, bool int8, bool values, const MoeArgs& a, hipStream_t s) {
   if (int8)
-    return kind == 0 ? moe_down<Int8<F32>>(a, s) : kind == 1 ? moe_down<Int8<F16>>(a, s) : moe_down<Int8<BF16>>(a, s);
-  return kind == 0 ? moe_down<F32>(a, s) : kind == 1 ? moe_down<F16>(a, s) : moe_down<BF16>(a, s);
+    return kind == 0   ? moe_up<Int8<F32>>(a, values, s)
+           : kind == 1 ? moe_up<Int8<F16>>(a, values, s)
+                       : moe_up<Int8<BF16>>(a, values, s);
+  return kind == 0 ? moe_up<F32>(a, false, s) : kind == 1 ? moe_up<F16>(a, false, s) : moe_up<BF16>(a, false, s);
+}
+hipError_t launch_moe_down(int kind, bool int8, bool values, const MoeArgs& a, hipStream_t s) {
+  if (int8)
+    return kind == 0   ? moe_down<Int8<F32>>(a, values, s)
+           : kind == 1 ? moe_down<Int8<F16>>(a, values, s)
+                       : moe_down<Int8<BF16>>(a, values, s);
+  return kind == 0 ? moe_down<F32>(a, false, s) : kind == 1 ? moe_down<F16>(a, false, s) : moe_down<BF16>(a, false, s);
 }
 
 }  // namespace llar_ffn

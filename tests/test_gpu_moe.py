@@ -239,6 +239,24 @@ def test_sizes(size, int8, dtype):
     moe_case(*size, dtype, "gelu", int8=int8, residual=True, away=0.4, seed=1)
 
 
+# many outputs: 32 columns a workgroup in the second kernel
+@pytest.mark.parametrize("dtype", DTYPES, ids=ids)
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("m", [3, 5, 20, 40, 64])
+def test_wide_outputs(m, int8, dtype):
+    moe_case(m, 72, 56, 6200, 5, 2, dtype, int8=int8, residual=True)
+    moe_case(m, 72, 200, 6161, 3, 1, dtype, int8=int8, away=0.2)
+
+
+# rows that a kernel's own workgroups quantise, and just beyond
+@pytest.mark.parametrize("dtype", DTYPES, ids=ids)
+def test_rows_quantized_on_the_way(dtype):
+    for size in ((1, 8192, 40, 24, 4, 2), (2, 8200, 40, 24, 4, 2), (2, 8191, 33, 40, 4, 3), (1, 100, 2047, 40, 16, 8),
+                 (1, 64, 2049, 40, 16, 8), (2, 40, 1000, 40, 8, 8), (16, 64, 256, 40, 8, 4), (16, 64, 257, 40, 8, 4),
+                 (17, 64, 64, 40, 8, 1), (13, 64, 40, 6200, 8, 5)):
+        moe_case(*size, dtype, int8=True, away=0.2)
+
+
 @pytest.mark.parametrize("dtype", DTYPES, ids=ids)
 @pytest.mark.parametrize("int8", [False, True])
 @pytest.mark.parametrize("layout", ["row", "halves", "pad", "off"])
