@@ -20,6 +20,8 @@ struct RouteArgs {
   float* weights;
   int32_t* experts;
 };
+constexpr int64_t kRouteSmallTokens = 256, kRouteSmall = 1 << 17;
+bool route_small(int64_t m, int64_t experts, int64_t k);  // one kernel, no logits in memory
 int route_splits(int64_t m, int64_t experts, int64_t k);
 hipError_t launch_route(int kind, const RouteArgs& a, hipStream_t s);
 

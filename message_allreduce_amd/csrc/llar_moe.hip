@@ -51,6 +51,7 @@ extern "C" {
 
 size_t llar_moe_route_workspace(int64_t m, int64_t experts, int64_t k) {
   if (m < 0 || experts < 0 || k < 0 || m > kMaxDim || experts > kMoeExperts || k > kMaxLine) return 0;
+  if (route_small(m, experts, k)) return 0;
   return align256((size_t)route_splits(m, experts, k) * m * experts * 8);
 }
 

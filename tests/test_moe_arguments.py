@@ -34,10 +34,12 @@ def test_route(L):
     assert call(ok[0], mat(8, 63)) == -1
     assert call(mat(4, 64, 1, 4), ok[1]) == -2 and call(ok[0], mat(8, 64, 1, 8)) == -2
     assert call(ok[0], mat(1025, 64)) == -2 and call(ok[0], mat(64, 64), top_k=33) == -2
-    assert call(*ok, space=4097) == -1 and call(*ok, n=L.llar_moe_route_workspace(4, 8, 64) - 1) == -1
+    wide = (mat(4, 8192), mat(64, 8192))
+    assert call(*ok, space=4097) == -1 and call(*wide, n=L.llar_moe_route_workspace(4, 64, 8192) - 1) == -1
     assert call(mat(0, 64), ok[1], weights=None) == 0 and call(*ok, top_k=0, ids=None) == 0  # nothing to do
-    assert L.llar_moe_route_workspace(4, 8, 64) >= 256 and L.llar_moe_route_workspace(4, 8, 0) >= 256
-    for bad in ((-1, 8, 64), (4, 1025, 64), (4, -1, 64), (4, 8, -1), (4, 8, 1 << 21)):
+    assert L.llar_moe_route_workspace(4, 64, 8192) >= 4 * 64 * 8 and L.llar_moe_route_workspace(4, 1024, 0) >= 4 * 1024 * 8
+    assert L.llar_moe_route_workspace(4, 8, 64) == 0              # one kernel
+    for bad in ((-1, 64, 8192), (4, 1025, 8192), (4, -1, 8192), (4, 64, -1), (4, 64, 1 << 21)):
         assert L.llar_moe_route_workspace(*bad) == 0
 
 
