@@ -636,7 +636,10 @@ __device__ __forceinline__ Place place(const GemmArgs& a, int BK, int wg, int to
 // 40 / 24 / 26 / 33, 1024 x 2048 x 2048 - / 21 / 16 / 18, 128 x 2048 x 2048 - / - / 13 / 10.5.
 template <class Shape>
 constexpr int kGemmLds = Shape::kGroups * Shape::kStages * (Shape::TM + Shape::TN) * 128;
-// The large tile's room for a quarter of every wave's residual (kLater).
+// Room behind it: 8-bit operands' scales; the large tile's for a quarter of every
+// wave's residual (kLater).
+template <class E, class Shape>
+constexpr int kScaleLds = E::kInt8 ? (Shape::TM + Shape::TN) * 4 : 0;
 constexpr int kResidLds = 8 * 64 * 32 * 2;
 
 template <class E, bool kXRows, bool kWRows, class Shape, bool kGated, bool kLater>
@@ -719,6 +722,25 @@ __device__ __forceinline__ void gemm_body(const GemmArgs& a, char* smem, int wg,
   bool later = false;
   if constexpr (kLater)
     later = starts_with_resid(a) && t1 - t0 > 8 && ((a.N | a.rld | ((int64_t)a.resid / 2)) & 7) == 0 && a.rld < 1 << 23;
+
+  // 8-bit operands' scales wait in LDS, behind the tiles: fetched at the end they cost
+  // every tile their latency.
+  lds_char* const scales = (lds_char*)smem + kGemmLds<Shape>;
+  auto fetch_scales = [&] {
+    if constexpr (E::kInt8) {
+      if (a.splits > 1) return;
+      for (int i = threadIdx.x; i < TM + Shape::TN; i += Shape::kAllThreads) {
+        const int n = i - TM, p = kGated && n >= TN ? 1 : 0, col = n0 + n - p * TN;
+        float v = 0.f;
+        if (i < TM) {
+          if (m0 + i < a.M) v = a.xscale[m0 + i];
+        } else if (col < a.N) {
+          v = a.wscale[p][col];
+        }
+        *(LLAR_LDS float*)(scales + i * 4) = v;
+      }
+    }
+  };
 
   // The first group's sums start with the bias, and with the residual if only
   // sums follow: its loads then overlap the first tiles', and the results need
@@ -805,6 +827,7 @@ __device__ __forceinline__ void gemm_body(const GemmArgs& a, char* smem, int wg,
         load_x(i, 1);
       }
       begin();
+      fetch_scales();
       wait_loads<kAhead>();
       turn();
       read_w(0, 0);
@@ -894,6 +917,7 @@ __device__ __forceinline__ void gemm_body(const GemmArgs& a, char* smem, int wg,
       wait_loads<0>();
     } else {
       begin();
+      fetch_scales();
     }
   } else {
     // a ring of buffers: all but one are on their way while one is multiplied
@@ -910,6 +934,7 @@ __device__ __forceinline__ void gemm_body(const GemmArgs& a, char* smem, int wg,
     const int rounds = (t1 - t0 + G - 1) / G;
     for (int i = 0; i < S - 1; i++) load(t0 + group + i * G, i);
     begin();
+    fetch_scales();
     int slot = 0;
     for (int r = 0; r < rounds; r++) {
       wait_loads<(S - 2) * kLoads>();
@@ -941,31 +966,32 @@ __device__ __forceinline__ void gemm_body(const GemmArgs& a, char* smem, int wg,
   if (!join_groups<E, Shape, G * kStages * kBuf>(acc, (lds_char*)smem)) return;
   if constexpr (E::kInt8) {
     // whole sums become values; a share of them is joined with the others' first
-    int lane = threadIdx.x & 63;
-    asm volatile("" : "+v"(lane));  // what depends on it would wait in registers through the loop
-    const int q = lane >> 4;
+    if (a.splits == 1) {
+      if (t0 >= t1) __syncthreads();  // no tile's barrier has made the scales visible
+      int lane = threadIdx.x & 63;
+      asm volatile("" : "+v"(lane));  // what depends on it would wait in registers through the loop
+      const int q = lane >> 4;
+      float xs[kXParts][FX];
 #pragma unroll
-    for (int p = 0; p < kWParts; p++)
+      for (int h = 0; h < kXParts; h++)
 #pragma unroll
-      for (int j = 0; j < FW; j++) {
-        const int col = n0 + wn * 16 * FW + p * kWStep + (kSpread ? q * 4 * FW + 4 * j : 16 * j + 4 * q);
-        const float* ws = a.wscale[kGated ? p : 0];
-        float scale[4];
+        for (int f = 0; f < FX; f++)
+          xs[h][f] = *(LLAR_LDS float*)(scales + (wm * 16 * FX + h * kXRowsPart + f * 16 + (lane & 15)) * 4);
 #pragma unroll
-        for (int i = 0; i < 4; i++) scale[i] = a.splits == 1 && col + i < a.N ? ws[col + i] : 0.f;
+      for (int p = 0; p < kWParts; p++)
 #pragma unroll
-        for (int h = 0; h < kXParts; h++)
+        for (int j = 0; j < FW; j++) {
+          const int n = wn * 16 * FW + p * (kGated ? TN : kWStep) + (kSpread ? q * 4 * FW + 4 * j : 16 * j + 4 * q);
+          const f32x4 ws = *(LLAR_LDS f32x4*)(scales + (TM + n) * 4);
 #pragma unroll
-          for (int f = 0; f < FX; f++) {
-            const int m = m0 + wm * 16 * FX + h * kXRowsPart + f * 16 + (lane & 15);
-            const float xs = a.splits == 1 && m < a.M ? a.xscale[m] : 0.f;
-            if (a.splits == 1) {
+          for (int h = 0; h < kXParts; h++)
+#pragma unroll
+            for (int f = 0; f < FX; f++)
 #pragma unroll
               for (int i = 0; i < 4; i++)
-                acc[h][p][f][j][i] = scaled(__float_as_int(acc[h][p][f][j][i]), xs, scale[i]);
-            }
-          }
-      }
+                acc[h][p][f][j][i] = scaled(__float_as_int(acc[h][p][f][j][i]), xs[h][f], ws[i]);
+        }
+    }
   }
   store_results<E, kXRows, kWRows, kGated, Shape, kXParts, kWParts, kSpread, G * kStages * kBuf, !E::kInt8>(
       a, acc, (lds_char*)smem, m0, n0, b, split, ktiles, t0, t1, BK);
@@ -974,7 +1000,7 @@ __device__ __forceinline__ void gemm_body(const GemmArgs& a, char* smem, int wg,
 template <class E, bool kXRows, bool kWRows, class Shape, bool kGated>
 __global__ __launch_bounds__(Shape::kAllThreads) void k_gemm(GemmArgs a) {
   constexpr bool kLater = Shape::kPaired && !kGated && !kWRows && !E::kInt8;
-  __shared__ __attribute__((aligned(1024))) char smem[kGemmLds<Shape> + (kLater ? kResidLds : 0)];
+  __shared__ __attribute__((aligned(1024))) char smem[kGemmLds<Shape> + kScaleLds<E, Shape> + (kLater ? kResidLds : 0)];
   gemm_body<E, kXRows, kWRows, Shape, kGated, kLater>(a, smem, blockIdx.x, gridDim.x);
 }
 
