@@ -263,9 +263,9 @@ __device__ __forceinline__ Frag<E> read_frag(lds_char* lds, uint32_t base, int f
   return out;
 }
 
-// What a whole sum stands for: three roundings of binary32, in an order that
-// neither overflows nor vanishes where the value does not.
-__device__ __forceinline__ float scaled(int sum, float xs, float ws) { return (float)sum * xs * ws; }
+// What a whole sum stands for: three roundings of binary32.  The weight's scale, an
+// ordinary number, comes first: a token's may be as large or as small as its values.
+__device__ __forceinline__ float scaled(int sum, float xs, float ws) { return (float)sum * ws * xs; }
 
 // Applies the epilogue to n neighbours of one output row and stores them.
 // acc0: the sums (gated: of the first projection), acc1: of the second.

@@ -31,6 +31,9 @@ hipError_t launch_pack8(const Pack8Args& a, hipStream_t s) {
 // NT threads a row, eight neighbours at a time; up to kKeep such pieces a thread
 // stay in registers between the maximum and the rounding, longer rows are read
 // twice.  The copies that the product behind it needs go into the same launch.
+// 4096 x 8192 bf16 22 us (4.6 TB/s), 16 x 8192 3 to 4.  Columns apart (a transposed
+// view) are read one by one, through the caches: 166 us; a workgroup that walks 32 rows
+// abreast took 182, and 54 instead of 7 at 64 rows.
 template <int NT>
 constexpr int kQuantThreads = NT < 256 ? 256 : NT;
 

@@ -45,7 +45,8 @@ def quantize_case(x):
 @pytest.mark.parametrize("dtype", DTYPES, ids=ids)
 @pytest.mark.parametrize("layout", ["row", "pad", "off", "col", "colpad"])
 def test_quantize_sizes_and_layouts(layout, dtype):
-    for rows, k in ((1, 1), (1, 8), (3, 7), (5, 130), (9, 2048), (4, 2049), (2, 8192), (3, 8200), (70, 520), (2, 20001)):
+    for rows, k in ((1, 1), (1, 8), (3, 7), (5, 130), (9, 2048), (4, 2049), (2, 8192), (3, 8200), (70, 520), (2, 20001),
+                    (64, 33), (200, 1), (129, 2047), (1100, 40), (1030, 2500), (1024, 9000)):
         quantize_case(Draw(rows + k, dtype)(rows, k, layout))
 
 
@@ -245,11 +246,28 @@ def test_scales_do_not_overflow_on_the_way():
     for m in (1, 3, 40):
         x = torch.full((m, 512), 127, dtype=torch.int8, device="cuda")
         w = torch.full((24, 512), 127, dtype=torch.int8, device="cuda")
-        for a, b in ((1e-30, 1e25), (1e25, 1e-30), (1e-20, 1e-15)):
+        for a, b in ((1e-30, 1e25), (1e25, 1e-30), (1e-20, 1e-15), (2e36, 1e-7), (1e-38, 1e3)):
             xs, ws = torch.full((m,), a, device="cuda"), torch.full((24,), b, device="cuda")
             y = llar.linear_int8(x, w, ws, x_scale=xs, dtype=torch.float32).double()
             want = 512 * 127 * 127 * xs[0].double() * ws[0].double()
             assert ((y - want).abs() <= 3.03 * 2.0 ** -24 * want).all(), (m, a, b)
+
+
+@pytest.mark.parametrize("m", [1, 4, 40])
+def test_tokens_at_the_ends_of_the_range(m):
+    """Values up to bfloat16's largest and down to its least, in one batch: no infinity and no zero on the way."""
+    d8 = Draw8(m)
+    x = Draw(m, torch.bfloat16)(m, 512)
+    x = x / x.abs().amax(1, keepdim=True)
+    x[m - 1] *= 3e38
+    if m > 1:
+        x[0] *= 1e-36
+    w, ws = d8(24, 512), d8.scales(24, 512) * 1e-4
+    y = llar.linear_int8(x, w, ws)
+    q, qs = quantized64(x)
+    want, err = value64(q, qs, w, ws)
+    assert torch.isfinite(want.float()).all()
+    check(y, want, err, "ends")
 
 
 @pytest.mark.parametrize("dtype", DTYPES, ids=ids)

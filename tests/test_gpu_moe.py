@@ -293,6 +293,32 @@ def test_choices(int8, dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES, ids=ids)
+def test_small_values_are_not_lost(dtype):
+    """Subnormal inputs and weights, and products of them that only the last weight makes large again."""
+    tiny = torch.finfo(dtype).smallest_normal
+    eps = torch.finfo(dtype).eps
+    for m in (1, 20):
+        w = Weights(1, dtype, 2, 16, 16, 16)
+        for t in (w.gate, w.up, w.down):
+            t.zero_()
+        x = torch.zeros(m, 16, dtype=dtype, device="cuda")
+        x[:, 0], x[:, 1] = tiny * eps * 3, 1.0            # subnormal in x
+        w.gate[:, 0, 1] = 1.0
+        w.up[:, 0, 0] = 1.0
+        w.down[:, 0, 0] = 1.0
+        w.gate[:, 1, 1] = 1.0
+        w.up[:, 1, 1] = tiny * eps * 5                    # subnormal in a weight
+        w.down[:, 1, 1] = 1.0
+        w.gate[:, 2, 1] = w.up[:, 2, 1] = 1.0
+        w.down[:, 2, 2] = tiny * eps * 7
+        e, a = choose(1, m, 2, 1)
+        a = torch.full_like(a, 1024.0)
+        y = w.call(x, e, a, activation="relu")
+        want = torch.tensor([3.0, 5.0, 7.0], device="cuda", dtype=torch.float64) * 1024 * tiny * eps
+        assert torch.equal(y[:, :3].double(), want.expand(m, 3)), (y[0, :3].double() / (tiny * eps)).tolist()
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=ids)
 @pytest.mark.parametrize("int8", [False, True])
 def test_what_is_not_finite_stays_with_its_tokens(int8, dtype):
     """A row of x, an expert's weights or scale, a routing weight: only the tokens that meet it see it."""
