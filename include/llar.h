@@ -391,9 +391,10 @@ int llar_moe_route(const llar_matrix* x, const llar_matrix* router, int top_k, l
                    float* weights, int32_t* experts, llar_dtype dtype, void* workspace, size_t workspace_bytes,
                    void* stream);
 
-/* Bytes of workspace of llar_moe_ffn for m tokens, inner width n and k inputs;
- * int8 != 0: with scales. */
-size_t llar_moe_workspace(int64_t m, int64_t n, int64_t k, int top_k, llar_dtype dtype, int int8);
+/* Bytes of workspace of llar_moe_ffn for m tokens, inner width n, k inputs and
+ * outs outputs; int8 != 0: with scales. */
+size_t llar_moe_workspace(int64_t m, int64_t n, int64_t k, int64_t outs, int64_t experts, int top_k, llar_dtype dtype,
+                          int int8);
 
 /* out[t] = sum over j < top_k of weights[t][j] (act(x[t] wg^T) * (x[t] wu^T)) wd^T + residual[t],
  * with the matrices of expert e = expert_ids[t][j]: w_gate and w_up E x n x k (the

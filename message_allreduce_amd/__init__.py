@@ -112,7 +112,7 @@ def lib() -> ctypes.CDLL:
         "llar_gated_ffn_int8": (i32, [vp] * 7 + [i32, i32, vp, sz, vp]),
         "llar_moe_route_workspace": (sz, [i64, i64, i64]),
         "llar_moe_route": (i32, [vp, vp, i32, i32, i32, vp, vp, i32, vp, sz, vp]),
-        "llar_moe_workspace": (sz, [i64, i64, i64, i32, i32, i32]),
+        "llar_moe_workspace": (sz, [i64, i64, i64, i64, i64, i32, i32, i32]),
         "llar_moe_ffn": (i32, [vp, vp, i32, vp, i32] + [vp] * 8 + [i32, i32, vp, sz, vp]),
     }
     for name, (res, args) in sig.items():

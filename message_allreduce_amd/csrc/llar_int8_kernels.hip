@@ -183,7 +183,9 @@ __global__ __launch_bounds__(kWaves * 64) void k_few_int8(GemmArgs a) {
   }
 }
 
-// The same for one or two rows of values, quantised by every workgroup for itself:
+// The same for one or two rows of values, quantised by every workgroup for itself
+// (cold weights bf16, 3584 -> 8192: one row 7.6 us, two 8.5; four rows would take 13.2,
+// against 2.9 + 7.8 with the quantisation before it):
 // the rows' loads go first, half of the weights' follow (all of them up to k = 4096),
 // and the maximum and the rounding take place while those are on their way.
 template <class Out, bool kGated, int kRows, int kWaves>

@@ -41,15 +41,18 @@ struct MoeArgs {
   const float* weights;
   const void* resid;
   void* out;
+  float* partial;        // [parts][T][outs], with more than one part
   int64_t xld, w_expert, wld, d_expert, dld, hld, rld, outld;
   int T, K, N, outs, E, top_k;
   int id_bytes, act;
+  int parts;
 };
 // int8 with `values`: the kernel's own workgroups quantise its rows, x (up to
-// kMoeValuesTokens of kMoeValuesK) and the inner ones (up to 16 tokens and
-// kMoeValuesRows choices of kMoeValuesBytes together).
-constexpr int kMoeValuesTokens = 2, kMoeValuesK = 8192, kMoeValuesRows = 64, kMoeValuesBytes = 16384;
+// kMoeValuesTokens of kMoeValuesK) and the inner ones (up to
+// kMoeValuesRows choices of kMoeValuesBytes together: two rows a wave).
+constexpr int kMoeValuesTokens = 2, kMoeValuesK = 8192, kMoeValuesRows = 16, kMoeValuesBytes = 16384;
 hipError_t launch_moe_up(int kind, bool int8, bool values, const MoeArgs& a, hipStream_t s);
+int moe_parts(int T, int64_t n, int64_t outs, int64_t experts, int top_k, int es);
 hipError_t launch_moe_down(int kind, bool int8, bool values, const MoeArgs& a, hipStream_t s);
 
 }  // namespace llar_ffn

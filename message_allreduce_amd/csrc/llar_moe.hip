@@ -22,13 +22,20 @@ int check_rows(const llar_matrix* m) {
 
 // The workspace of one pair of launches.
 struct Rooms {
-  size_t xq, xs, h, hq, hs;
+  size_t xq, xs, h, hq, hs, partial;
   int64_t xld, hld, hqld;
-  size_t total() const { return align256(xq) + align256(xs) + align256(h) + align256(hq) + align256(hs); }
+  size_t total() const {
+    return align256(xq) + align256(xs) + align256(h) + align256(hq) + align256(hs) + align256(partial);
+  }
 };
-Rooms rooms(int64_t m, int64_t n, int64_t k, int top_k, int es, bool int8) {
+Rooms rooms(int64_t m, int64_t n, int64_t k, int64_t outs, int64_t experts, int top_k, int es, bool int8) {
   const int64_t tokens = std::min<int64_t>(m, kMoeTokens), choices = tokens * top_k;
   Rooms r = {};
+  // the last tokens of a long batch are fewer and may be shared between more
+  for (const int64_t t : {tokens, m % kMoeTokens}) {
+    const int parts = moe_parts((int)t, n, outs, experts, top_k, int8 ? 1 : es);
+    if (parts > 1) r.partial = std::max(r.partial, (size_t)parts * t * outs * 4);
+  }
   if (int8) {
     r.xld = cdiv(k, 16) * 16;
     r.xq = (size_t)tokens * r.xld;
@@ -86,11 +93,12 @@ int llar_moe_route(const llar_matrix* x, const llar_matrix* router, int top_k, l
   return LLAR_OK;
 }
 
-size_t llar_moe_workspace(int64_t m, int64_t n, int64_t k, int top_k, llar_dtype dtype, int int8) {
-  if (!dtype_ok(dtype) || m < 0 || n < 0 || k < 0 || m > kMaxDim || n > kMaxLine || k > kMaxLine || top_k < 0 ||
-      top_k > kMoeTopK)
+size_t llar_moe_workspace(int64_t m, int64_t n, int64_t k, int64_t outs, int64_t experts, int top_k, llar_dtype dtype,
+                          int int8) {
+  if (!dtype_ok(dtype) || m < 0 || n < 0 || k < 0 || outs < 0 || experts < 0 || m > kMaxDim || n > kMaxLine ||
+      k > kMaxLine || outs > kMaxDim || experts > kMoeExperts || top_k < 0 || top_k > kMoeTopK)
     return 0;
-  return rooms(m, n, k, top_k, elem_size(dtype), int8 != 0).total();
+  return rooms(m, n, k, outs, experts, top_k, elem_size(dtype), int8 != 0).total();
 }
 
 int llar_moe_ffn(const llar_matrix* x, const void* expert_ids, int id_bytes, const float* weights, int top_k,
@@ -121,7 +129,7 @@ int llar_moe_ffn(const llar_matrix* x, const void* expert_ids, int id_bytes, con
   if (top_k > 0 && (!expert_ids || !weights)) return llar::fail(LLAR_ERR_ARG);
   const int es = elem_size(dtype);
   const int64_t n = w_gate->rows, k = x->cols;
-  const Rooms room = rooms(x->rows, n, k, top_k, es, int8);
+  const Rooms room = rooms(x->rows, n, k, out->cols, w_gate->experts, top_k, es, int8);
   if (workspace_bytes < room.total()) return llar::fail(LLAR_ERR_ARG);
   const hipStream_t s = (hipStream_t)stream;
 
@@ -131,6 +139,7 @@ int llar_moe_ffn(const llar_matrix* x, const void* expert_ids, int id_bytes, con
   void* const h = c.take(room.h);
   int8_t* const hq = (int8_t*)c.take(room.hq);
   float* const hs = (float*)c.take(room.hs);
+  float* const partial = (float*)c.take(room.partial);
   if (!c.ok) return llar::fail(LLAR_ERR_ARG);
 
   MoeArgs a = {};
@@ -158,13 +167,15 @@ int llar_moe_ffn(const llar_matrix* x, const void* expert_ids, int id_bytes, con
     a.T = (int)std::min<int64_t>(kMoeTokens, x->rows - t);
     a.ids = (const uint8_t*)expert_ids + t * top_k * id_bytes;
     a.weights = weights + t * top_k;
+    a.parts = moe_parts(a.T, n, a.outs, a.E, top_k, int8 ? 1 : es);
+    a.partial = partial;
     a.resid = residual ? (const uint8_t*)residual->data + t * a.rld * es : nullptr;
     a.out = (uint8_t*)out->data + t * a.outld * es;
     const void* rows = (const uint8_t*)x->data + t * xld * es;
     // few rows are quantised by the kernels that read them: two launches less (1 token, 8 of
-    // 64 experts 4096 x 1024)
+    // 64 experts 4096 x 1024: 16.7 + 10.4 us and 4 for each quantisation, now 17.8 + 11.8)
     const bool x_values = int8 && a.T <= kMoeValuesTokens && k <= kMoeValuesK && row_major(x);
-    const bool h_values = int8 && a.T <= 16 && a.T * top_k <= kMoeValuesRows && a.T * top_k * n <= kMoeValuesBytes;
+    const bool h_values = int8 && a.T <= kMoeValuesRows && a.T * top_k <= kMoeValuesRows && a.T * top_k * n <= kMoeValuesBytes;
     if (int8 && !x_values) {
       QuantArgs q = {};
       q.x = rows;

@@ -297,30 +297,39 @@ __device__ __forceinline__ int expert_at(const MoeArgs& a, int p) {
   return low < (uint32_t)a.E && (words == 1 || high == 0) ? (int)low : -1;
 }
 // Which places of the lane's token's list name expert e, a bit each: the choices go
-// over the lanes 64 at a time (id(p): the expert of choice p), and what a ballot says
-// of them is cut to the lane's token's part.
-template <class F>
-__device__ __forceinline__ uint32_t places_of(const MoeArgs& a, int e, F id) {
+// over the lanes 64 at a time, their loads eight at a time, and what a ballot says of
+// them is cut to the lane's token's part.
+__device__ __forceinline__ uint32_t places_of(const MoeArgs& a, int e) {
   const int lane = threadIdx.x & 63, choices = a.T * a.top_k, first = lane * a.top_k;
   uint64_t mine = 0;
-  for (int p0 = 0; p0 < choices; p0 += 64) {
-    const int p = p0 + lane;
-    const uint64_t named = __ballot(id(min(p, choices - 1)) == e && p < choices);
-    const int off = first - p0;
-    mine |= off >= 64 ? 0 : off >= 0 ? named >> off : -off < a.top_k ? named << -off : 0;
+  for (int p0 = 0; p0 < choices; p0 += 512) {
+    int id[8];
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+      const int p = p0 + 64 * i + lane;
+      id[i] = -1;
+      if (p0 + 64 * i < choices) id[i] = expert_at(a, min(p, choices - 1));
+      if (p >= choices) id[i] = -1;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+      if (p0 + 64 * i >= choices) break;
+      const uint64_t named = __ballot(id[i] == e);
+      const int off = first - p0 - 64 * i;
+      mine |= off >= 64 ? 0 : off >= 0 ? named >> off : -off < a.top_k ? named << -off : 0;
+    }
   }
   return lane < a.T ? (uint32_t)mine & (uint32_t)((1ull << a.top_k) - 1) : 0u;
 }
-// The tokens that have any of them: lane i gets the i-th such token and the first of
-// its places (256 times it); returns their number.
-__device__ __forceinline__ int gather_tokens(uint32_t places, int& member, int& to) {
+// Lane i gets the value of the i-th of the lanes in `chose`.
+__device__ __forceinline__ int gathered(uint64_t chose, int value) {
   const int lane = threadIdx.x & 63;
-  const uint64_t chose = __ballot(places != 0), below = (1ull << lane) - 1;
-  const int count = __popcll(chose);
-  to = (places ? __popcll(chose & below) : count + __popcll(~chose & below)) * 4;
-  member = __builtin_amdgcn_ds_permute(to, lane | (places ? __builtin_ctz(places) : 0) << 8);
-  return count;
+  const uint64_t below = (1ull << lane) - 1;
+  const int to = chose >> lane & 1 ? __popcll(chose & below) : __popcll(chose) + __popcll(~chose & below);
+  return __builtin_amdgcn_ds_permute(to * 4, value);
 }
+// A token and one of its places, as lanes hand them round.
+__device__ __forceinline__ int member_of(int token, int place) { return token | place << 8; }
 
 // Rows of whole numbers in LDS lie `moe_pitch` bytes apart: whole steps, and 16 more
 // so that rows do not meet in the banks.
@@ -379,6 +388,19 @@ __device__ __forceinline__ void moe_up_rows(const MoeArgs& a, const char* const 
       x[b] = (const char*)a.x + (live[b] ? t * a.xld * ES : 0) + q * (16 * G);
   }
   const char* at[2] = {w[0] + q * (16 * G), w[1] + q * (16 * G)};
+  // the scales that a thread's results need, ahead of the operands
+  float ws[2] = {1.f, 1.f}, xs[NB];
+#pragma unroll
+  for (int b = 0; b < NB; b++) xs[b] = 1.f;
+  if constexpr (E::kInt8) {
+    if (threadIdx.x < 256) {
+      const int64_t col = (int64_t)e * a.N + min(n0 + (int)threadIdx.x % 16, a.N - 1);
+#pragma unroll
+      for (int p = 0; p < 2; p++) ws[p] = a.wscale[p][col];
+#pragma unroll
+      for (int b = 0; b < NB; b++) xs[b] = xscale[min(__shfl(member, 16 * b + (int)threadIdx.x / 16) & 255, a.T - 1)];
+    }
+  }
   f32x4 acc[2][NB];
   clear<E>(acc);
   multiply_steps<E, 2, NB, G, U>(acc, at, x, live, a.K, wave, (a.K + kStep - 1) / kStep, kWaves);
@@ -391,9 +413,9 @@ __device__ __forceinline__ void moe_up_rows(const MoeArgs& a, const char* const 
 #pragma unroll
     for (int p = 0; p < 2; p++) *(f32x4*)&part[wave][p][r][4 * q] = acc[p][b];
     __syncthreads();
-    for (int i = threadIdx.x; i < 256; i += kWaves * 64) {
-      const int row = i / 16, col = i % 16;
-      const int m = __shfl(member, 16 * b + row);  // whole waves are in this loop
+    if (threadIdx.x < 256) {  // whole waves
+      const int row = threadIdx.x / 16, col = threadIdx.x % 16;
+      const int m = __shfl(member, 16 * b + row);
       float v[2];
 #pragma unroll
       for (int p = 0; p < 2; p++) {
@@ -401,18 +423,18 @@ __device__ __forceinline__ void moe_up_rows(const MoeArgs& a, const char* const 
 #pragma unroll
         for (int k = 1; k < kWaves; k++) v[p] = add_sums<E>(v[p], part[k][p][row][col]);
       }
-      if (16 * b + row >= count || n0 + col >= a.N) continue;
-      const int t = m & 255, j = m >> 8;
-      const int64_t to = (int64_t)(t * a.top_k + j) * a.hld + n0 + col;
-      if constexpr (E::kInt8) {
-        float g[1] = {scaled(__float_as_int(v[0]), xscale[t], a.wscale[0][(int64_t)e * a.N + n0 + col])};
-        const float u = scaled(__float_as_int(v[1]), xscale[t], a.wscale[1][(int64_t)e * a.N + n0 + col]);
-        act_values<F32, 1>(g, a.act);
-        ((float*)a.h)[to] = g[0] * u;
-      } else {
-        float g[1] = {v[0]};
-        act_values<E, 1>(g, a.act);
-        ((typename E::T*)a.h)[to] = E::from(g[0] * v[1]);
+      if (16 * b + row < count && n0 + col < a.N) {
+        const int64_t to = (int64_t)((m & 255) * a.top_k + (m >> 8)) * a.hld + n0 + col;
+        if constexpr (E::kInt8) {
+          float g[1] = {scaled(__float_as_int(v[0]), xs[b], ws[0])};
+          const float u = scaled(__float_as_int(v[1]), xs[b], ws[1]);
+          act_values<F32, 1>(g, a.act);
+          ((float*)a.h)[to] = g[0] * u;
+        } else {
+          float g[1] = {v[0]};
+          act_values<E, 1>(g, a.act);
+          ((typename E::T*)a.h)[to] = E::from(g[0] * v[1]);
+        }
       }
     }
   }
@@ -427,9 +449,11 @@ __global__ __launch_bounds__(kWaves * 64) void k_moe_up(MoeArgs a, int tiles, bo
   const int slot = blockIdx.x / tiles, n0 = (int)(blockIdx.x % tiles) * 16;
   const int e = by_choice ? expert_at(a, slot) : slot;
   if (e < 0) return;
-  int member, to;
-  const int count = gather_tokens(places_of(a, e, [&](int p) { return expert_at(a, p); }), member, to);
+  const uint32_t places = places_of(a, e);
+  const uint64_t chose = __ballot(places != 0);
+  const int count = __popcll(chose);
   if (count == 0) return;
+  const int member = gathered(chose, member_of(lane, places ? __builtin_ctz(places) : 0));
   if (by_choice) {
     const int first = __builtin_amdgcn_readfirstlane(member);
     if ((first & 255) * a.top_k + (first >> 8) != slot) return;
@@ -473,7 +497,7 @@ __device__ __forceinline__ void moe_down_rows(const MoeArgs& a, const char* cons
   bool live[NB];
   Row* h[NB];
   int token[NB];
-  float f[NB];
+  float f[NB], hs[NB], ds[P][4];
 #pragma unroll
   for (int b = 0; b < NB; b++) {
     live[b] = 16 * b + r < count;
@@ -481,7 +505,8 @@ __device__ __forceinline__ void moe_down_rows(const MoeArgs& a, const char* cons
     f[b] = __shfl(factor, 16 * b + r);
     token[b] = m & 255;
     const int p = live[b] ? (m & 255) * a.top_k + (m >> 8) : 0;
-    if constexpr (E::kInt8) f[b] *= live[b] ? hscale[p] : 0.f;
+    hs[b] = 1.f;
+    if constexpr (E::kInt8) hs[b] = hscale[p];
     if constexpr (kValues)
       h[b] = inner + p * pitch + q * (16 * G);
     else
@@ -490,29 +515,33 @@ __device__ __forceinline__ void moe_down_rows(const MoeArgs& a, const char* cons
   const char* at[P];
 #pragma unroll
   for (int p = 0; p < P; p++) at[p] = w[p] + q * (16 * G);
+  // scales are fetched with the first operands and used after the last
+#pragma unroll
+  for (int p = 0; p < P; p++)
+#pragma unroll
+    for (int v = 0; v < 4; v++) {
+      ds[p][v] = 1.f;
+      if constexpr (E::kInt8) ds[p][v] = a.dscale[(int64_t)e * a.outs + min(n0 + 16 * p + 4 * q + v, a.outs - 1)];
+    }
   f32x4 acc[P][NB];
   clear<E>(acc);
   // a step here is G chunks a lane; k0 and k1 count single ones
   multiply_steps<E, P, NB, G, U>(acc, at, h, live, a.N, k0 / G, (k1 + G - 1) / G, 1);
 #pragma unroll
-  for (int p = 0; p < P; p++) {
-    float scale[4] = {1.f, 1.f, 1.f, 1.f};
-    if constexpr (E::kInt8) {
+  for (int b = 0; b < NB; b++) {
+    if (!live[b]) continue;
+    if constexpr (E::kInt8) f[b] *= hs[b];
 #pragma unroll
-      for (int v = 0; v < 4; v++) scale[v] = a.dscale[(int64_t)e * a.outs + min(n0 + 16 * p + 4 * q + v, a.outs - 1)];
-    }
+    for (int p = 0; p < P; p++) {
+      f32x4* y = (f32x4*)(mine + (token[b] * P + p) * 16 + 4 * q);
+      f32x4 sum = *y;
 #pragma unroll
-    for (int b = 0; b < NB; b++)
-      if (live[b]) {
-        f32x4* y = (f32x4*)(mine + (token[b] * P + p) * 16 + 4 * q);
-        f32x4 sum = *y;
-#pragma unroll
-        for (int v = 0; v < 4; v++) {
-          const float c = acc[p][b][v];
-          sum[v] = fmaf(f[b], E::kInt8 ? (float)__float_as_int(c) * scale[v] : c, sum[v]);
-        }
-        *y = sum;
+      for (int v = 0; v < 4; v++) {
+        const float c = acc[p][b][v];
+        sum[v] = fmaf(f[b], E::kInt8 ? (float)__float_as_int(c) * ds[p][v] : c, sum[v]);
       }
+      *y = sum;
+    }
   }
 }
 
@@ -520,17 +549,19 @@ template <class E, int P, int NB, int kWaves, bool kValues>
 __global__ __launch_bounds__(kWaves * 64) void k_moe_down(MoeArgs a) {
   constexpr int ES = sizeof(typename E::X), kStep = 64 / ES, kEven = 2;  // waves' shares: whole pairs of chunks
   extern __shared__ __attribute__((aligned(16))) float part[];  // [kWaves][T][P][16]; kValues: and [choices][pitch]
-  __shared__ uint32_t bits[kMoeExperts / 32];
+  __shared__ uint32_t bits[kMoeExperts / 32], chosen[kMoeExperts][2];
   __shared__ int16_t ids[kMoeTokens * kMoeTopK], act[kMoeExperts];
   __shared__ float weights[kMoeTokens * kMoeTopK], own_scale[kValues ? kMoeValuesRows : 1];
   const int lane = threadIdx.x & 63, r = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int n0 = blockIdx.x * (16 * P);
+  const int share = blockIdx.x % a.parts, n0 = (int)(blockIdx.x / a.parts) * (16 * P);
   const int choices = a.T * a.top_k, rows = a.T * P * 16;
   float* mine = part + wave * rows;
   for (int i = lane * 4; i < rows; i += 256) *(f32x4*)(mine + i) = f32x4{0.f, 0.f, 0.f, 0.f};
-  // the experts that any token chose, in order
-  if (threadIdx.x < kMoeExperts / 32) bits[threadIdx.x] = 0;
+  // the experts that any token chose, in order, and for each the tokens
+  const int words = (a.E + 31) / 32;
+  if (threadIdx.x < words) bits[threadIdx.x] = 0;
+  for (int i = threadIdx.x; i < 2 * min(choices, a.E); i += kWaves * 64) (&chosen[0][0])[i] = 0;
   __syncthreads();
   for (int p = threadIdx.x; p < choices; p += kWaves * 64) {
     const int e = expert_at(a, p);
@@ -539,14 +570,16 @@ __global__ __launch_bounds__(kWaves * 64) void k_moe_down(MoeArgs a) {
     if (e >= 0) atomicOr(&bits[e >> 5], 1u << (e & 31));
   }
   __syncthreads();
+  for (int p = threadIdx.x; p < choices; p += kWaves * 64) {
+    const int e = ids[p], t = p / a.top_k;
+    if (e < 0) continue;
+    int rank = __popc(bits[e >> 5] & ((1u << (e & 31)) - 1));
+    for (int i = 0; i < e >> 5; i++) rank += __popc(bits[i]);
+    act[rank] = (int16_t)e;
+    atomicOr(&chosen[rank][t >> 5], 1u << (t & 31));
+  }
   int active = 0;
-  for (int e = threadIdx.x; e < kMoeExperts; e += kWaves * 64)
-    if (bits[e >> 5] >> (e & 31) & 1) {
-      int rank = __popc(bits[e >> 5] & ((1u << (e & 31)) - 1));
-      for (int i = 0; i < e >> 5; i++) rank += __popc(bits[i]);
-      act[rank] = (int16_t)e;
-    }
-  for (int i = 0; i < kMoeExperts / 32; i++) active += __popc(bits[i]);
+  for (int i = 0; i < words; i++) active += __popc(bits[i]);
   active = __builtin_amdgcn_readfirstlane(active);
   const int pitch = moe_pitch(a.N);
   lds_char* inner = (lds_char*)part + kWaves * rows * 4;
@@ -559,34 +592,56 @@ __global__ __launch_bounds__(kWaves * 64) void k_moe_down(MoeArgs a) {
   __syncthreads();
 
   const int steps = (a.N + kEven * kStep - 1) / (kEven * kStep);  // pairs of chunks of one expert
-  const int64_t all = (int64_t)active * steps;
-  int64_t s = all * wave / kWaves;
-  const int64_t s1 = all * (wave + 1) / kWaves;
+  const int64_t all = (int64_t)active * steps, runs = (int64_t)a.parts * kWaves, run = share * kWaves + wave;
+  int64_t s = all * run / runs;
+  const int64_t s1 = all * (run + 1) / runs;
   while (s < s1) {
     const int i = (int)(s / steps), k0 = (int)(s - (int64_t)i * steps);
     const int k1 = (int)min((int64_t)steps, k0 + (s1 - s));
     s += k1 - k0;
     const int e = __builtin_amdgcn_readfirstlane(act[i]);
-    const uint32_t places = places_of(a, e, [&](int p) { return (int)ids[p]; });
+    const uint64_t chose = (uint64_t)__builtin_amdgcn_readfirstlane(chosen[i][1]) << 32 |
+                           (uint32_t)__builtin_amdgcn_readfirstlane(chosen[i][0]);
+    const int count = __popcll(chose);
+    // the token's places of this expert: the first, and the sum of their weights
+    int place = 0;
     float sum = 0.f;
-    for (uint32_t left = places; left; left &= left - 1) sum += weights[lane * a.top_k + __builtin_ctz(left)];
-    int member, to;
-    const int count = gather_tokens(places, member, to);
-    const float factor = __int_as_float(__builtin_amdgcn_ds_permute(to, __float_as_int(sum)));
+    if (chose >> lane & 1) {
+      bool found = false;
+      for (int c0 = 0; c0 < a.top_k; c0 += 8) {
+        int id[8];
+        float weight[8];
+#pragma unroll
+        for (int c = 0; c < 8; c++) {
+          const int at = lane * a.top_k + min(c0 + c, a.top_k - 1);
+          id[c] = ids[at];
+          weight[c] = weights[at];
+        }
+#pragma unroll
+        for (int c = 0; c < 8; c++)
+          if (id[c] == e && c0 + c < a.top_k) {
+            sum += weight[c];
+            if (!found) place = c0 + c;
+            found = true;
+          }
+      }
+    }
+    const int member = gathered(chose, member_of(lane, place));
+    const float factor = __int_as_float(gathered(chose, __float_as_int(sum)));
     const char* w[P];
 #pragma unroll
     for (int p = 0; p < P; p++)
       w[p] = (const char*)a.wd + (e * a.d_expert + min(n0 + 16 * p + r, a.outs - 1) * a.dld) * ES;
-    auto run = [&](auto blocks) {
+    auto multiply = [&](auto blocks) {
       moe_down_rows<E, P, decltype(blocks)::value, kValues>(a, w, member, factor, count, e, n0, kEven * k0, kEven * k1, mine,
                                                             inner, pitch, hscale);
     };
     if (NB == 1 || count <= 16)
-      run(std::integral_constant<int, 1>());
+      multiply(std::integral_constant<int, 1>());
     else if (NB == 2 || count <= 32)
-      run(std::integral_constant<int, (NB < 2 ? NB : 2)>());
+      multiply(std::integral_constant<int, (NB < 2 ? NB : 2)>());
     else
-      run(std::integral_constant<int, NB>());
+      multiply(std::integral_constant<int, NB>());
   }
   __syncthreads();
   typedef typename E::T T;
@@ -596,70 +651,122 @@ __global__ __launch_bounds__(kWaves * 64) void k_moe_down(MoeArgs a) {
     float v = 0.f;
 #pragma unroll
     for (int k = 0; k < kWaves; k++) v += part[k * rows + i];
+    if (a.parts > 1) {
+      a.partial[((int64_t)share * a.T + t) * a.outs + c] = v;
+      continue;
+    }
     if (a.resid) v += E::to(((const T*)a.resid)[t * a.rld + c]);
     ((T*)a.out)[t * a.outld + c] = E::from(v);
   }
 }
 
 
+// The shares' sums, in their order, and the residual.
+template <class E>
+__global__ __launch_bounds__(256) void k_moe_join(MoeArgs a) {
+  typedef typename E::T T;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, count = (int64_t)a.T * a.outs;
+  if (i >= count) return;
+  float v = 0.f;
+#pragma unroll 8
+  for (int s = 0; s < a.parts; s++) v += a.partial[s * count + i];
+  const int64_t t = i / a.outs, c = i - t * a.outs;
+  if (a.resid) v += E::to(((const T*)a.resid)[t * a.rld + c]);
+  ((T*)a.out)[t * a.outld + c] = E::from(v);
+}
+
 // Eight waves a workgroup: two to four workgroups a CU cover each other's ends
 // (1 token, 8 of 64 experts 4096 x 1024 bf16: second kernel 15.1 us against 16.6 with
-// sixteen; 48 tokens, 8 experts 8192 x 3584 int8: first 99 against 107).
-constexpr int kMoeWaves = 8;
-
+// sixteen; 48 tokens, 8 experts 8192 x 3584 int8: first 99 against 107).  Sixteen where
+// there are too few workgroups for that (4 tokens, 2 of 16 experts 2048 x 512 fp32 17.5
+// against 18.6).
+template <class E, int kWaves>
+hipError_t moe_up(const MoeArgs& a, bool values, int64_t tiles, int64_t groups, bool by_choice, hipStream_t s) {
+  if (!launchable(groups, kWaves * 64)) return hipErrorInvalidConfiguration;
+  const dim3 grid((uint32_t)groups), block(kWaves * 64);
+  if constexpr (E::kInt8) {
+    if (values) {
+      if (a.T > kMoeValuesTokens) return hipErrorInvalidConfiguration;
+      k_moe_up<E, 1, kWaves, true><<<grid, block, a.T * moe_pitch(a.K), s>>>(a, (int)tiles, by_choice);
+      return hipGetLastError();
+    }
+  }
+  if (a.T <= 16)
+    k_moe_up<E, 1, kWaves, false><<<grid, block, 0, s>>>(a, (int)tiles, by_choice);
+  else if (a.T <= 32)
+    k_moe_up<E, 2, kWaves, false><<<grid, block, 0, s>>>(a, (int)tiles, by_choice);
+  else
+    k_moe_up<E, 4, kWaves, false><<<grid, block, 0, s>>>(a, (int)tiles, by_choice);
+  return hipGetLastError();
+}
 template <class E>
 hipError_t moe_up(const MoeArgs& a, bool values, hipStream_t s) {
   const int64_t choices = (int64_t)a.T * a.top_k;
   const bool by_choice = choices <= a.E;
   const int64_t tiles = ((int64_t)a.N + 15) / 16, groups = tiles * (by_choice ? choices : a.E);
   if (groups == 0) return hipSuccess;
-  if (!launchable(groups, kMoeWaves * 64)) return hipErrorInvalidConfiguration;
-  const dim3 grid((uint32_t)groups), block(kMoeWaves * 64);
-  if constexpr (E::kInt8) {
-    if (values) {
-      if (a.T > kMoeValuesTokens) return hipErrorInvalidConfiguration;
-      k_moe_up<E, 1, kMoeWaves, true><<<grid, block, a.T * moe_pitch(a.K), s>>>(a, (int)tiles, by_choice);
-      return hipGetLastError();
-    }
-  }
-  if (a.T <= 16)
-    k_moe_up<E, 1, kMoeWaves, false><<<grid, block, 0, s>>>(a, (int)tiles, by_choice);
-  else if (a.T <= 32)
-    k_moe_up<E, 2, kMoeWaves, false><<<grid, block, 0, s>>>(a, (int)tiles, by_choice);
-  else
-    k_moe_up<E, 4, kMoeWaves, false><<<grid, block, 0, s>>>(a, (int)tiles, by_choice);
-  return hipGetLastError();
+  return groups <= 320 ? moe_up<E, 16>(a, values, tiles, groups, by_choice, s)
+                       : moe_up<E, 8>(a, values, tiles, groups, by_choice, s);
 }
 
 template <class E, int P>
 hipError_t moe_down(const MoeArgs& a, bool values, hipStream_t s) {
-  const int64_t groups = ((int64_t)a.outs + 16 * P - 1) / (16 * P);
+  constexpr int kWaves = 8;
+  const int64_t groups = ((int64_t)a.outs + 16 * P - 1) / (16 * P) * a.parts;
   if (groups == 0 || a.T == 0) return hipSuccess;
-  if (!launchable(groups, kMoeWaves * 64)) return hipErrorInvalidConfiguration;
-  const dim3 grid((uint32_t)groups), block(kMoeWaves * 64);
-  const uint32_t lds = kMoeWaves * a.T * P * 16 * 4;
+  if (!launchable(groups, kWaves * 64)) return hipErrorInvalidConfiguration;
+  const dim3 grid((uint32_t)groups), block(kWaves * 64);
+  const uint32_t lds = kWaves * a.T * P * 16 * 4;
   if constexpr (E::kInt8) {
     if (values) {
       const int choices = a.T * a.top_k;
-      if (a.T > 16 || choices > kMoeValuesRows) return hipErrorInvalidConfiguration;
-      k_moe_down<E, P, 1, kMoeWaves, true><<<grid, block, lds + choices * moe_pitch(a.N), s>>>(a);
+      if (choices > kMoeValuesRows || a.T > kMoeValuesRows) return hipErrorInvalidConfiguration;
+      k_moe_down<E, P, 1, kWaves, true><<<grid, block, lds + choices * moe_pitch(a.N), s>>>(a);
       return hipGetLastError();
     }
   }
   if (a.T <= 16)
-    k_moe_down<E, P, 1, kMoeWaves, false><<<grid, block, lds, s>>>(a);
+    k_moe_down<E, P, 1, kWaves, false><<<grid, block, lds, s>>>(a);
   else if (a.T <= 32)
-    k_moe_down<E, P, 2, kMoeWaves, false><<<grid, block, lds, s>>>(a);
+    k_moe_down<E, P, 2, kWaves, false><<<grid, block, lds, s>>>(a);
   else
-    k_moe_down<E, P, 4, kMoeWaves, false><<<grid, block, lds, s>>>(a);
+    k_moe_down<E, P, 4, kWaves, false><<<grid, block, lds, s>>>(a);
   return hipGetLastError();
 }
+bool moe_wide(int T, int64_t outs) { return T > 4 && outs >= 32 * 192; }
 // Every workgroup reads the inner rows again, so it takes 32 columns where that
 // leaves enough workgroups (48 tokens, 8 experts, 8192 outputs int8: 48 us against 58;
 // 8 tokens bf16 94 against 100; but 24 tokens with 4096 outputs 78 against 55).
 template <class E>
 hipError_t moe_down(const MoeArgs& a, bool values, hipStream_t s) {
-  return a.T > 4 && a.outs >= 32 * 192 ? moe_down<E, 2>(a, values, s) : moe_down<E, 1>(a, values, s);
+  const hipError_t e = moe_wide(a.T, a.outs) ? moe_down<E, 2>(a, values, s) : moe_down<E, 1>(a, values, s);
+  if (e != hipSuccess || a.parts == 1) return e;
+  const int64_t groups = ((int64_t)a.T * a.outs + 255) / 256;
+  k_moe_join<E><<<dim3((uint32_t)groups), dim3(256), 0, s>>>(a);
+  return hipGetLastError();
+}
+
+// How many workgroups share the experts of a column tile: with few outputs and many
+// experts a wave would go from one expert to the next for long (59 tokens, 94 experts,
+// 479 outputs int8 56 us, now 10.7 and 2.8 for the join; 1 token, 6 experts, 477 outputs
+// fp16 12.7, now 7.0 and 1.8).  The costs in us: an expert, a pair of chunks, and the join
+// with its launch.  From 128 column tiles on the weights' bytes are the bound, and a join
+// only adds to them (24 tokens, 4096 outputs bf16 56 us, shared by two 65 and 4.7).
+int moe_parts(int T, int64_t n, int64_t outs, int64_t experts, int top_k, int es) {
+  const int64_t tiles = (outs + 15) / 16, choices = (int64_t)T * top_k;
+  if (moe_wide(T, outs) || choices == 0 || n == 0 || tiles == 0) return 1;
+  const int64_t steps = (n * es + 127) / 128, all = (choices < experts ? choices : experts) * steps;
+  int best = 1;
+  double least = 0;
+  for (int parts = 1; parts <= 16 && (parts == 1 || tiles * parts <= 256); parts *= 2) {
+    const double pairs = (double)all / (8 * parts);  // of a wave
+    const double cost = (pairs / steps + 1) * 2 + pairs * 0.5 + (parts > 1 ? 4.5 : 0);
+    if (parts == 1 || cost < least) {
+      least = cost;
+      best = parts;
+    }
+  }
+  return best;
 }
 
 hipError_t launch_moe_up(int kind, bool int8, bool values, const MoeArgs& a, hipStream_t s) {

@@ -798,7 +798,7 @@ static PyObject* py_moe_ffn(PyObject* self, PyObject* const* a, Py_ssize_t n_arg
     return NULL;
   }
   void* space;
-  const size_t bytes = llar_moe_workspace(c.xm.rows, wg.rows, c.xm.cols, (int)top_k, c.type, int8);
+  const size_t bytes = llar_moe_workspace(c.xm.rows, wg.rows, c.xm.cols, wd.rows, wg.experts, (int)top_k, c.type, int8);
   if (!(ws = room(&c, bytes, &space))) goto end;
   if (done(llar_moe_ffn(&c.xm, ids.data, ids.dtype == t_int64 ? 8 : 4, (const float*)w.data, (int)top_k, &wg, &wu, &wd,
                         gs, us, ds, has_r ? &r : NULL, &y, c.type, c.act, space, bytes, c.stream),

@@ -248,6 +248,16 @@ def test_wide_outputs(m, int8, dtype):
     moe_case(m, 72, 200, 6161, 3, 1, dtype, int8=int8, away=0.2)
 
 
+# few outputs and many experts: a column tile's experts shared between workgroups, also of a batch's last tokens alone
+@pytest.mark.parametrize("dtype", DTYPES, ids=ids)
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("size", [(59, 79, 227, 479, 94, 8), (16, 64, 1000, 24, 128, 4), (30, 40, 600, 130, 200, 6), (1, 64, 9000, 40, 40, 32),
+                                  (67, 40, 520, 72, 300, 5), (65, 40, 8000, 33, 24, 16)], ids=str)
+def test_many_experts_few_outputs(size, int8, dtype):
+    moe_case(*size, dtype, int8=int8, residual=True)
+    moe_case(*size, dtype, int8=int8, away=0.5, twice=True)
+
+
 # rows that a kernel's own workgroups quantise, and just beyond
 @pytest.mark.parametrize("dtype", DTYPES, ids=ids)
 def test_rows_quantized_on_the_way(dtype):

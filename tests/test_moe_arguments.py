@@ -72,10 +72,13 @@ def test_ffn(L):
         assert call(*ok, **scales) == -1
     long = [mat(4, 1 << 17), experts(8, 32, 1 << 17), experts(8, 32, 1 << 17), ok[3], ok[4]]
     assert call(*long, gs=4096, us=4096, ds=4096) == -2            # sums that may not fit 32 bits
-    need = L.llar_moe_workspace(4, 32, 64, 2, 2, 0)
-    assert need >= 4 * 2 * 32 * 2 and call(*ok, n=need - 1) == -1 and call(*ok, space=4097) == -1
-    assert L.llar_moe_workspace(4, 32, 64, 2, 2, 1) > need
-    assert L.llar_moe_workspace(1000, 32, 64, 2, 2, 1) == L.llar_moe_workspace(64, 32, 64, 2, 2, 1)
-    for bad in ((-1, 32, 64, 2, 2), (4, -1, 64, 2, 2), (4, 32, -1, 2, 2), (4, 32, 64, 33, 2), (4, 32, 64, -1, 2), (4, 32, 64, 2, 3)):
-        assert L.llar_moe_workspace(*bad, 1) == 0
+    def room(m=4, n=32, k=64, outs=64, count=8, top_k=2, dtype=2, int8=0):
+        return L.llar_moe_workspace(m, n, k, outs, count, top_k, dtype, int8)
+
+    assert room() >= 4 * 2 * 32 * 2 and call(*ok, n=room() - 1) == -1 and call(*ok, space=4097) == -1
+    assert room(int8=1) > room() and room(m=1024, int8=1) == room(m=64, int8=1)
+    assert room(m=64, n=4096, outs=48, count=1000, top_k=8) > 64 * 8 * 4096 * 2          # shares of a column tile's experts
+    for bad in ({"m": -1}, {"n": -1}, {"k": -1}, {"outs": -1}, {"count": -1}, {"count": 1025}, {"top_k": 33}, {"top_k": -1},
+                {"dtype": 3}, {"k": 1 << 21}):
+        assert room(**bad, int8=1) == 0
     assert call(*but(0, mat(0, 64))[:4], mat(0, 64), ids=None) == 0  # nothing to do
