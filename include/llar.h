@@ -322,8 +322,8 @@ int llar_gated_ffn_backward(const llar_matrix* dh, const llar_matrix* x, const l
                             llar_dtype dtype, llar_act act, void* workspace, size_t workspace_bytes, void* stream);
 
 /* ---- products of 8-bit whole numbers ------------------------------------ *
- * The same two products for decoding with weights of half the bytes: tokens
- * and output channels are rows of whole numbers -127 .. 127 with one binary32
+ * The same two products for serving with weights of half the bytes (they have
+ * no backward pass): tokens and output channels are rows of whole numbers -127 .. 127 with one binary32
  * scale each.  Sums are whole numbers and exact (k up to 2^17 - 1); a sum times
  * both scales, the epilogue in binary32, one rounding to `dtype`.  Streams,
  * workspaces, overlap, errors and sizes as for the calls above. */
@@ -401,7 +401,8 @@ size_t llar_moe_workspace(int64_t m, int64_t n, int64_t k, int64_t outs, int64_t
  * same strides), w_down E x outs x n, x m x k with contiguous rows, out m x outs.
  * expert_ids: m x top_k whole numbers of id_bytes 4 or 8; one outside 0 .. E - 1
  * (an expert of another rank, a padded token) adds nothing, and one that a token
- * names twice has both weights.  The inner rows are rounded to dtype once.
+ * names twice has both weights.  The inner rows are rounded to dtype once (in
+ * binary16 with that type's range).
  *
  * With gate_scale, up_scale (E x n) and down_scale (E x outs), all three, the
  * weights are int8: x (any strides) and the inner rows, unrounded, are quantised
