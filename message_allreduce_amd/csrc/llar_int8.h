@@ -29,9 +29,12 @@ hipError_t launch_pack8(const Pack8Args& a, hipStream_t s);
 // Both in one launch (copies.first is set here).
 hipError_t launch_quantize(int kind, const QuantArgs& a, const Pack8Args& copies, hipStream_t s);
 
-// Products with M <= kFewRows rows of x, any alignment.  kind: the results' type.
+// Products with M <= kFewRows8 rows of x, any alignment.  kind: the results' type.
 // values: x is of that type and not quantised yet, M <= kFewValuesRows, K <= kFewValuesK.
+constexpr int kFewRows8 = 32;
 constexpr int kFewValuesRows = 2, kFewValuesK = 8192;
+// Pairs of 16 weight rows, what its wider workgroups take.
+inline int64_t few_pairs(int64_t n, bool gated) { return (n + (gated ? 15 : 31)) / (gated ? 16 : 32); }
 hipError_t launch_few_int8(int kind, bool gated, bool values, const GemmArgs& a, hipStream_t s);
 
 // The join of a product split over k: whole sums, then scales and epilogue.

@@ -23,8 +23,22 @@ Operand operand8(const llar_matrix* m) {
   return o;
 }
 
-// Whether these sizes go to the kernel for few rows.
-Shape shape8(int64_t m, int64_t n, int64_t k, bool gated) { return choose(m, n, k, 1, 1, gated, 1, true, false); }
+// The tiles, or the kernel for few rows.  That one reads x anew for every 16 or 32
+// columns, so it has to give way where the columns are many against the rows, and with
+// more than 16 rows also where k is short against the columns.  Tile and few rows, us:
+//   3584 -> 8192          8 rows 11.8,  8.0   16 rows 12.0,  8.8   32 rows 12.8, 11.4
+//   8192 -> 3584, gated   8 rows 20.1, 13.4   16 rows 19.6, 15.4   32 rows 20.8, 19.7
+//   8192 -> 16384         8 rows 32.2, 27.0   16 rows 32.3, 33.4
+//   8192 -> 28672         8 rows 48.2, 46.2   16 rows 48.7, 58.7   17 rows 50.5, 66.6
+//   1536 -> 11008, gated  8 rows 12.5, 14.0   16 rows 12.8, 16.0
+//   8192 -> 1024                                                   17 rows 12.0, 15.3
+// More than 32 rows are always the tiles'.
+Shape shape8(int64_t m, int64_t n, int64_t k, bool gated) {
+  const int64_t pairs = few_pairs(n, gated);
+  const bool few = m <= 8 || (m <= 16 && pairs <= 512) || (m <= kFewRows8 && pairs <= 256 && 64 * pairs >= k);
+  if (few && m > 0 && n > 0 && n <= kFewColumns) return Shape{true, kTile64, 1, 1, 0};
+  return choose(m, n, k, 1, 1, gated, 1, false, false);
+}
 
 // Whether the kernel for few rows quantises them itself.
 bool takes_values(const Shape& sh, int64_t m, int64_t k) { return sh.few && m <= kFewValuesRows && k <= kFewValuesK; }

@@ -138,9 +138,9 @@ hipError_t launch_quantize(int kind, const QuantArgs& a, const Pack8Args& copies
 }
 
 // ---- few rows ------------------------------------------------------------------------
-// 16 P weight rows (gated: half of them of each projection) a workgroup, its waves
-// take the steps of k in turn.
-template <class Out, bool kGated, int P, int kWaves>
+// 16 P weight rows (gated: half of them of each projection) a workgroup times up to 16
+// NB rows of x, its waves take the steps of k in turn.
+template <class Out, bool kGated, int P, int NB, int kWaves>
 __global__ __launch_bounds__(kWaves * 64) void k_few_int8(GemmArgs a) {
   typedef Int8<Out> E;
   constexpr int kN = kGated ? 8 * P : 16 * P, G = 2;
@@ -155,31 +155,40 @@ __global__ __launch_bounds__(kWaves * 64) void k_few_int8(GemmArgs a) {
     const int i = 16 * p + r;
     w[p] = (const char*)a.w[kGated ? i / kN : 0] + min(n0 + i % kN, a.N - 1) * a.wld + q * (16 * G);
   }
-  const bool live[1] = {r < a.M};
-  const char* x[1] = {(const char*)a.x[0] + (live[0] ? r : 0) * a.xld + q * (16 * G)};
-  f32x4 acc[P][1];
+  bool live[NB];
+  const char* x[NB];
+#pragma unroll
+  for (int b = 0; b < NB; b++) {
+    live[b] = 16 * b + r < a.M;
+    x[b] = (const char*)a.x[0] + (live[b] ? 16 * b + r : 0) * a.xld + q * (16 * G);
+  }
+  f32x4 acc[P][NB];
   clear<E>(acc);
   constexpr int kStep = 64 * G;
-  multiply_steps<E, P, 1, G, 2>(acc, w, x, live, a.K, wave, (a.K + kStep - 1) / kStep, kWaves);
+  multiply_steps<E, P, NB, G, 2>(acc, w, x, live, a.K, wave, (a.K + kStep - 1) / kStep, kWaves);
 #pragma unroll
-  for (int p = 0; p < P; p++)
+  for (int b = 0; b < NB; b++) {
+    if (b > 0) __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 4; i++) part[p][wave][r][4 * q + i] = __float_as_int(acc[p][0][i]);
-  __syncthreads();
-  for (int i = threadIdx.x; i < a.M * kN; i += kWaves * 64) {
-    const int m = i / kN, n = i % kN;
-    if (n0 + n >= a.N) continue;
-    constexpr int kPlanes = kGated ? 2 : 1;
-    float v[kPlanes];
+    for (int p = 0; p < P; p++)
 #pragma unroll
-    for (int p = 0; p < kPlanes; p++) {
-      const int c = p * kN + n;
-      int sum = 0;
+      for (int i = 0; i < 4; i++) part[p][wave][r][4 * q + i] = __float_as_int(acc[p][b][i]);
+    __syncthreads();
+    for (int i = threadIdx.x; i < min(a.M - 16 * b, 16) * kN; i += kWaves * 64) {
+      const int row = i / kN, n = i % kN, m = 16 * b + row;
+      if (n0 + n >= a.N) continue;
+      constexpr int kPlanes = kGated ? 2 : 1;
+      float v[kPlanes];
 #pragma unroll
-      for (int k = 0; k < kWaves; k++) sum += part[c / 16][k][m][c % 16];
-      v[p] = scaled(sum, a.xscale[m], a.wscale[p][n0 + n]);
+      for (int p = 0; p < kPlanes; p++) {
+        const int c = p * kN + n;
+        int sum = 0;
+#pragma unroll
+        for (int k = 0; k < kWaves; k++) sum += part[c / 16][k][row][c % 16];
+        v[p] = scaled(sum, a.xscale[m], a.wscale[p][n0 + n]);
+      }
+      finish<E, kGated, 1>(a, 0, m, n0 + n, &v[0], &v[kPlanes - 1]);
     }
-    finish<E, kGated, 1>(a, 0, m, n0 + n, &v[0], &v[kPlanes - 1]);
   }
 }
 
@@ -275,18 +284,23 @@ __global__ __launch_bounds__(kWaves * 64, 8) void k_few_int8_values(GemmArgs a) 
 
 template <class Out, bool kGated>
 hipError_t few_int8(bool values, const GemmArgs& a, hipStream_t s) {
-  // x is read again by every workgroup: more columns where it is large
-  const bool wide = !values && a.M > 4 && a.N >= (kGated ? 16 : 32) * 192;
+  // x is read again by every workgroup, half as often where each takes twice the
+  // columns: for as long as those still give nearly every CU one workgroup and none two
+  // (16 rows, 3584 -> 8192: 8.8 us; 5 rows, 8192 -> 28672: 50.8 us, narrow 41.5).
+  const int64_t pairs = few_pairs(a.N, kGated);
+  const bool wide = !values && a.M > 4 && pairs >= 192 && pairs <= 256;
   constexpr int kWaves = 16;
-  const int cols = (kGated ? 8 : 16) * (wide ? 2 : 1);
+  const int cols = (kGated ? 8 : 16) * (wide || a.M > 16 ? 2 : 1);
   const int64_t groups = ((int64_t)a.N + cols - 1) / cols;
   if (groups == 0 || a.M == 0) return hipSuccess;
   if (!launchable(groups, kWaves * 64)) return hipErrorInvalidConfiguration;
   const dim3 grid((uint32_t)groups), block(kWaves * 64);
-  if (wide)
-    k_few_int8<Out, kGated, 2, kWaves><<<grid, block, 0, s>>>(a);
+  if (a.M > 16)
+    k_few_int8<Out, kGated, 2, 2, kWaves><<<grid, block, 0, s>>>(a);
+  else if (wide)
+    k_few_int8<Out, kGated, 2, 1, kWaves><<<grid, block, 0, s>>>(a);
   else if (!values)
-    k_few_int8<Out, kGated, 1, kWaves><<<grid, block, 0, s>>>(a);
+    k_few_int8<Out, kGated, 1, 1, kWaves><<<grid, block, 0, s>>>(a);
   else if (a.M == 1)
     k_few_int8_values<Out, kGated, 1, kWaves><<<grid, block, 0, s>>>(a);
   else

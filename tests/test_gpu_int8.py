@@ -136,11 +136,12 @@ def linear_case(m, n, k, dtype, act="none", bias=False, residual=False, given=Tr
     return y
 
 
-# rows on both sides of 16, and products that want each tile shape, whole in k and split between workgroups
+# rows on both sides of 8, 16 and 32, and products that want each tile shape, whole in k and split between workgroups
 SIZES = [(1, 1, 1), (1, 512, 512), (1, 77, 130), (2, 64, 8), (2, 40, 5000), (3, 200, 96), (16, 64, 64), (16, 33, 8200),
          (17, 33, 65), (31, 129, 72), (64, 64, 2048), (65, 640, 320), (128, 128, 128), (200, 513, 257), (257, 256, 64),
          (300, 264, 1000), (64, 40, 20000)]
-LARGE = [(17, 4100, 4000), (40, 72, 128), (100, 1096, 2000), (200, 2000, 8000), (500, 4100, 80), (500, 4104, 400),
+LARGE = [(9, 16500, 80), (16, 16600, 300), (20, 72, 8000), (31, 8200, 200), (32, 8100, 200), (17, 4100, 4000),
+         (40, 72, 128), (100, 1096, 2000), (200, 2000, 8000), (500, 4100, 80), (500, 4104, 400),
          (1000, 2000, 1008), (2000, 2000, 400), (2000, 4100, 80), (3000, 40, 4000), (3000, 4104, 1280), (4096, 4096, 256)]
 
 
