@@ -23,7 +23,7 @@ int check_rows(const llar_matrix* m) {
 // The workspace of one pair of launches.
 struct Rooms {
   size_t xq, xs, h, hq, hs, partial;
-  int64_t xld, hld, hqld;
+  int64_t xld, hld, hlow, hqld;
   size_t total() const {
     return align256(xq) + align256(xs) + align256(h) + align256(hq) + align256(hs) + align256(partial);
   }
@@ -46,7 +46,8 @@ Rooms rooms(int64_t m, int64_t n, int64_t k, int64_t outs, int64_t experts, int 
     r.hq = (size_t)choices * r.hqld;
     r.hs = (size_t)choices * 4;
   } else {
-    r.hld = cdiv(n, 16 / es) * (16 / es);
+    r.hlow = cdiv(n, 16 / es) * (16 / es);
+    r.hld = es == 2 ? 2 * r.hlow : r.hlow;  // binary16: two numbers for each
     r.h = (size_t)choices * r.hld * es;
   }
   return r;
@@ -196,6 +197,7 @@ int llar_moe_ffn(const llar_matrix* x, const void* expert_ids, int id_bytes, con
     }
     a.h = h;
     a.hld = room.hld;
+    a.hlow = room.hlow;
     if (launch_moe_up(dtype, int8, x_values, a, s) != hipSuccess) return llar::fail(LLAR_ERR_HIP);
     if (int8 && !h_values) {
       // rows of choices without an expert are whatever they were, and not read

@@ -188,7 +188,9 @@ def moe64(x, experts, weights, w, act, dtype):
             he = q.abs() * s * rel + torch.where(near & some, 1.01 * s, torch.zeros_like(s))
             h = q * s
         else:
-            he = he + 1.01 * U[dtype] * h.abs() + TINY[dtype]
+            # rounded once; fp16: and what that left lifted by 2^11 and rounded
+            he = he + (1.01 * U[dtype] ** 2 * h.abs() + TINY[dtype] * 2.0 ** -11 if dtype == torch.float16 else
+                       1.01 * U[dtype] * h.abs() + TINY[dtype])
         part = mm64(h, down.t())
         size = mm64(h.abs(), down.t().abs())
         y.index_add_(0, token, a * part)
@@ -326,6 +328,17 @@ def test_small_values_are_not_lost(dtype):
         y = w.call(x, e, a, activation="relu")
         want = torch.tensor([3.0, 5.0, 7.0], device="cuda", dtype=torch.float64) * 1024 * tiny * eps
         assert torch.equal(y[:, :3].double(), want.expand(m, 3)), (y[0, :3].double() / (tiny * eps)).tolist()
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=ids)
+@pytest.mark.parametrize("m", [2, 24, 60])
+def test_small_inner_rows_keep_their_digits(m, dtype):
+    """Inner rows around 2^-19, where fp16 has five digits, whose sums large weights bring back into its range."""
+    w = Weights(m, dtype, 6, 80, 72, 6200 if m == 24 else 96)
+    x = Draw(m, dtype)(m, 72) * 2.0 ** -9
+    e, a = choose(m, m, 6, 2)
+    a = a * 2.0 ** 14
+    check(w.call(x, e, a), *moe64(x, e, a, w, "silu", dtype), "inner rows of 2^-19, %d %s" % (m, dtype))
 
 
 @pytest.mark.parametrize("dtype", DTYPES, ids=ids)
