@@ -17,7 +17,8 @@ Python names mirror the C ABI::
     llar_destroy(h)
 
 and ``Communicator`` wraps them for torch tensors.  ``linear``, ``gated_ffn`` and
-their backward passes (module ``ffn``) compute the partial outputs themselves.
+their backward passes, their 8-bit forms and the mixture-of-experts layer (module
+``ffn``) compute the partial outputs themselves.
 """
 from __future__ import annotations
 

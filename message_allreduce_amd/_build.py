@@ -100,7 +100,7 @@ def _build_binding() -> bool:
     if compiler is None or not os.path.exists(os.path.join(python, "Python.h")):
         if os.path.exists(BINDING):
             os.remove(BINDING)
-        print("not built: %s (no %s), so linear, gated_ffn and their backward passes are not available from Python"
+        print("not built: %s (no %s), so linear, gated_ffn, moe_ffn and the like are not available from Python"
               % (os.path.basename(BINDING), "C compiler" if compiler is None else "Python.h in " + python),
               file=sys.stderr)
         return False

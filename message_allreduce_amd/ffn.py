@@ -1,6 +1,7 @@
 """Feed-forward operators of a tensor-parallel layer (torch tensors in, torch
 tensors out): the row-parallel matrix product with its epilogue, the gated
-block's column-parallel products, and both backward passes.  The kernels are
+block's column-parallel products, and both backward passes; for serving, the
+products with 8-bit weights and the mixture-of-experts layer.  The kernels are
 the library's (``include/llar.h``); this module checks and marshals arguments.
 
 Tensors are fp32, fp16 or bf16 device tensors of one type.  ``x`` and the other
