@@ -389,17 +389,18 @@ struct Inner {
 // binary32 where it is to be quantised.  A
 // workgroup takes 16 inner columns (16 rows of each projection) of one expert for all
 // the tokens that chose it, up to 64: its weights are read once.  Every wave finds
-// those tokens by itself, a token a lane, without a word of shared memory.  Bound by
+// those tokens by itself, a token a lane, without a word of shared memory.  Where the
+// card would be half empty it takes eight inner columns (P = 1).  Bound by
 // reading the weights: 1 token, 8 of 64 experts 4096 x 1024 bf16 28.5 us (4.7 TB/s, the
 // launch included), 16 tokens 181 (5.2); 48 tokens, 8 experts 8192 x 3584 int8 95 (4.9).
 //
 // With fewer choices than experts the grid has a slot for each choice, and the
 // slot of an expert's first choice does its work; else a slot for each expert.
-template <class E, int NB, int kWaves, bool kValues>
-__device__ __forceinline__ void moe_up_rows(const MoeArgs& a, const char* const (&w)[2], int member, int count, int e,
-                                            int n0, float (*part)[2][16][16], const lds_char* rows, int pitch,
+template <class E, int P, int NB, int kWaves, bool kValues>
+__device__ __forceinline__ void moe_up_rows(const MoeArgs& a, const char* const (&w)[P], int member, int count, int e,
+                                            int n0, float (*part)[P][16][16], const lds_char* rows, int pitch,
                                             const float* xscale) {
-  constexpr int G = NB <= 2 ? 2 : 1, U = 2, ES = sizeof(typename E::X), kStep = 64 * G / ES;
+  constexpr int G = NB <= 2 ? 2 : 1, U = 2, ES = sizeof(typename E::X), kStep = 64 * G / ES, kCols = 8 * P;
   const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   typedef std::conditional_t<kValues, const lds_char, const char> Row;
@@ -414,23 +415,25 @@ __device__ __forceinline__ void moe_up_rows(const MoeArgs& a, const char* const 
     else
       x[b] = (const char*)a.x + (live[b] ? t * a.xld * ES : 0) + q * (16 * G);
   }
-  const char* at[2] = {w[0] + q * (16 * G), w[1] + q * (16 * G)};
+  const char* at[P];
+#pragma unroll
+  for (int p = 0; p < P; p++) at[p] = w[p] + q * (16 * G);
   // the scales that a thread's results need, ahead of the operands
   float ws[2] = {1.f, 1.f}, xs[NB];
 #pragma unroll
   for (int b = 0; b < NB; b++) xs[b] = 1.f;
   if constexpr (E::kInt8) {
-    if (threadIdx.x < 256) {
-      const int64_t col = (int64_t)e * a.N + min(n0 + (int)threadIdx.x % 16, a.N - 1);
+    if (threadIdx.x < 16 * kCols) {
+      const int64_t col = (int64_t)e * a.N + min(n0 + (int)threadIdx.x % kCols, a.N - 1);
 #pragma unroll
       for (int p = 0; p < 2; p++) ws[p] = a.wscale[p][col];
 #pragma unroll
-      for (int b = 0; b < NB; b++) xs[b] = xscale[min(__shfl(member, 16 * b + (int)threadIdx.x / 16) & 255, a.T - 1)];
+      for (int b = 0; b < NB; b++) xs[b] = xscale[min(__shfl(member, 16 * b + (int)threadIdx.x / kCols) & 255, a.T - 1)];
     }
   }
-  f32x4 acc[2][NB];
+  f32x4 acc[P][NB];
   clear<E>(acc);
-  multiply_steps<E, 2, NB, G, U>(acc, at, x, live, a.K, wave, (a.K + kStep - 1) / kStep, kWaves);
+  multiply_steps<E, P, NB, G, U>(acc, at, x, live, a.K, wave, (a.K + kStep - 1) / kStep, kWaves);
 #pragma unroll
   for (int b = 0; b < NB; b++) {
     if (b > 0) {
@@ -438,17 +441,18 @@ __device__ __forceinline__ void moe_up_rows(const MoeArgs& a, const char* const 
       __syncthreads();
     }
 #pragma unroll
-    for (int p = 0; p < 2; p++) *(f32x4*)&part[wave][p][r][4 * q] = acc[p][b];
+    for (int p = 0; p < P; p++) *(f32x4*)&part[wave][p][r][4 * q] = acc[p][b];
     __syncthreads();
-    if (threadIdx.x < 256) {  // whole waves
-      const int row = threadIdx.x / 16, col = threadIdx.x % 16;
+    if (threadIdx.x < 16 * kCols) {  // whole waves
+      const int row = threadIdx.x / kCols, col = threadIdx.x % kCols;
       const int m = __shfl(member, 16 * b + row);
       float v[2];
 #pragma unroll
       for (int p = 0; p < 2; p++) {
-        v[p] = part[0][p][row][col];
+        const int i = p * kCols + col;  // weight row of the workgroup
+        v[p] = part[0][i / 16][row][i % 16];
 #pragma unroll
-        for (int k = 1; k < kWaves; k++) v[p] = add_sums<E>(v[p], part[k][p][row][col]);
+        for (int k = 1; k < kWaves; k++) v[p] = add_sums<E>(v[p], part[k][i / 16][row][i % 16]);
       }
       if (16 * b + row < count && n0 + col < a.N) {
         const int64_t to = (int64_t)((m & 255) * a.top_k + (m >> 8)) * a.hld + n0 + col;
@@ -467,13 +471,13 @@ __device__ __forceinline__ void moe_up_rows(const MoeArgs& a, const char* const 
   }
 }
 
-template <class E, int NB, int kWaves, bool kValues>
+template <class E, int P, int NB, int kWaves, bool kValues>
 __global__ __launch_bounds__(kWaves * 64) void k_moe_up(MoeArgs a, int tiles, bool by_choice) {
   extern __shared__ __attribute__((aligned(16))) char quantized[];  // kValues: [T][pitch]
-  __shared__ float part[kWaves][2][16][16], own_scale[kMoeValuesTokens];
+  __shared__ float part[kWaves][P][16][16], own_scale[kMoeValuesTokens];
   constexpr int ES = sizeof(typename E::X);
   const int lane = threadIdx.x & 63, r = lane & 15;
-  const int slot = blockIdx.x / tiles, n0 = (int)(blockIdx.x % tiles) * 16;
+  const int slot = blockIdx.x / tiles, n0 = (int)(blockIdx.x % tiles) * (8 * P);
   const int e = by_choice ? expert_at(a, slot) : slot;
   if (e < 0) return;
   const uint32_t places = places_of(a, e);
@@ -485,10 +489,12 @@ __global__ __launch_bounds__(kWaves * 64) void k_moe_up(MoeArgs a, int tiles, bo
     const int first = __builtin_amdgcn_readfirstlane(member);
     if ((first & 255) * a.top_k + (first >> 8) != slot) return;
   }
-  const char* w[2];
+  const char* w[P];
 #pragma unroll
-  for (int p = 0; p < 2; p++)
-    w[p] = (const char*)a.w[p] + (e * a.w_expert + min(n0 + r, a.N - 1) * a.wld) * ES;
+  for (int p = 0; p < P; p++) {
+    const int i = 16 * p + r;
+    w[p] = (const char*)a.w[i / (8 * P)] + (e * a.w_expert + min(n0 + i % (8 * P), a.N - 1) * a.wld) * ES;
+  }
   const int pitch = moe_pitch(a.K);
   const float* xscale = kValues ? own_scale : a.xscale;
   if constexpr (kValues) {
@@ -497,7 +503,7 @@ __global__ __launch_bounds__(kWaves * 64) void k_moe_up(MoeArgs a, int tiles, bo
                                                     (lds_char*)quantized + t * pitch, &own_scale[t], (uint32_t*)part);
   }
   auto run = [&](auto blocks) {
-    moe_up_rows<E, decltype(blocks)::value, kWaves, kValues>(a, w, member, count, e, n0, part, (lds_char*)quantized, pitch,
+    moe_up_rows<E, P, decltype(blocks)::value, kWaves, kValues>(a, w, member, count, e, n0, part, (lds_char*)quantized, pitch,
                                                              xscale);
   };
   if (NB == 1 || count <= 16)
@@ -712,34 +718,38 @@ __global__ __launch_bounds__(256) void k_moe_join(MoeArgs a) {
 // (1 token, 8 of 64 experts 4096 x 1024 bf16: second kernel 15.1 us against 16.6 with
 // sixteen; 48 tokens, 8 experts 8192 x 3584 int8: first 99 against 107).  Sixteen where
 // there are too few workgroups for that (4 tokens, 2 of 16 experts 2048 x 512 fp32 17.5
-// against 18.6).
-template <class E, int kWaves>
-hipError_t moe_up(const MoeArgs& a, bool values, int64_t tiles, int64_t groups, bool by_choice, hipStream_t s) {
+// against 18.6).  And half the columns a workgroup where twice as many still get a CU
+// each (both kernels, 1 token bf16, 2 of 8 experts 8192 x 448: 22.6 us against 29.4; 64
+// tokens 4096 x 256 24.9 against 28.9; but 32 tokens 8192 x 448, 224 workgroups, 50.4
+// against 45.6).
+template <class E, int P, int kWaves>
+hipError_t moe_up(const MoeArgs& a, bool values, bool by_choice, hipStream_t s) {
+  const int64_t tiles = ((int64_t)a.N + 8 * P - 1) / (8 * P), groups = tiles * (by_choice ? a.T * a.top_k : a.E);
+  if (groups == 0) return hipSuccess;
   if (!launchable(groups, kWaves * 64)) return hipErrorInvalidConfiguration;
   const dim3 grid((uint32_t)groups), block(kWaves * 64);
   if constexpr (E::kInt8) {
     if (values) {
       if (a.T > kMoeValuesTokens) return hipErrorInvalidConfiguration;
-      k_moe_up<E, 1, kWaves, true><<<grid, block, a.T * moe_pitch(a.K), s>>>(a, (int)tiles, by_choice);
+      k_moe_up<E, P, 1, kWaves, true><<<grid, block, a.T * moe_pitch(a.K), s>>>(a, (int)tiles, by_choice);
       return hipGetLastError();
     }
   }
   if (a.T <= 16)
-    k_moe_up<E, 1, kWaves, false><<<grid, block, 0, s>>>(a, (int)tiles, by_choice);
+    k_moe_up<E, P, 1, kWaves, false><<<grid, block, 0, s>>>(a, (int)tiles, by_choice);
   else if (a.T <= 32)
-    k_moe_up<E, 2, kWaves, false><<<grid, block, 0, s>>>(a, (int)tiles, by_choice);
+    k_moe_up<E, P, 2, kWaves, false><<<grid, block, 0, s>>>(a, (int)tiles, by_choice);
   else
-    k_moe_up<E, 4, kWaves, false><<<grid, block, 0, s>>>(a, (int)tiles, by_choice);
+    k_moe_up<E, P, 4, kWaves, false><<<grid, block, 0, s>>>(a, (int)tiles, by_choice);
   return hipGetLastError();
 }
 template <class E>
 hipError_t moe_up(const MoeArgs& a, bool values, hipStream_t s) {
   const int64_t choices = (int64_t)a.T * a.top_k;
   const bool by_choice = choices <= a.E;
-  const int64_t tiles = ((int64_t)a.N + 15) / 16, groups = tiles * (by_choice ? choices : a.E);
-  if (groups == 0) return hipSuccess;
-  return groups <= 320 ? moe_up<E, 16>(a, values, tiles, groups, by_choice, s)
-                       : moe_up<E, 8>(a, values, tiles, groups, by_choice, s);
+  const int64_t groups = ((int64_t)a.N + 15) / 16 * (by_choice ? choices : a.E);
+  if (groups <= 128) return moe_up<E, 1, 16>(a, values, by_choice, s);
+  return groups <= 320 ? moe_up<E, 2, 16>(a, values, by_choice, s) : moe_up<E, 2, 8>(a, values, by_choice, s);
 }
 
 template <class E, int P>

@@ -228,7 +228,7 @@ def moe_case(m, k, n, outs, count, top_k, dtype, act="silu", int8=False, residua
 
 
 # tokens, k, n, outputs, experts, top_k: fewer and more choices than experts, one block of 16 tokens and four, more than 64
-SIZES = [(1, 1, 1, 1, 1, 1), (1, 64, 32, 64, 8, 2), (1, 256, 96, 200, 64, 8), (2, 77, 45, 33, 5, 3), (3, 520, 264, 520, 12, 4),
+SIZES = [(1, 1, 1, 1, 1, 1), (1, 64, 32, 64, 8, 2), (2, 96, 400, 64, 8, 4), (1, 256, 96, 200, 64, 8), (2, 77, 45, 33, 5, 3), (3, 520, 264, 520, 12, 4),
          (7, 64, 128, 64, 3, 3), (16, 128, 64, 130, 8, 2), (17, 130, 72, 64, 40, 2), (32, 64, 48, 96, 4, 1), (33, 96, 80, 40, 16, 4),
          (48, 200, 100, 72, 8, 2), (64, 64, 33, 48, 100, 8), (64, 1032, 520, 264, 6, 2), (65, 72, 40, 64, 8, 2), (150, 64, 64, 40, 24, 3)]
 
