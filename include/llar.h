@@ -401,8 +401,9 @@ size_t llar_moe_workspace(int64_t m, int64_t n, int64_t k, int64_t outs, int64_t
  * same strides), w_down E x outs x n, x m x k with contiguous rows, out m x outs.
  * expert_ids: m x top_k whole numbers of id_bytes 4 or 8; one outside 0 .. E - 1
  * (an expert of another rank, a padded token) adds nothing, and one that a token
- * names twice has both weights.  The inner rows are rounded to bfloat16 once, and
- * kept in binary16 with twice its digits but its largest value, 65504.
+ * names twice has both weights.  The inner rows have 16 binary digits in
+ * bfloat16, and 22 in binary16 but its largest value, 65504 (beyond it they are
+ * infinite); the result is rounded once.
  *
  * With gate_scale, up_scale (E x n) and down_scale (E x outs), all three, the
  * weights are int8: x (any strides) and the inner rows, unrounded, are quantised

@@ -36,7 +36,7 @@ struct MoeArgs {
   const void* wd;        // [E][outs][n]
   const float* dscale;
   void* h;               // first kernel's output (int8: binary32); second kernel's input (int8: whole numbers)
-  int64_t hlow;          // binary16: from a value to what its rounding left
+  int64_t hlow;          // 16-bit types: from a value to what its rounding left
   const float* hscale;   // int8: of every choice
   const void* ids;
   const float* weights;

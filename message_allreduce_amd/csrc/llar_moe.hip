@@ -47,7 +47,7 @@ Rooms rooms(int64_t m, int64_t n, int64_t k, int64_t outs, int64_t experts, int 
     r.hs = (size_t)choices * 4;
   } else {
     r.hlow = cdiv(n, 16 / es) * (16 / es);
-    r.hld = es == 2 ? 2 * r.hlow : r.hlow;  // binary16: two numbers for each
+    r.hld = es == 2 ? 2 * r.hlow : r.hlow;  // 16-bit types: two numbers for each
     r.h = (size_t)choices * r.hld * es;
   }
   return r;

@@ -362,15 +362,18 @@ __device__ __forceinline__ void quantize_row(const typename V::T* x, int k, int 
   if constexpr (NT > 64) __syncthreads();
 }
 
-// The inner rows as the second kernel's matrix operands.  bfloat16: the value rounded,
-// which has binary32's range (the result's error 0.0024 instead of the output rounding's
-// own 0.0017; a second number would take 4 to 15 % more time).  binary16: also what that
-// rounding left, lifted by 2^11, because products of two small numbers are soon below its
-// 2^-14 and have few digits there (4 to 12 % of both kernels' time).
+// The inner rows as the second kernel's matrix operands: a 16-bit value, and as a second
+// one what its rounding left, so that the result is rounded once (error in the 2-norm
+// against binary64, bfloat16 0.0017 instead of 0.0024 with one number; binary16 0.00021
+// instead of 0.00033).  binary16's rest is lifted by 2^11, because products of two small
+// numbers are soon below its 2^-14 and have few digits there; bfloat16's has the range.
+// Both kernels take 3 to 13 % more time for it, since every workgroup reads the inner rows
+// (bfloat16 1 token 8 of 64 experts 4096 x 1024 44.4 -> 46.0 us, 64 tokens 311 -> 351;
+// 2 of 8 8192 x 3584 85 -> 89 and 292 -> 325).
 template <class E>
 struct Inner {
-  static constexpr bool kTwo = std::is_same_v<E, F16>;
-  static constexpr float kLift = 2048.f;
+  static constexpr bool kTwo = std::is_same_v<E, F16> || std::is_same_v<E, BF16>;
+  static constexpr float kLift = std::is_same_v<E, F16> ? 2048.f : 1.f;
   static __device__ __forceinline__ void put(typename E::T* to, int64_t low, float v) {
     const typename E::T high = E::from(v);
     *to = high;
