@@ -1,5 +1,7 @@
 // llar_int8_kernels.hip -- rows of whole numbers, their products for few tokens and
 // the join of a split one.  The tiled product is llar_gemm.h's.
+#include <algorithm>
+
 #include "llar_chunk.h"
 #include "llar_int8.h"
 
@@ -107,14 +109,26 @@ template <class E, bool kStrided>
 hipError_t quantize(const QuantArgs& a, Pack8Args copies, hipStream_t s) {
   auto launch = [&](auto kernel, int threads, int rows) {
     if (copies.count) copies.first[0] = 0;
-    int64_t groups = (a.M + rows - 1) / rows;
     for (int i = 0; i < copies.count; i++)
       copies.first[i + 1] = copies.first[i] + (copies.lines[i] * (copies.dld / 16) + threads - 1) / threads;
-    groups += copies.first[copies.count];
-    if (groups == 0) return hipSuccess;
-    if (!launchable(groups, threads)) return hipErrorInvalidConfiguration;
-    kernel<<<dim3((uint32_t)groups), dim3(threads), 0, s>>>(a, copies);
-    return hipGetLastError();
+    const int64_t copying = copies.count ? copies.first[copies.count] : 0;
+    if (!launchable(copying + 1, threads)) return hipErrorInvalidConfiguration;
+    if (copying == 0 && a.M == 0) return hipSuccess;
+    // more rows than fit below 2^32 threads (2^26 of up to 2048 columns) take further launches
+    const int64_t most = ((1ll << 32) - 1) / threads;
+    QuantArgs part = a;
+    part.M = std::min(a.M, (most - copying) * rows);
+    for (int64_t row = 0;;) {
+      const int64_t groups = (part.M + rows - 1) / rows + (row == 0 ? copying : 0);
+      kernel<<<dim3((uint32_t)groups), dim3(threads), 0, s>>>(part, copies);
+      const hipError_t e = hipGetLastError();
+      row += part.M;
+      if (e != hipSuccess || row == a.M) return e;
+      part.x = (const typename E::T*)a.x + row * a.xld;
+      part.q = a.q + row * a.qld;
+      part.scale = a.scale + row;
+      part.M = std::min(a.M - row, most * rows);
+    }
   };
   // Many rows: as few threads as hold the row in their registers.  Few: one piece a
   // thread, for the latency.
