@@ -158,7 +158,10 @@ __device__ __forceinline__ void route_choose(const RouteArgs& a, int64_t t, doub
     }
   }
   const bool live = lane < a.top_k;
-  const double score = !live ? 0. : a.sigmoid ? 1. / (1. + exp(-mine)) : exp(mine - top);
+  // Below e^-600 sigmoids are exponentials to binary64's last digit; shares of their sum are
+  // taken without the common factor, which would lead out of its range at e^-708.
+  const bool shares = !a.sigmoid || (a.normalize && top < -600.);
+  const double score = !live ? 0. : shares ? exp(mine - top) : 1. / (1. + exp(-mine));
   double sum = 1.;  // sigmoid scores stand by themselves unless they are normalised
   if (a.normalize) {
     sum = wave_sum(score);
