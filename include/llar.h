@@ -387,7 +387,7 @@ size_t llar_moe_route_workspace(int64_t m, int64_t experts, int64_t k);
  * weights[m][top_k]: the softmax of a token's logits over all experts, or each
  * logit's sigmoid, at its choices; normalize != 0: divided by their sum.  A NaN
  * logit is below all others, and makes its token's weights NaN.  x and router
- * are of type dtype with contiguous rows. */
+ * are of type dtype with contiguous rows.  Longer batches go 65536 tokens at a time. */
 int llar_moe_route(const llar_matrix* x, const llar_matrix* router, int top_k, llar_score score, int normalize,
                    float* weights, int32_t* experts, llar_dtype dtype, void* workspace, size_t workspace_bytes,
                    void* stream);

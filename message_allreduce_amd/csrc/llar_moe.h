@@ -16,10 +16,13 @@ struct RouteArgs {
   int64_t xld, wld;
   int M, E, K, top_k;
   int splits;  // shares of k
+  bool small;  // one kernel
   bool sigmoid, normalize;
   float* weights;
   int32_t* experts;
 };
+// Tokens of one pair of launches: room for their logits (binary64, 512 MiB at most), and far from 2^32 threads.
+constexpr int64_t kRouteTokens = 1 << 16;
 constexpr int64_t kRouteSmallTokens = 256, kRouteSmall = 1 << 17;
 bool route_small(int64_t m, int64_t experts, int64_t k);  // one kernel, no logits in memory
 int route_splits(int64_t m, int64_t experts, int64_t k);

@@ -60,7 +60,7 @@ extern "C" {
 size_t llar_moe_route_workspace(int64_t m, int64_t experts, int64_t k) {
   if (m < 0 || experts < 0 || k < 0 || m > kMaxDim || experts > kMoeExperts || k > kMaxLine) return 0;
   if (route_small(m, experts, k)) return 0;
-  return align256((size_t)route_splits(m, experts, k) * m * experts * 8);
+  return align256((size_t)route_splits(m, experts, k) * std::min(m, kRouteTokens) * experts * 8);
 }
 
 int llar_moe_route(const llar_matrix* x, const llar_matrix* router, int top_k, llar_score score, int normalize,
@@ -76,21 +76,24 @@ int llar_moe_route(const llar_matrix* x, const llar_matrix* router, int top_k, l
   if (!weights || !experts || workspace_bytes < llar_moe_route_workspace(x->rows, router->rows, x->cols))
     return llar::fail(LLAR_ERR_ARG);
   RouteArgs a = {};
-  a.x = x->data;
   a.w = router->data;
   a.xld = row_ld(x);
   a.wld = row_ld(router);
-  a.M = (int)x->rows;
   a.E = (int)router->rows;
   a.K = (int)x->cols;
   a.top_k = top_k;
   a.sigmoid = score == LLAR_SCORE_SIGMOID;
   a.normalize = normalize != 0;
-  a.weights = weights;
-  a.experts = experts;
-  a.splits = route_splits(a.M, a.E, a.K);
+  a.small = route_small(x->rows, a.E, a.K);
+  a.splits = route_splits(x->rows, a.E, a.K);
   a.logits = (double*)workspace;
-  LLAR_TRY(launch_route(dtype, a, (hipStream_t)stream) == hipSuccess ? LLAR_OK : LLAR_ERR_HIP);
+  for (int64_t t = 0; t < x->rows; t += kRouteTokens) {
+    a.M = (int)std::min(kRouteTokens, x->rows - t);
+    a.x = (const uint8_t*)x->data + t * a.xld * elem_size(dtype);
+    a.weights = weights + t * top_k;
+    a.experts = experts + t * top_k;
+    LLAR_TRY(launch_route(dtype, a, (hipStream_t)stream) == hipSuccess ? LLAR_OK : LLAR_ERR_HIP);
+  }
   return LLAR_OK;
 }
 

@@ -266,7 +266,7 @@ int route_splits(int64_t m, int64_t experts, int64_t k) {
 
 template <class E>
 hipError_t route(const RouteArgs& a, hipStream_t s) {
-  if (route_small(a.M, a.E, a.K)) {
+  if (a.small) {
     const dim3 grid((uint32_t)a.M), block(1024);
     if (a.E <= 16)
       k_route_token<E, 1><<<grid, block, 0, s>>>(a);
