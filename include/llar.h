@@ -408,7 +408,10 @@ size_t llar_moe_workspace(int64_t m, int64_t n, int64_t k, int64_t outs, int64_t
  *
  * With gate_scale, up_scale (E x n) and down_scale (E x outs), all three, the
  * weights are int8: x (any strides) and the inner rows, unrounded, are quantised
- * as llar_quantize_rows does, one scale each; k and n are at most 2^17 - 1. */
+ * as llar_quantize_rows does, one scale each; k and n are at most 2^17 - 1.
+ *
+ * LLAR_ERR_UNSUPPORTED for n times the experts (or the choices of 64 tokens, if
+ * those are fewer) or for outputs of 2^27 and more. */
 int llar_moe_ffn(const llar_matrix* x, const void* expert_ids, int id_bytes, const float* weights, int top_k,
                  const llar_experts* w_gate, const llar_experts* w_up, const llar_experts* w_down,
                  const float* gate_scale, const float* up_scale, const float* down_scale, const llar_matrix* residual,

@@ -56,6 +56,7 @@ struct MoeArgs {
 // kMoeValuesRows choices of kMoeValuesBytes together: two rows a wave).
 constexpr int kMoeValuesTokens = 2, kMoeValuesK = 8192, kMoeValuesRows = 16, kMoeValuesBytes = 16384;
 hipError_t launch_moe_up(int kind, bool int8, bool values, const MoeArgs& a, hipStream_t s);
+bool moe_wide(int T, int64_t outs);  // 32 columns a workgroup in the second kernel, else 16
 int moe_parts(int T, int64_t n, int64_t outs, int64_t experts, int top_k, int es);
 hipError_t launch_moe_down(int kind, bool int8, bool values, const MoeArgs& a, hipStream_t s);
 

@@ -53,6 +53,13 @@ Rooms rooms(int64_t m, int64_t n, int64_t k, int64_t outs, int64_t experts, int 
   return r;
 }
 
+// Whether both kernels of t tokens stay below 2^32 threads: workgroups of 512 there, for 16 inner columns of a
+// choice or an expert, and for 16 or 32 outputs.
+bool sizes_fit(int64_t t, int64_t n, int64_t outs, int64_t experts, int top_k) {
+  const int64_t slots = std::min(t * top_k, experts);
+  return launchable(cdiv(n, 16) * slots, 512) && launchable(cdiv(outs, moe_wide((int)t, outs) ? 32 : 16), 512);
+}
+
 }  // namespace
 
 extern "C" {
@@ -133,6 +140,8 @@ int llar_moe_ffn(const llar_matrix* x, const void* expert_ids, int id_bytes, con
   if (top_k > 0 && (!expert_ids || !weights)) return llar::fail(LLAR_ERR_ARG);
   const int es = elem_size(dtype);
   const int64_t n = w_gate->rows, k = x->cols;
+  for (const int64_t t : {std::min<int64_t>(x->rows, kMoeTokens), x->rows % kMoeTokens})
+    if (!sizes_fit(t, n, out->cols, w_gate->experts, top_k)) return llar::fail(LLAR_ERR_UNSUPPORTED);
   const Rooms room = rooms(x->rows, n, k, out->cols, w_gate->experts, top_k, es, int8);
   if (workspace_bytes < room.total()) return llar::fail(LLAR_ERR_ARG);
   const hipStream_t s = (hipStream_t)stream;
