@@ -2,7 +2,7 @@
 import pytest
 import torch
 
-from moe_reference import Layer, allowed, beyond, definition
+from moe_reference import SHARED, WIDE, Layer, allowed, beyond, definition
 from test_gpu_ffn import DTYPES, ids
 
 pytestmark = pytest.mark.gpu
@@ -23,3 +23,17 @@ def accuracy_case(size, dtype, int8=False):
 def test_one_rounding_at_the_end(size, dtype):
     """The inner rows keep more digits than the output's type has: the result is as one rounded once."""
     accuracy_case(size, dtype)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=ids)
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("size", SHARED, ids=str)
+def test_shared_column_tiles_and_long_rows(size, int8, dtype):
+    accuracy_case(size, dtype, int8)
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=ids)
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("size", WIDE, ids=str)
+def test_widths_of_a_rank(size, int8, dtype):
+    accuracy_case(size, dtype, int8)
