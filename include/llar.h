@@ -383,7 +383,9 @@ size_t llar_moe_route_workspace(int64_t m, int64_t experts, int64_t k);
 
 /* For each of the m tokens, rows of x (m x k), the top_k experts with the largest
  * logits x router^T (router: E x k), in falling order, of equals the lowest
- * number first; experts[m][top_k].  Logits are summed in binary64.
+ * number first; experts[m][top_k].  Logits are summed in binary64, equal rows of
+ * router in the same order; two that are nearer than its rounding (some k 2^-53 of
+ * their terms' magnitudes) may change places, and with m.
  * weights[m][top_k]: the softmax of a token's logits over all experts, or each
  * logit's sigmoid, at its choices; normalize != 0: divided by their sum.  A NaN
  * logit is below all others, and makes its token's weights NaN.  x and router

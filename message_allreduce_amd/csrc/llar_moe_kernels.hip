@@ -5,8 +5,8 @@
 namespace llar_ffn {
 
 // ---- the router's logits --------------------------------------------------------------
-// In binary64, so that which experts are chosen does not hang on the order of the
-// sums.  A workgroup takes 16 tokens by 16 experts and a share of k, its waves 128 k
+// In binary64: the choice is that of the exact sums unless two are within its rounding,
+// and equal rows of the router, summed in the same order, tie.  A workgroup takes 16 tokens by 16 experts and a share of k, its waves 128 k
 // at a time with all their loads in flight: lane (r, q) holds eight k of token r and
 // of expert r, widened, and the matrix unit multiplies four k at a time (which four
 // is the same for both).  k is shared between as many workgroups as the card holds:

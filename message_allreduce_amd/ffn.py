@@ -139,7 +139,8 @@ def moe_route(x, router, top_k, scoring="softmax", normalize=True, stream=None):
     """(weights, experts), (..., top_k) each: for every token of x (..., k) the ``top_k`` rows of ``router``
     (experts, k) with the largest products, in falling order, of equals the lowest number first (int32), and their
     ``scoring`` (float32): "softmax" over all experts, or each product's "sigmoid"; ``normalize``: divided by their
-    sum.  The products are summed in binary64."""
+    sum.  The products are summed in binary64; two that differ by less than its rounding may be taken in
+    either order, which may be another one with more tokens."""
     if scoring not in ("softmax", "sigmoid"):
         raise ValueError("unknown scoring %r (softmax or sigmoid)" % (scoring,))
     f = (_native or _setup()).moe_route
