@@ -158,8 +158,11 @@ def moe_ffn(x, experts, weights, w_gate, w_up, w_down, activation="silu", residu
     them; ``w_gate`` and ``w_up`` (E, n, k) with the same strides, ``w_down`` (E, outputs, n), contiguous along their
     last axis.  A number outside 0 .. E - 1 (an expert of another rank, a padded token) adds nothing; the output is
     then a partial one for the AllReduce.  With ``gate_scale``, ``up_scale`` (E, n) and ``down_scale`` (E, outputs),
-    float32, the weights are int8; x and the inner rows are quantised as ``quantize_rows`` does.  For a few tokens:
-    a chosen expert's weights are read once for every 64 of them."""
+    float32, the weights are int8; x and the inner rows are quantised as ``quantize_rows`` does.
+
+    The inner values of fp16 end at 65504 and are infinite beyond (``gated_ffn``'s do too); those of bf16, fp32 and
+    int8 weights have float32's range.  Made for a step's tokens: a chosen expert's weights are read once for every 64
+    of them, so 65 take as long as 64 and 1, and 128 twice as long as 64."""
     f = (_native or _setup()).moe_ffn
     args = (x, experts, weights, w_gate, w_up, w_down, gate_scale, up_scale, down_scale, activation, residual, out)
     r = NotImplemented if stream is not None else f(*args)

@@ -55,10 +55,10 @@ class Layer:
         w = torch.rand(m, top_k, generator=g, device=device) + 0.5
         self.weights = torch.where(torch.rand(m, top_k, generator=g, device=device) < 0.5, -w, w)
 
-    def call(self):
+    def call(self, **more):
         import message_allreduce_amd as llar
         scales = {"gate_scale": self.gate_scale, "up_scale": self.up_scale, "down_scale": self.down_scale} if self.int8 else {}
-        return llar.moe_ffn(self.x, self.experts, self.weights, self.gate, self.up, self.down, **scales)
+        return llar.moe_ffn(self.x, self.experts, self.weights, self.gate, self.up, self.down, **scales, **more)
 
 
 def rows_quantized(t):
