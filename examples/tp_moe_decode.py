@@ -14,8 +14,8 @@ channel, tokens and inner rows quantised on the way.
     python examples/tp_moe_decode.py [--ranks 8] [--hidden 4096] [--inner 8192] [--experts 64] [--top-k 8]
                                      [--tokens 1] [--split inner|experts] [--int8] [--steps 100]
 
-prints the difference from the same layer on one rank in binary32 and the time of a
-pass.
+prints the difference from the same layer on one rank in binary32, relative to its result
+(tokens and what the layer adds to them), and the time of a pass.
 """
 import argparse
 import os
@@ -86,7 +86,7 @@ class Layer:
 
 
 def run(ranks, hidden, inner, experts, top_k, tokens, split="inner", int8=False, steps=0):
-    """(device status, relative difference in the 2-norm of what the layer adds to x, seconds a pass)."""
+    """(device status, difference of the results in the 2-norm relative to theirs, x included, seconds a pass)."""
     layer = Layer(ranks, hidden, inner, experts, top_k, tokens, split, int8)
     x = torch.randn(tokens, hidden, device="cuda").bfloat16()
     y, want = layer.forward(x), layer.reference(x)
