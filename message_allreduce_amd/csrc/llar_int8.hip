@@ -25,7 +25,10 @@ Operand operand8(const llar_matrix* m) {
 
 // The tiles, or the kernel for few rows.  That one reads x anew for every 16 or 32
 // columns, so it has to give way where the columns are many against the rows, and with
-// more than 16 rows also where k is short against the columns.  Tile and few rows, us:
+// more than 16 rows also where they are few against k, which only a split of k, the
+// tiles', spreads over the card.  The bounds lie between these points, tile and few rows,
+// us; at two of them the slower one is taken (8 rows 1536 -> 11008 gated, 16 rows
+// 8192 -> 16384):
 //   3584 -> 8192          8 rows 11.8,  8.0   16 rows 12.0,  8.8   32 rows 12.8, 11.4
 //   8192 -> 3584, gated   8 rows 20.1, 13.4   16 rows 19.6, 15.4   32 rows 20.8, 19.7
 //   8192 -> 16384         8 rows 32.2, 27.0   16 rows 32.3, 33.4
