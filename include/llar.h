@@ -323,14 +323,15 @@ int llar_gated_ffn_backward(const llar_matrix* dh, const llar_matrix* x, const l
 
 /* ---- products of 8-bit whole numbers ------------------------------------ *
  * The same two products for serving with weights of half the bytes (they have
- * no backward pass): tokens and output channels are rows of whole numbers -127 .. 127 with one binary32
- * scale each.  Sums are whole numbers and exact (k up to 2^17 - 1); a sum times
- * both scales, the epilogue in binary32, one rounding to `dtype`.  Streams,
- * workspaces, overlap, errors and sizes as for the calls above. */
+ * no backward pass): tokens and output channels are rows of whole numbers
+ * -127 .. 127 with one binary32 scale each.  Sums are whole numbers and exact (k up
+ * to 2^17 - 1); a sum times its channel's scale, then its token's, and the epilogue
+ * in binary32, one rounding to `dtype`.  Streams, workspaces, overlap, errors and
+ * sizes as for the calls above. */
 
 /* scale[i] = max over j of |x[i][j]| / 127, rounded to binary32, and q[i][j] = the
  * whole number nearest to x[i][j] / scale[i], ties to even, at most 127 in
- * magnitude.  A row of zeros has scale 0 and zeros; a row with an infinity or
+ * magnitude.  A row of zeros, or of magnitudes below 2^-143, has scale 0 and zeros; a row with an infinity or
  * a NaN has scale NaN and zeros, so that what it is multiplied into is NaN.
  * x: any strides, of type dtype; q: int8, contiguous rows; scale: m contiguous.
  * Any number of rows up to 2^30 (past 2^22 to 2^26, by their length, in several launches). */

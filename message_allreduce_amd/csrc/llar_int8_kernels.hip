@@ -207,8 +207,8 @@ __global__ __launch_bounds__(kWaves * 64) void k_few_int8(GemmArgs a) {
 }
 
 // The same for one or two rows of values, quantised by every workgroup for itself
-// (cold weights bf16, 3584 -> 8192: one row 7.6 us, two 8.5; four rows would take 13.2,
-// against 2.9 + 7.8 with the quantisation before it):
+// (a call with weights that are not in the caches, bf16, 3584 -> 8192: one row 7.8 us, two
+// 9.4; four rows would take 13.2, against 11.3 with the quantisation before it):
 // the rows' loads go first, half of the weights' follow (all of them up to k = 4096),
 // and the maximum and the rounding take place while those are on their way.
 template <class Out, bool kGated, int kRows, int kWaves>

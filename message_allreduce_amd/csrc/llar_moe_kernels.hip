@@ -6,12 +6,13 @@ namespace llar_ffn {
 
 // ---- the router's logits --------------------------------------------------------------
 // In binary64: the choice is that of the exact sums unless two are within its rounding,
-// and equal rows of the router, summed in the same order, tie.  A workgroup takes 16 tokens by 16 experts and a share of k, its waves 128 k
-// at a time with all their loads in flight: lane (r, q) holds eight k of token r and
-// of expert r, widened, and the matrix unit multiplies four k at a time (which four
-// is the same for both).  k is shared between as many workgroups as the card holds:
-// 1 token, 64 experts, k 4096 bf16 4.6 us, the loads' latency; 64 tokens, 256 experts, k
-// 8192 11 us, of which the binary64 products are 3.4.
+// and equal rows of the router, summed in the same order, tie.  A workgroup takes 16
+// tokens by 16 experts and a share of k, its waves 128 k at a time with all their loads
+// in flight: lane (r, q) holds eight k of token r and of expert r, widened, and the
+// matrix unit multiplies four k at a time (which four is the same for both).  k is
+// shared between as many workgroups as the card holds: 1 token, 64 experts, k 4096 bf16
+// 4.5 us, the loads' latency; 64 tokens, 256 experts, k 8192 11 us, of which the binary64
+// products are 3.4.
 typedef double f64x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kRouteWaves = 4, kRouteSteps = 4, kRouteK = kRouteWaves * kRouteSteps * 32;
@@ -526,7 +527,8 @@ __global__ __launch_bounds__(kWaves * 64) void k_moe_up(MoeArgs a, int tiles, bo
 // chose the expert, as in the first kernel; when a wave leaves an expert it adds
 // their weighted sums to its own row of every such token in LDS.  No atomics: the
 // waves' rows are added in order.  Bound by reading the weights, and the inner rows
-// again by every workgroup: the same cases 15.3 us (4.4 TB/s), 88 (5.3) and 48 (4.9).
+// again by every workgroup, in bf16 two numbers each: the same cases 17 us (3.9 TB/s), 104
+// (4.5) and 48 (4.9).
 template <class E, int P, int NB, bool kValues>
 __device__ __forceinline__ void moe_down_rows(const MoeArgs& a, const char* const (&w)[P], int member, float factor,
                                               int count, int e, int n0, int k0, int k1, float* mine,
@@ -721,13 +723,13 @@ __global__ __launch_bounds__(256) void k_moe_join(MoeArgs a) {
 }
 
 // Eight waves a workgroup: two to four workgroups a CU cover each other's ends
-// (1 token, 8 of 64 experts 4096 x 1024 bf16: second kernel 15.1 us against 16.6 with
-// sixteen; 48 tokens, 8 experts 8192 x 3584 int8: first 99 against 107).  Sixteen where
+// (1 token, 8 of 64 experts 4096 x 1024 bf16: both kernels 46 us against 49 with sixteen
+// in the second; 48 tokens, 8 experts 8192 x 3584 int8: first 99 against 107).  Sixteen where
 // there are too few workgroups for that (4 tokens, 2 of 16 experts 2048 x 512 fp32 17.5
 // against 18.6).  And half the columns a workgroup where twice as many still get a CU
-// each (both kernels, 1 token bf16, 2 of 8 experts 8192 x 448: 22.6 us against 29.4; 64
-// tokens 4096 x 256 24.9 against 28.9; but 32 tokens 8192 x 448, 224 workgroups, 50.4
-// against 45.6).
+// each (both kernels, 1 token bf16, 2 of 8 experts 8192 x 448: 22.7 us against 29.4; 64
+// tokens 4096 x 256 26.8 against 31; but 32 tokens 8192 x 448, 224 workgroups, 52.2
+// against 47.2).
 template <class E, int P, int kWaves>
 hipError_t moe_up(const MoeArgs& a, bool values, bool by_choice, hipStream_t s) {
   const int64_t tiles = ((int64_t)a.N + 8 * P - 1) / (8 * P), groups = tiles * (by_choice ? a.T * a.top_k : a.E);
@@ -783,8 +785,9 @@ hipError_t moe_down(const MoeArgs& a, bool values, hipStream_t s) {
   return hipGetLastError();
 }
 // Every workgroup reads the inner rows again, so it takes 32 columns where that
-// leaves enough workgroups (48 tokens, 8 experts, 8192 outputs int8: 48 us against 58;
-// 8 tokens bf16 94 against 100; but 24 tokens with 4096 outputs 78 against 55).
+// leaves enough workgroups (both kernels, 2 of 8 experts 8192 x 3584: 48 tokens int8 152 us
+// against 163, 8 tokens bf16 253 against 261, 64 323 against 372; but 24 tokens, 4 of 32
+// experts 4096 x 1024, 183 against 154).
 bool moe_wide(int T, int64_t outs) { return T > 4 && outs >= 32 * 192; }
 
 template <class E>
@@ -801,7 +804,8 @@ hipError_t moe_down(const MoeArgs& a, bool values, hipStream_t s) {
 // 479 outputs int8 56 us, now 10.7 and 2.8 for the join; 1 token, 6 experts, 477 outputs
 // fp16 12.7, now 7.0 and 1.8).  The costs in us: an expert, a pair of chunks, and the join
 // with its launch.  From 128 column tiles on the weights' bytes are the bound, and a join
-// only adds to them (24 tokens, 4096 outputs bf16 56 us, shared by two 65 and 4.7).
+// only adds to them (24 tokens, 4 of 32 experts 4096 x 1024 bf16, both kernels 154 us, shared
+// by two 163).
 int moe_parts(int T, int64_t n, int64_t outs, int64_t experts, int top_k, int es) {
   const int64_t tiles = (outs + 15) / 16, choices = (int64_t)T * top_k;
   if (moe_wide(T, outs) || choices == 0 || n == 0 || tiles == 0) return 1;
