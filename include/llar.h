@@ -331,8 +331,9 @@ int llar_gated_ffn_backward(const llar_matrix* dh, const llar_matrix* x, const l
 
 /* scale[i] = max over j of |x[i][j]| / 127, rounded to binary32, and q[i][j] = the
  * whole number nearest to x[i][j] / scale[i], ties to even, at most 127 in
- * magnitude.  A row of zeros, or of magnitudes below 2^-143, has scale 0 and zeros; a row with an infinity or
- * a NaN has scale NaN and zeros, so that what it is multiplied into is NaN.
+ * magnitude.  A row of zeros, or of magnitudes below 2^-143, has scale 0 and zeros;
+ * a row with an infinity or a NaN has scale NaN and zeros, so that what it is
+ * multiplied into is NaN.
  * x: any strides, of type dtype; q: int8, contiguous rows; scale: m contiguous.
  * Any number of rows up to 2^30 (past 2^22 to 2^26, by their length, in several launches). */
 int llar_quantize_rows(const llar_matrix* x, const llar_matrix* q, float* scale, llar_dtype dtype, void* stream);

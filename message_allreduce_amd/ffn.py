@@ -103,8 +103,8 @@ def gated_ffn_backward(dh, x, w_gate, w_up, gate, up, activation="silu", input_g
 def quantize_rows(x, stream=None):
     """(q, scale): ``scale`` (float32) the largest magnitude of each row of x (..., k) over 127, ``q`` (int8, x's
     shape) the nearest whole numbers to ``x / scale``, ties to even.  Tokens are quantised so before
-    ``linear_int8``, and a weight's output channels, which are its rows.  A row of zeros (or below 2^-143) has scale 0; one with an
-    infinity or a NaN has scale NaN, and so do the products it enters."""
+    ``linear_int8``, and a weight's output channels, which are its rows.  A row of zeros, or of magnitudes below 2^-143,
+    has scale 0; one with an infinity or a NaN has scale NaN, and so do the products it enters."""
     f = (_native or _setup()).quantize_rows
     r = NotImplemented if stream is not None else f(x)
     return r if r is not NotImplemented else _elsewhere(x, stream, f, x)
